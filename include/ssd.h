@@ -457,6 +457,178 @@ ssd_status ssd_conv1d_silu(const ssd_conv_problem *prob, const void *xbc, const 
                            const int32_t *cu_seqlens, void *x, void *B, void *C,
                            void *history_out, void *stream);
 
+/* Activation checkpoints in 8 bits: what a training step keeps of an
+ * activation between its forward and its backward pass, 33 bytes for 32
+ * channels instead of 64 (bf16) or 128 (fp32).
+ *
+ * A checkpoint of a (rows, channels) tensor has one signed byte per element
+ * and one unsigned byte per block of 32 consecutive channels of a row (the
+ * last block of a row may be short). A block's elements share a step, a power
+ * of two:
+ *   step  = 2^s, s the least integer >= -125 for which the block's largest
+ *           magnitude, divided by the step, rounds to at most 127
+ *   q     = the element / step, rounded to nearest, ties to even
+ *   byte  = s + 127 (2 .. 249)
+ * An element is thus off by at most step / 2, and its value q * step is exact
+ * in bf16 and fp32 (but magnitudes from 127.5 * 2^121 on, the last 0.4% of the
+ * range, round to 2^128 and read as infinity). A block that holds an infinity or NaN has byte 255 and q
+ * = 0, and all of its values read as NaN. Values of bytes other than these
+ * are unspecified, but never cause an out-of-bounds access.
+ *   q          (rows, channels) int8, contiguous, 8-byte aligned
+ *   exponents  (rows, ceil(channels / 32)) uint8, contiguous */
+typedef struct ssd_checkpoint {
+  int8_t *q;
+  uint8_t *exponents;
+} ssd_checkpoint;
+
+/* Whole tensors to and from checkpoints. The tensor has `rows` rows of
+ * `channels` elements (a multiple of 8), `stride` elements apart (>= channels,
+ * a multiple of 16 bytes, at most 2^31 - 1), and is 16-byte aligned; rows up
+ * to 2^31 - 1, flags 0, dtype F32 or BF16. ssd_checkpoint_save reads it and
+ * writes the checkpoint, ssd_checkpoint_load the other way round (dst must not
+ * overlap the checkpoint). Errors: SSD_ERR_INVALID_ARG (malformed sizes, NULL
+ * or misaligned pointers), SSD_ERR_UNSUPPORTED (outside the set above),
+ * SSD_ERR_HIP; nothing is enqueued on error. One kernel each, no allocation,
+ * no workspace. */
+typedef struct ssd_checkpoint_problem {
+  int64_t rows;
+  int64_t stride;
+  int32_t channels;
+  int32_t dtype;      /* an ssd_dtype value */
+  uint32_t flags;
+} ssd_checkpoint_problem;
+ssd_status ssd_checkpoint_save(const ssd_checkpoint_problem *prob, const void *src,
+                               const ssd_checkpoint *checkpoint, void *stream);
+ssd_status ssd_checkpoint_load(const ssd_checkpoint_problem *prob,
+                               const ssd_checkpoint *checkpoint, void *dst, void *stream);
+
+/* ssd_conv1d_silu with an 8-bit checkpoint of its input (tokens, ch):
+ *   xbc given: the front as above, which also writes the checkpoint of xbc;
+ *   xbc NULL:  x, B and C recomputed from the checkpoint's values, as the
+ *              backward pass needs them (in_stride is then not used, and
+ *              history_out must be NULL: the exact inputs are not there).
+ * Every other argument, the layouts and the errors are those of
+ * ssd_conv1d_silu. */
+ssd_status ssd_conv1d_silu_checkpoint(const ssd_conv_problem *prob, const void *xbc,
+                                      const ssd_checkpoint *checkpoint, const float *weight,
+                                      const float *bias, const void *history_in,
+                                      const int32_t *cu_seqlens, void *x, void *B, void *C,
+                                      void *history_out, void *stream);
+
+/* The convolution front backwards: gradients of a loss with respect to its
+ * inputs, given those with respect to x, B, C and history_out. With e =
+ * [history rows, inputs] of a sequence of L tokens, pre as above and silu'(v)
+ * = sigmoid(v) (1 + v (1 - sigmoid(v))):
+ *   g[t, c]       = dout[t, c] * silu'(pre[t, c])
+ *   de[j, c]      = sum_k weight[c, k] * g[j - k, c]   (0 <= j - k < L)
+ *                   + dhistory_out[j - L, c]           (j >= L)
+ *   dweight[c, k] = sum over all sequences and t of g[t, c] * e[t + k, c]
+ *   dbias[c]      = sum over all sequences and t of g[t, c]
+ * de of the history rows is dhistory, that of the tokens dxbc. pre is
+ * recomputed from xbc or from an 8-bit checkpoint of it (the gradients are
+ * then those at the checkpoint's values); the forward outputs are not needed.
+ * Problem: as for ssd_conv1d_silu. Arguments (device pointers, 16-byte aligned
+ * where listed):
+ *   xbc, weight, bias, history_in, cu_seqlens   the forward inputs
+ *   checkpoint   of xbc, with xbc NULL; NULL where xbc is given
+ *   dx, dB, dC   (tokens, x_dim | bc_dim | bc_dim) dtype, aligned
+ *   dhistory_out (batch | num_seqs, width - 1, ch) dtype, aligned, NULL = zero
+ *   dxbc         row t at dxbc + t * dxbc_stride, channels [0, ch)  dtype (out),
+ *                aligned; dxbc_stride >= ch, a multiple of 16 bytes
+ *   dweight      (ch, width) fp32 (out)
+ *   dbias        (ch) fp32 (out), NULL = not written; without a bias it is the
+ *                gradient at zero
+ *   dhistory     (batch | num_seqs, width - 1, ch) dtype (out), aligned, NULL =
+ *                not written; without a history it is the gradient at zeros
+ *   workspace    at least ssd_conv1d_silu_backward_workspace_size() bytes,
+ *                256-byte aligned; contents on entry do not matter
+ * dweight and dbias are zero when there are no tokens. Sums are taken in a
+ * fixed order: equal calls give equal bits. Outputs must not overlap inputs
+ * or each other. Errors as for ssd_conv1d_silu, and SSD_ERR_WORKSPACE. */
+ssd_status ssd_conv1d_silu_backward_workspace_size(const ssd_conv_problem *prob, size_t *bytes);
+ssd_status ssd_conv1d_silu_backward(const ssd_conv_problem *prob, const void *xbc,
+                                    const ssd_checkpoint *checkpoint, const float *weight,
+                                    const float *bias, const void *history_in,
+                                    const int32_t *cu_seqlens, const void *dx, const void *dB,
+                                    const void *dC, const void *dhistory_out, void *dxbc,
+                                    int32_t dxbc_stride, float *dweight, float *dbias,
+                                    void *dhistory, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Group norm with SiLU, channels last: what stands between the layer's output
+ * and the output projection. Statistics are taken per token over groups of
+ * consecutive channels (never over tokens, so the layer stays causal). With
+ * silu(v) = v / (1 + exp(-v)), n = channels / groups, per token and group:
+ *   u   = x * silu(z)  (z given, default)  or  x
+ *   mu  = mean of u with SSD_NORM_CENTER, else 0
+ *   h   = (u - mu) / sqrt(mean of (u - mu)^2 + eps)
+ *   v   = h * weight + bias
+ *   out = v                 (z given, default: the gate, then the norm)
+ *       = v * silu(z)       (z given, SSD_NORM_BEFORE_GATE)
+ *       = silu(v)           (no z)
+ * One token per sequence (decoding) is the same call with few tokens.
+ *
+ * Problem: tokens >= 0; channels a multiple of groups; the group size a
+ * multiple of 8 up to 16384; dtype F32 or BF16 of x, z, out and their
+ * gradients; flags 0 or SSD_NORM_* bits; eps finite and >= 0; strides in
+ * elements between token rows, each >= channels, at most 2^31 - 1 and a
+ * multiple of 16 bytes (that of a tensor that is not given is not looked at).
+ * Arguments (device pointers owned by the caller, 16-byte aligned where
+ * listed):
+ *   x            rows at x_stride    dtype, aligned
+ *   z            rows at z_stride    dtype, aligned, NULL = no gate
+ *   weight, bias (channels) fp32, NULL = ones, zeros
+ *   out          rows at out_stride  dtype (out), aligned
+ *   x_checkpoint, z_checkpoint   8-bit checkpoints (tokens, channels) of x and
+ *                z, written on the way; both, or (without z) that of x, or
+ *                neither (NULL)
+ *   stream       a hipStream_t (NULL = the default stream)
+ * Arithmetic and sums are fp32 (squares overflow above about 1e18); bf16
+ * outputs are rounded once, to nearest even. Outputs must not overlap inputs
+ * or each other. Errors: SSD_ERR_INVALID_ARG (malformed sizes, NULL or
+ * misaligned pointers), SSD_ERR_UNSUPPORTED (outside the set above),
+ * SSD_ERR_HIP; nothing is enqueued on error. No allocation, no workspace. */
+#define SSD_NORM_CENTER 1u      /* subtract the group's mean */
+#define SSD_NORM_BEFORE_GATE 2u /* out = (norm(x) * weight + bias) * silu(z) */
+typedef struct ssd_norm_problem {
+  int64_t x_stride, z_stride, out_stride, dx_stride, dz_stride;
+  int32_t tokens, channels, groups;
+  int32_t dtype;      /* an ssd_dtype value */
+  uint32_t flags;
+  float eps;
+} ssd_norm_problem;
+ssd_status ssd_group_norm_silu(const ssd_norm_problem *prob, const void *x, const void *z,
+                               const float *weight, const float *bias, void *out,
+                               const ssd_checkpoint *x_checkpoint,
+                               const ssd_checkpoint *z_checkpoint, void *stream);
+
+/* Its backward pass. With dv = dout, dout * silu(z) or dout * silu'(v) (the
+ * three forms above in turn), g = dv * weight and means over a token's group:
+ *   dweight = sum over tokens of dv * h,  dbias = sum over tokens of dv
+ *   du = (g - [SSD_NORM_CENTER] mean(g) - h * mean(g * h)) / sqrt(... + eps)
+ *   dx = du * silu(z), dz = du * x * silu'(z)     (the gate, then the norm)
+ *   dx = du,           dz = dout * v * silu'(z)   (SSD_NORM_BEFORE_GATE)
+ *   dx = du                                       (no z)
+ * The statistics are recomputed from x and z, or from 8-bit checkpoints of
+ * them (x and z NULL; the gradients are then those at the checkpoints'
+ * values). dout has rows at out_stride, dx and dz at dx_stride and dz_stride
+ * (dtype, 16-byte aligned; dz only with a gate). dweight and dbias are
+ * (channels) fp32, NULL = not written; without weight or bias they are the
+ * gradients at ones or zeros, and without tokens zero. workspace: at least
+ * ssd_group_norm_silu_backward_workspace_size() bytes, 256-byte aligned
+ * (needed with dweight or dbias only); contents on entry do not matter. Sums
+ * are taken in a fixed order: equal calls give equal bits. Outputs must not
+ * overlap inputs or each other. Errors as above, and SSD_ERR_WORKSPACE. */
+ssd_status ssd_group_norm_silu_backward_workspace_size(const ssd_norm_problem *prob,
+                                                       size_t *bytes);
+ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *prob, const void *dout,
+                                        const void *x, const void *z,
+                                        const ssd_checkpoint *x_checkpoint,
+                                        const ssd_checkpoint *z_checkpoint, const float *weight,
+                                        const float *bias, void *dx, void *dz, float *dweight,
+                                        float *dbias, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
 /* Static text for a status code. */
 const char *ssd_status_string(ssd_status status);
 

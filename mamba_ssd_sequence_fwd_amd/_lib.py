@@ -21,6 +21,8 @@ SSD_DTYPE_F32, SSD_DTYPE_BF16 = 0, 1
 SSD_FLAG_GENERIC_KERNELS = 1
 SSD_FLAG_UNFUSED = 2
 SSD_FLAG_PER_SEQUENCE = 4
+SSD_NORM_CENTER, SSD_NORM_BEFORE_GATE = 1, 2
+CHECKPOINT_BLOCK = 32   # channels that share a scale in an 8-bit checkpoint
 
 
 class SSDError(RuntimeError):
@@ -62,6 +64,25 @@ class ConvProblem(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class NormProblem(ctypes.Structure):
+    _fields_ = [("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+                ("dz_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("eps", ctypes.c_float)]
+
+
+class CheckpointProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("stride", ctypes.c_int64),
+                ("channels", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+class CheckpointArg(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("exponents", ctypes.c_void_p)]
+
+
 MAX_STAGES = 12
 
 
@@ -83,6 +104,10 @@ EXPORTED = ("ssd_validate", "ssd_validate_cu_seqlens", "ssd_workspace_size",
             "ssd_forward_timed", "ssd_step",
             "ssd_selective_scan", "ssd_conv1d_silu",
             "ssd_backward_workspace_size", "ssd_backward", "ssd_backward_timed",
+            "ssd_conv1d_silu_checkpoint", "ssd_conv1d_silu_backward_workspace_size",
+            "ssd_conv1d_silu_backward", "ssd_group_norm_silu",
+            "ssd_group_norm_silu_backward_workspace_size", "ssd_group_norm_silu_backward",
+            "ssd_checkpoint_save", "ssd_checkpoint_load",
             "ssd_get_workspace_layout",
             "ssd_status_string", "ssd_last_error_detail")
 
@@ -115,6 +140,19 @@ def load(path: str = LIB_PATH):
         lib.ssd_forward_dt_softplus.argtypes = [P] + [vp] * 12 + [ctypes.c_size_t, vp]
         lib.ssd_selective_scan.argtypes = [ctypes.POINTER(ScanProblem)] + [vp] * 10
         lib.ssd_conv1d_silu.argtypes = [ctypes.POINTER(ConvProblem)] + [vp] * 10
+        CV, NM = ctypes.POINTER(ConvProblem), ctypes.POINTER(NormProblem)
+        KP, KA = ctypes.POINTER(CheckpointProblem), ctypes.POINTER(CheckpointArg)
+        szp = ctypes.POINTER(ctypes.c_size_t)
+        lib.ssd_conv1d_silu_checkpoint.argtypes = [CV, vp, KA] + [vp] * 9
+        lib.ssd_conv1d_silu_backward_workspace_size.argtypes = [CV, szp]
+        lib.ssd_conv1d_silu_backward.argtypes = ([CV, vp, KA] + [vp] * 9 + [ctypes.c_int32]
+                                                 + [vp] * 4 + [ctypes.c_size_t, vp])
+        lib.ssd_group_norm_silu.argtypes = [NM] + [vp] * 5 + [KA, KA, vp]
+        lib.ssd_group_norm_silu_backward_workspace_size.argtypes = [NM, szp]
+        lib.ssd_group_norm_silu_backward.argtypes = ([NM] + [vp] * 3 + [KA, KA] + [vp] * 7
+                                                     + [ctypes.c_size_t, vp])
+        lib.ssd_checkpoint_save.argtypes = [KP, vp, KA, vp]
+        lib.ssd_checkpoint_load.argtypes = [KP, KA, vp, vp]
         lib.ssd_backward_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
         lib.ssd_backward.argtypes = [P] + [vp] * 18 + [ctypes.c_size_t, vp]
         lib.ssd_backward_timed.argtypes = ([P] + [vp] * 18 + [ctypes.c_size_t, vp,
@@ -498,6 +536,159 @@ def selective_scan(x, delta, A, B, C, D=None, initial_state=None, *, want_final_
     return y, final_state
 
 
+class Checkpoint:
+    """An activation kept in 8 bits between the forward and the backward pass.
+
+    ``q`` (..., channels) int8 and ``exponents`` (..., ceil(channels / 32))
+    uint8, both contiguous, channels a multiple of 8: an element's value is
+    ``q * 2**(exponent of its block of 32 channels - 127)``, within half a step
+    of what was saved (a block that held an infinity or NaN reads as NaN).
+    ``dtype`` is the dtype of the tensor it stands for (bfloat16 or float32).
+    Written by :func:`checkpoint_save`, :func:`conv1d_silu` and
+    :func:`group_norm_silu`; read by :meth:`load`, :func:`conv1d_silu` and the
+    backward functions.
+    """
+    __slots__ = ("q", "exponents", "dtype")
+
+    def __init__(self, q, exponents, dtype):
+        if dtype not in _DTYPES:
+            raise ValueError("a checkpoint stands for a bfloat16 or float32 tensor")
+        if q.dim() < 1 or q.dtype != torch.int8 or not q.is_contiguous():
+            raise ValueError("q must be a contiguous int8 tensor")
+        if q.shape[-1] < 8 or q.shape[-1] % 8 != 0:
+            raise ValueError("channels (%d) must be a multiple of 8" % q.shape[-1])
+        shape = q.shape[:-1] + (-(-q.shape[-1] // CHECKPOINT_BLOCK),)
+        if (exponents.shape != shape or exponents.dtype != torch.uint8
+                or not exponents.is_contiguous() or exponents.device != q.device):
+            raise ValueError("exponents must be a contiguous %s uint8 tensor on %s"
+                             % (tuple(shape), q.device))
+        self.q, self.exponents, self.dtype = q, exponents, dtype
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    @property
+    def device(self):
+        return self.q.device
+
+    @property
+    def nbytes(self):
+        return self.q.numel() + self.exponents.numel()
+
+    def arg(self):
+        return CheckpointArg(self.q.data_ptr(), self.exponents.data_ptr())
+
+    def load(self, *, out=None, stream=None):
+        """The values, in ``dtype`` (exact; see ssd_checkpoint_load), in a new
+        tensor or in ``out`` (rows may be a slice of wider rows)."""
+        dev, ch = self.q.device, self.q.shape[-1]
+        _same_device(dev, out=out)
+        _on_gpu(dev)
+        stream = _stream_of(dev, stream)
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty(self.q.shape, device=dev, dtype=self.dtype)
+            elif out.shape != self.q.shape or out.dtype != self.dtype:
+                raise ValueError("out must be %s %s" % (tuple(self.q.shape), self.dtype))
+            rows, stride = _rows_of(out, "out")
+            prob = CheckpointProblem(rows, stride, ch, _DTYPES[self.dtype], 0)
+            _check(load().ssd_checkpoint_load(ctypes.byref(prob), self.arg(), _ptr(out),
+                                              ctypes.c_void_p(stream.cuda_stream)),
+                   "ssd_checkpoint_load")
+        return out
+
+
+def _stream_of(dev, stream):
+    """The stream to launch on: torch's current one on ``dev``, or the caller's,
+    which must be one of that device."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError("the stream is on %s, but the tensors are on %s" % (stream.device, dev))
+    return stream
+
+
+def _row_stride(t):
+    """Elements between the token rows of ``t`` (the last axis one row, its
+    elements contiguous, all leading axes one evenly spaced sequence of rows),
+    or None if the rows are not laid out like that."""
+    ch = t.shape[-1]
+    if t.is_contiguous():
+        return ch
+    if t.stride(-1) != 1 and ch > 1:
+        return None
+    step, rows = None, 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * rows:
+            return None
+        rows *= size
+    step = ch if step is None else step
+    if step < ch or step * t.element_size() % 16 or t.data_ptr() % 16:
+        return None
+    return step
+
+
+def _rows_of(t, name):
+    """(rows, row stride) of an output, whose rows must be addressable as they are."""
+    stride = _row_stride(t)
+    if stride is None:
+        raise ValueError("the token rows of %s must be evenly spaced, with contiguous channels, "
+                         "16-byte aligned" % name)
+    return t.numel() // t.shape[-1], stride
+
+
+def _rows_in(t):
+    """``t`` (or a contiguous copy, where its rows cannot be addressed as they
+    are) and its row stride; called on the stream the kernel runs on."""
+    stride = _row_stride(t)
+    if stride is not None and t.data_ptr() % 16 == 0:
+        return t, stride
+    t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.shape[-1]
+
+
+def _checkpoint_out(given, shape, dtype, dev):
+    """The Checkpoint a call fills: a new one for True, or the caller's."""
+    if given is True:
+        blocks = -(-shape[-1] // CHECKPOINT_BLOCK)
+        return Checkpoint(torch.empty(shape, device=dev, dtype=torch.int8),
+                          torch.empty(shape[:-1] + (blocks,), device=dev, dtype=torch.uint8),
+                          dtype)
+    if not isinstance(given, Checkpoint):
+        raise ValueError("checkpoint must be True, False or a Checkpoint to fill")
+    if tuple(given.shape) != tuple(shape) or given.dtype != dtype or given.device != dev:
+        raise ValueError("the checkpoint to fill must be %s for %s on %s"
+                         % (tuple(shape), dtype, dev))
+    return given
+
+
+def checkpoint_save(t, *, checkpoint=True, stream=None):
+    """Keep tensor ``t`` (..., channels) in 8 bits (ssd_checkpoint_save): returns
+    a new :class:`Checkpoint`, or fills the one given. ``t`` is bfloat16 or
+    float32, channels a multiple of 8; its rows may be a slice of wider rows."""
+    _on_gpu(t.device)
+    if t.dim() < 1 or t.dtype not in _DTYPES:
+        raise ValueError("the tensor must be bfloat16 or float32 with a channel axis")
+    if t.shape[-1] < 8 or t.shape[-1] % 8 != 0:
+        raise ValueError("channels (%d) must be a multiple of 8" % t.shape[-1])
+    dev = t.device
+    stream = _stream_of(dev, stream)
+    with torch.cuda.stream(stream):
+        ck = _checkpoint_out(checkpoint, tuple(t.shape), t.dtype, dev)
+        t, stride = _rows_in(t)
+        prob = CheckpointProblem(t.numel() // t.shape[-1], stride, t.shape[-1],
+                                 _DTYPES[t.dtype], 0)
+        _check(load().ssd_checkpoint_save(ctypes.byref(prob), _ptr(t), ck.arg(),
+                                          ctypes.c_void_p(stream.cuda_stream)),
+               "ssd_checkpoint_save")
+    return ck
+
+
 def _check_offsets(cu, tokens: int):
     """Host check of packed offsets: 0 = cu[0] <= ... <= cu[-1] = tokens."""
     c = cu.detach().to("cpu", torch.int64)
@@ -508,10 +699,16 @@ def _check_offsets(cu, tokens: int):
 
 def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None, *,
                 want_history=True, x=None, B=None, C=None, history_out=None,
-                check_cu_seqlens=True, stream=None):
+                checkpoint=False, check_cu_seqlens=True, stream=None):
     """The convolution front (ssd_conv1d_silu): causal depthwise conv1d over
     the packed channels [x | B | C], then SiLU. Returns (x, B, C,
     history_out).
+
+    With ``checkpoint=True`` (or a :class:`Checkpoint` of xbc's shape to fill)
+    the call also keeps xbc in 8 bits on the way and returns that Checkpoint
+    as a fifth value. xbc may itself be a Checkpoint: x, B and C are then
+    recomputed from its values in its dtype, as the backward pass needs them,
+    and history_out is None.
 
     xbc is (batch, L, ch) (dense) or (tokens, ch) with ``cu_seqlens``, ch =
     x_dim + 2 * bc_dim, channels contiguous; its rows may be a slice of wider
@@ -519,10 +716,22 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
     float32; history (sequences, K - 1, ch) in xbc's dtype or None. Outputs
     have xbc's leading shape with x_dim, bc_dim, bc_dim channels.
     """
+    kept = xbc if isinstance(xbc, Checkpoint) else None
+    if kept is not None:
+        if checkpoint is not False:
+            raise ValueError("xbc is a checkpoint already")
+        if history_out is not None:
+            raise ValueError("a checkpoint does not hold the exact history_out")
+        want_history = False
+        dtype, xbc = kept.dtype, kept.q
+    else:
+        dtype = xbc.dtype
+        if isinstance(checkpoint, Checkpoint):
+            _same_device(xbc.device, checkpoint=checkpoint.q)
     _same_device(xbc.device, weight=weight, bias=bias, history=history, x=x, B=B, C=C,
                  history_out=history_out)
     _on_gpu(xbc.device)
-    if xbc.dtype not in _DTYPES:
+    if dtype not in _DTYPES:
         raise ValueError("xbc must be bfloat16 or float32")
     ch = x_dim + 2 * bc_dim
     if xbc.shape[-1] != ch or xbc.stride(-1) != 1:
@@ -556,14 +765,14 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
     if bias is not None and (tuple(bias.shape) != (ch,) or bias.dtype != torch.float32):
         raise ValueError("bias must be (%d,) float32" % ch)
     hshape = (nseq, K - 1, ch)
-    if history is not None and (tuple(history.shape) != hshape or history.dtype != xbc.dtype):
-        raise ValueError("history must be %s %s" % (hshape, xbc.dtype))
+    if history is not None and (tuple(history.shape) != hshape or history.dtype != dtype):
+        raise ValueError("history must be %s %s" % (hshape, dtype))
     for name, t, shape in (("x", x, lead + (x_dim,)), ("B", B, lead + (bc_dim,)),
                            ("C", C, lead + (bc_dim,)), ("history_out", history_out, hshape)):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != xbc.dtype
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype
                               or not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous %s %s tensor" % (name, shape, xbc.dtype))
-    prob = ConvProblem(batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[xbc.dtype], 0)
+            raise ValueError("%s must be a contiguous %s %s tensor" % (name, shape, dtype))
+    prob = ConvProblem(batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     # copies and outputs are made on the stream the kernel runs on (see step())
@@ -572,13 +781,26 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
         bias = bias.contiguous() if bias is not None else None
         history = history.contiguous() if history is not None else None
         if x is None:
-            x = torch.empty(lead + (x_dim,), device=dev, dtype=xbc.dtype)
+            x = torch.empty(lead + (x_dim,), device=dev, dtype=dtype)
         if B is None:
-            B = torch.empty(lead + (bc_dim,), device=dev, dtype=xbc.dtype)
+            B = torch.empty(lead + (bc_dim,), device=dev, dtype=dtype)
         if C is None:
-            C = torch.empty(lead + (bc_dim,), device=dev, dtype=xbc.dtype)
+            C = torch.empty(lead + (bc_dim,), device=dev, dtype=dtype)
         if history_out is None and want_history:
-            history_out = torch.empty(hshape, device=dev, dtype=xbc.dtype)
+            history_out = torch.empty(hshape, device=dev, dtype=dtype)
+        if checkpoint is not False:
+            save = _checkpoint_out(checkpoint, tuple(xbc.shape), dtype, dev)
+            _check(load().ssd_conv1d_silu_checkpoint(
+                ctypes.byref(prob), _ptr(xbc), save.arg(), _ptr(weight), _ptr(bias),
+                _ptr(history), _ptr(cu_dev), _ptr(x), _ptr(B), _ptr(C), _ptr(history_out),
+                ctypes.c_void_p(stream.cuda_stream)), "ssd_conv1d_silu_checkpoint")
+            return x, B, C, history_out, save
+        if kept is not None:
+            _check(load().ssd_conv1d_silu_checkpoint(
+                ctypes.byref(prob), None, kept.arg(), _ptr(weight), _ptr(bias), _ptr(history),
+                _ptr(cu_dev), _ptr(x), _ptr(B), _ptr(C), None,
+                ctypes.c_void_p(stream.cuda_stream)), "ssd_conv1d_silu_checkpoint")
+            return x, B, C, None
     _check(load().ssd_conv1d_silu(ctypes.byref(prob), _ptr(xbc), _ptr(weight), _ptr(bias),
                                   _ptr(history), _ptr(cu_dev), _ptr(x), _ptr(B), _ptr(C),
                                   _ptr(history_out), ctypes.c_void_p(stream.cuda_stream)),
@@ -679,3 +901,224 @@ def backward(x, dt, A, B, C, D, initial_state, dy, dfinal_state=None, chunk_size
     """SSD backward pass (ssd_backward): a dict of gradients (see BackwardPlan)."""
     return BackwardPlan(x, dt, A, B, C, D, initial_state, dy, dfinal_state, chunk_size,
                         cu_seqlens).run()
+
+
+def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens=None, *,
+                         dhistory_out=None, dxbc=None, check_cu_seqlens=True, stream=None):
+    """The convolution front backwards (ssd_conv1d_silu_backward): a dict with
+    dxbc, dweight, dbias and dhistory (None without a history).
+
+    xbc, weight, bias, history and cu_seqlens as given to :func:`conv1d_silu`
+    (xbc may be a :class:`Checkpoint` of it). dx, dB and dC are the gradients
+    of its outputs, as :func:`backward` returns them or with their channels
+    flattened; dhistory_out that of history_out, or None. dxbc (optional
+    output, shaped like xbc) may be a slice of wider rows. dbias without a
+    bias is the gradient at zero.
+    """
+    kept = xbc if isinstance(xbc, Checkpoint) else None
+    dtype = xbc.dtype
+    u = kept.q if kept is not None else xbc
+    dev = u.device
+    _same_device(dev, weight=weight, bias=bias, dx=dx, dB=dB, dC=dC, history=history,
+                 dhistory_out=dhistory_out, dxbc=dxbc)
+    _on_gpu(dev)
+    if dtype not in _DTYPES:
+        raise ValueError("xbc must be bfloat16 or float32")
+    packed = cu_seqlens is not None
+    if u.dim() != (2 if packed else 3):
+        raise ValueError("packed xbc must be (tokens, channels)" if packed else
+                         "dense xbc must be (batch, seqlen, channels)")
+    lead, ch = tuple(u.shape[:-1]), int(u.shape[-1])
+    if packed:
+        batch, L, num_seqs = 1, lead[0], int(cu_seqlens.numel()) - 1
+        nseq = num_seqs
+        if num_seqs < 1:
+            raise ValueError("cu_seqlens must hold at least two offsets")
+        if check_cu_seqlens or cu_seqlens.device.type == "cpu":
+            _check_offsets(cu_seqlens, L)
+    else:
+        (batch, L), num_seqs = lead, 0
+        nseq = batch
+    dims = []
+    for name, t in (("dx", dx), ("dB", dB), ("dC", dC)):
+        if tuple(t.shape[:len(lead)]) != lead or t.dtype != dtype or t.dim() <= len(lead):
+            raise ValueError("%s must be %s + channels, %s" % (name, lead, dtype))
+        n = 1
+        for size in t.shape[len(lead):]:
+            n *= size
+        dims.append(n)
+    x_dim, bc_dim = dims[0], dims[1]
+    if dims[2] != bc_dim or x_dim + 2 * bc_dim != ch:
+        raise ValueError("dx, dB, dC have %d, %d, %d channels, but xbc has %d"
+                         % (dims[0], dims[1], dims[2], ch))
+    K = int(weight.shape[1]) if weight.dim() == 2 else 0
+    if tuple(weight.shape) != (ch, K) or weight.dtype != torch.float32:
+        raise ValueError("weight must be (%d, K) float32" % ch)
+    if bias is not None and (tuple(bias.shape) != (ch,) or bias.dtype != torch.float32):
+        raise ValueError("bias must be (%d,) float32" % ch)
+    hshape = (nseq, K - 1, ch)
+    for name, t in (("history", history), ("dhistory_out", dhistory_out)):
+        if t is not None and (tuple(t.shape) != hshape or t.dtype != dtype):
+            raise ValueError("%s must be %s %s" % (name, hshape, dtype))
+    if dxbc is not None and (tuple(dxbc.shape) != lead + (ch,) or dxbc.dtype != dtype):
+        raise ValueError("dxbc must be %s %s" % (lead + (ch,), dtype))
+    stream = _stream_of(dev, stream)
+    # copies, outputs and the workspace are made on the stream the kernels run on
+    with torch.cuda.stream(stream):
+        cu_dev = cu_seqlens.to(device=dev, dtype=torch.int32).contiguous() if packed else None
+        if dxbc is None:
+            dxbc = torch.empty(lead + (ch,), device=dev, dtype=dtype)
+        _, out_stride = _rows_of(dxbc, "dxbc")
+        in_stride = ch
+        if kept is None:
+            u, in_stride = _rows_in(u)
+        dx, dB, dC = (t.contiguous() for t in (dx, dB, dC))
+        weight = weight.contiguous()
+        bias, history, dhistory_out = (t.contiguous() if t is not None else None
+                                       for t in (bias, history, dhistory_out))
+        dweight = torch.empty((ch, K), device=dev, dtype=torch.float32)
+        dbias = torch.empty(ch, device=dev, dtype=torch.float32)
+        dhistory = (torch.empty(hshape, device=dev, dtype=dtype) if history is not None else None)
+        prob = ConvProblem(batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
+        n = ctypes.c_size_t(0)
+        _check(load().ssd_conv1d_silu_backward_workspace_size(ctypes.byref(prob), ctypes.byref(n)),
+               "ssd_conv1d_silu_backward_workspace_size")
+        ws = torch.empty(max(n.value, 256), device=dev, dtype=torch.uint8)
+        _check(load().ssd_conv1d_silu_backward(
+            ctypes.byref(prob), None if kept is not None else _ptr(u),
+            kept.arg() if kept is not None else None, _ptr(weight), _ptr(bias), _ptr(history),
+            _ptr(cu_dev), _ptr(dx), _ptr(dB), _ptr(dC), _ptr(dhistory_out), _ptr(dxbc),
+            out_stride, _ptr(dweight), _ptr(dbias), _ptr(dhistory), _ptr(ws),
+            ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream.cuda_stream)),
+            "ssd_conv1d_silu_backward")
+    return dict(dxbc=dxbc, dweight=dweight, dbias=dbias, dhistory=dhistory)
+
+
+def _norm_problem(shape, dtype, groups, eps, center, norm_before_gate):
+    channels = int(shape[-1])
+    tokens = 1
+    for size in shape[:-1]:
+        tokens *= int(size)
+    flags = (SSD_NORM_CENTER if center else 0) | (SSD_NORM_BEFORE_GATE if norm_before_gate else 0)
+    return NormProblem(channels, channels, channels, channels, channels, tokens, channels,
+                       groups, _DTYPES[dtype], flags, eps)
+
+
+def _affine(weight, bias, channels):
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and (tuple(t.shape) != (channels,) or t.dtype != torch.float32):
+            raise ValueError("%s must be (%d,) float32" % (name, channels))
+
+
+def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, center=False,
+                    norm_before_gate=False, checkpoint=False, out=None, stream=None):
+    """Group norm with SiLU, channels last (ssd_group_norm_silu): the gate
+    between the layer's output and the output projection. Returns ``out``.
+
+    x (..., channels), bfloat16 or float32; z like x or None; weight, bias
+    (channels,) float32 or None. Every token is normalised over ``groups``
+    groups of consecutive channels (a multiple of 8 up to 16384 each), by its
+    root mean square, or with ``center`` by its mean and standard deviation:
+    norm(x * silu(z)) * weight + bias; with ``norm_before_gate``
+    (norm(x) * weight + bias) * silu(z); without z silu(norm(x) * weight + bias).
+    x, z and out may be slices of wider rows. With ``checkpoint=True`` x and z
+    are also kept in 8 bits on the way: returns (out, x's Checkpoint, z's or
+    None); a pair of Checkpoints is filled instead.
+    """
+    if x.dim() < 1 or x.shape[-1] < 1 or x.dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float32 with a channel axis")
+    dev, dtype, shape = x.device, x.dtype, tuple(x.shape)
+    _same_device(dev, weight=weight, bias=bias, z=z, out=out)
+    _on_gpu(dev)
+    for name, t in (("z", z), ("out", out)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+            raise ValueError("%s must be %s %s" % (name, shape, dtype))
+    if norm_before_gate and z is None:
+        raise ValueError("norm_before_gate needs z")
+    _affine(weight, bias, shape[-1])
+    prob = _norm_problem(shape, dtype, groups, eps, center, norm_before_gate)
+    stream = _stream_of(dev, stream)
+    # copies and outputs are made on the stream the kernel runs on
+    with torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(shape, device=dev, dtype=dtype)
+        _, prob.out_stride = _rows_of(out, "out")
+        kx = kz = None
+        if checkpoint is not False:
+            gx, gz = (True, True) if checkpoint is True else checkpoint
+            kx = _checkpoint_out(gx, shape, dtype, dev)
+            kz = _checkpoint_out(gz, shape, dtype, dev) if z is not None else None
+        x, prob.x_stride = _rows_in(x)
+        if z is not None:
+            z, prob.z_stride = _rows_in(z)
+        weight = weight.contiguous() if weight is not None else None
+        bias = bias.contiguous() if bias is not None else None
+        _check(load().ssd_group_norm_silu(
+            ctypes.byref(prob), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(out),
+            kx.arg() if kx is not None else None, kz.arg() if kz is not None else None,
+            ctypes.c_void_p(stream.cuda_stream)), "ssd_group_norm_silu")
+    return out if checkpoint is False else (out, kx, kz)
+
+
+def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5,
+                             center=False, norm_before_gate=False, dx=None, dz=None,
+                             stream=None):
+    """:func:`group_norm_silu` backwards (ssd_group_norm_silu_backward): a dict
+    with dx, dz (None without z), dweight and dbias (each None without the
+    parameter).
+
+    The forward inputs and options as given there; x and z may both be
+    :class:`Checkpoint` of the inputs. dout, and the optional outputs dx and
+    dz, are shaped like x and may be slices of wider rows.
+    """
+    dtype, shape, dev = x.dtype, tuple(x.shape), x.device
+    if isinstance(x, Checkpoint) != isinstance(z, Checkpoint) and z is not None:
+        raise ValueError("x and z must both be tensors or both checkpoints")
+    kept = isinstance(x, Checkpoint)
+    _same_device(dev, dout=dout, weight=weight, bias=bias, z=z, dx=dx, dz=dz)
+    _on_gpu(dev)
+    if dout is None:
+        raise ValueError("dout is required")
+    if dtype not in _DTYPES or len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("x must be bfloat16 or float32 with a channel axis")
+    for name, t in (("dout", dout), ("z", z), ("dx", dx), ("dz", dz)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+            raise ValueError("%s must be %s %s" % (name, shape, dtype))
+    if z is None and (norm_before_gate or dz is not None):
+        raise ValueError("norm_before_gate and dz need z")
+    _affine(weight, bias, shape[-1])
+    prob = _norm_problem(shape, dtype, groups, eps, center, norm_before_gate)
+    n = ctypes.c_size_t(0)
+    if weight is not None or bias is not None:
+        _check(load().ssd_group_norm_silu_backward_workspace_size(ctypes.byref(prob),
+                                                                  ctypes.byref(n)),
+               "ssd_group_norm_silu_backward_workspace_size")
+    stream = _stream_of(dev, stream)
+    # copies, outputs and the workspace are made on the stream the kernels run on
+    with torch.cuda.stream(stream):
+        if dx is None:
+            dx = torch.empty(shape, device=dev, dtype=dtype)
+        if dz is None and z is not None:
+            dz = torch.empty(shape, device=dev, dtype=dtype)
+        _, prob.dx_stride = _rows_of(dx, "dx")
+        if dz is not None:
+            _, prob.dz_stride = _rows_of(dz, "dz")
+        dout, prob.out_stride = _rows_in(dout)
+        if not kept:
+            x, prob.x_stride = _rows_in(x)
+            if z is not None:
+                z, prob.z_stride = _rows_in(z)
+        dweight = (torch.empty(shape[-1], device=dev, dtype=torch.float32)
+                   if weight is not None else None)
+        dbias = (torch.empty(shape[-1], device=dev, dtype=torch.float32)
+                 if bias is not None else None)
+        weight = weight.contiguous() if weight is not None else None
+        bias = bias.contiguous() if bias is not None else None
+        ws = torch.empty(n.value, device=dev, dtype=torch.uint8) if n.value else None
+        _check(load().ssd_group_norm_silu_backward(
+            ctypes.byref(prob), _ptr(dout), None if kept else _ptr(x), None if kept else _ptr(z),
+            x.arg() if kept else None, z.arg() if kept and z is not None else None,
+            _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias), _ptr(ws),
+            ctypes.c_size_t(n.value), ctypes.c_void_p(stream.cuda_stream)),
+            "ssd_group_norm_silu_backward")
+    return dict(dx=dx, dz=dz, dweight=dweight, dbias=dbias)

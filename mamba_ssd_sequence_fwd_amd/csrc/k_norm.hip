@@ -1,0 +1,464 @@
+// k_norm.hip -- group norm with SiLU, channels last: what stands between the
+// SSD layer's output and the output projection, forward and backward.
+//
+// Per token and group of n channels, with s(z) = z / (1 + e^-z):
+//   u = x s(z) (gate first) or x;  mu = mean(u) if centred, else 0
+//   r = 1 / sqrt(mean((u - mu)^2) + eps);  h = (u - mu) r;  v = h w + b
+//   out = v (gate first),  v s(z) (gate last)  or  s(v) (no gate)
+// and backwards, dv being dout, dout s(z) or dout s'(v):
+//   dw += dv h;  db += dv;  g = dv w;  du = r (g - [mean(g)] - h mean(g h))
+//   dx = du s(z), dz = du x s'(z) (gate first);  dx = du, dz = dout v s'(z)
+//   (gate last);  dx = du (no gate)
+//
+// A row of a group is read once and held in registers by a team: a power of
+// two of lanes inside a wave for groups up to 512 channels (no barrier), one
+// workgroup for wider ones. Every lane owns 8 channels (16 bytes of bf16), R
+// times, and keeps them over all the rows it walks, so the affine weights are
+// loaded once and the gradients of the weights are summed in registers; each
+// workgroup writes one row of partial sums. The next row's loads are issued
+// before the current row's sums. All sums are fp32; the partial rows are added
+// in fp64. Squares are summed as they are: |u| above about 1e18 overflows.
+#include "norm.h"
+
+namespace ssd {
+
+namespace {
+
+// Where the inputs come from and what is kept of them.
+enum : int { kPlain = 0, kCkpt = 1 };
+
+constexpr int kTeamThreads = 256;  // workgroup of the in-wave teams
+constexpr int kMaxWaves = 16;
+
+template <int Ctrl>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(
+                 __builtin_amdgcn_update_dpp(0, __float_as_int(v), Ctrl, 0xf, 0xf, true));
+}
+
+// Sum over aligned teams of `team` lanes (a power of two up to 64), the same
+// bits on every lane: each step adds the two halves in both orders. Inside
+// rows of 16 by DPP (quad swaps, then mirrors of values equal per quad or
+// half row), across rows by lane exchanges.
+__device__ __forceinline__ float team_sum(float v, int team) {
+  constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
+  if (team > 1) v = dpp_add<kXor1>(v);
+  if (team > 2) v = dpp_add<kXor2>(v);
+  if (team > 4) v = dpp_add<kHalfMirror>(v);
+  if (team > 8) v = dpp_add<kMirror>(v);
+  if (team > 16) v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401f));
+  if (team > 32) v += __shfl_xor(v, 32);
+  return v;
+}
+
+// Sums of N values over the team. A workgroup team leaves each wave's sums in
+// LDS (two buffers taken in turn, so one barrier suffices) and every thread
+// adds the waves' in the same order.
+template <bool WIDE, int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], int team, float (*lds)[kMaxWaves * 4],
+                                          int &turn) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = team_sum(v[i], WIDE ? 64 : team);
+  if (WIDE) {
+    const int nw = team >> 6;
+    float *buf = lds[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[(threadIdx.x >> 6) * 4 + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+    for (int w = 0; w < nw; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += buf[w * 4 + i];
+  }
+}
+
+// The lane's place: its channels for each r and whether they exist (lanes
+// without channels load channel 0's and store nothing, so loads need no
+// branch).
+template <bool WIDE, int R>
+struct Place {
+  int c[R];
+  bool live[R];
+  __device__ __forceinline__ explicit Place(const NormArgs &a) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      int g, in;
+      if (WIDE) {
+        g = blockIdx.x;
+        in = (r * a.team + threadIdx.x) * 8;
+      } else {
+        const int per = kTeamThreads / a.team;
+        g = blockIdx.x * per + threadIdx.x / a.team;
+        in = (threadIdx.x & (a.team - 1)) * 8;
+      }
+      live[r] = g < a.G && in < a.gs;
+      c[r] = live[r] ? g * a.gs + in : 0;
+    }
+  }
+};
+
+template <int R>
+__device__ __forceinline__ void load_affine(const float *p, float otherwise, const int (&c)[R],
+                                            const bool (&live)[R], float (&v)[R][8]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[r][k] = p && live[r] ? p[c[r] + k] : otherwise;
+}
+
+template <typename T, int MODE, int CK, int R, bool WIDE>
+__global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm(NormArgs a) {
+  __shared__ float lds[2][kMaxWaves * 4];
+  const Place<WIDE, R> at(a);
+  float w[R][8], b[R][8];
+  load_affine(a.w, 1.f, at.c, at.live, w);
+  load_affine(a.b, 0.f, at.c, at.live, b);
+  constexpr bool kGated = MODE != kNoGate;
+  Row8<T> xr[R], zr[R];
+  auto fetch = [&](int row) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      xr[r].load(a.x, (size_t)row * a.x_stride + at.c[r]);
+      if (kGated) zr[r].load(a.z, (size_t)row * a.z_stride + at.c[r]);
+    }
+  };
+  int turn = 0;
+  int row = blockIdx.y;
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += gridDim.y) {
+    float x[R][8], z[R][8], u[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      xr[r].widen(x[r]);
+      if (kGated) zr[r].widen(z[r]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (!at.live[r]) x[r][k] = z[r][k] = 0.f;
+        u[r][k] = MODE == kGateFirst ? x[r][k] * silu(z[r][k]) : x[r][k];
+      }
+    }
+    if (row + (int)gridDim.y < a.rows) fetch(row + gridDim.y);
+    if (CK == kCkpt) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        store_ckpt(a.xk, (size_t)row, a.C, at.c[r], x[r], at.live[r]);
+        if (kGated) store_ckpt(a.zk, (size_t)row, a.C, at.c[r], z[r], at.live[r]);
+      }
+    }
+    if (a.center) {
+      float m[1] = {0.f};
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[0] += u[r][k];
+      team_sums<WIDE>(m, a.team, lds, turn);
+      const float mu = m[0] * a.inv_n;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[r][k] = at.live[r] ? u[r][k] - mu : 0.f;
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[0] += u[r][k] * u[r][k];
+    team_sums<WIDE>(q, a.team, lds, turn);
+    const float rs = 1.f / sqrtf(q[0] * a.inv_n + a.eps);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = u[r][k] * rs * w[r][k] + b[r][k];
+        o[k] = MODE == kGateFirst ? v : MODE == kGateLast ? v * silu(z[r][k]) : silu(v);
+      }
+      if (at.live[r]) Row8<T>::store(a.out, (size_t)row * a.out_stride + at.c[r], o);
+    }
+  }
+}
+
+template <typename T, int CK> struct NormRowOf { typedef Row8<T> type; };
+template <typename T> struct NormRowOf<T, kCkpt> { typedef RowQ8 type; };
+
+template <typename T>
+__device__ __forceinline__ void load_row(Row8<T> &r, const void *p, int64_t stride, const Ckpt &,
+                                         int, int row, int c) {
+  r.load(p, (size_t)row * stride + c);
+}
+__device__ __forceinline__ void load_row(RowQ8 &r, const void *, int64_t, const Ckpt &k, int C,
+                                         int row, int c) {
+  r.load(k, (size_t)row, C, c);
+}
+
+template <typename T, int MODE, int CK, int R, bool WIDE>
+__global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm_backward(NormArgs a) {
+  __shared__ float lds[2][kMaxWaves * 4];
+  const Place<WIDE, R> at(a);
+  float w[R][8], b[R][8], dw[R][8], db[R][8];
+  load_affine(a.w, 1.f, at.c, at.live, w);
+  load_affine(a.b, 0.f, at.c, at.live, b);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[r][k] = db[r][k] = 0.f;
+  constexpr bool kGated = MODE != kNoGate;
+  typename NormRowOf<T, CK>::type xr[R], zr[R];
+  Row8<T> dr[R];
+  auto fetch = [&](int row) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      load_row(xr[r], a.x, a.x_stride, a.xk, a.C, row, at.c[r]);
+      if (kGated) load_row(zr[r], a.z, a.z_stride, a.zk, a.C, row, at.c[r]);
+      dr[r].load(a.dout, (size_t)row * a.out_stride + at.c[r]);
+    }
+  };
+  int turn = 0;
+  int row = blockIdx.y;
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += gridDim.y) {
+    float x[R][8], sz[R][8], dsz[R][8], d[R][8], u[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float z[8];
+      xr[r].widen(x[r]);
+      if (kGated) zr[r].widen(z);
+      dr[r].widen(d[r]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (!at.live[r]) x[r][k] = z[k] = d[r][k] = 0.f;
+        if (kGated) {
+          const float s = sigmoid(z[k]);
+          sz[r][k] = z[k] * s;
+          dsz[r][k] = s * (1.f + z[k] * (1.f - s));
+        }
+        u[r][k] = MODE == kGateFirst ? x[r][k] * sz[r][k] : x[r][k];
+      }
+    }
+    if (row + (int)gridDim.y < a.rows) fetch(row + gridDim.y);
+    float mu = 0.f;
+    if (a.center) {
+      float m[1] = {0.f};
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[0] += u[r][k];
+      team_sums<WIDE>(m, a.team, lds, turn);
+      mu = m[0] * a.inv_n;
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        u[r][k] = at.live[r] ? u[r][k] - mu : 0.f;
+        q[0] += u[r][k] * u[r][k];
+      }
+    team_sums<WIDE>(q, a.team, lds, turn);
+    const float rs = 1.f / sqrtf(q[0] * a.inv_n + a.eps);
+    // u becomes h; v and g from here
+    float v[R][8], g[R][8], m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float h = u[r][k] * rs;
+        u[r][k] = h;
+        v[r][k] = h * w[r][k] + b[r][k];
+        float dv = d[r][k];
+        if (MODE == kGateLast) dv *= sz[r][k];
+        if (MODE == kNoGate) {
+          const float s = sigmoid(v[r][k]);
+          dv *= s * (1.f + v[r][k] * (1.f - s));
+        }
+        dw[r][k] += dv * h;
+        db[r][k] += dv;
+        g[r][k] = dv * w[r][k];
+        m[0] += g[r][k] * h;
+        m[1] += g[r][k];
+      }
+    team_sums<WIDE>(m, a.team, lds, turn);
+    const float mgh = m[0] * a.inv_n, mg = a.center ? m[1] * a.inv_n : 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float dx[8], dz[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float du = rs * (g[r][k] - mg - u[r][k] * mgh);
+        dx[k] = MODE == kGateFirst ? du * sz[r][k] : du;
+        if (MODE == kGateFirst) dz[k] = du * x[r][k] * dsz[r][k];
+        if (MODE == kGateLast) dz[k] = d[r][k] * v[r][k] * dsz[r][k];
+      }
+      if (at.live[r]) {
+        Row8<T>::store(a.dx, (size_t)row * a.dx_stride + at.c[r], dx);
+        if (kGated) Row8<T>::store(a.dz, (size_t)row * a.dz_stride + at.c[r], dz);
+      }
+    }
+  }
+  if (a.part) {
+    float *p = a.part + (size_t)blockIdx.y * 2 * a.C;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (at.live[r]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          p[at.c[r] + k] = dw[r][k];
+          p[a.C + at.c[r] + k] = db[r][k];
+        }
+      }
+  }
+}
+
+// Teams: lanes per group (in-wave) or threads per workgroup.
+struct Team {
+  bool wide;
+  int r, size, xblocks;
+};
+Team team_of(const NormArgs &a) {
+  Team t{};
+  const int lanes = a.gs / 8;
+  t.r = 1;
+  if (lanes <= 64) {
+    t.size = 1;
+    while (t.size < lanes) t.size *= 2;
+    const int per = kTeamThreads / t.size;
+    t.xblocks = (a.G + per - 1) / per;
+  } else {
+    t.wide = true;
+    t.r = lanes > 1024 ? 2 : 1;
+    t.size = ((lanes + t.r - 1) / t.r + 63) / 64 * 64;
+    t.xblocks = a.G;
+  }
+  return t;
+}
+
+// Workgroups along the rows: enough to fill the card a few times over.
+int row_blocks(const NormArgs &a, const Team &t) {
+  const int threads = t.wide ? t.size : kTeamThreads;
+  int want = (2048 * 256 / threads + t.xblocks - 1) / t.xblocks;
+  if (want < 1) want = 1;
+  if (want > 65535) want = 65535;
+  return a.rows < want ? a.rows : want;
+}
+
+template <typename T, int MODE>
+hipError_t launch_forward(NormArgs a, hipStream_t s) {
+  const Team t = team_of(a);
+  a.team = t.size;
+  const dim3 grid(t.xblocks, row_blocks(a, t)), block(t.wide ? t.size : kTeamThreads);
+  // fused checkpoints need whole blocks inside a group; others are written by
+  // a pass of their own
+  const bool fused = a.gs % kCkptBlock == 0;
+  if (a.xk.q && !fused) {
+    constexpr bool bf = sizeof(T) == 2;
+    hipError_t e = launch_ckpt_save(a.x, a.x_stride, a.rows, a.C, bf, a.xk, s);
+    if (e == hipSuccess && a.z) e = launch_ckpt_save(a.z, a.z_stride, a.rows, a.C, bf, a.zk, s);
+    if (e != hipSuccess) return e;
+  }
+#define SSD_NORM(CK)                                                              \
+  do {                                                                            \
+    if (!t.wide)                                                                  \
+      hipLaunchKernelGGL((k_norm<T, MODE, CK, 1, false>), grid, block, 0, s, a);  \
+    else if (t.r == 1)                                                            \
+      hipLaunchKernelGGL((k_norm<T, MODE, CK, 1, true>), grid, block, 0, s, a);   \
+    else                                                                          \
+      hipLaunchKernelGGL((k_norm<T, MODE, CK, 2, true>), grid, block, 0, s, a);   \
+  } while (0)
+  if (a.xk.q && fused)
+    SSD_NORM(kCkpt);
+  else
+    SSD_NORM(kPlain);
+#undef SSD_NORM
+  return hipGetLastError();
+}
+
+template <typename T, int MODE>
+hipError_t launch_back(NormArgs a, hipStream_t s) {
+  const Team t = team_of(a);
+  a.team = t.size;
+  const dim3 grid(t.xblocks, a.nparts), block(t.wide ? t.size : kTeamThreads);
+#define SSD_NORM(CK)                                                                      \
+  do {                                                                                    \
+    if (!t.wide)                                                                          \
+      hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, 1, false>), grid, block, 0, s, a); \
+    else if (t.r == 1)                                                                    \
+      hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, 1, true>), grid, block, 0, s, a);  \
+    else                                                                                  \
+      hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, 2, true>), grid, block, 0, s, a);  \
+  } while (0)
+  if (a.xk.q)
+    SSD_NORM(kCkpt);
+  else
+    SSD_NORM(kPlain);
+#undef SSD_NORM
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int norm_row_blocks(const NormArgs &a) { return a.rows > 0 ? row_blocks(a, team_of(a)) : 0; }
+
+hipError_t launch_norm(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s) {
+  switch (mode) {
+    case kGateFirst:
+      return bf16_io ? launch_forward<bf16, kGateFirst>(a, s) : launch_forward<float, kGateFirst>(a, s);
+    case kGateLast:
+      return bf16_io ? launch_forward<bf16, kGateLast>(a, s) : launch_forward<float, kGateLast>(a, s);
+    default:
+      return bf16_io ? launch_forward<bf16, kNoGate>(a, s) : launch_forward<float, kNoGate>(a, s);
+  }
+}
+
+hipError_t launch_norm_backward(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s) {
+  switch (mode) {
+    case kGateFirst:
+      return bf16_io ? launch_back<bf16, kGateFirst>(a, s) : launch_back<float, kGateFirst>(a, s);
+    case kGateLast:
+      return bf16_io ? launch_back<bf16, kGateLast>(a, s) : launch_back<float, kGateLast>(a, s);
+    default:
+      return bf16_io ? launch_back<bf16, kNoGate>(a, s) : launch_back<float, kNoGate>(a, s);
+  }
+}
+
+// ---- column sums of partial rows ------------------------------------------------
+// 64 columns per workgroup, 16 slices of the rows, added in fp64.
+namespace {
+constexpr int kSumSlices = 16;
+__global__ __launch_bounds__(1024) void k_column_sums(const float *part, int n, int taps, int ch,
+                                                      float *dw, float *db) {
+  __shared__ double lds[kSumSlices][64];
+  const int64_t cols = (int64_t)(taps + 1) * ch;
+  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int64_t j = (int64_t)blockIdx.x * 64 + lane;
+  double sum = 0.0;
+  if (j < cols) {
+#pragma unroll 8
+    for (int i = slice; i < n; i += kSumSlices) sum += (double)part[(size_t)i * cols + j];
+  }
+  lds[slice][lane] = sum;
+  __syncthreads();
+  if (slice == 0 && j < cols) {
+    for (int i = 1; i < kSumSlices; ++i) sum += lds[i][lane];
+    const int k = (int)(j / ch), c = (int)(j - (int64_t)k * ch);
+    if (k < taps) {
+      if (dw) dw[(size_t)c * taps + k] = (float)sum;
+    } else if (db) {
+      db[c] = (float)sum;
+    }
+  }
+}
+}  // namespace
+
+hipError_t launch_column_sums(const float *part, int n, int taps, int ch, float *dw, float *db,
+                              hipStream_t s) {
+  const int64_t cols = (int64_t)(taps + 1) * ch;
+  hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, part, n,
+                     taps, ch, dw, db);
+  return hipGetLastError();
+}
+
+}  // namespace ssd
