@@ -7,7 +7,9 @@ every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -585,37 +587,49 @@ class Checkpoint:
         dev, ch = self.q.device, self.q.shape[-1]
         _same_device(dev, out=out)
         _on_gpu(dev)
-        stream = _stream_of(dev, stream)
-        with torch.cuda.stream(stream):
+        context, handle = _stream_of(dev, stream)
+        with context:
             if out is None:
                 out = torch.empty(self.q.shape, device=dev, dtype=self.dtype)
             elif out.shape != self.q.shape or out.dtype != self.dtype:
                 raise ValueError("out must be %s %s" % (tuple(self.q.shape), self.dtype))
-            rows, stride = _rows_of(out, "out")
-            prob = CheckpointProblem(rows, stride, ch, _DTYPES[self.dtype], 0)
-            _check(load().ssd_checkpoint_load(ctypes.byref(prob), self.arg(), _ptr(out),
-                                              ctypes.c_void_p(stream.cuda_stream)),
+            stride = _stride_of_out(out, "out")
+            prob = CheckpointProblem(out.numel() // ch, stride, ch, _DTYPES[self.dtype], 0)
+            _check(load().ssd_checkpoint_load(prob, self.arg(), out.data_ptr(), handle),
                    "ssd_checkpoint_load")
         return out
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _stream_of(dev, stream):
-    """The stream to launch on: torch's current one on ``dev``, or the caller's,
-    which must be one of that device."""
+    """(context, handle) of the stream to launch on: torch's current one on
+    ``dev``, or the caller's, which must be one of that device. Copies, outputs
+    and workspaces made in the context belong to that stream, and ``dev`` is
+    the current device in it; none is needed where both are so already."""
     if stream is None:
-        return torch.cuda.current_stream(dev)
-    if stream.device != dev:
+        stream = torch.cuda.current_stream(dev)
+        if torch.cuda.current_device() == dev.index:
+            return _NO_CONTEXT, stream.cuda_stream
+    elif stream.device != dev:
         raise ValueError("the stream is on %s, but the tensors are on %s" % (stream.device, dev))
-    return stream
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _row_stride(t):
     """Elements between the token rows of ``t`` (the last axis one row, its
-    elements contiguous, all leading axes one evenly spaced sequence of rows),
-    or None if the rows are not laid out like that."""
-    ch = t.shape[-1]
+    elements contiguous, all leading axes one evenly spaced sequence of rows,
+    16-byte aligned), or None if the rows are not laid out like that."""
+    if t.data_ptr() & 15:
+        return None
     if t.is_contiguous():
-        return ch
+        return t.shape[-1]
+    ch = t.shape[-1]
     if t.stride(-1) != 1 and ch > 1:
         return None
     step, rows = None, 1
@@ -628,25 +642,23 @@ def _row_stride(t):
             return None
         rows *= size
     step = ch if step is None else step
-    if step < ch or step * t.element_size() % 16 or t.data_ptr() % 16:
-        return None
-    return step
+    return step if step >= ch and step * t.element_size() % 16 == 0 else None
 
 
-def _rows_of(t, name):
-    """(rows, row stride) of an output, whose rows must be addressable as they are."""
+def _stride_of_out(t, name):
+    """The row stride of an output, whose rows must be addressable as they are."""
     stride = _row_stride(t)
     if stride is None:
         raise ValueError("the token rows of %s must be evenly spaced, with contiguous channels, "
                          "16-byte aligned" % name)
-    return t.numel() // t.shape[-1], stride
+    return stride
 
 
 def _rows_in(t):
     """``t`` (or a contiguous copy, where its rows cannot be addressed as they
     are) and its row stride; called on the stream the kernel runs on."""
     stride = _row_stride(t)
-    if stride is not None and t.data_ptr() % 16 == 0:
+    if stride is not None:
         return t, stride
     t = t.clone(memory_format=torch.contiguous_format)
     return t, t.shape[-1]
@@ -677,14 +689,13 @@ def checkpoint_save(t, *, checkpoint=True, stream=None):
     if t.shape[-1] < 8 or t.shape[-1] % 8 != 0:
         raise ValueError("channels (%d) must be a multiple of 8" % t.shape[-1])
     dev = t.device
-    stream = _stream_of(dev, stream)
-    with torch.cuda.stream(stream):
+    context, handle = _stream_of(dev, stream)
+    with context:
         ck = _checkpoint_out(checkpoint, tuple(t.shape), t.dtype, dev)
         t, stride = _rows_in(t)
         prob = CheckpointProblem(t.numel() // t.shape[-1], stride, t.shape[-1],
                                  _DTYPES[t.dtype], 0)
-        _check(load().ssd_checkpoint_save(ctypes.byref(prob), _ptr(t), ck.arg(),
-                                          ctypes.c_void_p(stream.cuda_stream)),
+        _check(load().ssd_checkpoint_save(prob, t.data_ptr(), ck.arg(), handle),
                "ssd_checkpoint_save")
     return ck
 
@@ -744,14 +755,13 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
         num_seqs = int(cu_seqlens.numel()) - 1
         if check_cu_seqlens or cu_seqlens.device.type == "cpu":
             _check_offsets(cu_seqlens, L)
-        cu_dev = cu_seqlens.to(device=dev, dtype=torch.int32).contiguous()
         nseq, lead = num_seqs, (L,)
         in_stride = xbc.stride(0) if L > 1 else ch
     else:
         if xbc.dim() != 3:
             raise ValueError("dense xbc must be (batch, seqlen, channels)")
         batch, L = int(xbc.shape[0]), int(xbc.shape[1])
-        num_seqs, cu_dev, nseq, lead = 0, None, batch, (batch, L)
+        num_seqs, nseq, lead = 0, batch, (batch, L)
         # token row t = b * L + l sits at b * stride(0) + l * stride(1)
         if L > 1:
             if batch > 1 and xbc.stride(0) != L * xbc.stride(1):
@@ -773,10 +783,11 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
                               or not t.is_contiguous()):
             raise ValueError("%s must be a contiguous %s %s tensor" % (name, shape, dtype))
     prob = ConvProblem(batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    context, handle = _stream_of(dev, stream)
     # copies and outputs are made on the stream the kernel runs on (see step())
-    with torch.cuda.stream(stream):
+    with context:
+        cu = (cu_seqlens.to(device=dev, dtype=torch.int32).contiguous() if cu_seqlens is not None
+              else None)
         weight = weight.contiguous()
         bias = bias.contiguous() if bias is not None else None
         history = history.contiguous() if history is not None else None
@@ -788,23 +799,18 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
             C = torch.empty(lead + (bc_dim,), device=dev, dtype=dtype)
         if history_out is None and want_history:
             history_out = torch.empty(hshape, device=dev, dtype=dtype)
-        if checkpoint is not False:
-            save = _checkpoint_out(checkpoint, tuple(xbc.shape), dtype, dev)
-            _check(load().ssd_conv1d_silu_checkpoint(
-                ctypes.byref(prob), _ptr(xbc), save.arg(), _ptr(weight), _ptr(bias),
-                _ptr(history), _ptr(cu_dev), _ptr(x), _ptr(B), _ptr(C), _ptr(history_out),
-                ctypes.c_void_p(stream.cuda_stream)), "ssd_conv1d_silu_checkpoint")
-            return x, B, C, history_out, save
+        tensors = (_addr(weight), _addr(bias), _addr(history), _addr(cu), _addr(x), _addr(B),
+                   _addr(C), _addr(history_out), handle)
         if kept is not None:
-            _check(load().ssd_conv1d_silu_checkpoint(
-                ctypes.byref(prob), None, kept.arg(), _ptr(weight), _ptr(bias), _ptr(history),
-                _ptr(cu_dev), _ptr(x), _ptr(B), _ptr(C), None,
-                ctypes.c_void_p(stream.cuda_stream)), "ssd_conv1d_silu_checkpoint")
-            return x, B, C, None
-    _check(load().ssd_conv1d_silu(ctypes.byref(prob), _ptr(xbc), _ptr(weight), _ptr(bias),
-                                  _ptr(history), _ptr(cu_dev), _ptr(x), _ptr(B), _ptr(C),
-                                  _ptr(history_out), ctypes.c_void_p(stream.cuda_stream)),
-           "ssd_conv1d_silu")
+            _check(load().ssd_conv1d_silu_checkpoint(prob, None, kept.arg(), *tensors),
+                   "ssd_conv1d_silu_checkpoint")
+        elif checkpoint is not False:
+            save = _checkpoint_out(checkpoint, tuple(xbc.shape), dtype, dev)
+            _check(load().ssd_conv1d_silu_checkpoint(prob, xbc.data_ptr(), save.arg(), *tensors),
+                   "ssd_conv1d_silu_checkpoint")
+            return x, B, C, history_out, save
+        else:
+            _check(load().ssd_conv1d_silu(prob, xbc.data_ptr(), *tensors), "ssd_conv1d_silu")
     return x, B, C, history_out
 
 
@@ -962,13 +968,13 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
             raise ValueError("%s must be %s %s" % (name, hshape, dtype))
     if dxbc is not None and (tuple(dxbc.shape) != lead + (ch,) or dxbc.dtype != dtype):
         raise ValueError("dxbc must be %s %s" % (lead + (ch,), dtype))
-    stream = _stream_of(dev, stream)
+    context, handle = _stream_of(dev, stream)
     # copies, outputs and the workspace are made on the stream the kernels run on
-    with torch.cuda.stream(stream):
+    with context:
         cu_dev = cu_seqlens.to(device=dev, dtype=torch.int32).contiguous() if packed else None
         if dxbc is None:
             dxbc = torch.empty(lead + (ch,), device=dev, dtype=dtype)
-        _, out_stride = _rows_of(dxbc, "dxbc")
+        out_stride = _stride_of_out(dxbc, "dxbc")
         in_stride = ch
         if kept is None:
             u, in_stride = _rows_in(u)
@@ -979,35 +985,65 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
         dweight = torch.empty((ch, K), device=dev, dtype=torch.float32)
         dbias = torch.empty(ch, device=dev, dtype=torch.float32)
         dhistory = (torch.empty(hshape, device=dev, dtype=dtype) if history is not None else None)
-        prob = ConvProblem(batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
-        n = ctypes.c_size_t(0)
-        _check(load().ssd_conv1d_silu_backward_workspace_size(ctypes.byref(prob), ctypes.byref(n)),
-               "ssd_conv1d_silu_backward_workspace_size")
-        ws = torch.empty(max(n.value, 256), device=dev, dtype=torch.uint8)
+        sizes = (batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
+        n = _conv_backward_bytes(*sizes)
+        ws = torch.empty(n, device=dev, dtype=torch.uint8) if n else None
         _check(load().ssd_conv1d_silu_backward(
-            ctypes.byref(prob), None if kept is not None else _ptr(u),
-            kept.arg() if kept is not None else None, _ptr(weight), _ptr(bias), _ptr(history),
-            _ptr(cu_dev), _ptr(dx), _ptr(dB), _ptr(dC), _ptr(dhistory_out), _ptr(dxbc),
-            out_stride, _ptr(dweight), _ptr(dbias), _ptr(dhistory), _ptr(ws),
-            ctypes.c_size_t(ws.numel()), ctypes.c_void_p(stream.cuda_stream)),
+            ConvProblem(*sizes), None if kept is not None else u.data_ptr(),
+            kept.arg() if kept is not None else None, weight.data_ptr(), _addr(bias),
+            _addr(history), _addr(cu_dev), dx.data_ptr(), dB.data_ptr(), dC.data_ptr(),
+            _addr(dhistory_out), dxbc.data_ptr(), out_stride, dweight.data_ptr(),
+            dbias.data_ptr(), _addr(dhistory), _addr(ws), n, handle),
             "ssd_conv1d_silu_backward")
     return dict(dxbc=dxbc, dweight=dweight, dbias=dbias, dhistory=dhistory)
 
 
-def _norm_problem(shape, dtype, groups, eps, center, norm_before_gate):
-    channels = int(shape[-1])
-    tokens = 1
-    for size in shape[:-1]:
-        tokens *= int(size)
+@functools.lru_cache(maxsize=256)
+def _conv_backward_bytes(*sizes):
+    """Workspace bytes of a front's backward pass, by its sizes."""
+    n = ctypes.c_size_t(0)
+    _check(load().ssd_conv1d_silu_backward_workspace_size(ConvProblem(*sizes), ctypes.byref(n)),
+           "ssd_conv1d_silu_backward_workspace_size")
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_backward_bytes(*sizes):
+    """Workspace bytes of a norm's backward pass, by its sizes."""
+    n = ctypes.c_size_t(0)
+    _check(load().ssd_group_norm_silu_backward_workspace_size(NormProblem(0, 0, 0, 0, 0, *sizes),
+                                                              ctypes.byref(n)),
+           "ssd_group_norm_silu_backward_workspace_size")
+    return n.value
+
+
+def _norm_sizes(x, groups, eps, center, norm_before_gate):
+    """(tokens, channels, groups, dtype, flags, eps) of a NormProblem."""
+    shape = x.shape
+    channels = shape[-1] if len(shape) else 0
+    if channels < 1 or x.dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float32 with a channel axis")
     flags = (SSD_NORM_CENTER if center else 0) | (SSD_NORM_BEFORE_GATE if norm_before_gate else 0)
-    return NormProblem(channels, channels, channels, channels, channels, tokens, channels,
-                       groups, _DTYPES[dtype], flags, eps)
+    return shape.numel() // channels, channels, groups, _DTYPES[x.dtype], flags, eps
 
 
-def _affine(weight, bias, channels):
+def _norm_tensors(x, channels, like, weight, bias):
+    """Checks of a norm's tensors: ``like`` (name -> tensor or None) are laid
+    out as x, the parameters (channels,) float32; all on x's device."""
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    for name, t in like.items():
+        if t is not None:
+            if t.device != dev:
+                _same_device(dev, **{name: t})
+            if t.shape != shape or t.dtype != dtype:
+                raise ValueError("%s must be %s %s" % (name, tuple(shape), dtype))
     for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None and (tuple(t.shape) != (channels,) or t.dtype != torch.float32):
-            raise ValueError("%s must be (%d,) float32" % (name, channels))
+        if t is not None:
+            if t.device != dev:
+                _same_device(dev, **{name: t})
+            if t.shape != (channels,) or t.dtype != torch.float32:
+                raise ValueError("%s must be (%d,) float32" % (name, channels))
+    _on_gpu(dev)
 
 
 def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, center=False,
@@ -1025,38 +1061,30 @@ def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, ce
     are also kept in 8 bits on the way: returns (out, x's Checkpoint, z's or
     None); a pair of Checkpoints is filled instead.
     """
-    if x.dim() < 1 or x.shape[-1] < 1 or x.dtype not in _DTYPES:
-        raise ValueError("x must be bfloat16 or float32 with a channel axis")
-    dev, dtype, shape = x.device, x.dtype, tuple(x.shape)
-    _same_device(dev, weight=weight, bias=bias, z=z, out=out)
-    _on_gpu(dev)
-    for name, t in (("z", z), ("out", out)):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
-            raise ValueError("%s must be %s %s" % (name, shape, dtype))
+    sizes = _norm_sizes(x, groups, eps, center, norm_before_gate)
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    _norm_tensors(x, sizes[1], {"z": z, "out": out}, weight, bias)
     if norm_before_gate and z is None:
         raise ValueError("norm_before_gate needs z")
-    _affine(weight, bias, shape[-1])
-    prob = _norm_problem(shape, dtype, groups, eps, center, norm_before_gate)
-    stream = _stream_of(dev, stream)
+    context, handle = _stream_of(dev, stream)
     # copies and outputs are made on the stream the kernel runs on
-    with torch.cuda.stream(stream):
+    with context:
         if out is None:
             out = torch.empty(shape, device=dev, dtype=dtype)
-        _, prob.out_stride = _rows_of(out, "out")
+        out_stride = _stride_of_out(out, "out")
         kx = kz = None
         if checkpoint is not False:
             gx, gz = (True, True) if checkpoint is True else checkpoint
-            kx = _checkpoint_out(gx, shape, dtype, dev)
-            kz = _checkpoint_out(gz, shape, dtype, dev) if z is not None else None
-        x, prob.x_stride = _rows_in(x)
-        if z is not None:
-            z, prob.z_stride = _rows_in(z)
+            kx = _checkpoint_out(gx, tuple(shape), dtype, dev)
+            kz = _checkpoint_out(gz, tuple(shape), dtype, dev) if z is not None else None
+        x, x_stride = _rows_in(x)
+        z, z_stride = _rows_in(z) if z is not None else (None, 0)
         weight = weight.contiguous() if weight is not None else None
         bias = bias.contiguous() if bias is not None else None
         _check(load().ssd_group_norm_silu(
-            ctypes.byref(prob), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(out),
-            kx.arg() if kx is not None else None, kz.arg() if kz is not None else None,
-            ctypes.c_void_p(stream.cuda_stream)), "ssd_group_norm_silu")
+            NormProblem(x_stride, z_stride, out_stride, 0, 0, *sizes), x.data_ptr(), _addr(z),
+            _addr(weight), _addr(bias), out.data_ptr(), kx.arg() if kx is not None else None,
+            kz.arg() if kz is not None else None, handle), "ssd_group_norm_silu")
     return out if checkpoint is False else (out, kx, kz)
 
 
@@ -1071,54 +1099,45 @@ def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=
     :class:`Checkpoint` of the inputs. dout, and the optional outputs dx and
     dz, are shaped like x and may be slices of wider rows.
     """
-    dtype, shape, dev = x.dtype, tuple(x.shape), x.device
-    if isinstance(x, Checkpoint) != isinstance(z, Checkpoint) and z is not None:
-        raise ValueError("x and z must both be tensors or both checkpoints")
     kept = isinstance(x, Checkpoint)
-    _same_device(dev, dout=dout, weight=weight, bias=bias, z=z, dx=dx, dz=dz)
-    _on_gpu(dev)
+    if z is not None and isinstance(z, Checkpoint) != kept:
+        raise ValueError("x and z must both be tensors or both checkpoints")
+    sizes = _norm_sizes(x, groups, eps, center, norm_before_gate)
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    _norm_tensors(x, sizes[1], {"dout": dout, "z": z, "dx": dx, "dz": dz}, weight, bias)
     if dout is None:
         raise ValueError("dout is required")
-    if dtype not in _DTYPES or len(shape) < 1 or shape[-1] < 1:
-        raise ValueError("x must be bfloat16 or float32 with a channel axis")
-    for name, t in (("dout", dout), ("z", z), ("dx", dx), ("dz", dz)):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
-            raise ValueError("%s must be %s %s" % (name, shape, dtype))
     if z is None and (norm_before_gate or dz is not None):
         raise ValueError("norm_before_gate and dz need z")
-    _affine(weight, bias, shape[-1])
-    prob = _norm_problem(shape, dtype, groups, eps, center, norm_before_gate)
-    n = ctypes.c_size_t(0)
-    if weight is not None or bias is not None:
-        _check(load().ssd_group_norm_silu_backward_workspace_size(ctypes.byref(prob),
-                                                                  ctypes.byref(n)),
-               "ssd_group_norm_silu_backward_workspace_size")
-    stream = _stream_of(dev, stream)
+    context, handle = _stream_of(dev, stream)
     # copies, outputs and the workspace are made on the stream the kernels run on
-    with torch.cuda.stream(stream):
+    with context:
         if dx is None:
             dx = torch.empty(shape, device=dev, dtype=dtype)
         if dz is None and z is not None:
             dz = torch.empty(shape, device=dev, dtype=dtype)
-        _, prob.dx_stride = _rows_of(dx, "dx")
-        if dz is not None:
-            _, prob.dz_stride = _rows_of(dz, "dz")
-        dout, prob.out_stride = _rows_in(dout)
+        dx_stride = _stride_of_out(dx, "dx")
+        dz_stride = _stride_of_out(dz, "dz") if dz is not None else 0
+        dout, out_stride = _rows_in(dout)
+        x_stride = z_stride = 0
         if not kept:
-            x, prob.x_stride = _rows_in(x)
-            if z is not None:
-                z, prob.z_stride = _rows_in(z)
-        dweight = (torch.empty(shape[-1], device=dev, dtype=torch.float32)
-                   if weight is not None else None)
-        dbias = (torch.empty(shape[-1], device=dev, dtype=torch.float32)
-                 if bias is not None else None)
-        weight = weight.contiguous() if weight is not None else None
-        bias = bias.contiguous() if bias is not None else None
-        ws = torch.empty(n.value, device=dev, dtype=torch.uint8) if n.value else None
+            x, x_stride = _rows_in(x)
+            z, z_stride = _rows_in(z) if z is not None else (None, 0)
+        dweight = dbias = ws = None
+        n = 0
+        if weight is not None:
+            weight = weight.contiguous()
+            dweight = torch.empty(sizes[1], device=dev, dtype=torch.float32)
+        if bias is not None:
+            bias = bias.contiguous()
+            dbias = torch.empty(sizes[1], device=dev, dtype=torch.float32)
+        if weight is not None or bias is not None:
+            n = _norm_backward_bytes(*sizes)
+            ws = torch.empty(n, device=dev, dtype=torch.uint8) if n else None
         _check(load().ssd_group_norm_silu_backward(
-            ctypes.byref(prob), _ptr(dout), None if kept else _ptr(x), None if kept else _ptr(z),
+            NormProblem(x_stride, z_stride, out_stride, dx_stride, dz_stride, *sizes),
+            dout.data_ptr(), None if kept else x.data_ptr(), None if kept else _addr(z),
             x.arg() if kept else None, z.arg() if kept and z is not None else None,
-            _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias), _ptr(ws),
-            ctypes.c_size_t(n.value), ctypes.c_void_p(stream.cuda_stream)),
-            "ssd_group_norm_silu_backward")
+            _addr(weight), _addr(bias), dx.data_ptr(), _addr(dz), _addr(dweight), _addr(dbias),
+            _addr(ws), n, handle), "ssd_group_norm_silu_backward")
     return dict(dx=dx, dz=dz, dweight=dweight, dbias=dbias)

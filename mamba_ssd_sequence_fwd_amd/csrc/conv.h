@@ -57,6 +57,7 @@ constexpr int kConvBwdWaves = 4;   // tiles per workgroup
 // Fill in the tile geometry (tile, seq_tiles, tiles) for a problem whose
 // sizes are set; the workgroups along the tokens.
 int conv_bwd_geometry(ConvBwdArgs &a);
+int conv_bwd_channel_blocks(const ConvBwdArgs &a);  // workgroups along the channels
 hipError_t launch_conv_backward(const ConvBwdArgs &a, int width, bool bf16_io, hipStream_t s);
 
 }  // namespace ssd

@@ -19,26 +19,40 @@
 // a table; slots past a sequence's end only write zeros to the partial sums.
 // The sums of a workgroup's tiles are joined in LDS and written as one row of
 // partial sums; k_column_sums adds those rows.
+#include <type_traits>
+
 #include "conv.h"
 
 namespace ssd {
 
 namespace {
 
-template <typename T, bool CK> struct BwdRowOf { typedef Row8<T> type; };
-template <typename T> struct BwdRowOf<T, true> { typedef RowQ8 type; };
+constexpr int kLane = 4;  // channels per lane
+
+template <typename T, int C> struct RowsOf { typedef Row8<T> Plain; typedef RowQ8 Kept; };
+template <typename T> struct RowsOf<T, 4> { typedef Row4<T> Plain; typedef RowQ4 Kept; };
+template <typename T> using Row = typename RowsOf<T, kLane>::Plain;
+template <typename T, bool CK>
+using BwdRow = std::conditional_t<CK, typename RowsOf<T, kLane>::Kept, Row<T>>;
 
 template <typename T>
-__device__ __forceinline__ void load_u(Row8<T> &r, const ConvBwdArgs &a, int t, int c0) {
+__device__ __forceinline__ void load_u(Row<T> &r, const ConvBwdArgs &a, int t, int c0) {
   r.load(a.xbc, (size_t)t * a.in_stride + c0);
 }
-__device__ __forceinline__ void load_u(RowQ8 &r, const ConvBwdArgs &a, int t, int c0) {
+template <typename T>
+__device__ __forceinline__ void load_u(typename RowsOf<T, kLane>::Kept &r, const ConvBwdArgs &a,
+                                       int t, int c0) {
   r.load(a.ck, (size_t)t, a.ch, c0);
 }
 
 template <int K, typename T, bool CK>
-__global__ __launch_bounds__(64 * kConvBwdWaves) void k_conv_backward(ConvBwdArgs a, int cblocks) {
-  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+__global__ __launch_bounds__(64 * kConvBwdWaves)
+__attribute__((amdgpu_waves_per_eu(4))) void k_conv_backward(ConvBwdArgs a, int cblocks) {
+  constexpr int P = K - 1;
+  // rows in flight per lane, a multiple of P so that the windows come round to
+  // the same registers
+  constexpr int kBatch = P == 3 ? 3 : sizeof(T) == 2 ? 4 : 2;
+  static_assert(kBatch >= P && kBatch % P == 0, "a first batch covers the steps before the tile's own");
   // one contiguous range of workgroups per XCD: tiles that share halo rows
   // meet in one L2
   const int nb = gridDim.x, bid = blockIdx.x;
@@ -47,9 +61,9 @@ __global__ __launch_bounds__(64 * kConvBwdWaves) void k_conv_backward(ConvBwdArg
   const int tb = lb / cblocks;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cg = ((lb - tb * cblocks) * 64 + lane) * 8;
+  const int cg = ((lb - tb * cblocks) * 64 + lane) * kLane;
   const bool live = cg < a.ch;
-  const int c0 = live ? cg : a.ch - 8;
+  const int c0 = live ? cg : a.ch - kLane;
   const int slot = tb * kConvBwdWaves + wave;
 
   // The tile [t0, t1) of sequence s = [ss, se); len < 0: nothing to do.
@@ -83,9 +97,9 @@ __global__ __launch_bounds__(64 * kConvBwdWaves) void k_conv_backward(ConvBwdArg
     }
   }
 
-  float dw[8][K], db[8];
+  float dw[kLane][K], db[kLane];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < kLane; ++c) {
     db[c] = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) dw[c][k] = 0.f;
@@ -93,136 +107,143 @@ __global__ __launch_bounds__(64 * kConvBwdWaves) void k_conv_backward(ConvBwdArg
 
   if (some && se > ss) {
     // Array and column of this lane's output gradients.
-    const void *src;
-    int dcol, dstride;
-    if (c0 < a.x_dim) {
-      src = a.dx; dcol = c0; dstride = a.x_dim;
-    } else if (c0 < a.x_dim + a.bc_dim) {
-      src = a.dB; dcol = c0 - a.x_dim; dstride = a.bc_dim;
-    } else {
-      src = a.dC; dcol = c0 - a.x_dim - a.bc_dim; dstride = a.bc_dim;
+    const char *dsrc;
+    int dstride;
+    {
+      const void *src;
+      int dcol;
+      if (c0 < a.x_dim) {
+        src = a.dx; dcol = c0; dstride = a.x_dim;
+      } else if (c0 < a.x_dim + a.bc_dim) {
+        src = a.dB; dcol = c0 - a.x_dim; dstride = a.bc_dim;
+      } else {
+        src = a.dC; dcol = c0 - a.x_dim - a.bc_dim; dstride = a.bc_dim;
+      }
+      dsrc = static_cast<const char *>(src) + (size_t)dcol * sizeof(T);
+      dstride *= (int)sizeof(T);
     }
-    typename BwdRowOf<T, CK>::type u[kBatch], un[kBatch];
-    Row8<T> d[kBatch], dn[kBatch];
-    const int steps = t1 - t0 + K - 1;
+    BwdRow<T, CK> u[kBatch];
+    Row<T> d[kBatch];
+    // row t of the inputs and of the gradients, into the registers that the
+    // row kBatch before it left
+    auto fetch = [&](int j, int t) __attribute__((always_inline)) {
+      t = min(t, se - 1);
+      load_u<T>(u[j], a, t, c0);
+      d[j].load(dsrc + (size_t)t * dstride, 0);
+    };
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int t = min(t0 + j, se - 1);
-      load_u(u[j], a, t, c0);
-      d[j].load(src, (size_t)t * dstride + dcol);
-    }
-    float w[8][K], bias[8];
+    for (int j = 0; j < kBatch; ++j) fetch(j, t0 + j);
+    float w[kLane][K], bias[kLane];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < kLane; ++c) {
 #pragma unroll
       for (int k = 0; k < K; ++k) w[c][k] = a.w[(size_t)(c0 + c) * K + k];
       bias[c] = a.bias ? a.bias[c0 + c] : 0.f;
     }
-    float win[K - 1][8], gwin[K - 1][8];
+    float win[P][kLane], gwin[P][kLane];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-      const int tok = t0 - (K - 1) + j;
+    for (int j = 0; j < P; ++j) {
+      const int tok = t0 - P + j;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) win[j][c] = gwin[j][c] = 0.f;
+      for (int c = 0; c < kLane; ++c) win[j][c] = gwin[j][c] = 0.f;
       if (tok >= ss) {
-        typename BwdRowOf<T, CK>::type r;
-        load_u(r, a, tok, c0);
+        BwdRow<T, CK> r;
+        load_u<T>(r, a, tok, c0);
         r.widen(win[j]);
       } else if (a.hist_in) {
-        Row8<T> r;
-        r.load(a.hist_in, ((size_t)s * (K - 1) + (tok - ss + K - 1)) * a.ch + c0);
+        Row<T> r;
+        r.load(a.hist_in, ((size_t)s * P + (tok - ss + P)) * a.ch + c0);
         r.widen(win[j]);
       }
     }
-    for (int i0 = 0; i0 < steps; i0 += kBatch) {
+    // One step; inside: a token of the tile whose de is one of its tokens'.
+    auto step = [&](auto inside_, int j, int t) __attribute__((always_inline)) {
+      constexpr bool inside = decltype(inside_)::value;
+      float cur[kLane], dd[kLane], de[kLane];
+      u[j].widen(cur);
+      d[j].widen(dd);
+      fetch(j, t + kBatch);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int t = min(t0 + i0 + kBatch + j, se - 1);
-        load_u(un[j], a, t, c0);
-        dn[j].load(src, (size_t)t * dstride + dcol);
+      for (int c = 0; c < kLane; ++c) {
+        float pre = bias[c] + w[c][K - 1] * cur[c];
+#pragma unroll
+        for (int k = 0; k < P; ++k) pre += w[c][k] * win[k][c];
+        // g = d s (1 + pre (1 - s))
+        const float sg = sigmoid(pre), ds = dd[c] * sg;
+        float g = ds + ds * (pre - pre * sg);
+        if (!inside) g = t < se ? g : 0.f;
+        de[c] = w[c][0] * g;
+#pragma unroll
+        for (int k = 1; k < K; ++k) de[c] += w[c][k] * gwin[K - 1 - k][c];
+        if (inside || t < t1) {
+          db[c] += g;
+          dw[c][K - 1] += g * cur[c];
+#pragma unroll
+          for (int k = 0; k < P; ++k) dw[c][k] += g * win[k][c];
+        }
+#pragma unroll
+        for (int k = 0; k + 1 < P; ++k) {
+          win[k][c] = win[k + 1][c];
+          gwin[k][c] = gwin[k + 1][c];
+        }
+        win[P - 1][c] = cur[c];
+        gwin[P - 1][c] = g;
       }
+      // de belongs to row t - ss of [history, inputs]; lanes past the last
+      // channel repeat the last lane's stores
+      if (inside) {
+        Row<T>::store(a.dxbc, (size_t)(t - P) * a.out_stride + c0, de);
+      } else {
+        if (a.dhist_out && t >= se) {
+          Row<T> r;
+          float v[kLane];
+          r.load(a.dhist_out, ((size_t)s * P + (t - se)) * a.ch + c0);
+          r.widen(v);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int t = t0 + i0 + j;
-        if (i0 + j < steps) {
-          float cur[8], dd[8], g[8], de[8];
-          u[j].widen(cur);
-          d[j].widen(dd);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float pre = bias[c] + w[c][K - 1] * cur[c];
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) pre += w[c][k] * win[k][c];
-            const float sg = sigmoid(pre);
-            g[c] = t < se ? dd[c] * (sg * (1.f + pre * (1.f - sg))) : 0.f;
-            de[c] = w[c][0] * g[c];
-#pragma unroll
-            for (int k = 1; k < K; ++k) de[c] += w[c][k] * gwin[K - 1 - k][c];
-          }
-          if (t < t1) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              db[c] += g[c];
-              dw[c][K - 1] += g[c] * cur[c];
-#pragma unroll
-              for (int k = 0; k < K - 1; ++k) dw[c][k] += g[c] * win[k][c];
-            }
-          }
-          // de belongs to row t - ss of [history, inputs]
-          if (a.dhist_out && t >= se) {
-            Row8<T> r;
-            float v[8];
-            r.load(a.dhist_out, ((size_t)s * (K - 1) + (t - se)) * a.ch + c0);
-            r.widen(v);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) de[c] += v[c];
-          }
-          if (t - ss >= K - 1) {
-            if (live && i0 + j >= K - 1)
-              Row8<T>::store(a.dxbc, (size_t)(t - (K - 1)) * a.out_stride + c0, de);
-          } else if (live && a.dhist) {
-            Row8<T>::store(a.dhist, ((size_t)s * (K - 1) + (t - ss)) * a.ch + c0, de);
-          }
-#pragma unroll
-          for (int k = 0; k + 1 < K - 1; ++k)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              win[k][c] = win[k + 1][c];
-              gwin[k][c] = gwin[k + 1][c];
-            }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            win[K - 2][c] = cur[c];
-            gwin[K - 2][c] = g[c];
-          }
+          for (int c = 0; c < kLane; ++c) de[c] += v[c];
+        }
+        if (t - ss >= P) {
+          if (t - t0 >= P)
+            Row<T>::store(a.dxbc, (size_t)(t - P) * a.out_stride + c0, de);
+        } else if (a.dhist) {
+          Row<T>::store(a.dhist, ((size_t)s * P + (t - ss)) * a.ch + c0, de);
         }
       }
+    };
+    const int end = t1 + P;
+    auto checked = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        u[j] = un[j];
-        d[j] = dn[j];
-      }
+      for (int j = 0; j < kBatch; ++j)
+        if (t + j < end) step(std::false_type(), j, t + j);
+    };
+    int t = t0;
+    checked(t);
+    t += kBatch;
+    for (; t + kBatch <= t1; t += kBatch) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) step(std::true_type(), j, t + j);
     }
-  } else if (some && a.dhist && live) {
+    for (; t < end; t += kBatch) checked(t);
+  } else if (some && a.dhist) {
     // no tokens: the history passes through
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float v[kLane] = {};
       const size_t at = ((size_t)s * (K - 1) + j) * a.ch + c0;
       if (a.dhist_out) {
-        Row8<T> r;
+        Row<T> r;
         r.load(a.dhist_out, at);
         r.widen(v);
       }
-      Row8<T>::store(a.dhist, at, v);
+      Row<T>::store(a.dhist, at, v);
     }
   }
 
   // Join the tiles of the workgroup.
-  __shared__ float lds[kConvBwdWaves - 1][K + 1][8][64];
+  __shared__ float lds[kConvBwdWaves - 1][K + 1][kLane][64];
   if (wave > 0) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < kLane; ++c) {
 #pragma unroll
       for (int k = 0; k < K; ++k) lds[wave - 1][k][c][lane] = dw[c][k];
       lds[wave - 1][K][c][lane] = db[c];
@@ -234,7 +255,7 @@ __global__ __launch_bounds__(64 * kConvBwdWaves) void k_conv_backward(ConvBwdArg
     for (int k = 0; k <= K; ++k) {
       float *p = a.part + ((size_t)tb * (K + 1) + k) * a.ch + c0;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < kLane; ++c) {
         float v = k < K ? dw[c][k < K ? k : 0] : db[c];
 #pragma unroll
         for (int o = 0; o < kConvBwdWaves - 1; ++o) v += lds[o][k][c][lane];
@@ -246,7 +267,7 @@ __global__ __launch_bounds__(64 * kConvBwdWaves) void k_conv_backward(ConvBwdArg
 
 template <int K, typename T>
 hipError_t launch_width(const ConvBwdArgs &a, hipStream_t s) {
-  const int cblocks = (a.ch / 8 + 63) / 64;
+  const int cblocks = conv_bwd_channel_blocks(a);
   const int tblocks = (a.tiles + kConvBwdWaves - 1) / kConvBwdWaves;
   const dim3 grid((unsigned)(cblocks * tblocks)), block(64 * kConvBwdWaves);
   if (a.ck.q)
@@ -256,17 +277,30 @@ hipError_t launch_width(const ConvBwdArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tokens per tile. Shorter tiles spread the work more evenly, longer ones
+// repeat fewer steps at their ends: from a checkpoint the kernel is bound by
+// its arithmetic (2 x 16384 tokens, 8192 channels: 288 us with 60 tokens, 298
+// with 36), from 16 bits by memory (131,604 packed tokens, 5376 channels: 786
+// us with 36, 809 with 60). Few tokens take the shortest, so that there are
+// workgroups for every compute unit.
+constexpr int kTile = 36, kCkptTile = 60, kShortTile = 12;
+constexpr int kFewBlocks = 256;
+
 }  // namespace
 
+int conv_bwd_channel_blocks(const ConvBwdArgs &a) { return (a.ch / kLane + 63) / 64; }
+
 int conv_bwd_geometry(ConvBwdArgs &a) {
-  a.tile = 61;  // with the K - 1 = 3 steps past the end, 64 steps
-  if (a.cu) {
-    a.seq_tiles = 0;
-    a.tiles = a.T / a.tile + a.nseq;
-  } else {
-    a.seq_tiles = a.seqlen > 0 ? (a.seqlen + a.tile - 1) / a.tile : 1;
-    a.tiles = a.nseq * a.seq_tiles;
-  }
+  auto slots = [&](int tile) {
+    return a.cu ? (int64_t)a.T / tile + a.nseq
+                : (int64_t)a.nseq * (a.seqlen > 0 ? (a.seqlen + tile - 1) / tile : 1);
+  };
+  const int64_t blocks = (slots(kTile) + kConvBwdWaves - 1) / kConvBwdWaves;
+  a.tile = blocks * conv_bwd_channel_blocks(a) < kFewBlocks ? kShortTile
+           : a.ck.q                                         ? kCkptTile
+                                                            : kTile;
+  a.tiles = (int32_t)slots(a.tile);
+  a.seq_tiles = a.cu ? 0 : a.seqlen > 0 ? (a.seqlen + a.tile - 1) / a.tile : 1;
   return (a.tiles + kConvBwdWaves - 1) / kConvBwdWaves;
 }
 

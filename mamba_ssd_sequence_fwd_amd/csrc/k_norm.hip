@@ -83,7 +83,14 @@ template <bool WIDE, int R>
 struct Place {
   int c[R];
   bool live[R];
+  int row, step;  // first row, and rows between one of the lane's rows and the next
   __device__ __forceinline__ explicit Place(const NormArgs &a) {
+    // in-wave teams of few channels take several rows side by side
+    const int need = a.G * a.team;
+    const int sub = !WIDE && a.subs > 1 ? threadIdx.x / need : 0;
+    row = blockIdx.y * a.subs + sub;
+    if (sub >= a.subs) row = a.rows;  // lanes left over
+    step = gridDim.y * a.subs;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       int g, in;
@@ -91,9 +98,9 @@ struct Place {
         g = blockIdx.x;
         in = (r * a.team + threadIdx.x) * 8;
       } else {
-        const int per = kTeamThreads / a.team;
-        g = blockIdx.x * per + threadIdx.x / a.team;
-        in = (threadIdx.x & (a.team - 1)) * 8;
+        const int per = blockDim.x / a.team, lane = threadIdx.x - sub * need;
+        g = blockIdx.x * per + lane / a.team;
+        in = (r * a.team + (lane & (a.team - 1))) * 8;
       }
       live[r] = g < a.G && in < a.gs;
       c[r] = live[r] ? g * a.gs + in : 0;
@@ -101,13 +108,25 @@ struct Place {
   }
 };
 
+// Weights or biases of the lane's channels (float arrays of any alignment).
 template <int R>
 __device__ __forceinline__ void load_affine(const float *p, float otherwise, const int (&c)[R],
-                                            const bool (&live)[R], float (&v)[R][8]) {
+                                            float (&v)[R][8]) {
+  const bool wide = ((uintptr_t)p & 15) == 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
+    if (p == nullptr) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[r][k] = p && live[r] ? p[c[r] + k] : otherwise;
+      for (int k = 0; k < 8; ++k) v[r][k] = otherwise;
+    } else if (wide) {
+      Row8<float> q;
+      q.load(p, c[r]);
+      q.widen(v[r]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[r][k] = p[c[r] + k];
+    }
+  }
 }
 
 template <typename T, int MODE, int CK, int R, bool WIDE>
@@ -115,21 +134,21 @@ __global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm(NormArgs a)
   __shared__ float lds[2][kMaxWaves * 4];
   const Place<WIDE, R> at(a);
   float w[R][8], b[R][8];
-  load_affine(a.w, 1.f, at.c, at.live, w);
-  load_affine(a.b, 0.f, at.c, at.live, b);
+  load_affine(a.w, 1.f, at.c, w);
+  load_affine(a.b, 0.f, at.c, b);
   constexpr bool kGated = MODE != kNoGate;
   Row8<T> xr[R], zr[R];
   auto fetch = [&](int row) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      xr[r].load(a.x, (size_t)row * a.x_stride + at.c[r]);
-      if (kGated) zr[r].load(a.z, (size_t)row * a.z_stride + at.c[r]);
+      xr[r].load_once(a.x, (size_t)row * a.x_stride + at.c[r]);
+      if (kGated) zr[r].load_once(a.z, (size_t)row * a.z_stride + at.c[r]);
     }
   };
   int turn = 0;
-  int row = blockIdx.y;
+  int row = at.row;
   if (row < a.rows) fetch(row);
-  for (; row < a.rows; row += gridDim.y) {
+  for (; row < a.rows; row += at.step) {
     float x[R][8], z[R][8], u[R][8];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -141,7 +160,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm(NormArgs a)
         u[r][k] = MODE == kGateFirst ? x[r][k] * silu(z[r][k]) : x[r][k];
       }
     }
-    if (row + (int)gridDim.y < a.rows) fetch(row + gridDim.y);
+    if (row + at.step < a.rows) fetch(row + at.step);
     if (CK == kCkpt) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -188,110 +207,170 @@ template <typename T> struct NormRowOf<T, kCkpt> { typedef RowQ8 type; };
 template <typename T>
 __device__ __forceinline__ void load_row(Row8<T> &r, const void *p, int64_t stride, const Ckpt &,
                                          int, int row, int c) {
-  r.load(p, (size_t)row * stride + c);
+  r.load_once(p, (size_t)row * stride + c);
 }
 __device__ __forceinline__ void load_row(RowQ8 &r, const void *, int64_t, const Ckpt &k, int C,
                                          int row, int c) {
-  r.load(k, (size_t)row, C, c);
+  r.load_once(k, (size_t)row, C, c);
 }
 
-template <typename T, int MODE, int CK, int R, bool WIDE>
-__global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm_backward(NormArgs a) {
+// Hide that the raw row still holds what was widened from it: after a barrier
+// the fp32 copies are made again (a shift or mask each) instead of held in
+// twice the registers.
+__device__ __forceinline__ void forget(Row8<bf16> &r) {
+  asm volatile("" : "+v"(r.q.x), "+v"(r.q.y), "+v"(r.q.z), "+v"(r.q.w));
+}
+__device__ __forceinline__ void forget(Row8<float> &) {}
+__device__ __forceinline__ void forget(RowQ8 &r) { asm volatile("" : "+v"(r.q.x), "+v"(r.q.y)); }
+
+template <typename T, int MODE, int CK, bool BIAS, int R, bool WIDE, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
   __shared__ float lds[2][kMaxWaves * 4];
   const Place<WIDE, R> at(a);
-  float w[R][8], b[R][8], dw[R][8], db[R][8];
-  load_affine(a.w, 1.f, at.c, at.live, w);
-  load_affine(a.b, 0.f, at.c, at.live, b);
+  float w[R][8], dw[R][8], db[R][BIAS ? 8 : 1], b[R][BIAS ? 8 : 1];
+  load_affine(a.w, 1.f, at.c, w);
+  if constexpr (BIAS) load_affine(a.b, 0.f, at.c, b);
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[r][k] = db[r][k] = 0.f;
+    for (int k = 0; k < 8; ++k) {
+      dw[r][k] = 0.f;
+      if (BIAS) db[r][BIAS ? k : 0] = 0.f;
+    }
   constexpr bool kGated = MODE != kNoGate;
-  typename NormRowOf<T, CK>::type xr[R], zr[R];
-  Row8<T> dr[R];
+  typedef typename NormRowOf<T, CK>::type In;
+  In xr[R], zr[R], xn[R], zn[R];
+  Row8<T> dr[R], dn[R];
   auto fetch = [&](int row) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      load_row(xr[r], a.x, a.x_stride, a.xk, a.C, row, at.c[r]);
-      if (kGated) load_row(zr[r], a.z, a.z_stride, a.zk, a.C, row, at.c[r]);
-      dr[r].load(a.dout, (size_t)row * a.out_stride + at.c[r]);
+      load_row(xn[r], a.x, a.x_stride, a.xk, a.C, row, at.c[r]);
+      if (kGated) load_row(zn[r], a.z, a.z_stride, a.zk, a.C, row, at.c[r]);
+      dn[r].load_once(a.dout, (size_t)row * a.out_stride + at.c[r]);
     }
   };
+  // (the widest groups have no registers for a second row)
+  constexpr bool kAhead = R * THREADS <= 1024;
   int turn = 0;
-  int row = blockIdx.y;
-  if (row < a.rows) fetch(row);
-  for (; row < a.rows; row += gridDim.y) {
-    float x[R][8], sz[R][8], dsz[R][8], d[R][8], u[R][8];
+  int row = at.row;
+  if (kAhead && row < a.rows) fetch(row);
+  for (; row < a.rows; row += at.step) {
+    if (!kAhead) fetch(row);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float z[8];
-      xr[r].widen(x[r]);
-      if (kGated) zr[r].widen(z);
-      dr[r].widen(d[r]);
+      xr[r] = xn[r];
+      if (kGated) zr[r] = zn[r];
+      dr[r] = dn[r];
+    }
+    if (kAhead && row + at.step < a.rows) fetch(row + at.step);
+    // silu(z) and its derivative are kept over the sums; u and g are made again
+    float sz[R][8], dsz[R][8];
+    auto widen_u = [&](int r, float (&x)[8], float (&u)[8]) {
+      xr[r].widen(x);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (!at.live[r]) x[r][k] = z[k] = d[r][k] = 0.f;
-        if (kGated) {
+      for (int k = 0; k < 8; ++k) u[k] = MODE == kGateFirst ? x[k] * sz[r][k] : x[k];
+    };
+    auto widen_g = [&](int r, float (&d)[8], float (&dv)[8]) {
+      dr[r].widen(d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dv[k] = MODE == kGateLast ? d[k] * sz[r][k] : d[k];
+    };
+    if (kGated) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float z[8];
+        zr[r].widen(z);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
           const float s = sigmoid(z[k]);
           sz[r][k] = z[k] * s;
-          dsz[r][k] = s * (1.f + z[k] * (1.f - s));
+          dsz[r][k] = s * ((1.f + z[k]) - sz[r][k]);
         }
-        u[r][k] = MODE == kGateFirst ? x[r][k] * sz[r][k] : x[r][k];
       }
     }
-    if (row + (int)gridDim.y < a.rows) fetch(row + gridDim.y);
-    float mu = 0.f;
+    float mu = 0.f, mg = 0.f;
     if (a.center) {
-      float m[1] = {0.f};
+      float m[2] = {0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        float x[8], u[8], d[8], dv[8];
+        widen_u(r, x, u);
+        widen_g(r, d, dv);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m[0] += u[r][k];
+        for (int k = 0; k < 8; ++k) {
+          m[0] += at.live[r] ? u[k] : 0.f;
+          m[1] += at.live[r] ? dv[k] * w[r][k] : 0.f;
+        }
+        forget(xr[r]);
+        forget(dr[r]);
+      }
       team_sums<WIDE>(m, a.team, lds, turn);
       mu = m[0] * a.inv_n;
+      if (kGated) mg = m[1] * a.inv_n;
     }
-    float q[1] = {0.f};
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        u[r][k] = at.live[r] ? u[r][k] - mu : 0.f;
-        q[0] += u[r][k] * u[r][k];
-      }
-    team_sums<WIDE>(q, a.team, lds, turn);
-    const float rs = 1.f / sqrtf(q[0] * a.inv_n + a.eps);
-    // u becomes h; v and g from here
-    float v[R][8], g[R][8], m[2] = {0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float h = u[r][k] * rs;
-        u[r][k] = h;
-        v[r][k] = h * w[r][k] + b[r][k];
-        float dv = d[r][k];
-        if (MODE == kGateLast) dv *= sz[r][k];
-        if (MODE == kNoGate) {
-          const float s = sigmoid(v[r][k]);
-          dv *= s * (1.f + v[r][k] * (1.f - s));
-        }
-        dw[r][k] += dv * h;
-        db[r][k] += dv;
-        g[r][k] = dv * w[r][k];
-        m[0] += g[r][k] * h;
-        m[1] += g[r][k];
-      }
-    team_sums<WIDE>(m, a.team, lds, turn);
-    const float mgh = m[0] * a.inv_n, mg = a.center ? m[1] * a.inv_n : 0.f;
+    // with a gate dv does not depend on the statistics, so the sums of
+    // (u - mu)^2 and g (u - mu) are one reduction
+    float q[2] = {0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float dx[8], dz[8];
+      float x[8], u[8], d[8], dv[8];
+      widen_u(r, x, u);
+      widen_g(r, d, dv);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float du = rs * (g[r][k] - mg - u[r][k] * mgh);
+        const float c = at.live[r] ? u[k] - mu : 0.f;
+        q[0] += c * c;
+        if (kGated) q[1] += dv[k] * w[r][k] * c;
+      }
+      forget(xr[r]);
+      forget(dr[r]);
+    }
+    team_sums<WIDE>(q, a.team, lds, turn);
+    const float rs = 1.f / sqrtf(q[0] * a.inv_n + a.eps);
+    float mgh = rs * q[1] * a.inv_n;
+    if (!kGated) {
+      float m[2] = {0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x[8], d[8];
+        xr[r].widen(x);
+        dr[r].widen(d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float h = at.live[r] ? (x[k] - mu) * rs : 0.f;
+          float v = h * w[r][k];
+          if (BIAS) v += b[r][BIAS ? k : 0];
+          const float s = sigmoid(v);
+          const float dv = at.live[r] ? d[k] * (s * (1.f + (v - v * s))) : 0.f;
+          sz[r][k] = dv;   // (no gate: the registers hold dv)
+          m[0] += dv * w[r][k] * h;
+          m[1] += dv * w[r][k];
+        }
+        forget(xr[r]);
+      }
+      team_sums<WIDE>(m, a.team, lds, turn);
+      mgh = m[0] * a.inv_n;
+      mg = a.center ? m[1] * a.inv_n : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float x[8], u[8], d[8], dv[8], dx[8], dz[8];
+      widen_u(r, x, u);
+      widen_g(r, d, dv);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float h = (u[k] - mu) * rs;
+        const float e = MODE == kNoGate ? sz[r][k] : dv[k];
+        dw[r][k] += e * h;
+        if (BIAS) db[r][BIAS ? k : 0] += e;
+        const float du = rs * (e * w[r][k] - mg - h * mgh);
         dx[k] = MODE == kGateFirst ? du * sz[r][k] : du;
-        if (MODE == kGateFirst) dz[k] = du * x[r][k] * dsz[r][k];
-        if (MODE == kGateLast) dz[k] = d[r][k] * v[r][k] * dsz[r][k];
+        if (MODE == kGateFirst) dz[k] = du * x[k] * dsz[r][k];
+        if (MODE == kGateLast) {
+          float v = h * w[r][k];
+          if (BIAS) v += b[r][BIAS ? k : 0];
+          dz[k] = d[k] * v * dsz[r][k];
+        }
       }
       if (at.live[r]) {
         Row8<T>::store(a.dx, (size_t)row * a.dx_stride + at.c[r], dx);
@@ -300,14 +379,18 @@ __global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm_backward(No
     }
   }
   if (a.part) {
-    float *p = a.part + (size_t)blockIdx.y * 2 * a.C;
+    // (walkers without rows write zeros)
+    const int walker = !WIDE && a.subs > 1 ? blockIdx.y * a.subs + threadIdx.x / (a.G * a.team)
+                                           : blockIdx.y;
+    const bool mine = WIDE || a.subs == 1 || (int)threadIdx.x / (a.G * a.team) < a.subs;
+    float *p = a.part + (size_t)walker * (BIAS ? 2 : 1) * a.C;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (at.live[r]) {
+      if (mine && at.live[r]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           p[at.c[r] + k] = dw[r][k];
-          p[a.C + at.c[r] + k] = db[r][k];
+          if (BIAS) p[a.C + at.c[r] + k] = db[r][BIAS ? k : 0];
         }
       }
   }
@@ -316,40 +399,66 @@ __global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm_backward(No
 // Teams: lanes per group (in-wave) or threads per workgroup.
 struct Team {
   bool wide;
-  int r, size, xblocks;
+  int r, size, threads, xblocks, subs;
 };
 Team team_of(const NormArgs &a) {
   Team t{};
   const int lanes = a.gs / 8;
   t.r = 1;
+  t.subs = 1;
   if (lanes <= 64) {
     t.size = 1;
     while (t.size < lanes) t.size *= 2;
-    const int per = kTeamThreads / t.size;
-    t.xblocks = (a.G + per - 1) / per;
+    const int64_t need = (int64_t)a.G * t.size;
+    if (need <= 128) {
+      // a row takes part of a workgroup: several side by side
+      t.threads = 256;
+      t.subs = (int)(256 / need);
+      t.xblocks = 1;
+    } else {
+      // the workgroup size with the fewest lanes left over in the last one
+      int64_t best = 0;
+      for (int n = 256; n >= 64; n -= 64) {
+        if (n % t.size) continue;
+        const int64_t all = (need + n - 1) / n * n;
+        if (!best || all < best) {
+          best = all;
+          t.threads = n;
+        }
+      }
+      t.xblocks = (int)(best / t.threads);
+    }
   } else {
     t.wide = true;
     t.r = lanes > 1024 ? 2 : 1;
-    t.size = ((lanes + t.r - 1) / t.r + 63) / 64 * 64;
+    t.size = t.threads = ((lanes + t.r - 1) / t.r + 63) / 64 * 64;
     t.xblocks = a.G;
   }
   return t;
 }
 
-// Workgroups along the rows: enough to fill the card a few times over.
-int row_blocks(const NormArgs &a, const Team &t) {
-  const int threads = t.wide ? t.size : kTeamThreads;
-  int want = (2048 * 256 / threads + t.xblocks - 1) / t.xblocks;
-  if (want < 1) want = 1;
-  if (want > 65535) want = 65535;
-  return a.rows < want ? a.rows : want;
+// Workgroups along the rows: what the card holds at once at `waves` waves per
+// compute unit, or where rows are many and `least` is given, so many that each
+// lane walks `least` rows; all walk the same number up to one.
+int row_blocks(const NormArgs &a, const Team &t, int waves, int least, int most) {
+  constexpr int kUnits = 256;
+  int per = waves * 64 / t.threads;
+  if (per < 1) per = 1;
+  int64_t n = (int64_t)kUnits * per / t.xblocks * t.subs;
+  if (least > 0 && (a.rows + least - 1) / least > n) n = (a.rows + least - 1) / least;
+  if (n > (int64_t)most * t.subs) n = (int64_t)most * t.subs;
+  if (n < 1) n = 1;
+  const int64_t rounds = (a.rows + n - 1) / n;
+  n = (a.rows + rounds - 1) / rounds;
+  return (int)((n + t.subs - 1) / t.subs);
 }
 
 template <typename T, int MODE>
 hipError_t launch_forward(NormArgs a, hipStream_t s) {
   const Team t = team_of(a);
   a.team = t.size;
-  const dim3 grid(t.xblocks, row_blocks(a, t)), block(t.wide ? t.size : kTeamThreads);
+  a.subs = t.subs;
+  const dim3 grid(t.xblocks, row_blocks(a, t, 32, t.wide ? 6 : 3, 65535)), block(t.threads);
   // fused checkpoints need whole blocks inside a group; others are written by
   // a pass of their own
   const bool fused = a.gs % kCkptBlock == 0;
@@ -376,31 +485,43 @@ hipError_t launch_forward(NormArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, int CK, bool BIAS>
 hipError_t launch_back(NormArgs a, hipStream_t s) {
   const Team t = team_of(a);
   a.team = t.size;
-  const dim3 grid(t.xblocks, a.nparts), block(t.wide ? t.size : kTeamThreads);
-#define SSD_NORM(CK)                                                                      \
-  do {                                                                                    \
-    if (!t.wide)                                                                          \
-      hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, 1, false>), grid, block, 0, s, a); \
-    else if (t.r == 1)                                                                    \
-      hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, 1, true>), grid, block, 0, s, a);  \
-    else                                                                                  \
-      hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, 2, true>), grid, block, 0, s, a);  \
-  } while (0)
-  if (a.xk.q)
-    SSD_NORM(kCkpt);
+  a.subs = t.subs;
+  const dim3 grid(t.xblocks, a.nparts / t.subs), block(t.threads);
+#define SSD_NORM(R, WIDE, THREADS) \
+  hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, BIAS, R, WIDE, THREADS>), grid, block, 0, s, a)
+  if (!t.wide)
+    SSD_NORM(1, false, kTeamThreads);
+  else if (t.r == 1 && t.threads <= 512)
+    SSD_NORM(1, true, 512);
+  else if (t.r == 1)
+    SSD_NORM(1, true, 1024);
+  else if (t.threads <= 512)
+    SSD_NORM(2, true, 512);
   else
-    SSD_NORM(kPlain);
+    SSD_NORM(2, true, 1024);
 #undef SSD_NORM
   return hipGetLastError();
 }
 
+template <typename T, int MODE>
+hipError_t launch_back(const NormArgs &a, hipStream_t s) {
+  const bool bias = a.b != nullptr || a.sum_b;
+  if (a.xk.q)
+    return bias ? launch_back<T, MODE, kCkpt, true>(a, s) : launch_back<T, MODE, kCkpt, false>(a, s);
+  return bias ? launch_back<T, MODE, kPlain, true>(a, s) : launch_back<T, MODE, kPlain, false>(a, s);
+}
+
 }  // namespace
 
-int norm_row_blocks(const NormArgs &a) { return a.rows > 0 ? row_blocks(a, team_of(a)) : 0; }
+int norm_partial_rows(const NormArgs &a) {
+  if (a.rows == 0) return 0;
+  const Team t = team_of(a);
+  return row_blocks(a, t, 12, 0, 2048 / t.subs) * t.subs;
+}
 
 hipError_t launch_norm(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s) {
   switch (mode) {
@@ -429,9 +550,8 @@ hipError_t launch_norm_backward(const NormArgs &a, NormMode mode, bool bf16_io, 
 namespace {
 constexpr int kSumSlices = 16;
 __global__ __launch_bounds__(1024) void k_column_sums(const float *part, int n, int taps, int ch,
-                                                      float *dw, float *db) {
+                                                      int64_t cols, float *dw, float *db) {
   __shared__ double lds[kSumSlices][64];
-  const int64_t cols = (int64_t)(taps + 1) * ch;
   const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
   const int64_t j = (int64_t)blockIdx.x * 64 + lane;
   double sum = 0.0;
@@ -453,11 +573,11 @@ __global__ __launch_bounds__(1024) void k_column_sums(const float *part, int n, 
 }
 }  // namespace
 
-hipError_t launch_column_sums(const float *part, int n, int taps, int ch, float *dw, float *db,
-                              hipStream_t s) {
-  const int64_t cols = (int64_t)(taps + 1) * ch;
+hipError_t launch_column_sums(const float *part, int n, int rows, int taps, int ch, float *dw,
+                              float *db, hipStream_t s) {
+  const int64_t cols = (int64_t)rows * ch;
   hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, part, n,
-                     taps, ch, dw, db);
+                     taps, ch, cols, dw, db);
   return hipGetLastError();
 }
 

@@ -140,7 +140,7 @@ ssd_status conv_backward_geometry(const ssd_conv_problem *p, const int32_t *cu, 
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences exceed the int32 tile index",
                 (long long)T, (long long)nseq);
   *tblocks = ssd::conv_bwd_geometry(*a);
-  if (*tblocks * ((a->ch / 8 + 63) / 64) > INT32_MAX)
+  if (*tblocks * ssd::conv_bwd_channel_blocks(*a) > INT32_MAX)
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens x %d channels too large for one launch",
                 (long long)T, a->ch);
   return SSD_OK;
@@ -214,7 +214,7 @@ ssd_status check_gate(const ssd_norm_problem *p, bool gated) {
 }
 
 size_t norm_backward_bytes(const ssd::NormArgs &a) {
-  return (size_t)ssd::norm_row_blocks(a) * 2 * a.C * sizeof(float);
+  return (size_t)ssd::norm_partial_rows(a) * 2 * a.C * sizeof(float);
 }
 
 ssd_status check_workspace(const void *ws, size_t have, size_t need) {
@@ -293,7 +293,7 @@ ssd_status ssd_conv1d_silu_backward_workspace_size(const ssd_conv_problem *p, si
   ssd_status st = check_conv(p, &some, &T, &nseq);
   if (st != SSD_OK) return st;
   if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
-  ssd::ConvBwdArgs a{};
+  ssd::ConvBwdArgs a{};  // (a checkpoint takes no more tiles than the tensor)
   st = conv_backward_geometry(p, &some, T, nseq, &a, &tblocks);
   if (st != SSD_OK) return st;
   *bytes = conv_backward_bytes(a, p->width, tblocks);
@@ -332,12 +332,12 @@ ssd_status ssd_conv1d_silu_backward(const ssd_conv_problem *p, const void *xbc,
     return fail(SSD_ERR_INVALID_ARG, "xbc, dx, dB, dC, dxbc and the histories must be 16-byte "
                 "aligned");
   ssd::ConvBwdArgs a{};
+  a.ck = ckpt_of(checkpoint);
   st = conv_backward_geometry(p, cu_seqlens, T, nseq, &a, &tblocks);
   if (st != SSD_OK) return st;
   st = check_workspace(workspace, workspace_bytes, conv_backward_bytes(a, p->width, tblocks));
   if (st != SSD_OK) return st;
   a.xbc = xbc;
-  a.ck = ckpt_of(checkpoint);
   a.w = weight;
   a.bias = bias;
   a.hist_in = history_in;
@@ -352,7 +352,8 @@ ssd_status ssd_conv1d_silu_backward(const ssd_conv_problem *p, const void *xbc,
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = ssd::launch_conv_backward(a, p->width, p->dtype == SSD_DTYPE_BF16, s);
   if (e == hipSuccess)
-    e = ssd::launch_column_sums(a.part, (int)tblocks, p->width, a.ch, dweight, dbias, s);
+    e = ssd::launch_column_sums(a.part, (int)tblocks, p->width + 1, p->width, a.ch, dweight, dbias,
+                                s);
   if (e != hipSuccess)
     return fail(SSD_ERR_HIP, "convolution backward launch failed: %s", hipGetErrorString(e));
   return SSD_OK;
@@ -413,6 +414,8 @@ ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *p, const void *d
   ssd::NormArgs a = norm_args(p);
   const bool gated = z != nullptr || z_checkpoint != nullptr;
   const bool sums = dweight != nullptr || dbias != nullptr;
+  a.b = bias;
+  a.sum_b = dbias != nullptr;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (p->tokens > 0) {
     if ((st = check_gate(p, gated)) != SSD_OK) return st;
@@ -439,11 +442,10 @@ ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *p, const void *d
     a.xk = ckpt_of(x_checkpoint);
     a.zk = ckpt_of(z_checkpoint);
     a.w = weight;
-    a.b = bias;
     a.dout = dout;
     a.dx = dx;
     a.dz = dz;
-    a.nparts = ssd::norm_row_blocks(a);
+    a.nparts = ssd::norm_partial_rows(a);
     a.part = sums ? static_cast<float *>(workspace) : nullptr;
     const hipError_t e = ssd::launch_norm_backward(a, norm_mode(p, gated),
                                                    p->dtype == SSD_DTYPE_BF16, s);
@@ -451,7 +453,9 @@ ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *p, const void *d
       return fail(SSD_ERR_HIP, "group norm backward launch failed: %s", hipGetErrorString(e));
   }
   if (sums) {
-    const hipError_t e = ssd::launch_column_sums(a.part, a.nparts, 1, a.C, dweight, dbias, s);
+    const int rows = a.b != nullptr || a.sum_b ? 2 : 1;
+    const hipError_t e =
+        ssd::launch_column_sums(a.part, a.nparts, rows, 1, a.C, dweight, dbias, s);
     if (e != hipSuccess)
       return fail(SSD_ERR_HIP, "group norm backward launch failed: %s", hipGetErrorString(e));
   }

@@ -21,26 +21,28 @@ struct NormArgs {
   void *out;          // forward: rows at out_stride
   const void *dout;   // backward: rows at out_stride
   void *dx, *dz;      // backward: rows at dx_stride, dz_stride
-  float *part;        // backward: (row blocks, 2, C) partial sums of dw and db
+  float *part;        // backward: (nparts, 1 or 2, C) partial sums of dw (and db), or null
   Ckpt xk, zk;        // forward: written; backward: read
   int64_t x_stride, z_stride, out_stride, dx_stride, dz_stride;  // elements
   int32_t rows, C, G, gs;
   int32_t center;     // subtract the group's mean
   int32_t team;       // lanes per group (a power of two up to 64), or threads per workgroup
-  int32_t nparts;     // backward: row blocks
+  int32_t subs;       // rows a workgroup takes side by side (in-wave teams)
+  int32_t nparts;     // backward: rows of partial sums
+  int32_t sum_b;      // backward: db is wanted
   float eps, inv_n;   // inv_n = 1 / gs
 };
 
 constexpr int kNormMaxGroup = 16384;  // channels of a group the kernels hold on chip
-// Row blocks of the backward pass (rows of partial sums in the workspace).
-int norm_row_blocks(const NormArgs &a);
+// Rows of partial sums of the backward pass (one per row walker).
+int norm_partial_rows(const NormArgs &a);
 hipError_t launch_norm(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s);
 
-// Column sums of part (n, taps + 1, ch): column (k, c) goes to dw[c * taps + k]
-// for k < taps and to db[c] for k = taps (db null: not written).
-hipError_t launch_column_sums(const float *part, int n, int taps, int ch, float *dw, float *db,
-                              hipStream_t s);
+// Column sums of part (n, rows, ch): column (k, c) goes to dw[c * taps + k] for
+// k < taps and to db[c] for k = taps (a null array is not written).
+hipError_t launch_column_sums(const float *part, int n, int rows, int taps, int ch, float *dw,
+                              float *db, hipStream_t s);
 
 // Whole-tensor checkpoints: rows of T at `stride` to and from a checkpoint.
 hipError_t launch_ckpt_save(const void *src, int64_t stride, int64_t rows, int channels,

@@ -10,9 +10,18 @@ namespace ssd {
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+// Two values rounded to nearest even, in one instruction as a pair.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
 
 // Eight consecutive elements of one row, widened exactly to fp32, and back.
+// load_once reads with the nontemporal hint, for rows no other lane reads.
 // Rows are stored with nontemporal stores: nothing in the call reads them
 // again, and keeping them out of the caches was measured 20-25% faster on the
 // 2.7B-shaped front (nontemporal loads as well were slower).
@@ -21,6 +30,11 @@ template <> struct Row8<bf16> {
   uint4 q;
   __device__ __forceinline__ void load(const void *p, size_t i) {
     q = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(p) + i);
+  }
+  __device__ __forceinline__ void load_once(const void *p, size_t i) {
+    const u32x4_t v = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x4_t *>(static_cast<const bf16 *>(p) + i));
+    q = make_uint4(v[0], v[1], v[2], v[3]);
   }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -33,11 +47,7 @@ template <> struct Row8<bf16> {
   static __device__ __forceinline__ void store(void *p, size_t i, const float (&v)[8]) {
     u32x4_t q;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bf16 lo = (bf16)v[2 * k], hi = (bf16)v[2 * k + 1];
-      q[k] = (uint32_t)__builtin_bit_cast(uint16_t, lo) |
-             ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
-    }
+    for (int k = 0; k < 4; ++k) q[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
     __builtin_nontemporal_store(q, reinterpret_cast<u32x4_t *>(static_cast<bf16 *>(p) + i));
   }
 };
@@ -48,6 +58,12 @@ template <> struct Row8<float> {
     a = s[0];
     b = s[1];
   }
+  __device__ __forceinline__ void load_once(const void *p, size_t i) {
+    const f32x4_t *s = reinterpret_cast<const f32x4_t *>(static_cast<const float *>(p) + i);
+    const f32x4_t u = __builtin_nontemporal_load(s), v = __builtin_nontemporal_load(s + 1);
+    a = make_float4(u[0], u[1], u[2], u[3]);
+    b = make_float4(v[0], v[1], v[2], v[3]);
+  }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -57,6 +73,40 @@ template <> struct Row8<float> {
     const f32x4_t lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
     __builtin_nontemporal_store(lo, d);
     __builtin_nontemporal_store(hi, d + 1);
+  }
+};
+
+// Four consecutive elements of one row, for kernels that hold much per channel.
+template <typename T> struct Row4;
+template <> struct Row4<bf16> {
+  uint2 q;
+  __device__ __forceinline__ void load(const void *p, size_t i) {
+    q = *reinterpret_cast<const uint2 *>(static_cast<const bf16 *>(p) + i);
+  }
+  __device__ __forceinline__ void widen(float (&v)[4]) const {
+    v[0] = __uint_as_float(q.x << 16);
+    v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16);
+    v[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(void *p, size_t i, const float (&v)[4]) {
+    u32x2_t q;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) q[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2_t *>(static_cast<bf16 *>(p) + i));
+  }
+};
+template <> struct Row4<float> {
+  float4 a;
+  __device__ __forceinline__ void load(const void *p, size_t i) {
+    a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+  }
+  __device__ __forceinline__ void widen(float (&v)[4]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+  static __device__ __forceinline__ void store(void *p, size_t i, const float (&v)[4]) {
+    const f32x4_t q = {v[0], v[1], v[2], v[3]};
+    __builtin_nontemporal_store(q, reinterpret_cast<f32x4_t *>(static_cast<float *>(p) + i));
   }
 };
 
@@ -106,12 +156,32 @@ struct RowQ8 {
     q = *reinterpret_cast<const uint2 *>(k.q + row * channels + c0);
     e = k.e[row * ckpt_blocks(channels) + c0 / kCkptBlock];
   }
+  __device__ __forceinline__ void load_once(const Ckpt &k, size_t row, int channels, int c0) {
+    const u32x2_t v = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x2_t *>(k.q + row * channels + c0));
+    q = make_uint2(v[0], v[1]);
+    e = k.e[row * ckpt_blocks(channels) + c0 / kCkptBlock];
+  }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     const float step = __uint_as_float(e << 23);
     const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       v[k] = step * (float)(((int32_t)(w[k / 4] << (24 - 8 * (k & 3)))) >> 24);
+  }
+};
+
+// Four channels of a checkpoint row.
+struct RowQ4 {
+  uint32_t q, e;
+  __device__ __forceinline__ void load(const Ckpt &k, size_t row, int channels, int c0) {
+    q = *reinterpret_cast<const uint32_t *>(k.q + row * channels + c0);
+    e = k.e[row * ckpt_blocks(channels) + c0 / kCkptBlock];
+  }
+  __device__ __forceinline__ void widen(float (&v)[4]) const {
+    const float step = __uint_as_float(e << 23);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = step * (float)(((int32_t)(q << (24 - 8 * k))) >> 24);
   }
 };
 
