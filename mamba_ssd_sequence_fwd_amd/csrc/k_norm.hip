@@ -28,7 +28,7 @@ namespace {
 enum : int { kPlain = 0, kCkpt = 1 };
 
 constexpr int kTeamThreads = 256;  // workgroup of the in-wave teams
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = 8;
 
 template <int Ctrl>
 __device__ __forceinline__ float dpp_add(float v) {
@@ -129,8 +129,8 @@ __device__ __forceinline__ void load_affine(const float *p, float otherwise, con
   }
 }
 
-template <typename T, int MODE, int CK, int R, bool WIDE>
-__global__ __launch_bounds__(WIDE ? 1024 : kTeamThreads) void k_norm(NormArgs a) {
+template <typename T, int MODE, int CK, int R, bool WIDE, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_norm(NormArgs a) {
   __shared__ float lds[2][kMaxWaves * 4];
   const Place<WIDE, R> at(a);
   float w[R][8], b[R][8];
@@ -227,9 +227,35 @@ template <typename T, int MODE, int CK, bool BIAS, int R, bool WIDE, int THREADS
 __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
   __shared__ float lds[2][kMaxWaves * 4];
   const Place<WIDE, R> at(a);
-  float w[R][8], dw[R][8], db[R][BIAS ? 8 : 1], b[R][BIAS ? 8 : 1];
-  load_affine(a.w, 1.f, at.c, w);
-  if constexpr (BIAS) load_affine(a.b, 0.f, at.c, b);
+  // With 4 parts a lane there are no registers for a second row, and in fp32
+  // or with a bias none for the weights either: those are read again, from
+  // L2, for each row (4096 tokens of 16384 channels, fp32 with a bias: 516 us;
+  // held, and spilled, 803).
+  constexpr bool kAhead = R < 4, kRoom = R < 4 || (sizeof(T) == 2 && !BIAS);
+  float dw[R][8], db[R][BIAS ? 8 : 1];
+  float ws[kRoom ? R : 1][8], bs[kRoom && BIAS ? R : 1][8];
+  if constexpr (kRoom) {
+    load_affine<R>(a.w, 1.f, at.c, ws);
+    if constexpr (BIAS) load_affine<R>(a.b, 0.f, at.c, bs);
+  }
+  auto weights = [&](int r, float (&w)[8], float (&b)[8]) {
+    if constexpr (kRoom) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[k] = ws[kRoom ? r : 0][k];
+        b[k] = BIAS ? bs[kRoom && BIAS ? r : 0][k] : 0.f;
+      }
+    } else {
+      const int c[1] = {at.c[r]};
+      float v[1][8];
+      load_affine<1>(a.w, 1.f, c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = v[0][k];
+      if (BIAS) load_affine<1>(a.b, 0.f, c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[k] = BIAS ? v[0][k] : 0.f;
+    }
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -249,8 +275,6 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
       dn[r].load_once(a.dout, (size_t)row * a.out_stride + at.c[r]);
     }
   };
-  // (the widest groups have no registers for a second row)
-  constexpr bool kAhead = R * THREADS <= 1024;
   int turn = 0;
   int row = at.row;
   if (kAhead && row < a.rows) fetch(row);
@@ -293,13 +317,14 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
       float m[2] = {0.f, 0.f};
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float x[8], u[8], d[8], dv[8];
+        float x[8], u[8], d[8], dv[8], w[8], b[8];
         widen_u(r, x, u);
         widen_g(r, d, dv);
+        weights(r, w, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           m[0] += at.live[r] ? u[k] : 0.f;
-          m[1] += at.live[r] ? dv[k] * w[r][k] : 0.f;
+          m[1] += at.live[r] ? dv[k] * w[k] : 0.f;
         }
         forget(xr[r]);
         forget(dr[r]);
@@ -313,14 +338,15 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
     float q[2] = {0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float x[8], u[8], d[8], dv[8];
+      float x[8], u[8], d[8], dv[8], w[8], b[8];
       widen_u(r, x, u);
       widen_g(r, d, dv);
+      if (kGated) weights(r, w, b);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float c = at.live[r] ? u[k] - mu : 0.f;
         q[0] += c * c;
-        if (kGated) q[1] += dv[k] * w[r][k] * c;
+        if (kGated) q[1] += dv[k] * w[k] * c;
       }
       forget(xr[r]);
       forget(dr[r]);
@@ -332,19 +358,19 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
       float m[2] = {0.f, 0.f};
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float x[8], d[8];
+        float x[8], d[8], w[8], b[8];
         xr[r].widen(x);
         dr[r].widen(d);
+        weights(r, w, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float h = at.live[r] ? (x[k] - mu) * rs : 0.f;
-          float v = h * w[r][k];
-          if (BIAS) v += b[r][BIAS ? k : 0];
+          const float v = h * w[k] + b[k];
           const float s = sigmoid(v);
           const float dv = at.live[r] ? d[k] * (s * (1.f + (v - v * s))) : 0.f;
           sz[r][k] = dv;   // (no gate: the registers hold dv)
-          m[0] += dv * w[r][k] * h;
-          m[1] += dv * w[r][k];
+          m[0] += dv * w[k] * h;
+          m[1] += dv * w[k];
         }
         forget(xr[r]);
       }
@@ -354,23 +380,20 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float x[8], u[8], d[8], dv[8], dx[8], dz[8];
+      float x[8], u[8], d[8], dv[8], dx[8], dz[8], w[8], b[8];
       widen_u(r, x, u);
       widen_g(r, d, dv);
+      weights(r, w, b);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float h = (u[k] - mu) * rs;
         const float e = MODE == kNoGate ? sz[r][k] : dv[k];
         dw[r][k] += e * h;
         if (BIAS) db[r][BIAS ? k : 0] += e;
-        const float du = rs * (e * w[r][k] - mg - h * mgh);
+        const float du = rs * (e * w[k] - mg - h * mgh);
         dx[k] = MODE == kGateFirst ? du * sz[r][k] : du;
         if (MODE == kGateFirst) dz[k] = du * x[k] * dsz[r][k];
-        if (MODE == kGateLast) {
-          float v = h * w[r][k];
-          if (BIAS) v += b[r][BIAS ? k : 0];
-          dz[k] = d[k] * v * dsz[r][k];
-        }
+        if (MODE == kGateLast) dz[k] = d[k] * (h * w[k] + b[k]) * dsz[r][k];
       }
       if (at.live[r]) {
         Row8<T>::store(a.dx, (size_t)row * a.dx_stride + at.c[r], dx);
@@ -396,12 +419,21 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
   }
 }
 
-// Teams: lanes per group (in-wave) or threads per workgroup.
+// How the lanes are dealt to the groups. In-wave teams: `size` lanes per
+// group. Workgroup teams: `size` threads with R parts of 8 channels each.
 struct Team {
   bool wide;
   int r, size, threads, xblocks, subs;
 };
-Team team_of(const NormArgs &a) {
+
+// Groups of up to 64 lanes stay inside a wave; up to 512 lanes take a wave per
+// 64; wider ones take 4 or 8 waves with 2 to 4 parts a lane. More waves than 8
+// a group, or a number that the 4 SIMDs of a compute unit do not share evenly,
+// cost more than lanes without channels: 16384 tokens of one group of 5120
+// channels (640 lanes) take 97 us forward and 164 us backward with 10 waves of
+// one part, 86 us with 4 waves of 3 (forward), 150 us with 8 waves of 2
+// (backward).
+Team team_of(const NormArgs &a, int r_wide, int threads_wide) {
   Team t{};
   const int lanes = a.gs / 8;
   t.r = 1;
@@ -410,15 +442,15 @@ Team team_of(const NormArgs &a) {
     t.size = 1;
     while (t.size < lanes) t.size *= 2;
     const int64_t need = (int64_t)a.G * t.size;
-    if (need <= 128) {
+    if (need <= kTeamThreads / 2) {
       // a row takes part of a workgroup: several side by side
-      t.threads = 256;
-      t.subs = (int)(256 / need);
+      t.threads = kTeamThreads;
+      t.subs = (int)(kTeamThreads / need);
       t.xblocks = 1;
     } else {
       // the workgroup size with the fewest lanes left over in the last one
       int64_t best = 0;
-      for (int n = 256; n >= 64; n -= 64) {
+      for (int n = kTeamThreads; n >= 64; n -= 64) {
         if (n % t.size) continue;
         const int64_t all = (need + n - 1) / n * n;
         if (!best || all < best) {
@@ -430,11 +462,31 @@ Team team_of(const NormArgs &a) {
     }
   } else {
     t.wide = true;
-    t.r = lanes > 1024 ? 2 : 1;
-    t.size = t.threads = ((lanes + t.r - 1) / t.r + 63) / 64 * 64;
     t.xblocks = a.G;
+    if (lanes <= 512) {
+      t.threads = (lanes + 63) / 64 * 64;
+    } else if (lanes <= r_wide * threads_wide) {
+      t.r = r_wide;
+      t.threads = threads_wide;
+    } else if (lanes <= 1024) {
+      t.r = 1024 / threads_wide;
+      t.threads = threads_wide;
+    } else {
+      t.r = 4;
+      t.threads = 512;
+    }
+    t.size = t.threads;
   }
   return t;
+}
+
+// Forward: 4 waves of 3 or 4 parts. Backward: 8 waves of 2 parts; from 8-bit
+// checkpoints, whose loads are shorter, 4 waves of 3 up to 768 lanes (140 us
+// at the shape above against 168 us with 8 waves of 2).
+Team forward_team(const NormArgs &a) { return team_of(a, 3, 256); }
+Team backward_team(const NormArgs &a) {
+  const int lanes = a.gs / 8;
+  return a.xk.q && lanes <= 768 ? team_of(a, 3, 256) : team_of(a, 2, 512);
 }
 
 // Workgroups along the rows: what the card holds at once at `waves` waves per
@@ -453,12 +505,31 @@ int row_blocks(const NormArgs &a, const Team &t, int waves, int least, int most)
   return (int)((n + t.subs - 1) / t.subs);
 }
 
+// Forward: in-wave teams run best as many short workgroups (32768 tokens of 8
+// groups of 512: 131 us with 3 rows each, 158 us with 32 waves a unit that
+// stay), workgroup teams as few that stay (one group of 5120: 86 us with 8
+// waves a unit, 92 with 4 rows each; groups of 1024 to 4096: 69 us at 16, 71
+// to 72 with 6 rows).
+int forward_blocks(const NormArgs &a, const Team &t) {
+  if (!t.wide) return row_blocks(a, t, 32, 3, 65535);
+  return row_blocks(a, t, t.r == 1 ? 16 : 8, 0, 65535);
+}
+
+// Backward: every walker costs a row of partial sums, and more loads in
+// flight do not help: 8 waves a unit (16384 tokens of groups of 1024 to 4096:
+// 113 to 117 us; 12 waves 119 to 125), from checkpoints, with half the bytes
+// a load, 16 (110 to 111 us; 8 waves 125 to 135). Lanes of several parts hold
+// twice the loads: 8.
+int backward_blocks(const NormArgs &a, const Team &t) {
+  return row_blocks(a, t, a.xk.q && t.r == 1 ? 16 : 8, 0, 2048 / t.subs);
+}
+
 template <typename T, int MODE>
 hipError_t launch_forward(NormArgs a, hipStream_t s) {
-  const Team t = team_of(a);
+  const Team t = forward_team(a);
   a.team = t.size;
   a.subs = t.subs;
-  const dim3 grid(t.xblocks, row_blocks(a, t, 32, t.wide ? 6 : 3, 65535)), block(t.threads);
+  const dim3 grid(t.xblocks, forward_blocks(a, t)), block(t.threads);
   // fused checkpoints need whole blocks inside a group; others are written by
   // a pass of their own
   const bool fused = a.gs % kCkptBlock == 0;
@@ -468,41 +539,46 @@ hipError_t launch_forward(NormArgs a, hipStream_t s) {
     if (e == hipSuccess && a.z) e = launch_ckpt_save(a.z, a.z_stride, a.rows, a.C, bf, a.zk, s);
     if (e != hipSuccess) return e;
   }
-#define SSD_NORM(CK)                                                              \
-  do {                                                                            \
-    if (!t.wide)                                                                  \
-      hipLaunchKernelGGL((k_norm<T, MODE, CK, 1, false>), grid, block, 0, s, a);  \
-    else if (t.r == 1)                                                            \
-      hipLaunchKernelGGL((k_norm<T, MODE, CK, 1, true>), grid, block, 0, s, a);   \
-    else                                                                          \
-      hipLaunchKernelGGL((k_norm<T, MODE, CK, 2, true>), grid, block, 0, s, a);   \
+#define SSD_NORM_K(CK, R, WIDE, THREADS) \
+  hipLaunchKernelGGL((k_norm<T, MODE, CK, R, WIDE, THREADS>), grid, block, 0, s, a)
+#define SSD_NORM(CK)                       \
+  do {                                     \
+    if (!t.wide)                           \
+      SSD_NORM_K(CK, 1, false, 256);       \
+    else if (t.r == 1)                     \
+      SSD_NORM_K(CK, 1, true, 512);        \
+    else if (t.r == 3)                     \
+      SSD_NORM_K(CK, 3, true, 256);        \
+    else                                   \
+      SSD_NORM_K(CK, 4, true, 512);        \
   } while (0)
   if (a.xk.q && fused)
     SSD_NORM(kCkpt);
   else
     SSD_NORM(kPlain);
 #undef SSD_NORM
+#undef SSD_NORM_K
   return hipGetLastError();
 }
 
 template <typename T, int MODE, int CK, bool BIAS>
 hipError_t launch_back(NormArgs a, hipStream_t s) {
-  const Team t = team_of(a);
+  const Team t = backward_team(a);
   a.team = t.size;
   a.subs = t.subs;
   const dim3 grid(t.xblocks, a.nparts / t.subs), block(t.threads);
 #define SSD_NORM(R, WIDE, THREADS) \
   hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, BIAS, R, WIDE, THREADS>), grid, block, 0, s, a)
   if (!t.wide)
-    SSD_NORM(1, false, kTeamThreads);
-  else if (t.r == 1 && t.threads <= 512)
-    SSD_NORM(1, true, 512);
+    SSD_NORM(1, false, 256);
   else if (t.r == 1)
-    SSD_NORM(1, true, 1024);
-  else if (t.threads <= 512)
+    SSD_NORM(1, true, 512);
+  else if (t.r == 2)
     SSD_NORM(2, true, 512);
-  else
-    SSD_NORM(2, true, 1024);
+  else if (t.r == 4)
+    SSD_NORM(4, true, 512);
+  else if constexpr (CK == kCkpt)
+    SSD_NORM(3, true, 256);
 #undef SSD_NORM
   return hipGetLastError();
 }
@@ -519,8 +595,8 @@ hipError_t launch_back(const NormArgs &a, hipStream_t s) {
 
 int norm_partial_rows(const NormArgs &a) {
   if (a.rows == 0) return 0;
-  const Team t = team_of(a);
-  return row_blocks(a, t, 12, 0, 2048 / t.subs) * t.subs;
+  const Team t = backward_team(a);
+  return backward_blocks(a, t) * t.subs;
 }
 
 hipError_t launch_norm(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s) {

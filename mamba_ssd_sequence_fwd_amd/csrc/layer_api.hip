@@ -213,8 +213,14 @@ ssd_status check_gate(const ssd_norm_problem *p, bool gated) {
   return SSD_OK;
 }
 
-size_t norm_backward_bytes(const ssd::NormArgs &a) {
-  return (size_t)ssd::norm_partial_rows(a) * 2 * a.C * sizeof(float);
+// Enough for both sources of the inputs, whose geometries differ.
+size_t norm_backward_bytes(ssd::NormArgs a) {
+  static int8_t some;
+  a.xk.q = nullptr;
+  const int plain = ssd::norm_partial_rows(a);
+  a.xk.q = &some;
+  const int kept = ssd::norm_partial_rows(a);
+  return (size_t)(plain > kept ? plain : kept) * 2 * a.C * sizeof(float);
 }
 
 ssd_status check_workspace(const void *ws, size_t have, size_t need) {
