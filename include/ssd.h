@@ -568,8 +568,8 @@ ssd_status ssd_conv1d_silu_backward(const ssd_conv_problem *prob, const void *xb
  *       = silu(v)           (no z)
  * One token per sequence (decoding) is the same call with few tokens.
  *
- * Problem: tokens >= 0; channels a multiple of groups; the group size a
- * multiple of 8 up to 16384; dtype F32 or BF16 of x, z, out and their
+ * Problem: tokens >= 0 (up to 2^30 - 1); channels a multiple of groups; the
+ * group size a multiple of 8 up to 16384; dtype F32 or BF16 of x, z, out and their
  * gradients; flags 0 or SSD_NORM_* bits; eps finite and >= 0; strides in
  * elements between token rows, each >= channels, at most 2^31 - 1 and a
  * multiple of 16 bytes (that of a tensor that is not given is not looked at).

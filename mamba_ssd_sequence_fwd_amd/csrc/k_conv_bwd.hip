@@ -53,15 +53,10 @@ __attribute__((amdgpu_waves_per_eu(4))) void k_conv_backward(ConvBwdArgs a, int 
   // the same registers
   constexpr int kBatch = P == 3 ? 3 : sizeof(T) == 2 ? 4 : 2;
   static_assert(kBatch >= P && kBatch % P == 0, "a first batch covers the steps before the tile's own");
-  // one contiguous range of workgroups per XCD: tiles that share halo rows
-  // meet in one L2
-  const int nb = gridDim.x, bid = blockIdx.x;
-  const int xq = nb >> 3, xr = nb & 7, xcd = bid & 7;
-  const int lb = xcd * xq + min(xcd, xr) + (bid >> 3);
-  const int tb = lb / cblocks;
+  const int tb = blockIdx.x / cblocks;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cg = ((lb - tb * cblocks) * 64 + lane) * kLane;
+  const int cg = ((blockIdx.x - tb * cblocks) * 64 + lane) * kLane;
   const bool live = cg < a.ch;
   const int c0 = live ? cg : a.ch - kLane;
   const int slot = tb * kConvBwdWaves + wave;

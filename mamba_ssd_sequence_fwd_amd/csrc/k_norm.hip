@@ -76,9 +76,10 @@ __device__ __forceinline__ void team_sums(float (&v)[N], int team, float (*lds)[
   }
 }
 
-// The lane's place: its channels for each r and whether they exist (lanes
-// without channels load channel 0's and store nothing, so loads need no
-// branch).
+// The lane's place: its channels for each r and whether they exist. Lanes
+// without channels load channel 0's, so that loads need no branch, and store
+// nothing; their terms of a sum are replaced, not multiplied, by zero, since
+// channel 0 of another group may hold infinities or NaN.
 template <bool WIDE, int R>
 struct Place {
   int c[R];
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
       for (int k = 0; k < 8; ++k) {
         const float c = at.live[r] ? u[k] - mu : 0.f;
         q[0] += c * c;
-        if (kGated) q[1] += dv[k] * w[k] * c;
+        if (kGated) q[1] += at.live[r] ? dv[k] * w[k] * c : 0.f;
       }
       forget(xr[r]);
       forget(dr[r]);
@@ -369,8 +370,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
           const float s = sigmoid(v);
           const float dv = at.live[r] ? d[k] * (s * (1.f + (v - v * s))) : 0.f;
           sz[r][k] = dv;   // (no gate: the registers hold dv)
-          m[0] += dv * w[k] * h;
-          m[1] += dv * w[k];
+          m[0] += at.live[r] ? dv * w[k] * h : 0.f;
+          m[1] += at.live[r] ? dv * w[k] : 0.f;
         }
         forget(xr[r]);
       }
@@ -490,15 +491,16 @@ Team backward_team(const NormArgs &a) {
 }
 
 // Workgroups along the rows: what the card holds at once at `waves` waves per
-// compute unit, or where rows are many and `least` is given, so many that each
-// lane walks `least` rows; all walk the same number up to one.
-int row_blocks(const NormArgs &a, const Team &t, int waves, int least, int most) {
+// compute unit, but no more than `cap` row walkers; or where rows are many, so
+// many that each lane walks `most` rows. All walk the same number up to one.
+int row_blocks(const NormArgs &a, const Team &t, int waves, int64_t cap, int most) {
   constexpr int kUnits = 256;
   int per = waves * 64 / t.threads;
   if (per < 1) per = 1;
   int64_t n = (int64_t)kUnits * per / t.xblocks * t.subs;
-  if (least > 0 && (a.rows + least - 1) / least > n) n = (a.rows + least - 1) / least;
-  if (n > (int64_t)most * t.subs) n = (int64_t)most * t.subs;
+  if (n > cap) n = cap;
+  if ((a.rows + (int64_t)most - 1) / most > n) n = (a.rows + (int64_t)most - 1) / most;
+  if (n > (int64_t)65535 * t.subs) n = (int64_t)65535 * t.subs;
   if (n < 1) n = 1;
   const int64_t rounds = (a.rows + n - 1) / n;
   n = (a.rows + rounds - 1) / rounds;
@@ -511,17 +513,18 @@ int row_blocks(const NormArgs &a, const Team &t, int waves, int least, int most)
 // waves a unit, 92 with 4 rows each; groups of 1024 to 4096: 69 us at 16, 71
 // to 72 with 6 rows).
 int forward_blocks(const NormArgs &a, const Team &t) {
-  if (!t.wide) return row_blocks(a, t, 32, 3, 65535);
-  return row_blocks(a, t, t.r == 1 ? 16 : 8, 0, 65535);
+  if (!t.wide) return row_blocks(a, t, 32, INT32_MAX, 3);
+  return row_blocks(a, t, t.r == 1 ? 16 : 8, INT32_MAX, INT32_MAX);
 }
 
 // Backward: every walker costs a row of partial sums, and more loads in
 // flight do not help: 8 waves a unit (16384 tokens of groups of 1024 to 4096:
 // 113 to 117 us; 12 waves 119 to 125), from checkpoints, with half the bytes
 // a load, 16 (110 to 111 us; 8 waves 125 to 135). Lanes of several parts hold
-// twice the loads: 8.
+// twice the loads: 8. No walker adds up more
+// than 256 rows in fp32 (up to 16 million tokens).
 int backward_blocks(const NormArgs &a, const Team &t) {
-  return row_blocks(a, t, a.xk.q && t.r == 1 ? 16 : 8, 0, 2048 / t.subs);
+  return row_blocks(a, t, a.xk.q && t.r == 1 ? 16 : 8, 2048, 256);
 }
 
 template <typename T, int MODE>

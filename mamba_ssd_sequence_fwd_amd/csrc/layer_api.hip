@@ -171,8 +171,9 @@ ssd_status check_norm(const ssd_norm_problem *p) {
   if (gs % 8 != 0 || gs > ssd::kNormMaxGroup)
     return fail(SSD_ERR_UNSUPPORTED, "group size %d is not a multiple of 8 up to %d", gs,
                 ssd::kNormMaxGroup);
-  if (p->channels > INT32_MAX / 8)
-    return fail(SSD_ERR_UNSUPPORTED, "channels %d too many", p->channels);
+  if (p->channels > INT32_MAX / 8 || p->tokens > INT32_MAX / 2)
+    return fail(SSD_ERR_UNSUPPORTED, "%d tokens x %d channels too large for 32-bit indexing",
+                p->tokens, p->channels);
   return SSD_OK;
 }
 

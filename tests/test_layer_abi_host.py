@@ -52,6 +52,7 @@ NORM_BAD = [
     ({"eps": float("inf")}, ssd.SSD_ERR_INVALID_ARG),
     ({"dtype": 3}, ssd.SSD_ERR_UNSUPPORTED),
     ({"groups": 24}, ssd.SSD_ERR_UNSUPPORTED),                       # 4 channels a group
+    ({"tokens": 1 << 30}, ssd.SSD_ERR_UNSUPPORTED),
     ({"channels": 16392, "groups": 1, "x_stride": 16392, "z_stride": 16392,
       "out_stride": 16392, "dx_stride": 16392, "dz_stride": 16392}, ssd.SSD_ERR_UNSUPPORTED),
     ({"x_stride": 88}, ssd.SSD_ERR_INVALID_ARG),
@@ -124,14 +125,18 @@ def test_norm_backward_refuses_pointers(lib):
     assert lib.ssd_group_norm_silu_backward_workspace_size(ctypes.byref(NP()), None) == bad
 
 
-def test_norm_backward_workspace_does_not_grow_with_many_tokens(lib):
-    """The partial rows are bounded: a long batch takes no more than 2048."""
+def test_norm_backward_workspace_is_small(lib):
+    """At most 2048 partial rows of 8 bytes a channel, or one for 256 tokens
+    where that is more (and up to one workgroup's rows over)."""
     n = ctypes.c_size_t(0)
     for channels, groups in ((5120, 1), (4096, 8), (64, 8), (8, 1)):
-        p = NP(tokens=1 << 24, channels=channels, groups=groups)
-        assert lib.ssd_group_norm_silu_backward_workspace_size(ctypes.byref(p),
-                                                               ctypes.byref(n)) == ssd.SSD_OK
-        assert 0 < n.value <= 2048 * 2 * channels * 4
+        for tokens in (1, 100, 1 << 14, 1 << 23):   # (65535 is the most a grid takes)
+            p = NP(tokens=tokens, channels=channels, groups=groups)
+            assert lib.ssd_group_norm_silu_backward_workspace_size(
+                ctypes.byref(p), ctypes.byref(n)) == ssd.SSD_OK
+            walkers = n.value // (8 * channels)
+            assert 0 < walkers and -(-tokens // walkers) <= 256
+            assert walkers <= max(2048, -(-tokens // 256)) + 256
 
 
 # ---- convolution front -------------------------------------------------------------

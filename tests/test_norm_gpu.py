@@ -154,6 +154,56 @@ def test_norm_special_values():
     assert torch.isfinite(g["dx"][3]).all() and torch.count_nonzero(g["dz"][0]) == 0
 
 
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("C,G", [(120, 5), (1040, 2), (24, 3), (8704, 2)])
+def test_norm_groups_do_not_see_each_other(C, G, ckpt):
+    """Groups that leave lanes over: NaN and infinities in the first group (and
+    in its weights) change no bit of the others, forward and backward."""
+    rng = np.random.default_rng(9)
+    T, gs = 5, C // G
+    x, z, d = (rows(rng, T, C, "bf16")[0] for _ in range(3))
+    w, b = torch.randn(C, device="cuda"), torch.randn(C, device="cuda")
+    print("[gpu] group norm between groups %d/%d" % (C, G), flush=True)
+
+    def both(**kw):
+        zz = None if kw.pop("none", False) else z
+        out, kx, kz = ssd.group_norm_silu(x, w, b, zz, groups=G, checkpoint=True, **kw)
+        src = (kx, kz) if ckpt else (x, zz)
+        g = ssd.group_norm_silu_backward(d, src[0], w, b, src[1], groups=G, **kw)
+        torch.cuda.synchronize()
+        return [t for t in (out, g["dx"], g["dz"], g["dweight"], g["dbias"]) if t is not None]
+
+    forms = (dict(), dict(center=True), dict(norm_before_gate=True, center=True), dict(none=True),
+             dict(none=True, center=True))
+    clean = [both(**dict(f)) for f in forms]
+    # whole checkpoint blocks of the first group (a block that holds NaN reads as NaN)
+    first = gs if not ckpt else gs // 32 * 32
+    if first == 0:
+        pytest.skip("the first group has no checkpoint block of its own")
+    for t in (x, d):
+        t[1, 0], t[2, 0], t[3, 0] = float("nan"), float("inf"), -float("inf")
+    z[1, 1] = float("nan")
+    w[0], b[0] = float("inf"), float("nan")
+    for f, want in zip(forms, clean):
+        for got, ref in zip(both(**dict(f)), want):
+            assert torch.equal(got[..., gs:], ref[..., gs:]), f
+
+
+def test_norm_sums_of_many_rows():
+    """dweight and dbias over 200,000 tokens of few channels: each walker adds
+    at most 256 rows in fp32, the walkers in fp64."""
+    T, C = 200000, 64
+    g = torch.Generator("cuda").manual_seed(1)
+    x, z, d = (torch.randn(T, C, device="cuda", generator=g) for _ in range(3))
+    w, b = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    print("[gpu] group norm sums of many rows", flush=True)
+    got = ssd.group_norm_silu_backward(d, x, w, b, z, groups=2)
+    torch.cuda.synchronize()
+    want, size = norm_backward(d.cpu(), x.cpu(), z.cpu(), w.cpu(), b.cpu(), 2, 1e-5, False, "first")
+    for k in ("dx", "dz", "dweight", "dbias"):
+        check(k, got[k], want[k], size[k], "fp32", 512)
+
+
 def test_norm_without_tokens():
     w, b = torch.ones(64, device="cuda"), torch.ones(64, device="cuda")
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
