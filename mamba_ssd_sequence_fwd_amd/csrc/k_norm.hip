@@ -403,11 +403,28 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
     }
   }
   if (a.part) {
-    // (walkers without rows write zeros)
-    const int walker = !WIDE && a.subs > 1 ? blockIdx.y * a.subs + threadIdx.x / (a.G * a.team)
-                                           : blockIdx.y;
-    const bool mine = WIDE || a.subs == 1 || (int)threadIdx.x / (a.G * a.team) < a.subs;
-    float *p = a.part + (size_t)walker * (BIAS ? 2 : 1) * a.C;
+    float *p = a.part + (size_t)blockIdx.y * (BIAS ? 2 : 1) * a.C;
+    bool mine = true;
+    if constexpr (!WIDE) {
+      // rows side by side: joined in the order of the rows
+      if (a.subs > 1) {
+        __shared__ float join[8][kTeamThreads];
+        const int need = a.G * a.team;
+        mine = (int)threadIdx.x < need;
+        auto joined = [&](float (&v)[8]) {
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) join[k][threadIdx.x] = v[k];
+          __syncthreads();
+          if (mine)
+            for (int i = 1; i < a.subs; ++i)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] += join[k][threadIdx.x + i * need];
+        };
+        joined(dw[0]);
+        if constexpr (BIAS) joined(db[0]);
+      }
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (mine && at.live[r]) {
@@ -491,14 +508,14 @@ Team backward_team(const NormArgs &a) {
 }
 
 // Workgroups along the rows: what the card holds at once at `waves` waves per
-// compute unit, but no more than `cap` row walkers; or where rows are many, so
-// many that each lane walks `most` rows. All walk the same number up to one.
-int row_blocks(const NormArgs &a, const Team &t, int waves, int64_t cap, int most) {
+// compute unit, but no more than `cap`; or where rows are many, so many that
+// each lane walks `most` rows. All walk the same number up to one.
+int row_blocks(const NormArgs &a, const Team &t, int waves, int cap, int most) {
   constexpr int kUnits = 256;
   int per = waves * 64 / t.threads;
   if (per < 1) per = 1;
   int64_t n = (int64_t)kUnits * per / t.xblocks * t.subs;
-  if (n > cap) n = cap;
+  if (n > (int64_t)cap * t.subs) n = (int64_t)cap * t.subs;
   if ((a.rows + (int64_t)most - 1) / most > n) n = (a.rows + (int64_t)most - 1) / most;
   if (n > (int64_t)65535 * t.subs) n = (int64_t)65535 * t.subs;
   if (n < 1) n = 1;
@@ -513,16 +530,16 @@ int row_blocks(const NormArgs &a, const Team &t, int waves, int64_t cap, int mos
 // waves a unit, 92 with 4 rows each; groups of 1024 to 4096: 69 us at 16, 71
 // to 72 with 6 rows).
 int forward_blocks(const NormArgs &a, const Team &t) {
-  if (!t.wide) return row_blocks(a, t, 32, INT32_MAX, 3);
-  return row_blocks(a, t, t.r == 1 ? 16 : 8, INT32_MAX, INT32_MAX);
+  if (!t.wide) return row_blocks(a, t, 32, 65535, 3);
+  return row_blocks(a, t, t.r == 1 ? 16 : 8, 65535, INT32_MAX);
 }
 
-// Backward: every walker costs a row of partial sums, and more loads in
+// Backward: every workgroup costs a row of partial sums, and more loads in
 // flight do not help: 8 waves a unit (16384 tokens of groups of 1024 to 4096:
 // 113 to 117 us; 12 waves 119 to 125), from checkpoints, with half the bytes
 // a load, 16 (110 to 111 us; 8 waves 125 to 135). Lanes of several parts hold
-// twice the loads: 8. No walker adds up more
-// than 256 rows in fp32 (up to 16 million tokens).
+// twice the loads: 8. No lane adds up more than 256 rows in fp32 (up to 16
+// million tokens).
 int backward_blocks(const NormArgs &a, const Team &t) {
   return row_blocks(a, t, a.xk.q && t.r == 1 ? 16 : 8, 2048, 256);
 }
@@ -569,7 +586,7 @@ hipError_t launch_back(NormArgs a, hipStream_t s) {
   const Team t = backward_team(a);
   a.team = t.size;
   a.subs = t.subs;
-  const dim3 grid(t.xblocks, a.nparts / t.subs), block(t.threads);
+  const dim3 grid(t.xblocks, a.nparts), block(t.threads);
 #define SSD_NORM(R, WIDE, THREADS) \
   hipLaunchKernelGGL((k_norm_backward<T, MODE, CK, BIAS, R, WIDE, THREADS>), grid, block, 0, s, a)
   if (!t.wide)
@@ -599,7 +616,7 @@ hipError_t launch_back(const NormArgs &a, hipStream_t s) {
 int norm_partial_rows(const NormArgs &a) {
   if (a.rows == 0) return 0;
   const Team t = backward_team(a);
-  return backward_blocks(a, t) * t.subs;
+  return backward_blocks(a, t);
 }
 
 hipError_t launch_norm(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s) {

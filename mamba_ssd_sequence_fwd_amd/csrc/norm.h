@@ -34,7 +34,7 @@ struct NormArgs {
 };
 
 constexpr int kNormMaxGroup = 16384;  // channels of a group the kernels hold on chip
-// Rows of partial sums of the backward pass (one per row walker).
+// Rows of partial sums of the backward pass (one per workgroup along the rows).
 int norm_partial_rows(const NormArgs &a);
 hipError_t launch_norm(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs &a, NormMode mode, bool bf16_io, hipStream_t s);
