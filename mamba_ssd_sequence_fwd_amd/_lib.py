@@ -587,12 +587,13 @@ class Checkpoint:
         """The values, in ``dtype`` (exact; see ssd_checkpoint_load), in a new
         tensor or in ``out`` (rows may be a slice of wider rows)."""
         dev, ch = self.q.device, self.q.shape[-1]
-        _same_device(dev, out=out)
+        if out is not None:
+            _same_device(dev, out=out)
         _on_gpu(dev)
         context, handle = _stream_of(dev, stream)
         with context:
             if out is None:
-                out = torch.empty(self.q.shape, device=dev, dtype=self.dtype)
+                out = self.q.new_empty(self.q.shape, dtype=self.dtype)
             elif out.shape != self.q.shape or out.dtype != self.dtype:
                 raise ValueError("out must be %s %s" % (tuple(self.q.shape), self.dtype))
             stride = _stride_of_out(out, "out")
@@ -673,10 +674,14 @@ def _rows_in(t):
 def _checkpoint_out(given, shape, dtype, dev):
     """The Checkpoint a call fills: a new one for True, or the caller's."""
     if given is True:
-        blocks = -(-shape[-1] // CHECKPOINT_BLOCK)
-        return Checkpoint(torch.empty(shape, device=dev, dtype=torch.int8),
-                          torch.empty(shape[:-1] + (blocks,), device=dev, dtype=torch.uint8),
-                          dtype)
+        if shape[-1] % 8:
+            raise ValueError("channels (%d) must be a multiple of 8" % shape[-1])
+        new = object.__new__(Checkpoint)        # (nothing of it needs checking)
+        new.q = torch.empty(shape, device=dev, dtype=torch.int8)
+        new.exponents = torch.empty(shape[:-1] + (-(-shape[-1] // CHECKPOINT_BLOCK),), device=dev,
+                                    dtype=torch.uint8)
+        new.dtype = dtype
+        return new
     if not isinstance(given, Checkpoint):
         raise ValueError("checkpoint must be True, False or a Checkpoint to fill")
     if tuple(given.shape) != tuple(shape) or given.dtype != dtype or given.device != dev:

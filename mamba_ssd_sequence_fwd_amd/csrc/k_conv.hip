@@ -22,42 +22,12 @@
 // next batch issued before the current one is used. Sequence starts reset the
 // window from the history, and a sequence's last token writes its final
 // history (the last K - 1 inputs, oldest first).
-//
-// The same walk also keeps the input in 8 bits on the way (kSave: the widened
-// row is quantised before the window slides, the row's 64 bytes a wave reads
-// per 32 channels adding 33 to write and none to read), and recomputes the
-// outputs from such a checkpoint (kFrom). When saving, the channel groups of
-// a row are counted up to whole blocks of 4 lanes, which share a scale: lanes
-// past the last channel carry zeros and store nothing.
 #include "conv.h"
 
 namespace ssd {
 
 constexpr int kConvBatch = 8;
 static_assert(kConvTile % kConvBatch == 0, "tile must hold whole batches");
-
-// What the walk does with an 8-bit checkpoint of the input: nothing, write it
-// on the way, or read it in the input's place.
-enum : int { kNoCkpt = 0, kSave = 1, kFrom = 2 };
-
-template <typename T, int CK> struct ConvRowOf { typedef Row8<T> type; };
-template <typename T> struct ConvRowOf<T, kFrom> { typedef RowQ8 type; };
-template <typename T, int CK> using ConvRow = typename ConvRowOf<T, CK>::type;
-
-template <typename T>
-__device__ __forceinline__ void load_in(Row8<T> &r, const ConvArgs &a, int t, int c0) {
-  r.load(a.xbc, (size_t)t * a.in_stride + c0);
-}
-__device__ __forceinline__ void load_in(RowQ8 &r, const ConvArgs &a, int t, int c0) {
-  r.load(a.ck, (size_t)t, a.ch, c0);
-}
-__device__ __forceinline__ void save_in(const ConvArgs &a, int t, int c0, const float (&cur)[8],
-                                        bool live) {
-  float v[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) v[c] = live ? cur[c] : 0.f;
-  store_ckpt(a.ck, (size_t)t, a.ch, c0, v, live);
-}
 
 // The K - 1 history rows of sequence s for this lane's channels (zeros when
 // there is no history).
@@ -101,19 +71,19 @@ __device__ __forceinline__ void conv_token(const float (&w)[8][K], const float (
 // A full tile inside one sequence whose K - 1 predecessors are in the same
 // sequence: no boundary, every load and store unconditional, so the waits
 // for each batch of loads are exact. Leaves the last K - 1 inputs in win.
-template <int K, typename T, int CK>
+template <int K, typename T>
 __device__ __forceinline__ void conv_tile_interior(const ConvArgs &a, int t0, int c0,
                                                    const float (&w)[8][K],
                                                    const float (&bias)[8], void *dst,
-                                                   int dcol, int dstride, bool live,
+                                                   int dcol, int dstride,
                                                    float (&win)[K - 1][8]) {
-  ConvRow<T, CK> head[K - 1], rows[kConvBatch], next[kConvBatch];
+  Row8<T> head[K - 1], rows[kConvBatch], next[kConvBatch];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j)
-    load_in(head[j], a, t0 - (K - 1) + j, c0);
+    head[j].load(a.xbc, (size_t)(t0 - (K - 1) + j) * a.in_stride + c0);
 #pragma unroll
   for (int u = 0; u < kConvBatch; ++u)
-    load_in(rows[u], a, t0 + u, c0);
+    rows[u].load(a.xbc, (size_t)(t0 + u) * a.in_stride + c0);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) head[j].widen(win[j]);
 #pragma unroll
@@ -121,23 +91,21 @@ __device__ __forceinline__ void conv_tile_interior(const ConvArgs &a, int t0, in
     if (tb + kConvBatch < kConvTile) {
 #pragma unroll
       for (int u = 0; u < kConvBatch; ++u)
-        load_in(next[u], a, t0 + tb + kConvBatch + u, c0);
+        next[u].load(a.xbc, (size_t)(t0 + tb + kConvBatch + u) * a.in_stride + c0);
     }
 #pragma unroll
     for (int u = 0; u < kConvBatch; ++u) {
       float cur[8], out[8];
       rows[u].widen(cur);
-      if (CK == kSave) save_in(a, t0 + tb + u, c0, cur, live);
       conv_token<K>(w, bias, win, cur, out);
-      if (CK != kSave || live)
-        Row8<T>::store(dst, (size_t)(t0 + tb + u) * dstride + dcol, out);
+      Row8<T>::store(dst, (size_t)(t0 + tb + u) * dstride + dcol, out);
     }
 #pragma unroll
     for (int u = 0; u < kConvBatch; ++u) rows[u] = next[u];
   }
 }
 
-template <int K, typename T, int CK>
+template <int K, typename T>
 __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
   // Workgroups are dealt to the 8 XCDs in turn; renumber them so that each
   // XCD runs one contiguous range, keeping neighbouring token tiles (which
@@ -148,9 +116,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
   const int64_t gid = (int64_t)lb * kConvThreads + threadIdx.x;
   const int tile = (int)(gid / a.groups);
   if (tile >= a.tiles) return;
-  const int cg = (int)(gid - (int64_t)tile * a.groups) * 8;
-  const bool live = CK != kSave || cg < a.ch;
-  const int c0 = live ? cg : a.ch - 8;
+  const int c0 = (int)(gid - (int64_t)tile * a.groups) * 8;
   const int t0 = tile * kConvTile, t1 = min(t0 + kConvTile, a.T);
 
   // The sequence holding t0: [ss, se).
@@ -192,8 +158,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
   // The window: the K - 1 inputs before t0, oldest first.
   float win[K - 1][8];
   if (t1 - t0 == kConvTile && t0 >= K - 1 && t0 - (K - 1) >= ss && t1 <= se) {
-    conv_tile_interior<K, T, CK>(a, t0, c0, w, bias, dst, dcol, dstride, live, win);
-    if (t1 == se && a.hist_out && live) {
+    conv_tile_interior<K, T>(a, t0, c0, w, bias, dst, dcol, dstride, win);
+    if (t1 == se && a.hist_out) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
         Row8<T>::store(a.hist_out, ((size_t)s * (K - 1) + j) * a.ch + c0, win[j]);
@@ -207,8 +173,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
   for (int j = 0; j < K - 1; ++j) {
     const int tok = t0 - (K - 1) + j;
     if (tok >= ss && tok >= 0) {
-      ConvRow<T, CK> row;
-      load_in(row, a, tok, c0);
+      Row8<T> row;
+      row.load(a.xbc, (size_t)tok * a.in_stride + c0);
       row.widen(win[j]);
     } else {
       const int hj = (K - 1) - (ss - tok);
@@ -221,10 +187,10 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
     }
   }
 
-  ConvRow<T, CK> rows[kConvBatch], next[kConvBatch];
+  Row8<T> rows[kConvBatch], next[kConvBatch];
 #pragma unroll
   for (int u = 0; u < kConvBatch; ++u)
-    if (t0 + u < t1) load_in(rows[u], a, t0 + u, c0);
+    if (t0 + u < t1) rows[u].load(a.xbc, (size_t)(t0 + u) * a.in_stride + c0);
 
 #pragma unroll
   for (int tb = 0; tb < kConvTile; tb += kConvBatch) {
@@ -232,7 +198,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
     if (tb + kConvBatch < kConvTile) {
 #pragma unroll
       for (int u = 0; u < kConvBatch; ++u)
-        if (tn + u < t1) load_in(next[u], a, tn + u, c0);
+        if (tn + u < t1) next[u].load(a.xbc, (size_t)(tn + u) * a.in_stride + c0);
     }
 #pragma unroll
     for (int u = 0; u < kConvBatch; ++u) {
@@ -254,10 +220,9 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_silu(ConvArgs a) {
         }
         float cur[8], out[8];
         rows[u].widen(cur);
-        if (CK == kSave) save_in(a, t, c0, cur, live);
         conv_token<K>(w, bias, win, cur, out);
-        if (CK != kSave || live) Row8<T>::store(dst, (size_t)t * dstride + dcol, out);
-        if (t == se - 1 && a.hist_out && live) {
+        Row8<T>::store(dst, (size_t)t * dstride + dcol, out);
+        if (t == se - 1 && a.hist_out) {
 #pragma unroll
           for (int j = 0; j < K - 1; ++j)
             Row8<T>::store(a.hist_out, ((size_t)s * (K - 1) + j) * a.ch + c0, win[j]);
@@ -287,18 +252,11 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_history_of_empty(ConvArgs
 }
 
 template <int K, typename T>
-static hipError_t launch_width(const ConvArgs &a, int ck, hipStream_t st) {
+static hipError_t launch_width(const ConvArgs &a, hipStream_t st) {
   if (a.T > 0) {
-    ConvArgs g = a;
-    if (ck == kSave) g.groups = (a.groups + kCkptLanes - 1) / kCkptLanes * kCkptLanes;
-    const int64_t threads = (int64_t)g.tiles * g.groups;
-    const dim3 blocks((unsigned)((threads + kConvThreads - 1) / kConvThreads));
-    if (ck == kSave)
-      hipLaunchKernelGGL((k_conv_silu<K, T, kSave>), blocks, dim3(kConvThreads), 0, st, g);
-    else if (ck == kFrom)
-      hipLaunchKernelGGL((k_conv_silu<K, T, kFrom>), blocks, dim3(kConvThreads), 0, st, g);
-    else
-      hipLaunchKernelGGL((k_conv_silu<K, T, kNoCkpt>), blocks, dim3(kConvThreads), 0, st, g);
+    const int64_t threads = (int64_t)a.tiles * a.groups;
+    const unsigned blocks = (unsigned)((threads + kConvThreads - 1) / kConvThreads);
+    hipLaunchKernelGGL((k_conv_silu<K, T>), dim3(blocks), dim3(kConvThreads), 0, st, a);
   }
   // Empty sequences exist only when packed (a zero length) or when the dense
   // rows have no tokens.
@@ -312,11 +270,10 @@ static hipError_t launch_width(const ConvArgs &a, int ck, hipStream_t st) {
 }
 
 hipError_t launch_conv(const ConvArgs &a, int width, bool bf16_io, hipStream_t st) {
-  const int ck = !a.ck.q ? kNoCkpt : a.xbc ? kSave : kFrom;
   switch (width) {
-    case 2: return bf16_io ? launch_width<2, bf16>(a, ck, st) : launch_width<2, float>(a, ck, st);
-    case 3: return bf16_io ? launch_width<3, bf16>(a, ck, st) : launch_width<3, float>(a, ck, st);
-    case 4: return bf16_io ? launch_width<4, bf16>(a, ck, st) : launch_width<4, float>(a, ck, st);
+    case 2: return bf16_io ? launch_width<2, bf16>(a, st) : launch_width<2, float>(a, st);
+    case 3: return bf16_io ? launch_width<3, bf16>(a, st) : launch_width<3, float>(a, st);
+    case 4: return bf16_io ? launch_width<4, bf16>(a, st) : launch_width<4, float>(a, st);
     default: return hipErrorInvalidValue;
   }
 }

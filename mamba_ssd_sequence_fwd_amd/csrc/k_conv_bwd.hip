@@ -8,16 +8,13 @@
 //   dw_k = sum_t g_t e_{t+k},   dbias = sum_t g_t
 // de_j for j < K - 1 is the history's gradient, the rest the inputs'.
 //
-// Each lane owns 8 channels and walks one tile of tokens of one sequence,
+// Each lane owns 4 channels and walks one tile of tokens of one sequence,
 // with the last K - 1 inputs and the last K - 1 values of g in registers: at
 // step t it computes g_t, adds to dw and dbias and emits de_t. A tile runs
 // K - 1 steps past its end (the next tokens' g, or zeros after the last
 // token), and its first K - 1 emissions belong to the tile before it, or to
-// the history at a sequence's start. Tiles never cross a sequence: tile slot
-// j belongs to the last sequence s with first(s) <= j, where first(s) =
-// cu[s] / tile + s leaves every sequence enough slots (at least one) without
-// a table; slots past a sequence's end only write zeros to the partial sums.
-// The sums of a workgroup's tiles are joined in LDS and written as one row of
+// the history at a sequence's start. Tiles never cross a sequence (TileMap);
+// slots without tokens only write zeros to the partial sums. The sums of a workgroup's tiles are joined in LDS and written as one row of
 // partial sums; k_column_sums adds those rows.
 #include <type_traits>
 
@@ -61,36 +58,9 @@ __attribute__((amdgpu_waves_per_eu(4))) void k_conv_backward(ConvBwdArgs a, int 
   const int c0 = live ? cg : a.ch - kLane;
   const int slot = tb * kConvBwdWaves + wave;
 
-  // The tile [t0, t1) of sequence s = [ss, se); len < 0: nothing to do.
-  int s = 0, ss = 0, se = 0, t0 = 0, t1 = 0;
-  bool some = slot < a.tiles;
-  if (some) {
-    int first;
-    if (a.cu) {
-      int lo = 0, hi = a.nseq - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] / a.tile + mid <= slot) lo = mid; else hi = mid - 1;
-      }
-      s = lo;
-      ss = a.cu[s];
-      se = a.cu[s + 1];
-      first = ss / a.tile + s;
-      // offsets that are no partition of the tokens must not lead outside them
-      if (ss < 0 || se < ss || se > a.T || slot < first) some = false;
-    } else {
-      s = slot / a.seq_tiles;
-      ss = s * a.seqlen;
-      se = ss + a.seqlen;
-      first = s * a.seq_tiles;
-    }
-    if (some) {
-      const int64_t lt = (int64_t)(slot - first) * a.tile;
-      some = lt == 0 || lt < se - ss;
-      t0 = ss + (int)(some ? lt : 0);
-      t1 = min(t0 + a.tile, se);
-    }
-  }
+  Tile tile{};
+  const bool some = tile_of(a.map, slot, tile);
+  const int s = tile.s, ss = tile.ss, se = tile.se, t0 = tile.t0, t1 = tile.t1;
 
   float dw[kLane][K], db[kLane];
 #pragma unroll
@@ -263,7 +233,7 @@ __attribute__((amdgpu_waves_per_eu(4))) void k_conv_backward(ConvBwdArgs a, int 
 template <int K, typename T>
 hipError_t launch_width(const ConvBwdArgs &a, hipStream_t s) {
   const int cblocks = conv_bwd_channel_blocks(a);
-  const int tblocks = (a.tiles + kConvBwdWaves - 1) / kConvBwdWaves;
+  const int tblocks = (a.map.slots + kConvBwdWaves - 1) / kConvBwdWaves;
   const dim3 grid((unsigned)(cblocks * tblocks)), block(64 * kConvBwdWaves);
   if (a.ck.q)
     hipLaunchKernelGGL((k_conv_backward<K, T, true>), grid, block, 0, s, a, cblocks);
@@ -286,21 +256,15 @@ constexpr int kFewBlocks = 256;
 int conv_bwd_channel_blocks(const ConvBwdArgs &a) { return (a.ch / kLane + 63) / 64; }
 
 int conv_bwd_geometry(ConvBwdArgs &a) {
-  auto slots = [&](int tile) {
-    return a.cu ? (int64_t)a.T / tile + a.nseq
-                : (int64_t)a.nseq * (a.seqlen > 0 ? (a.seqlen + tile - 1) / tile : 1);
-  };
-  const int64_t blocks = (slots(kTile) + kConvBwdWaves - 1) / kConvBwdWaves;
-  a.tile = blocks * conv_bwd_channel_blocks(a) < kFewBlocks ? kShortTile
-           : a.ck.q                                         ? kCkptTile
-                                                            : kTile;
-  a.tiles = (int32_t)slots(a.tile);
-  a.seq_tiles = a.cu ? 0 : a.seqlen > 0 ? (a.seqlen + a.tile - 1) / a.tile : 1;
-  return (a.tiles + kConvBwdWaves - 1) / kConvBwdWaves;
+  const int64_t blocks = (tile_slots(a.map, kTile) + kConvBwdWaves - 1) / kConvBwdWaves;
+  set_tile(a.map, blocks * conv_bwd_channel_blocks(a) < kFewBlocks ? kShortTile
+                  : a.ck.q                                         ? kCkptTile
+                                                                   : kTile);
+  return (a.map.slots + kConvBwdWaves - 1) / kConvBwdWaves;
 }
 
 hipError_t launch_conv_backward(const ConvBwdArgs &a, int width, bool bf16_io, hipStream_t s) {
-  if (a.tiles == 0) return hipSuccess;
+  if (a.map.slots == 0) return hipSuccess;
   switch (width) {
     case 2: return bf16_io ? launch_width<2, bf16>(a, s) : launch_width<2, float>(a, s);
     case 3: return bf16_io ? launch_width<3, bf16>(a, s) : launch_width<3, float>(a, s);

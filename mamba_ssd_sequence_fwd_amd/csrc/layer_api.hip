@@ -75,12 +75,22 @@ ssd_status check_conv(const ssd_conv_problem *p, const int32_t *cu_seqlens, int6
   *T = (int64_t)p->batch * p->seqlen;
   *nseq = varlen ? p->num_seqs : p->batch;
   const int64_t tiles = (*T + ssd::kConvTile - 1) / ssd::kConvTile;
-  const int64_t groups = (int64_t)ssd::ckpt_blocks((int)ch) * ssd::kCkptLanes;
   if (*T > INT32_MAX - ssd::kConvTile ||
-      (tiles * groups + ssd::kConvThreads - 1) / ssd::kConvThreads > INT32_MAX ||
-      (*nseq * groups + ssd::kConvThreads - 1) / ssd::kConvThreads > INT32_MAX)
+      (tiles * (ch / 8) + ssd::kConvThreads - 1) / ssd::kConvThreads > INT32_MAX ||
+      (*nseq * (ch / 8) + ssd::kConvThreads - 1) / ssd::kConvThreads > INT32_MAX)
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens x %lld channels too large for one launch",
                 (long long)*T, (long long)ch);
+  return SSD_OK;
+}
+
+// Bounds of the kernels that walk tiles of at least 12 tokens, 256 channels
+// and 4 tiles to a workgroup.
+ssd_status check_tiles(const ssd_conv_problem *p, int64_t T, int64_t nseq) {
+  const int64_t ch = (int64_t)p->x_dim + 2 * (int64_t)p->bc_dim;
+  if (T + 2 * nseq > INT32_MAX / 2 ||
+      ((T / 12 + nseq) / 4 + 1) * (ch / 256 + 1) > INT32_MAX)
+    return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences x %lld channels too large for "
+                "one launch", (long long)T, (long long)nseq, (long long)ch);
   return SSD_OK;
 }
 
@@ -91,6 +101,7 @@ ssd_status conv_forward(const ssd_conv_problem *p, const void *xbc, const ssd_ch
   int64_t T = 0, nseq = 0;
   ssd_status st = check_conv(p, cu_seqlens, &T, &nseq);
   if (st != SSD_OK) return st;
+  if (ck && (st = check_tiles(p, T, nseq)) != SSD_OK) return st;
   if (nseq == 0 || (T == 0 && !history_out)) return SSD_OK;
   if (!weight) return fail(SSD_ERR_INVALID_ARG, "weight must be non-NULL");
   if (T > 0 && ((!xbc && !ck) || (p->x_dim > 0 && !x) || (p->bc_dim > 0 && (!B || !C))))
@@ -117,9 +128,10 @@ ssd_status conv_forward(const ssd_conv_problem *p, const void *xbc, const ssd_ch
   a.in_stride = p->in_stride;
   a.groups = a.ch / 8;
   a.tiles = (int32_t)((T + ssd::kConvTile - 1) / ssd::kConvTile);
-  a.ck = ckpt_of(ck);
-  const hipError_t e = ssd::launch_conv(a, p->width, p->dtype == SSD_DTYPE_BF16,
-                                        static_cast<hipStream_t>(stream));
+  const bool bf = p->dtype == SSD_DTYPE_BF16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = ck && T > 0 ? ssd::launch_conv_ckpt(a, ckpt_of(ck), p->width, bf, s)
+                                   : ssd::launch_conv(a, p->width, bf, s);
   if (e != hipSuccess)
     return fail(SSD_ERR_HIP, "convolution kernel launch failed: %s", hipGetErrorString(e));
   return SSD_OK;
@@ -128,21 +140,17 @@ ssd_status conv_forward(const ssd_conv_problem *p, const void *xbc, const ssd_ch
 // Geometry of the front's backward pass: tile blocks, or an error.
 ssd_status conv_backward_geometry(const ssd_conv_problem *p, const int32_t *cu, int64_t T,
                                   int64_t nseq, ssd::ConvBwdArgs *a, int64_t *tblocks) {
-  a->cu = p->num_seqs > 0 ? cu : nullptr;
-  a->T = (int32_t)T;
-  a->seqlen = p->seqlen;
-  a->nseq = (int32_t)nseq;
+  ssd_status st;
+  a->map.cu = p->num_seqs > 0 ? cu : nullptr;
+  a->map.T = (int32_t)T;
+  a->map.seqlen = p->seqlen;
+  a->map.nseq = (int32_t)nseq;
   a->ch = p->x_dim + 2 * p->bc_dim;
   a->x_dim = p->x_dim;
   a->bc_dim = p->bc_dim;
   a->in_stride = p->in_stride;
-  if (T + 2 * nseq > INT32_MAX / 2)
-    return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences exceed the int32 tile index",
-                (long long)T, (long long)nseq);
+  if ((st = check_tiles(p, T, nseq)) != SSD_OK) return st;
   *tblocks = ssd::conv_bwd_geometry(*a);
-  if (*tblocks * ssd::conv_bwd_channel_blocks(*a) > INT32_MAX)
-    return fail(SSD_ERR_UNSUPPORTED, "%lld tokens x %d channels too large for one launch",
-                (long long)T, a->ch);
   return SSD_OK;
 }
 
