@@ -157,7 +157,6 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormArgs a) {
       if (kGated) zr[r].widen(z[r]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (!at.live[r]) x[r][k] = z[r][k] = 0.f;
         u[r][k] = MODE == kGateFirst ? x[r][k] * silu(z[r][k]) : x[r][k];
       }
     }
@@ -172,21 +171,27 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormArgs a) {
     if (a.center) {
       float m[1] = {0.f};
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        float part = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m[0] += u[r][k];
+        for (int k = 0; k < 8; ++k) part += u[r][k];
+        m[0] += at.live[r] ? part : 0.f;
+      }
       team_sums<WIDE>(m, a.team, lds, turn);
       const float mu = m[0] * a.inv_n;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[r][k] = at.live[r] ? u[r][k] - mu : 0.f;
+        for (int k = 0; k < 8; ++k) u[r][k] -= mu;
     }
     float q[1] = {0.f};
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      float part = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[0] += u[r][k] * u[r][k];
+      for (int k = 0; k < 8; ++k) part += u[r][k] * u[r][k];
+      q[0] += at.live[r] ? part : 0.f;
+    }
     team_sums<WIDE>(q, a.team, lds, turn);
     const float rs = 1.f / sqrtf(q[0] * a.inv_n + a.eps);
 #pragma unroll
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
         for (int k = 0; k < 8; ++k) {
           const float s = sigmoid(z[k]);
           sz[r][k] = z[k] * s;
-          dsz[r][k] = s * ((1.f + z[k]) - sz[r][k]);
+          dsz[r][k] = s + sz[r][k] * (1.f - s);
         }
       }
     }
@@ -322,11 +327,14 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
         widen_u(r, x, u);
         widen_g(r, d, dv);
         weights(r, w, b);
+        float p0 = 0.f, p1 = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          m[0] += at.live[r] ? u[k] : 0.f;
-          m[1] += at.live[r] ? dv[k] * w[k] : 0.f;
+          p0 += u[k];
+          p1 += dv[k] * w[k];
         }
+        m[0] += at.live[r] ? p0 : 0.f;
+        m[1] += at.live[r] ? p1 : 0.f;
         forget(xr[r]);
         forget(dr[r]);
       }
@@ -343,12 +351,15 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
       widen_u(r, x, u);
       widen_g(r, d, dv);
       if (kGated) weights(r, w, b);
+      float p0 = 0.f, p1 = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float c = at.live[r] ? u[k] - mu : 0.f;
-        q[0] += c * c;
-        if (kGated) q[1] += at.live[r] ? dv[k] * w[k] * c : 0.f;
+        const float c = u[k] - mu;
+        p0 += c * c;
+        if (kGated) p1 += dv[k] * w[k] * c;
       }
+      q[0] += at.live[r] ? p0 : 0.f;
+      q[1] += at.live[r] ? p1 : 0.f;
       forget(xr[r]);
       forget(dr[r]);
     }
@@ -363,22 +374,27 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
         xr[r].widen(x);
         dr[r].widen(d);
         weights(r, w, b);
+        float p0 = 0.f, p1 = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float h = at.live[r] ? (x[k] - mu) * rs : 0.f;
+          const float h = (x[k] - mu) * rs;
           const float v = h * w[k] + b[k];
           const float s = sigmoid(v);
-          const float dv = at.live[r] ? d[k] * (s * (1.f + (v - v * s))) : 0.f;
+          const float ds = d[k] * s, dv = ds + ds * (v - v * s);
           sz[r][k] = dv;   // (no gate: the registers hold dv)
-          m[0] += at.live[r] ? dv * w[k] * h : 0.f;
-          m[1] += at.live[r] ? dv * w[k] : 0.f;
+          p0 += dv * w[k] * h;
+          p1 += dv * w[k];
         }
+        m[0] += at.live[r] ? p0 : 0.f;
+        m[1] += at.live[r] ? p1 : 0.f;
         forget(xr[r]);
       }
       team_sums<WIDE>(m, a.team, lds, turn);
       mgh = m[0] * a.inv_n;
       mg = a.center ? m[1] * a.inv_n : 0.f;
     }
+    // du = r (g - mean(g) - h mean(g h)) with r taken into each term, h = c r
+    const float mgr = rs * mg, mghr = rs * rs * mgh;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float x[8], u[8], d[8], dv[8], dx[8], dz[8], w[8], b[8];
@@ -387,14 +403,15 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
       weights(r, w, b);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float h = (u[k] - mu) * rs;
+        const float c = u[k] - mu;
         const float e = MODE == kNoGate ? sz[r][k] : dv[k];
-        dw[r][k] += e * h;
+        const float er = e * rs;
+        dw[r][k] += er * c;
         if (BIAS) db[r][BIAS ? k : 0] += e;
-        const float du = rs * (e * w[k] - mg - h * mgh);
+        const float du = (er * w[k] - mgr) - c * mghr;
         dx[k] = MODE == kGateFirst ? du * sz[r][k] : du;
         if (MODE == kGateFirst) dz[k] = du * x[k] * dsz[r][k];
-        if (MODE == kGateLast) dz[k] = d[k] * (h * w[k] + b[k]) * dsz[r][k];
+        if (MODE == kGateLast) dz[k] = d[k] * (c * rs * w[k] + b[k]) * dsz[r][k];
       }
       if (at.live[r]) {
         Row8<T>::store(a.dx, (size_t)row * a.dx_stride + at.c[r], dx);
