@@ -583,7 +583,8 @@ ssd_status ssd_conv1d_silu_backward(const ssd_conv_problem *prob, const void *xb
  *                z, written on the way; both, or (without z) that of x, or
  *                neither (NULL)
  *   stream       a hipStream_t (NULL = the default stream)
- * Arithmetic and sums are fp32 (squares overflow above about 1e18); bf16
+ * Arithmetic and sums are fp32 (squares overflow above about 1e18, and with
+ * eps 0 a group of zeros divides by zero); bf16
  * outputs are rounded once, to nearest even. Outputs must not overlap inputs
  * or each other. Errors: SSD_ERR_INVALID_ARG (malformed sizes, NULL or
  * misaligned pointers), SSD_ERR_UNSUPPORTED (outside the set above),

@@ -624,6 +624,18 @@ def _stream_of(dev, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
+# The C structures hold sizes in 32 bits, into which ctypes would wrap larger
+# ones; the library itself takes fewer tokens than this.
+_MOST_TOKENS = 1 << 30
+
+
+def _dense(t):
+    """``t``, or a copy where it is not contiguous or not 16-byte aligned."""
+    if t is None or (t.is_contiguous() and not t.data_ptr() & 15):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -956,6 +968,9 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
     else:
         (batch, L), num_seqs = lead, 0
         nseq = batch
+    if batch * L >= _MOST_TOKENS or nseq >= _MOST_TOKENS:
+        raise ValueError("%d tokens in %d sequences are more than one call takes"
+                         % (batch * L, nseq))
     dims = []
     for name, t in (("dx", dx), ("dB", dB), ("dC", dC)):
         if tuple(t.shape[:len(lead)]) != lead or t.dtype != dtype or t.dim() <= len(lead):
@@ -989,10 +1004,12 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
         in_stride = ch
         if kept is None:
             u, in_stride = _rows_in(u)
-        dx, dB, dC = (t.contiguous() for t in (dx, dB, dC))
+        if max(in_stride, out_stride) >= 1 << 31:
+            raise ValueError("the rows of xbc or dxbc are too far apart")
+        dx, dB, dC, history, dhistory_out = (_dense(t) for t in (dx, dB, dC, history,
+                                                                 dhistory_out))
         weight = weight.contiguous()
-        bias, history, dhistory_out = (t.contiguous() if t is not None else None
-                                       for t in (bias, history, dhistory_out))
+        bias = bias.contiguous() if bias is not None else None
         dweight, dbias = weight.new_empty((ch, K)), weight.new_empty(ch)
         dhistory = dx.new_empty(hshape) if history is not None else None
         sizes = (batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
@@ -1033,8 +1050,14 @@ def _norm_sizes(x, groups, eps, center, norm_before_gate):
     channels = shape[-1] if len(shape) else 0
     if channels < 1 or x.dtype not in _DTYPES:
         raise ValueError("x must be bfloat16 or float32 with a channel axis")
+    tokens = shape.numel() // channels
+    if tokens >= _MOST_TOKENS:
+        raise ValueError("%d tokens are more than one call takes" % tokens)
+    if not 0 < groups <= channels:
+        raise ValueError("groups (%d) must be between 1 and the channel count %d"
+                         % (groups, channels))
     flags = (SSD_NORM_CENTER if center else 0) | (SSD_NORM_BEFORE_GATE if norm_before_gate else 0)
-    return shape.numel() // channels, channels, groups, _DTYPES[x.dtype], flags, eps
+    return tokens, channels, groups, _DTYPES[x.dtype], flags, eps
 
 
 def _norm_tensors(x, channels, like, weight, bias):

@@ -132,10 +132,17 @@ def test_conv_backward_into_a_slice():
         inp["xbc"].cuda().view(2, 300, ch), inp["weight"].cuda(), inp["bias"].cuda(),
         dx.view(2, 300, 2, 64), dB.view(2, 300, 1, 32), dC.view(2, 300, 2, 16),
         inp["history"].cuda(), dhistory_out=dh.cuda())
+    # gradients and histories that must be copied first: strided, or 2 bytes off
+    off = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+    odd = ssd.conv1d_silu_backward(
+        off(inp["xbc"].cuda().view(2, 300, ch)), inp["weight"].cuda(), inp["bias"].cuda(),
+        off(dx.view(2, 300, 128)), dB.view(2, 300, 32).transpose(0, 1).contiguous().transpose(0, 1),
+        off(dC.view(2, 300, 32)), off(inp["history"].cuda()), dhistory_out=off(dh.cuda()))
     torch.cuda.synchronize()
     for k in want:
         assert torch.equal(got[k], want[k]), k
         assert torch.equal(heads[k], want[k]), k
+        assert torch.equal(odd[k], want[k]), k
     assert (wide[:, :, :32] == 3).all() and (wide[:, :, 32 + ch:] == 3).all()
 
 

@@ -320,3 +320,17 @@ def test_conv_refuses_a_checkpoint_of_a_checkpoint():
         ssd.conv1d_silu(k, w, None, 64, 16, checkpoint=True)
     with pytest.raises(ValueError, match="history_out"):
         ssd.conv1d_silu(k, w, None, 64, 16, history_out=torch.zeros(2, 3, 96))
+
+
+def test_binding_refuses_sizes_that_would_wrap():
+    """Sizes past 32 bits are refused before they are put into a C structure."""
+    far = _meta(2 ** 32 + 5, 8)
+    with pytest.raises(ValueError, match="tokens"):
+        ssd.group_norm_silu(far)
+    with pytest.raises(ValueError, match="tokens"):
+        ssd.group_norm_silu_backward(far, far)
+    with pytest.raises(ValueError, match="groups"):
+        ssd.group_norm_silu(_meta(4, 64), groups=2 ** 32 + 1)
+    for groups in (0, -1, 65):
+        with pytest.raises(ValueError, match="groups"):
+            ssd.group_norm_silu(_meta(4, 64), groups=groups)
