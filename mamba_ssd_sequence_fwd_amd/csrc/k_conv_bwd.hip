@@ -14,8 +14,20 @@
 // K - 1 steps past its end (the next tokens' g, or zeros after the last
 // token), and its first K - 1 emissions belong to the tile before it, or to
 // the history at a sequence's start. Tiles never cross a sequence (TileMap);
-// slots without tokens only write zeros to the partial sums. The sums of a workgroup's tiles are joined in LDS and written as one row of
-// partial sums; k_column_sums adds those rows.
+// slots without tokens only write zeros to the partial sums. The sums of a
+// workgroup's tiles are joined in LDS and written as one row of partial sums;
+// k_column_sums adds those rows.
+//
+// The taps, their sums, the bias's and the two windows are 16 K - 4 registers a
+// lane for 4 channels, which leaves 4 waves a SIMD (8 channels: 2). Steps
+// inside a tile run without a branch, kBatch rows in flight, each loaded into
+// the registers that the row kBatch before it leaves. Some 26 vector
+// instructions an element, two of them at a quarter of the rate, are 80 us at
+// 8 x 2048 tokens of 5376 channels, against 85 us of memory from a checkpoint
+// at a copy's 5.2 TB/s: both bound it. Measured, K = 4, bf16, caches cold:
+// that size from 8 bits 99 to 103 us for 443 MB; 124,399 packed tokens of 5376
+// channels 749 to 778 us for 4.01 GB (5.2 to 5.4 TB/s, and the counters show a
+// fifth more read, the rows that neighbouring tiles share).
 #include <type_traits>
 
 #include "conv.h"
@@ -26,19 +38,15 @@ namespace {
 
 constexpr int kLane = 4;  // channels per lane
 
-template <typename T, int C> struct RowsOf { typedef Row8<T> Plain; typedef RowQ8 Kept; };
-template <typename T> struct RowsOf<T, 4> { typedef Row4<T> Plain; typedef RowQ4 Kept; };
-template <typename T> using Row = typename RowsOf<T, kLane>::Plain;
-template <typename T, bool CK>
-using BwdRow = std::conditional_t<CK, typename RowsOf<T, kLane>::Kept, Row<T>>;
+template <typename T> using Row = Row4<T>;
+template <typename T, bool CK> using BwdRow = std::conditional_t<CK, RowQ4, Row<T>>;
 
 template <typename T>
 __device__ __forceinline__ void load_u(Row<T> &r, const ConvBwdArgs &a, int t, int c0) {
   r.load(a.xbc, (size_t)t * a.in_stride + c0);
 }
 template <typename T>
-__device__ __forceinline__ void load_u(typename RowsOf<T, kLane>::Kept &r, const ConvBwdArgs &a,
-                                       int t, int c0) {
+__device__ __forceinline__ void load_u(RowQ4 &r, const ConvBwdArgs &a, int t, int c0) {
   r.load(a.ck, (size_t)t, a.ch, c0);
 }
 
@@ -245,11 +253,14 @@ hipError_t launch_width(const ConvBwdArgs &a, hipStream_t s) {
 // Tokens per tile. Shorter tiles spread the work more evenly, longer ones
 // repeat fewer steps at their ends: from a checkpoint the kernel is bound by
 // its arithmetic (2 x 16384 tokens, 8192 channels: 288 us with 60 tokens, 298
-// with 36), from 16 bits by memory (131,604 packed tokens, 5376 channels: 786
+// with 36), from 16 bits by memory (124,399 packed tokens, 5376 channels: 786
 // us with 36, 809 with 60). Few tokens take the shortest, so that there are
-// workgroups for every compute unit.
+// workgroups for every compute unit (5376 channels, bf16 and 8 bits, caches
+// warm: 1024 tokens 15 us with 12, 18 and 24 us with the longer; 2048 tokens, 315
+// workgroups of 36, 21 and 22 against 24 and 26; 4096 tokens, 609, 37 and 35
+// against 32 and 36; 8192 tokens 64 and 60 against 54 and 49).
 constexpr int kTile = 36, kCkptTile = 60, kShortTile = 12;
-constexpr int kFewBlocks = 256;
+constexpr int kFewBlocks = 480;
 
 }  // namespace
 

@@ -18,6 +18,14 @@
 // workgroup writes one row of partial sums. The next row's loads are issued
 // before the current row's sums. All sums are fp32; the partial rows are added
 // in fp64. Squares are summed as they are: |u| above about 1e18 overflows.
+//
+// Both directions are bound by HBM. Measured, caches cold, bf16, gate first:
+// 16384 tokens of one group of 5120 channels forward 86 us for 503 MB (5.8
+// TB/s), backward 147 to 155 us for 839 MB (5.4 to 5.7 TB/s); 32768 tokens of 8
+// groups of 512 forward 131 us for 805 MB (6.1 TB/s), with both inputs kept in
+// 8 bits 190 us for 1082 MB (5.7 TB/s), backward from them 205 to 222 us for
+// 1082 MB (4.9 to 5.3 TB/s; 41 vector instructions an element are 140 us of
+// it). One token of 5120 channels takes 4.8 us.
 #include "norm.h"
 
 namespace ssd {
@@ -517,7 +525,9 @@ Team team_of(const NormArgs &a, int r_wide, int threads_wide) {
 
 // Forward: 4 waves of 3 or 4 parts. Backward: 8 waves of 2 parts; from 8-bit
 // checkpoints, whose loads are shorter, 4 waves of 3 up to 768 lanes (140 us
-// at the shape above against 168 us with 8 waves of 2).
+// at the shape above against 168 us with 8 waves of 2; 8192 tokens of 5632
+// channels 80 against 84; past 768 lanes 4 waves of 4 lose, 115 us against 111
+// at 8192 x 8192).
 Team forward_team(const NormArgs &a) { return team_of(a, 3, 256); }
 Team backward_team(const NormArgs &a) {
   const int lanes = a.gs / 8;
