@@ -792,6 +792,9 @@ def conv1d_silu(xbc, weight, bias, x_dim, bc_dim, history=None, cu_seqlens=None,
             in_stride = xbc.stride(1)
         else:
             in_stride = xbc.stride(0) if batch > 1 else ch
+    if batch * L >= 1 << 31 or nseq >= 1 << 31 or in_stride >= 1 << 31:
+        raise ValueError("%d tokens in %d sequences, %d elements apart, are more than one call "
+                         "takes" % (batch * L, nseq, in_stride))
     K = int(weight.shape[1]) if weight.dim() == 2 else 0
     if tuple(weight.shape) != (ch, K) or weight.dtype != torch.float32:
         raise ValueError("weight must be (%d, K) float32" % ch)
@@ -941,8 +944,8 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
     (xbc may be a :class:`Checkpoint` of it). dx, dB and dC are the gradients
     of its outputs, as :func:`backward` returns them or with their channels
     flattened; dhistory_out that of history_out, or None. dxbc (optional
-    output, shaped like xbc) may be a slice of wider rows. dbias without a
-    bias is the gradient at zero.
+    output, shaped like xbc) may be a slice of wider rows and must not overlap
+    the inputs. dbias without a bias is the gradient at zero.
     """
     kept = xbc if isinstance(xbc, Checkpoint) else None
     dtype = xbc.dtype
@@ -1079,6 +1082,16 @@ def _norm_tensors(x, channels, like, weight, bias):
     _on_gpu(dev)
 
 
+def _pair(checkpoint):
+    """The caller's pair of Checkpoints to fill, of x and of z (or None)."""
+    if not isinstance(checkpoint, (tuple, list)) or len(checkpoint) != 2:
+        raise ValueError("checkpoint must be True, False or a pair of Checkpoints to fill")
+    x, z = checkpoint
+    if x is not True and x is z:
+        raise ValueError("x and z need a Checkpoint each")
+    return x, z
+
+
 def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, center=False,
                     norm_before_gate=False, checkpoint=False, out=None, stream=None):
     """Group norm with SiLU, channels last (ssd_group_norm_silu): the gate
@@ -1092,7 +1105,8 @@ def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, ce
     (norm(x) * weight + bias) * silu(z); without z silu(norm(x) * weight + bias).
     x, z and out may be slices of wider rows. With ``checkpoint=True`` x and z
     are also kept in 8 bits on the way: returns (out, x's Checkpoint, z's or
-    None); a pair of Checkpoints is filled instead.
+    None); a pair of Checkpoints is filled instead. Outputs must not overlap
+    inputs.
     """
     sizes = _norm_sizes(x, groups, eps, center, norm_before_gate)
     dev, dtype, shape = x.device, x.dtype, x.shape
@@ -1107,7 +1121,7 @@ def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, ce
         out_stride = _stride_of_out(out, "out")
         kx = kz = None
         if checkpoint is not False:
-            gx, gz = (True, True) if checkpoint is True else checkpoint
+            gx, gz = (True, True) if checkpoint is True else _pair(checkpoint)
             kx = _checkpoint_out(gx, tuple(shape), dtype, dev)
             kz = _checkpoint_out(gz, tuple(shape), dtype, dev) if z is not None else None
         x, x_stride = _rows_in(x)
@@ -1130,7 +1144,8 @@ def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=
 
     The forward inputs and options as given there; x and z may both be
     :class:`Checkpoint` of the inputs. dout, and the optional outputs dx and
-    dz, are shaped like x and may be slices of wider rows.
+    dz, are shaped like x and may be slices of wider rows. Outputs must not
+    overlap inputs.
     """
     kept = isinstance(x, Checkpoint)
     if z is not None and isinstance(z, Checkpoint) != kept:

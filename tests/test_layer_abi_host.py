@@ -334,3 +334,30 @@ def test_binding_refuses_sizes_that_would_wrap():
     for groups in (0, -1, 65):
         with pytest.raises(ValueError, match="groups"):
             ssd.group_norm_silu(_meta(4, 64), groups=groups)
+
+
+def test_front_refuses_sizes_past_32_bits(monkeypatch):
+    # sizes that the C structure's 32 bits would wrap to small valid ones
+    monkeypatch.setattr(_lib, "_on_gpu", lambda dev: None)
+    w, many = _meta(8, 4, dtype=torch.float32), (1 << 32) + 8
+    kept = ssd.Checkpoint(_meta(1, many, 8, dtype=torch.int8),
+                          _meta(1, many, 1, dtype=torch.uint8), torch.bfloat16)
+    for xbc in (_meta(1, many, 8), _meta(1 << 20, 1 << 12, 8), kept):
+        with pytest.raises(ValueError, match="more than one call takes"):
+            ssd.conv1d_silu(xbc, w, None, 8, 0)
+    far = torch.empty_strided((1, 2, 8), (1 << 33, 1 << 32, 1), dtype=torch.bfloat16,
+                              device="meta")
+    with pytest.raises(ValueError, match="more than one call takes"):
+        ssd.conv1d_silu(far, w, None, 8, 0)
+
+
+def test_norm_refuses_what_is_not_a_pair_to_fill(monkeypatch):
+    monkeypatch.setattr(_lib, "_on_gpu", lambda dev: None)
+    monkeypatch.setattr(_lib, "_stream_of", lambda dev, stream: (_lib._NO_CONTEXT, None))
+    x, z = _meta(5, 64), _meta(5, 64)
+    one = ssd.Checkpoint(_meta(5, 64, dtype=torch.int8), _meta(5, 2, dtype=torch.uint8), x.dtype)
+    for given in (one, (one,), (one, one), (one, one, one)):
+        with pytest.raises(ValueError, match="pair|each"):
+            ssd.group_norm_silu(x, z=z, checkpoint=given)
+    with pytest.raises(ValueError, match="True, False or a Checkpoint"):
+        ssd.group_norm_silu(x, z=z, checkpoint=(one, None))
