@@ -26,8 +26,10 @@
 // 8 x 2048 tokens of 5376 channels, against 85 us of memory from a checkpoint
 // at a copy's 5.2 TB/s: both bound it. Measured, K = 4, bf16, caches cold:
 // that size from 8 bits 99 to 103 us for 443 MB; 124,399 packed tokens of 5376
-// channels 749 to 778 us for 4.01 GB (5.2 to 5.4 TB/s, and the counters show a
-// fifth more read, the rows that neighbouring tiles share).
+// channels 749 to 778 us for 4.01 GB (5.2 to 5.4 TB/s, a copy's rate).
+// Three of four tiles taking the g of their last K - 1 steps from the next wave
+// through LDS read 5% less and took as long; 8 waves a workgroup halve the
+// partial sums and took 2% off that size, 15% onto 8192 tokens from 8 bits.
 #include <type_traits>
 
 #include "conv.h"
@@ -98,9 +100,10 @@ __attribute__((amdgpu_waves_per_eu(4))) void k_conv_backward(ConvBwdArgs a, int 
     BwdRow<T, CK> u[kBatch];
     Row<T> d[kBatch];
     // row t of the inputs and of the gradients, into the registers that the
-    // row kBatch before it left
+    // row kBatch before it left (past the walk's last row that one again)
+    const int end = t1 + P, last = min(end, se) - 1;
     auto fetch = [&](int j, int t) __attribute__((always_inline)) {
-      t = min(t, se - 1);
+      t = min(t, last);
       load_u<T>(u[j], a, t, c0);
       d[j].load(dsrc + (size_t)t * dstride, 0);
     };
@@ -183,7 +186,6 @@ __attribute__((amdgpu_waves_per_eu(4))) void k_conv_backward(ConvBwdArgs a, int 
         }
       }
     };
-    const int end = t1 + P;
     auto checked = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)

@@ -187,6 +187,42 @@ def test_conv_backward_full_workload_sampled():
         check(k, pick(k), want[k], size[k], "bf16" if k == "dxbc" else "fp32", 160)
 
 
+@pytest.mark.parametrize("K,dtype,lens,keep", [
+    (4, torch.bfloat16, None, False), (4, torch.bfloat16, [1201, 0, 3, 36, 1260], True),
+    (3, torch.float32, [1, 2499], False), (2, torch.float32, None, True)])
+def test_conv_backward_many_channels_sampled(K, dtype, lens, keep):
+    """65,536 channels; sampled channels against the oracle (channels are
+    independent)."""
+    x_dim, bc_dim, T = 65024, 256, 2500
+    ch, dev = x_dim + 2 * bc_dim, "cuda"
+    name = "bf16" if dtype == torch.bfloat16 else "fp32"
+    g = torch.Generator(device=dev).manual_seed(4800 + K)
+    rand = lambda *shape, dt=dtype: torch.randn(shape, device=dev, generator=g,
+                                                dtype=torch.float32).to(dt)
+    nseq = 2 if lens is None else len(lens)
+    u, w, b = rand(T, ch), rand(ch, K, dt=torch.float32), rand(ch, dt=torch.float32)
+    grads = [rand(T, n) for n in (x_dim, bc_dim, bc_dim)]
+    hist, dh = rand(nseq, K - 1, ch), rand(nseq, K - 1, ch)
+    cu = None if lens is None else torch.tensor(np.cumsum([0] + lens), dtype=torch.int32)
+    lead = (lambda t: t.view(2, T // 2, -1)) if lens is None else (lambda t: t)
+    xbc = ssd.checkpoint_save(lead(u)) if keep else lead(u)
+    print("[gpu] conv backward many channels", K, dtype, lens, keep, flush=True)
+    got = ssd.conv1d_silu_backward(xbc, w, b, *(lead(t) for t in grads), hist, cu,
+                                   dhistory_out=dh)
+    torch.cuda.synchronize()
+    sel = torch.as_tensor([0, 5, 255, 256, 32767, 65023, 65024, 65279, 65280, 65535], device=dev)
+    seen = xbc.load().reshape(T, ch) if keep else u
+    cpu = lambda t: t.cpu()
+    bounds = dense_bounds(2, T // 2) if lens is None else varlen_bounds(cu.tolist())
+    want, size = conv_backward(cpu(seen[:, sel]), cpu(w[sel]), cpu(b[sel]), bounds,
+                               cpu(torch.cat(grads, 1)[:, sel]), cpu(hist[:, :, sel]),
+                               cpu(dh[:, :, sel]))
+    pick = dict(dxbc=got["dxbc"].reshape(T, ch)[:, sel], dweight=got["dweight"][sel],
+                dbias=got["dbias"][sel], dhistory=got["dhistory"][:, :, sel])
+    for k, v in pick.items():
+        check(k, v, want[k], size[k], name if k in ("dxbc", "dhistory") else "fp32", 160)
+
+
 def test_conv_backward_offsets_that_are_no_partition():
     """Device offsets that are not checked (descending, negative, past the end)
     stay inside the tensors: nothing but the outputs changes."""
