@@ -192,44 +192,53 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kXor2, 0xf, 0xf, true));
 }
 
-// Quantise a lane's eight channels; the lanes of a quad hold one block (lanes
-// past the last channel hold zeros). Rounding to nearest even comes from one
-// fused multiply-add onto 1.5 * 2^23, whose low byte is then the int8: the
-// product by a power of two is exact.
-__device__ __forceinline__ void quantise8(const float (&v)[8], uint2 &q, uint32_t &e) {
+// Quantise a lane's N = 8 or 4 channels; the lanes of a quad or of two
+// neighbouring quads hold one block (lanes past the last channel hold zeros).
+// Rounding to nearest even comes from one fused multiply-add onto 1.5 * 2^23,
+// whose low byte is then the int8: the product by a power of two is exact.
+template <int N>
+__device__ __forceinline__ void quantise(const float (&v)[N], uint32_t (&q)[N / 4], uint32_t &e) {
   uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+  for (int k = 0; k < N; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
   m = quad_max(m);
+  if (N == 4) {
+    constexpr int kHalfMirror = 0x141;  // the other quad of eight lanes
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kHalfMirror, 0xf, 0xf, true));
+  }
   // the exponent field of the step: 127 steps hold the block unless its
   // largest mantissa is at least 127.5 / 64, which rounds up to 128
   const bool bad = m >= 0x7f800000u;
   const int b = max((int)((m + 0x10000u) >> 23) - 6, 2);
   const float inv = __uint_as_float((uint32_t)(254 - min(b, 249)) << 23);
-  uint32_t w[8];
+  uint32_t w[N];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__builtin_fmaf(v[k], inv, 12582912.f));
+  for (int k = 0; k < N; ++k) w[k] = __float_as_uint(__builtin_fmaf(v[k], inv, 12582912.f));
   // low bytes of four words into one
-  auto pack = [](uint32_t a, uint32_t c, uint32_t d, uint32_t f) {
-    const uint32_t lo = __builtin_amdgcn_perm(c, a, 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(f, d, 0x04000c0cu);
-    return lo | hi;
-  };
-  q.x = bad ? 0u : pack(w[0], w[1], w[2], w[3]);
-  q.y = bad ? 0u : pack(w[4], w[5], w[6], w[7]);
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k) {
+    const uint32_t lo = __builtin_amdgcn_perm(w[4 * k + 1], w[4 * k], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(w[4 * k + 3], w[4 * k + 2], 0x04000c0cu);
+    q[k] = bad ? 0u : lo | hi;
+  }
   e = bad ? 255u : (uint32_t)b;
 }
 
 // Store a lane's part of a checkpoint row (the first lane of each block
 // stores its byte); `live` is false on lanes past the last channel.
+template <int N>
 __device__ __forceinline__ void store_ckpt(const Ckpt &k, size_t row, int channels, int c0,
-                                           const float (&v)[8], bool live) {
-  uint2 q;
-  uint32_t e;
-  quantise8(v, q, e);
+                                           const float (&v)[N], bool live) {
+  uint32_t q[N / 4], e;
+  quantise<N>(v, q, e);
   if (live) {
-    const u32x2_t s = {q.x, q.y};
-    __builtin_nontemporal_store(s, reinterpret_cast<u32x2_t *>(k.q + row * channels + c0));
+    int8_t *to = k.q + row * channels + c0;
+    if constexpr (N == 8) {
+      const u32x2_t s = {q[0], q[1]};
+      __builtin_nontemporal_store(s, reinterpret_cast<u32x2_t *>(to));
+    } else {
+      __builtin_nontemporal_store(q[0], reinterpret_cast<uint32_t *>(to));
+    }
     if (c0 % kCkptBlock == 0)
       k.e[row * ckpt_blocks(channels) + c0 / kCkptBlock] = (uint8_t)e;
   }
