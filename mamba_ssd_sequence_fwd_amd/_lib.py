@@ -974,52 +974,46 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
     if batch * L >= _MOST_TOKENS or nseq >= _MOST_TOKENS:
         raise ValueError("%d tokens in %d sequences are more than one call takes"
                          % (batch * L, nseq))
-    dims = []
-    for name, t in (("dx", dx), ("dB", dB), ("dC", dC)):
-        if tuple(t.shape[:len(lead)]) != lead or t.dtype != dtype or t.dim() <= len(lead):
-            raise ValueError("%s must be %s + channels, %s" % (name, lead, dtype))
-        n = 1
-        for size in t.shape[len(lead):]:
-            n *= size
-        dims.append(n)
-    x_dim, bc_dim = dims[0], dims[1]
-    if dims[2] != bc_dim or x_dim + 2 * bc_dim != ch:
+    x_dim, bc_dim, also = (_channels_after(lead, name, t, dtype)
+                           for name, t in (("dx", dx), ("dB", dB), ("dC", dC)))
+    if also != bc_dim or x_dim + 2 * bc_dim != ch:
         raise ValueError("dx, dB, dC have %d, %d, %d channels, but xbc has %d"
-                         % (dims[0], dims[1], dims[2], ch))
-    K = int(weight.shape[1]) if weight.dim() == 2 else 0
-    if tuple(weight.shape) != (ch, K) or weight.dtype != torch.float32:
+                         % (x_dim, bc_dim, also, ch))
+    K = weight.shape[1] if weight.dim() == 2 else 0
+    if weight.shape != (ch, K) or weight.dtype != torch.float32:
         raise ValueError("weight must be (%d, K) float32" % ch)
-    if bias is not None and (tuple(bias.shape) != (ch,) or bias.dtype != torch.float32):
+    if bias is not None and (bias.shape != (ch,) or bias.dtype != torch.float32):
         raise ValueError("bias must be (%d,) float32" % ch)
     hshape = (nseq, K - 1, ch)
     for name, t in (("history", history), ("dhistory_out", dhistory_out)):
-        if t is not None and (tuple(t.shape) != hshape or t.dtype != dtype):
+        if t is not None and (t.shape != hshape or t.dtype != dtype):
             raise ValueError("%s must be %s %s" % (name, hshape, dtype))
-    if dxbc is not None and (tuple(dxbc.shape) != lead + (ch,) or dxbc.dtype != dtype):
+    if dxbc is not None and (dxbc.shape != u.shape or dxbc.dtype != dtype):
         raise ValueError("dxbc must be %s %s" % (lead + (ch,), dtype))
     context, handle = _stream_of(dev, stream)
     # copies, outputs and the workspace are made on the stream the kernels run on
     with context:
         cu_dev = cu_seqlens.to(device=dev, dtype=torch.int32).contiguous() if packed else None
         if dxbc is None:
-            dxbc = dx.new_empty(lead + (ch,))
-        out_stride = _stride_of_out(dxbc, "dxbc")
+            dxbc, out_stride = dx.new_empty(lead + (ch,)), ch
+        else:
+            out_stride = _stride_of_out(dxbc, "dxbc")
         in_stride = ch
         if kept is None:
             u, in_stride = _rows_in(u)
         if max(in_stride, out_stride) >= 1 << 31:
             raise ValueError("the rows of xbc or dxbc are too far apart")
-        dx, dB, dC, history, dhistory_out = (_dense(t) for t in (dx, dB, dC, history,
-                                                                 dhistory_out))
+        dx, dB, dC = _dense(dx), _dense(dB), _dense(dC)
+        history, dhistory_out = _dense(history), _dense(dhistory_out)
         weight = weight.contiguous()
         bias = bias.contiguous() if bias is not None else None
         dweight, dbias = weight.new_empty((ch, K)), weight.new_empty(ch)
         dhistory = dx.new_empty(hshape) if history is not None else None
         sizes = (batch, L, num_seqs, x_dim, bc_dim, K, in_stride, _DTYPES[dtype], 0)
-        n = _conv_backward_bytes(*sizes)
+        prob, n = _conv_backward_bytes(*sizes)
         ws = torch.empty(n, device=dev, dtype=torch.uint8) if n else None
         _check(load().ssd_conv1d_silu_backward(
-            ConvProblem(*sizes), None if kept is not None else u.data_ptr(),
+            prob, None if kept is not None else u.data_ptr(),
             kept.arg() if kept is not None else None, weight.data_ptr(), _addr(bias),
             _addr(history), _addr(cu_dev), dx.data_ptr(), dB.data_ptr(), dC.data_ptr(),
             _addr(dhistory_out), dxbc.data_ptr(), out_stride, dweight.data_ptr(),
@@ -1030,11 +1024,20 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
 
 @functools.lru_cache(maxsize=256)
 def _conv_backward_bytes(*sizes):
-    """Workspace bytes of a front's backward pass, by its sizes."""
-    n = ctypes.c_size_t(0)
-    _check(load().ssd_conv1d_silu_backward_workspace_size(ConvProblem(*sizes), ctypes.byref(n)),
+    """The problem (read only) and workspace bytes of a front's backward pass,
+    by its sizes."""
+    prob, n = ConvProblem(*sizes), ctypes.c_size_t(0)
+    _check(load().ssd_conv1d_silu_backward_workspace_size(prob, ctypes.byref(n)),
            "ssd_conv1d_silu_backward_workspace_size")
-    return n.value
+    return prob, n.value
+
+
+def _channels_after(lead, name, t, dtype):
+    """Channels of a gradient shaped ``lead`` + one or more axes of them."""
+    shape, n = t.shape, len(lead)
+    if len(shape) <= n or shape[:n] != lead or t.dtype != dtype:
+        raise ValueError("%s must be %s + channels, %s" % (name, lead, dtype))
+    return shape[n] if len(shape) == n + 1 else shape[n:].numel()
 
 
 @functools.lru_cache(maxsize=256)
@@ -1117,8 +1120,9 @@ def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, ce
     # copies and outputs are made on the stream the kernel runs on
     with context:
         if out is None:
-            out = x.new_empty(shape)
-        out_stride = _stride_of_out(out, "out")
+            out, out_stride = x.new_empty(shape), sizes[1]
+        else:
+            out_stride = _stride_of_out(out, "out")
         kx = kz = None
         if checkpoint is not False:
             gx, gz = (True, True) if checkpoint is True else _pair(checkpoint)
@@ -1152,7 +1156,8 @@ def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=
         raise ValueError("x and z must both be tensors or both checkpoints")
     sizes = _norm_sizes(x, groups, eps, center, norm_before_gate)
     dev, dtype, shape = x.device, x.dtype, x.shape
-    _norm_tensors(x, sizes[1], {"dout": dout, "z": z, "dx": dx, "dz": dz}, weight, bias)
+    channels = sizes[1]
+    _norm_tensors(x, channels, {"dout": dout, "z": z, "dx": dx, "dz": dz}, weight, bias)
     if dout is None:
         raise ValueError("dout is required")
     if z is None and (norm_before_gate or dz is not None):
@@ -1160,12 +1165,15 @@ def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=
     context, handle = _stream_of(dev, stream)
     # copies, outputs and the workspace are made on the stream the kernels run on
     with context:
+        dx_stride = dz_stride = channels
         if dx is None:
             dx = dout.new_empty(shape)
-        if dz is None and z is not None:
+        else:
+            dx_stride = _stride_of_out(dx, "dx")
+        if dz is not None:
+            dz_stride = _stride_of_out(dz, "dz")
+        elif z is not None:
             dz = dout.new_empty(shape)
-        dx_stride = _stride_of_out(dx, "dx")
-        dz_stride = _stride_of_out(dz, "dz") if dz is not None else 0
         dout, out_stride = _rows_in(dout)
         x_stride = z_stride = 0
         if not kept:
@@ -1175,10 +1183,10 @@ def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=
         n = 0
         if weight is not None:
             weight = weight.contiguous()
-            dweight = weight.new_empty(sizes[1])
+            dweight = weight.new_empty(channels)
         if bias is not None:
             bias = bias.contiguous()
-            dbias = bias.new_empty(sizes[1])
+            dbias = bias.new_empty(channels)
         if weight is not None or bias is not None:
             n = _norm_backward_bytes(*sizes)
             ws = torch.empty(n, device=dev, dtype=torch.uint8) if n else None
