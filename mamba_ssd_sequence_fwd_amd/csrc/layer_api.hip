@@ -14,6 +14,9 @@ namespace {
 using ssd::fail;
 
 constexpr size_t kAlign = 256;  // of workspaces
+// A launch takes fewer than 2^32 threads along x: workgroups of 256 threads,
+// and columns of k_column_sums (1024 threads for 64 of them).
+constexpr int64_t kMostBlocks = (1 << 24) - 1, kMostColumns = (1 << 28) - 64;
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -88,7 +91,7 @@ ssd_status check_conv(const ssd_conv_problem *p, const int32_t *cu_seqlens, int6
 ssd_status check_tiles(const ssd_conv_problem *p, int64_t T, int64_t nseq) {
   const int64_t ch = (int64_t)p->x_dim + 2 * (int64_t)p->bc_dim;
   if (T + 2 * nseq > INT32_MAX / 2 ||
-      ((T / 12 + nseq) / 4 + 1) * (ch / 256 + 1) > INT32_MAX)
+      ((T / 12 + nseq) / 4 + 1) * (ch / 256 + 1) > kMostBlocks)
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences x %lld channels too large for "
                 "one launch", (long long)T, (long long)nseq, (long long)ch);
   return SSD_OK;
@@ -150,6 +153,8 @@ ssd_status conv_backward_geometry(const ssd_conv_problem *p, const int32_t *cu, 
   a->bc_dim = p->bc_dim;
   a->in_stride = p->in_stride;
   if ((st = check_tiles(p, T, nseq)) != SSD_OK) return st;
+  if ((int64_t)a->ch * (p->width + 1) > kMostColumns)
+    return fail(SSD_ERR_UNSUPPORTED, "%d channels are too many for one launch", a->ch);
   *tblocks = ssd::conv_bwd_geometry(*a);
   return SSD_OK;
 }
@@ -179,7 +184,7 @@ ssd_status check_norm(const ssd_norm_problem *p) {
   if (gs % 8 != 0 || gs > ssd::kNormMaxGroup)
     return fail(SSD_ERR_UNSUPPORTED, "group size %d is not a multiple of 8 up to %d", gs,
                 ssd::kNormMaxGroup);
-  if (p->channels > INT32_MAX / 8 || p->tokens > INT32_MAX / 2)
+  if (2 * (int64_t)p->channels > kMostColumns || p->tokens > INT32_MAX / 2)
     return fail(SSD_ERR_UNSUPPORTED, "%d tokens x %d channels too large for 32-bit indexing",
                 p->tokens, p->channels);
   return SSD_OK;
@@ -262,7 +267,7 @@ ssd_status check_ckpt_problem(const ssd_checkpoint_problem *p, const void *tenso
                 "stride %lld must be >= the channel count %d and a multiple of 16 bytes",
                 (long long)p->stride, p->channels);
   if (p->rows > INT32_MAX ||
-      (p->rows + 3) / 4 * (p->channels / 8 + 4) / 256 + 1 > INT32_MAX)
+      (p->rows + 3) / 4 * (p->channels / 8 + 4) / 256 + 1 > kMostBlocks)
     return fail(SSD_ERR_UNSUPPORTED, "%lld rows x %d channels too large for one launch",
                 (long long)p->rows, p->channels);
   if (p->rows == 0) return SSD_OK;

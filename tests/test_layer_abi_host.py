@@ -361,3 +361,23 @@ def test_norm_refuses_what_is_not_a_pair_to_fill(monkeypatch):
             ssd.group_norm_silu(x, z=z, checkpoint=given)
     with pytest.raises(ValueError, match="True, False or a Checkpoint"):
         ssd.group_norm_silu(x, z=z, checkpoint=(one, None))
+
+
+def test_refuses_what_no_launch_holds(lib):
+    """Sizes whose grids would pass 2^32 threads are refused before a launch."""
+    n = ctypes.c_size_t(0)
+    no = ssd.SSD_ERR_UNSUPPORTED
+    many = CP(batch=1, seqlen=(1 << 30) - 8, x_dim=8, bc_dim=0, in_stride=8)
+    assert lib.ssd_conv1d_silu_backward_workspace_size(ctypes.byref(many), ctypes.byref(n)) == no
+    assert _conv_ck(lib, many, ck=CK(), hist_out=None) == no
+    wide = CP(batch=1, seqlen=1, x_dim=1 << 26, bc_dim=0, in_stride=1 << 26)
+    assert lib.ssd_conv1d_silu_backward_workspace_size(ctypes.byref(wide), ctypes.byref(n)) == no
+    c = 1 << 27
+    p = NP(tokens=1, channels=c, groups=c // 64, **{k + "_stride": c for k in
+                                                    ("x", "z", "out", "dx", "dz")})
+    assert _norm(lib, p) == no
+    for fn in (lib.ssd_checkpoint_save, lib.ssd_checkpoint_load):
+        prob, ck = KP(rows=1 << 30, channels=256, stride=256), CK()
+        a = (_addr(0), ctypes.byref(ck)) if fn is lib.ssd_checkpoint_save else \
+            (ctypes.byref(ck), _addr(0))
+        assert fn(ctypes.byref(prob), *a, None) == no
