@@ -555,20 +555,22 @@ int row_blocks(const NormArgs &a, const Team &t, int waves, int cap, int most) {
 // groups of 512: 131 us with 3 rows each, 158 us with 32 waves a unit that
 // stay), workgroup teams as few that stay (one group of 5120: 86 us with 8
 // waves a unit, 92 with 4 rows each; groups of 1024 to 4096: 69 us at 16, 71
-// to 72 with 6 rows).
+// to 72 with 6 rows; in fp32, with twice the bytes a load, 8: 32768 tokens of
+// 1024 channels 78 us against 82).
 int forward_blocks(const NormArgs &a, const Team &t) {
   if (!t.wide) return row_blocks(a, t, 32, 65535, 3);
-  return row_blocks(a, t, t.r == 1 ? 16 : 8, 65535, INT32_MAX);
+  return row_blocks(a, t, t.r == 1 && a.bf16_io ? 16 : 8, 65535, INT32_MAX);
 }
 
 // Backward: every workgroup costs a row of partial sums, and more loads in
 // flight do not help: 8 waves a unit (16384 tokens of groups of 1024 to 4096:
-// 113 to 117 us; 12 waves 119 to 125), from checkpoints, with half the bytes
-// a load, 16 (110 to 111 us; 8 waves 125 to 135). Lanes of several parts hold
-// twice the loads: 8. No lane adds up more than 256 rows in fp32 (up to 16
-// million tokens).
+// 113 to 117 us; 12 waves 119 to 125), from checkpoints of bf16, with half the
+// bytes a load, 16 (110 to 111 us; 8 waves 125 to 135; of fp32, whose gradients
+// are as wide as ever, 8: 8192 tokens of 8 groups of 512 97 us against 110).
+// Lanes of several parts hold twice the loads: 8. No lane adds up more than 256
+// rows in fp32 (up to 16 million tokens).
 int backward_blocks(const NormArgs &a, const Team &t) {
-  return row_blocks(a, t, a.xk.q && t.r == 1 ? 16 : 8, 2048, 256);
+  return row_blocks(a, t, a.xk.q && a.bf16_io && t.r == 1 ? 16 : 8, 2048, 256);
 }
 
 template <typename T, int MODE>

@@ -206,6 +206,7 @@ ssd::NormArgs norm_args(const ssd_norm_problem *p) {
   a.G = p->groups;
   a.gs = p->channels / p->groups;
   a.center = (p->flags & SSD_NORM_CENTER) ? 1 : 0;
+  a.bf16_io = p->dtype == SSD_DTYPE_BF16;
   a.eps = p->eps;
   a.inv_n = 1.f / (float)a.gs;
   a.x_stride = p->x_stride;

@@ -30,6 +30,7 @@ struct NormArgs {
   int32_t subs;       // rows a workgroup takes side by side (in-wave teams)
   int32_t nparts;     // backward: rows of partial sums
   int32_t sum_b;      // backward: db is wanted
+  int32_t bf16_io;    // tensors are bf16, else fp32
   float eps, inv_n;   // inv_n = 1 / gs
 };
 
