@@ -507,6 +507,8 @@ ssd_status ssd_checkpoint_load(const ssd_checkpoint_problem *prob,
  *   xbc NULL:  x, B and C recomputed from the checkpoint's values, as the
  *              backward pass needs them (in_stride is then not used, and
  *              history_out must be NULL: the exact inputs are not there).
+ * Without tokens xbc and the checkpoint's arrays may be NULL, and history_out
+ * is the initial history, as above.
  * Every other argument, the layouts and the errors are those of
  * ssd_conv1d_silu. */
 ssd_status ssd_conv1d_silu_checkpoint(const ssd_conv_problem *prob, const void *xbc,

@@ -298,9 +298,10 @@ ssd_status ssd_conv1d_silu_checkpoint(const ssd_conv_problem *p, const void *xbc
                                       void *history_out, void *stream) {
   ssd::clear_detail();
   if (!checkpoint) return fail(SSD_ERR_INVALID_ARG, "checkpoint must be non-NULL");
-  if (!xbc && history_out)
-    return fail(SSD_ERR_INVALID_ARG, "a checkpoint does not hold the exact history");
+  // without tokens xbc is NULL too (an empty tensor's address), and the history passes through
   const bool tokens = p && (int64_t)p->batch * p->seqlen > 0;
+  if (tokens && !xbc && history_out)
+    return fail(SSD_ERR_INVALID_ARG, "a checkpoint does not hold the exact history");
   ssd_status st = tokens ? check_ckpt(checkpoint, "checkpoint") : SSD_OK;
   if (st != SSD_OK) return st;
   return conv_forward(p, xbc, checkpoint, weight, bias, history_in, cu_seqlens, x, B, C,

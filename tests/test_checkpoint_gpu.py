@@ -139,3 +139,29 @@ def test_conv_front_saves_and_recomputes(name, hist):
         g = again[k].double().cpu().numpy().reshape(want[k].shape)
         rtol = 2.0 ** -8 if dtype == "bf16" else 1e-5
         assert (np.abs(g - want[k]) <= atol + rtol * np.abs(want[k])).all(), k
+
+
+@pytest.mark.parametrize("hist", [False, True])
+@pytest.mark.parametrize("packed", [False, True])
+def test_conv_front_without_tokens_is_kept(packed, hist):
+    """No tokens and checkpoint=True: the history passes through (zeros without
+    one), the checkpoint is empty, and x, B and C come back from it empty."""
+    nseq, x_dim, bc_dim, K = 4, 64, 16, 4
+    ch = x_dim + 2 * bc_dim
+    lead = (0,) if packed else (nseq, 0)
+    g = torch.Generator().manual_seed(4900)
+    w, b = torch.randn(ch, K, generator=g).cuda(), torch.randn(ch, generator=g).cuda()
+    h = torch.randn(nseq, K - 1, ch, generator=g).to(torch.bfloat16).cuda() if hist else None
+    cu = torch.zeros(nseq + 1, dtype=torch.int32, device="cuda") if packed else None
+    xbc = torch.empty(lead + (ch,), dtype=torch.bfloat16, device="cuda")
+    print("[gpu] conv front without tokens, kept", flush=True)
+    x, B, C, out, kept_ = ssd.conv1d_silu(xbc, w, b, x_dim, bc_dim, h, cu, checkpoint=True)
+    given = ssd.conv1d_silu(xbc, w, b, x_dim, bc_dim, h, cu, checkpoint=kept_)
+    again = ssd.conv1d_silu(kept_, w, b, x_dim, bc_dim, h, cu)
+    torch.cuda.synchronize()
+    want = h if hist else torch.zeros(nseq, K - 1, ch, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(out, want) and torch.equal(given[3], want) and again[3] is None
+    assert kept_.shape == lead + (ch,) and kept_.exponents.shape == lead + (3,)
+    assert given[4] is kept_ and kept_.load().shape == lead + (ch,)
+    for got in ((x, B, C), again[:3]):
+        assert [t.shape for t in got] == [lead + (n,) for n in (x_dim, bc_dim, bc_dim)]

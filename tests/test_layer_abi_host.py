@@ -166,6 +166,14 @@ def test_conv_checkpoint_refuses(lib):
     assert _conv_ck(lib, CP(batch=0), ck=CK()) == ssd.SSD_OK
 
 
+def test_conv_without_tokens_keeps_its_history(lib):
+    """No tokens: xbc is an empty tensor's NULL, which does not stand for a
+    recomputation, so history_out is allowed (no sequences: nothing is launched)."""
+    for ck in (CK(), CK(q=None, e=None)):
+        assert _conv_ck(lib, CP(batch=0), xbc=None, ck=ck) == ssd.SSD_OK
+        assert _conv_ck(lib, CP(), xbc=None, ck=CK()) == ssd.SSD_ERR_INVALID_ARG
+
+
 def _conv_back(lib, prob, ck=None, cu=None, stride=96, wsb=1 << 40, **over):
     names = ["xbc", "weight", "bias", "hist", "dx", "dB", "dC", "dho", "dxbc", "dw", "db", "dh",
              "ws"]
