@@ -529,8 +529,8 @@ ssd_status ssd_conv1d_silu_checkpoint(const ssd_conv_problem *prob, const void *
  * de of the history rows is dhistory, that of the tokens dxbc. pre is
  * recomputed from xbc or from an 8-bit checkpoint of it (the gradients are
  * then those at the checkpoint's values); the forward outputs are not needed.
- * Problem: as for ssd_conv1d_silu. Arguments (device pointers, 16-byte aligned
- * where listed):
+ * Problem: as for ssd_conv1d_silu; in_stride is used with xbc only, and not by
+ * the workspace size. Arguments (device pointers, 16-byte aligned where listed):
  *   xbc, weight, bias, history_in, cu_seqlens   the forward inputs
  *   checkpoint   of xbc, with xbc NULL; NULL where xbc is given
  *   dx, dB, dC   (tokens, x_dim | bc_dim | bc_dim) dtype, aligned

@@ -44,8 +44,9 @@ ssd::Ckpt ckpt_of(const ssd_checkpoint *k) {
 // ---- convolution front ---------------------------------------------------------
 
 // The sizes of a front problem; `T` tokens and `nseq` sequences on success.
-ssd_status check_conv(const ssd_conv_problem *p, const int32_t *cu_seqlens, int64_t *T,
-                      int64_t *nseq) {
+// in_stride is that of xbc: looked at unless a checkpoint is read in its place.
+ssd_status check_conv(const ssd_conv_problem *p, const int32_t *cu_seqlens, bool strided,
+                      int64_t *T, int64_t *nseq) {
   ssd::clear_detail();
   if (!p) return fail(SSD_ERR_INVALID_ARG, "problem is NULL");
   if (p->batch < 0 || p->seqlen < 0 || p->num_seqs < 0 || p->x_dim < 0 || p->bc_dim < 0)
@@ -66,7 +67,7 @@ ssd_status check_conv(const ssd_conv_problem *p, const int32_t *cu_seqlens, int6
     return fail(SSD_ERR_INVALID_ARG, "channel count %lld out of range",
                 (long long)ch);
   const size_t esz = element_bytes(p->dtype);
-  if (p->in_stride < ch || ((size_t)p->in_stride * esz) % 16 != 0)
+  if (strided && (p->in_stride < ch || ((size_t)p->in_stride * esz) % 16 != 0))
     return fail(SSD_ERR_INVALID_ARG,
                 "in_stride %d must be >= the channel count %lld and a multiple of 16 bytes",
                 p->in_stride, (long long)ch);
@@ -102,7 +103,7 @@ ssd_status conv_forward(const ssd_conv_problem *p, const void *xbc, const ssd_ch
                         const int32_t *cu_seqlens, void *x, void *B, void *C, void *history_out,
                         void *stream) {
   int64_t T = 0, nseq = 0;
-  ssd_status st = check_conv(p, cu_seqlens, &T, &nseq);
+  ssd_status st = check_conv(p, cu_seqlens, xbc || !ck, &T, &nseq);
   if (st != SSD_OK) return st;
   if (ck && (st = check_tiles(p, T, nseq)) != SSD_OK) return st;
   if (nseq == 0 || (T == 0 && !history_out)) return SSD_OK;
@@ -312,7 +313,7 @@ ssd_status ssd_conv1d_silu_backward_workspace_size(const ssd_conv_problem *p, si
   // only the sizes matter here; any non-NULL offsets stand for the packed form
   static const int32_t some = 0;
   int64_t T = 0, nseq = 0, tblocks = 0;
-  ssd_status st = check_conv(p, &some, &T, &nseq);
+  ssd_status st = check_conv(p, &some, false, &T, &nseq);
   if (st != SSD_OK) return st;
   if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
   ssd::ConvBwdArgs a{};  // (a checkpoint takes no more tiles than the tensor)
@@ -331,7 +332,7 @@ ssd_status ssd_conv1d_silu_backward(const ssd_conv_problem *p, const void *xbc,
                                     void *dhistory, void *workspace, size_t workspace_bytes,
                                     void *stream) {
   int64_t T = 0, nseq = 0, tblocks = 0;
-  ssd_status st = check_conv(p, cu_seqlens, &T, &nseq);
+  ssd_status st = check_conv(p, cu_seqlens, xbc || !checkpoint, &T, &nseq);
   if (st != SSD_OK) return st;
   if (!weight || !dweight)
     return fail(SSD_ERR_INVALID_ARG, "weight and dweight must be non-NULL");

@@ -2,6 +2,8 @@
 convolution front, bit for bit against the fp64 oracle of the form."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -165,3 +167,35 @@ def test_conv_front_without_tokens_is_kept(packed, hist):
     assert given[4] is kept_ and kept_.load().shape == lead + (ch,)
     for got in ((x, B, C), again[:3]):
         assert [t.shape for t in got] == [lead + (n,) for n in (x_dim, bc_dim, bc_dim)]
+
+
+def test_conv_from_a_checkpoint_does_not_look_at_the_input_stride():
+    """The C calls with in_stride 0 and xbc NULL: what the binding's calls give."""
+    x_dim, bc_dim, K, L = 64, 16, 4, 37
+    ch = x_dim + 2 * bc_dim
+    g = torch.Generator().manual_seed(4901)
+    w, b = torch.randn(ch, K, generator=g).cuda(), torch.randn(ch, generator=g).cuda()
+    kept_ = ssd.checkpoint_save(torch.randn(2, L, ch, generator=g).to(torch.bfloat16).cuda())
+    d = [torch.randn(2, L, n, generator=g).to(torch.bfloat16).cuda()
+         for n in (x_dim, bc_dim, bc_dim)]
+    print("[gpu] conv front from a checkpoint, in_stride 0", flush=True)
+    want = ssd.conv1d_silu(kept_, w, b, x_dim, bc_dim)[:3]
+    wg = ssd.conv1d_silu_backward(kept_, w, b, *d)
+    p = ssd.ConvProblem(2, L, 0, x_dim, bc_dim, K, 0, ssd.SSD_DTYPE_BF16, 0)
+    out = [torch.zeros_like(t) for t in want]
+    lib, stream = ssd.load(), torch.cuda.current_stream().cuda_stream
+    assert lib.ssd_conv1d_silu_checkpoint(p, None, kept_.arg(), w.data_ptr(), b.data_ptr(), None,
+                                          None, *(t.data_ptr() for t in out), None,
+                                          stream) == ssd.SSD_OK
+    n = ctypes.c_size_t(0)
+    assert lib.ssd_conv1d_silu_backward_workspace_size(p, ctypes.byref(n)) == ssd.SSD_OK
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    dxbc, dw, db = torch.zeros_like(wg["dxbc"]), torch.zeros_like(w), torch.zeros_like(b)
+    assert lib.ssd_conv1d_silu_backward(p, None, kept_.arg(), w.data_ptr(), b.data_ptr(), None,
+                                        None, *(t.data_ptr() for t in d), None, dxbc.data_ptr(),
+                                        ch, dw.data_ptr(), db.data_ptr(), None, ws.data_ptr(),
+                                        n.value, stream) == ssd.SSD_OK
+    torch.cuda.synchronize()
+    for got, ref in zip(out + [dxbc, dw, db], list(want) + [wg[k] for k in ("dxbc", "dweight",
+                                                                             "dbias")]):
+        assert torch.equal(got, ref)

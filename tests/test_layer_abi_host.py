@@ -224,6 +224,25 @@ def test_conv_backward_refuses_pointers(lib):
     assert lib.ssd_conv1d_silu_backward_workspace_size(ctypes.byref(packed), None) == bad
 
 
+@pytest.mark.parametrize("in_stride", [0, 88, 100])
+def test_conv_from_a_checkpoint_needs_no_input_stride(lib, in_stride):
+    """in_stride belongs to xbc: looked at where xbc is given, and only there.
+    (No sequences or no workspace: the calls end before a launch.)"""
+    n, want = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    size = lib.ssd_conv1d_silu_backward_workspace_size
+    assert size(ctypes.byref(CP()), ctypes.byref(want)) == ssd.SSD_OK
+    assert size(ctypes.byref(CP(in_stride=in_stride)), ctypes.byref(n)) == ssd.SSD_OK
+    assert n.value == want.value
+    p, none = CP(in_stride=in_stride), CP(batch=0, in_stride=in_stride)
+    assert _conv_ck(lib, none, xbc=None, ck=CK(), hist_out=None) == ssd.SSD_OK
+    assert _conv_back(lib, p, xbc=None, ck=CK(), ws=None) == ssd.SSD_ERR_WORKSPACE
+    bad = ssd.SSD_ERR_INVALID_ARG
+    assert _conv_ck(lib, p, ck=CK()) == bad
+    assert _conv_ck(lib, none, ck=CK()) == bad
+    assert _conv_back(lib, p) == bad
+    assert b"in_stride" in lib.ssd_last_error_detail()
+
+
 # ---- checkpoints -------------------------------------------------------------------
 
 
