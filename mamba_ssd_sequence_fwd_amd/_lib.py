@@ -227,8 +227,17 @@ def _same_device(dev, **tensors):
     of the first input): a host pointer handed to a kernel would fault the GPU
     instead of raising. Checked before anything is launched."""
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, but the other inputs are on %s" % (name, t.device, dev))
+        if t is not None:
+            if isinstance(t, Checkpoint):
+                _refuse_checkpoint(name)
+            if t.device != dev:
+                raise ValueError("%s is on %s, but the other inputs are on %s"
+                                 % (name, t.device, dev))
+
+
+def _refuse_checkpoint(name):
+    """A Checkpoint (which has a tensor's shape, dtype and device) where a tensor belongs."""
+    raise ValueError("%s is a Checkpoint, but must be a tensor (load() gives its values)" % name)
 
 
 def _on_gpu(dev):
@@ -706,6 +715,8 @@ def checkpoint_save(t, *, checkpoint=True, stream=None):
     """Keep tensor ``t`` (..., channels) in 8 bits (ssd_checkpoint_save): returns
     a new :class:`Checkpoint`, or fills the one given. ``t`` is bfloat16 or
     float32, channels a multiple of 8; its rows may be a slice of wider rows."""
+    if isinstance(t, Checkpoint):
+        _refuse_checkpoint("tensor")
     _on_gpu(t.device)
     if t.dim() < 1 or t.dtype not in _DTYPES:
         raise ValueError("the tensor must be bfloat16 or float32 with a channel axis")
@@ -1068,17 +1079,19 @@ def _norm_sizes(x, groups, eps, center, norm_before_gate):
 
 def _norm_tensors(x, channels, like, weight, bias):
     """Checks of a norm's tensors: ``like`` (name -> tensor or None) are laid
-    out as x, the parameters (channels,) float32; all on x's device."""
+    out as x, the parameters (channels,) float32; all on x's device. z is a
+    Checkpoint where x is one, nothing else may be."""
     shape, dtype, dev = x.shape, x.dtype, x.device
+    kept = isinstance(x, Checkpoint)
     for name, t in like.items():
         if t is not None:
-            if t.device != dev:
-                _same_device(dev, **{name: t})
+            if t.device != dev or isinstance(t, Checkpoint):
+                _same_device(dev, **{name: t.q if kept and name == "z" else t})
             if t.shape != shape or t.dtype != dtype:
                 raise ValueError("%s must be %s %s" % (name, tuple(shape), dtype))
     for name, t in (("weight", weight), ("bias", bias)):
         if t is not None:
-            if t.device != dev:
+            if isinstance(t, Checkpoint) or t.device != dev:
                 _same_device(dev, **{name: t})
             if t.shape != (channels,) or t.dtype != torch.float32:
                 raise ValueError("%s must be (%d,) float32" % (name, channels))
@@ -1111,6 +1124,8 @@ def group_norm_silu(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, ce
     None); a pair of Checkpoints is filled instead. Outputs must not overlap
     inputs.
     """
+    if isinstance(x, Checkpoint):
+        _refuse_checkpoint("x")
     sizes = _norm_sizes(x, groups, eps, center, norm_before_gate)
     dev, dtype, shape = x.device, x.dtype, x.shape
     _norm_tensors(x, sizes[1], {"z": z, "out": out}, weight, bias)

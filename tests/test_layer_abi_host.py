@@ -408,3 +408,49 @@ def test_refuses_what_no_launch_holds(lib):
         a = (_addr(0), ctypes.byref(ck)) if fn is lib.ssd_checkpoint_save else \
             (ctypes.byref(ck), _addr(0))
         assert fn(ctypes.byref(prob), *a, None) == no
+
+
+def test_a_checkpoint_where_a_tensor_belongs_is_refused(monkeypatch):
+    """A Checkpoint has a tensor's shape, dtype and device: refused by name, not
+    by a missing attribute."""
+    monkeypatch.setattr(_lib, "_on_gpu", lambda dev: None)
+
+    def K(*shape, dtype=torch.bfloat16):
+        return ssd.Checkpoint(_meta(*shape, dtype=torch.int8),
+                              _meta(*shape[:-1], -(-shape[-1] // 32), dtype=torch.uint8), dtype)
+
+    def refused(name, call, *a, **kw):
+        with pytest.raises(ValueError, match="^%s is a Checkpoint" % name):
+            call(*a, **kw)
+
+    t, f = _meta(5, 64), torch.float32
+    refused("x", ssd.group_norm_silu, K(5, 64))
+    refused("z", ssd.group_norm_silu, t, z=K(5, 64))
+    refused("out", ssd.group_norm_silu, t, out=K(5, 64))
+    refused("weight", ssd.group_norm_silu, t, K(64, dtype=f))
+    refused("bias", ssd.group_norm_silu, t, None, K(64, dtype=f))
+    back = ssd.group_norm_silu_backward
+    for x in (t, K(5, 64)):
+        refused("dout", back, K(5, 64), x)
+        refused("dx", back, t, x, dx=K(5, 64))
+        refused("dz", back, t, x, z=x, dz=K(5, 64))
+    away = ssd.Checkpoint(torch.zeros(5, 64, dtype=torch.int8),
+                          torch.zeros(5, 2, dtype=torch.uint8), torch.bfloat16)
+    with pytest.raises(ValueError, match="z is on cpu"):
+        back(t, K(5, 64), z=away)
+    refused("tensor", ssd.checkpoint_save, K(5, 64))
+    refused("out", K(5, 64).load, out=K(5, 64))
+    ch = 64 + 2 * 16
+    w, b = _meta(ch, 4, dtype=f), _meta(ch, dtype=f)
+    for xbc in (_meta(2, 32, ch), K(2, 32, ch)):
+        refused("history", ssd.conv1d_silu, xbc, w, b, 64, 16, K(2, 3, ch))
+        for name, n in (("x", 64), ("B", 16), ("C", 16)):
+            refused(name, ssd.conv1d_silu, xbc, w, b, 64, 16, **{name: K(2, 32, n)})
+        for name, k in (("dx", K(2, 32, 64)), ("dB", K(2, 32, 16)), ("dC", K(2, 32, 16)),
+                        ("history", K(2, 3, ch)), ("dhistory_out", K(2, 3, ch)),
+                        ("dxbc", K(2, 32, ch)), ("weight", K(ch, 8, dtype=f)),
+                        ("bias", K(ch, dtype=f))):
+            a = dict(weight=w, bias=b, dx=_meta(2, 32, 64), dB=_meta(2, 32, 16),
+                     dC=_meta(2, 32, 16))
+            a[name] = k
+            refused(name, ssd.conv1d_silu_backward, xbc, **a)
