@@ -2,6 +2,8 @@
 against the fp64 oracle; bounds in layer_helpers."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -201,6 +203,102 @@ def test_norm_sums_of_many_rows():
     torch.cuda.synchronize()
     want, size = norm_backward(d.cpu(), x.cpu(), z.cpu(), w.cpu(), b.cpu(), 2, 1e-5, False, "first")
     for k in ("dx", "dz", "dweight", "dbias"):
+        check(k, got[k], want[k], size[k], "fp32", 512)
+
+
+def _partial_rows(T, C, G, dtype):
+    """Rows of partial sums of the backward pass (the most of both sources)."""
+    p = ssd.NormProblem(C, C, C, C, C, T, C, G,
+                        ssd.SSD_DTYPE_BF16 if dtype == "bf16" else ssd.SSD_DTYPE_F32, 0, 1e-5)
+    n = ctypes.c_size_t(0)
+    assert ssd.load().ssd_group_norm_silu_backward_workspace_size(p, ctypes.byref(n)) == ssd.SSD_OK
+    return n.value // (8 * C)
+
+
+@pytest.mark.parametrize("T,gs,dtype,gate,center,affine", [
+    # one part a lane
+    (205, 1040, "bf16", "first", False, "wb"), (205, 1040, "fp32", "last", True, "wb"),
+    # three (forward, and backward from 8 bits; backward from tensors two), the last nearly empty
+    (67, 4104, "bf16", "last", True, "wb"), (67, 4104, "bf16", "none", False, "w"),
+    (67, 4104, "fp32", "first", False, "wb"), (67, 4104, "fp32", "last", True, "wb"),
+    (67, 4104, "fp32", "none", True, "wb"),
+    (67, 5120, "bf16", "first", True, "wb"), (67, 5120, "bf16", "last", False, "w"),
+    (67, 5120, "bf16", "none", True, "wb"), (67, 5120, "fp32", "first", False, "w"),
+    (67, 5120, "fp32", "last", True, "wb"), (67, 5120, "fp32", "none", False, "wb"),
+    # four forward, two backward
+    (67, 8192, "bf16", "first", False, "wb"), (67, 8192, "fp32", "last", True, "wb"),
+    # four
+    (67, 16384, "bf16", "last", True, "wb"), (67, 16384, "fp32", "first", False, "wb"),
+    (67, 16384, "fp32", "none", True, "w"),
+])
+def test_norm_workgroups_walk_several_rows(T, gs, dtype, gate, center, affine):
+    """Groups wider than a wave, of which every workgroup takes several rows in
+    turn and some one row fewer: the next row's loads, the sums' buffers taken
+    in turn and the gradients summed over rows. 16 groups, of which the first
+    and the last are compared with the oracle; dout holds whole numbers, so
+    that dbias (gate first) is exact whatever the order of its sum. At most 8
+    rows a lane: the bounds of layer_helpers hold as they are."""
+    G = 16
+    C = G * gs
+    rng = np.random.default_rng(T + gs)
+    x, xn = rows(rng, T, C, dtype)
+    z, zn = rows(rng, T, C, dtype, spread=0.0) if gate != "none" else (None, None)
+    dn = rng.integers(-8, 9, (T, C)).astype(np.float64)
+    d = torch.from_numpy(dn).to(DT[dtype]).cuda()
+    w = (1 + 0.2 * rng.standard_normal(C)).astype(np.float32) if "w" in affine else None
+    b = (0.2 * rng.standard_normal(C)).astype(np.float32) if "b" in affine else None
+    dev = lambda a: None if a is None else torch.from_numpy(a).cuda()
+    kw = dict(groups=G, eps=1e-5, center=center, norm_before_gate=gate == "last")
+    print("[gpu] group norm rows in turn %d x 16 x %d %s %s" % (T, gs, dtype, gate), flush=True)
+    assert T > 2 * _partial_rows(T, C, G, dtype)
+    out = ssd.group_norm_silu(x, dev(w), dev(b), z, **kw)
+    same, kx, kz = ssd.group_norm_silu(x, dev(w), dev(b), z, checkpoint=True, **kw)
+    plain = ssd.group_norm_silu_backward(d, x, dev(w), dev(b), z, **kw)
+    kept_ = ssd.group_norm_silu_backward(d, kx, dev(w), dev(b), kz, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out, same)
+    for k, t in ((kx, x), (kz, z)):
+        if t is not None:
+            ref = ssd.checkpoint_save(t)
+            assert torch.equal(k.q, ref.q) and torch.equal(k.exponents, ref.exponents)
+    if gate == "first" and b is not None:
+        for g in (plain, kept_):
+            assert np.array_equal(g["dbias"].cpu().numpy(), dn.sum(axis=0))
+    xk = kx.load().double().cpu().numpy()
+    zk = None if z is None else kz.load().double().cpu().numpy()
+    for at in (slice(0, gs), slice(C - gs, C)):
+        cut = lambda a: None if a is None else a[..., at]
+        want, size = norm(cut(xn), cut(zn), cut(w), cut(b), 1, 1e-5, center, gate)
+        check("out", out[:, at], want, size, dtype, 160)
+        for g, xv, zv in ((plain, xn, zn), (kept_, xk, zk)):
+            want, size = norm_backward(cut(dn), cut(xv), cut(zv), cut(w), cut(b), 1, 1e-5, center,
+                                       gate)
+            for k in ("dx", "dz", "dweight", "dbias"):
+                if g[k] is not None:
+                    check(k, g[k][..., at], want[k], size[k],
+                          "fp32" if k in ("dweight", "dbias") else dtype, 512)
+
+
+def test_norm_sums_of_rows_side_by_side():
+    """One group of 8 channels: a workgroup takes 256 rows side by side, whose
+    shares of dweight and dbias are joined in fp32 before the partial rows are
+    written. A lane's own 9 rows and 255 joins in turn: C = 480 + 9 + 255 (512
+    of layer_helpers counts 32 rows). dout holds whole numbers: dbias is exact."""
+    T, C = (1 << 20) + 37, 8
+    rng = np.random.default_rng(7)
+    x, xn = rows(rng, T, C, "fp32")
+    z, zn = rows(rng, T, C, "fp32", spread=0.0)
+    dn = rng.integers(-8, 9, (T, C)).astype(np.float64)
+    d = torch.from_numpy(dn).float().cuda()
+    w, b = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    print("[gpu] group norm rows side by side", flush=True)
+    got = ssd.group_norm_silu_backward(d, x, w, b, z)
+    torch.cuda.synchronize()
+    assert -(-T // 256) > 8 * _partial_rows(T, C, 1, "fp32")
+    want, size = norm_backward(dn, xn, zn, None, None, 1, 1e-5, False, "first")
+    assert np.array_equal(got["dbias"].cpu().numpy(), want["dbias"])
+    check("dweight", got["dweight"], want["dweight"], size["dweight"], "fp32", 480 + 9 + 255)
+    for k in ("dx", "dz"):
         check(k, got[k], want[k], size[k], "fp32", 512)
 
 
