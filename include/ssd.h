@@ -503,10 +503,12 @@ ssd_status ssd_checkpoint_load(const ssd_checkpoint_problem *prob,
                                const ssd_checkpoint *checkpoint, void *dst, void *stream);
 
 /* ssd_conv1d_silu with an 8-bit checkpoint of its input (tokens, ch):
- *   xbc given: the front as above, which also writes the checkpoint of xbc;
- *   xbc NULL:  x, B and C recomputed from the checkpoint's values, as the
- *              backward pass needs them (in_stride is then not used, and
- *              history_out must be NULL: the exact inputs are not there).
+ *   xbc given: the front as above, with equal bits, which also writes the
+ *              checkpoint of xbc;
+ *   xbc NULL:  x, B and C recomputed from the checkpoint's values, with the
+ *              bits that the front gives on them, as the backward pass needs
+ *              them (in_stride is then not used, and history_out must be NULL:
+ *              the exact inputs are not there).
  * Without tokens xbc and the checkpoint's arrays may be NULL, and history_out
  * is the initial history, as above.
  * Every other argument, the layouts and the errors are those of

@@ -5,8 +5,10 @@
 // The mathematics are those of the front (k_conv.hip):
 //   pre[t, c] = bias[c] + sum_k w[c, k] u[t - (K - 1) + k, c]
 //   out[t, c] = pre / (1 + exp(-pre))
-// and the checkpoint is that of u (rows.h). Keeping it adds 33 bytes to write
-// per 32 channels and none to read; from it 33 bytes are read instead of 64.
+// with the terms of pre added in that kernel's order, so that outputs are equal
+// bit for bit, and the checkpoint is that of u (rows.h). Keeping it adds 33
+// bytes to write per 32 channels and none to read; from it 33 bytes are read
+// instead of 64.
 //
 // Each lane owns 4 channels and walks one tile of tokens of one sequence
 // (TileMap) with the last K - 1 inputs in registers; eight lanes share a block

@@ -199,3 +199,32 @@ def test_conv_from_a_checkpoint_does_not_look_at_the_input_stride():
     for got, ref in zip(out + [dxbc, dw, db], list(want) + [wg[k] for k in ("dxbc", "dweight",
                                                                              "dbias")]):
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_conv_front_outputs_do_not_depend_on_the_checkpoint(dtype, K, bias):
+    """Two kernels, the same sums in the same order: keeping the input changes no
+    bit of x, B, C and the history, and x, B and C from the checkpoint are those
+    of its values."""
+    print("[gpu] conv front with and without a checkpoint %s K=%d" % (dtype, K), flush=True)
+    for batch, seqlen, lens, x_dim, bc_dim, hist in (
+            (3, 515, None, 256, 64, True), (1, 0, [7, 1, 0, 300, 2, 3, 99, 513], 1304, 24, True),
+            (2, 77, None, 40, 0, False), (2, 1500, None, 2560, 128, False)):
+        inp = si.make_conv_inputs(batch, seqlen, x_dim, bc_dim, K, dtype, seed=4902,
+                                  seq_lens=lens, history=hist)
+        xbc = inp["xbc"].cuda()
+        if lens is None:
+            xbc = xbc.view(batch, seqlen, x_dim + 2 * bc_dim)
+        args = (inp["weight"].cuda(), inp["bias"].cuda() if bias else None, x_dim, bc_dim,
+                inp["history"].cuda() if hist else None, inp["cu_seqlens"])
+        plain = ssd.conv1d_silu(xbc, *args)
+        saved = ssd.conv1d_silu(xbc, *args, checkpoint=True)
+        again = ssd.conv1d_silu(saved[4], *args)
+        direct = ssd.conv1d_silu(saved[4].load(), *args)
+        torch.cuda.synchronize()
+        for k in range(4):
+            assert torch.equal(saved[k], plain[k]), k
+        for k in range(3):
+            assert torch.equal(again[k], direct[k]), k
