@@ -16,8 +16,9 @@
 // times, and keeps them over all the rows it walks, so the affine weights are
 // loaded once and the gradients of the weights are summed in registers; each
 // workgroup writes one row of partial sums. The next row's loads are issued
-// before the current row's sums. All sums are fp32; the partial rows are added
-// in fp64. Squares are summed as they are: |u| above about 1e18 overflows.
+// before the current row's sums. All sums are fp32, rows side by side in a
+// workgroup are joined in fp32 in turn, and the partial rows are added in fp64.
+// Squares are summed as they are: |u| above about 1e18 overflows.
 //
 // Both directions are bound by HBM. Measured, caches cold, bf16, gate first:
 // 16384 tokens of one group of 5120 channels forward 86 us for 503 MB (5.8
@@ -25,7 +26,12 @@
 // groups of 512 forward 131 us for 805 MB (6.1 TB/s), with both inputs kept in
 // 8 bits 190 us for 1082 MB (5.7 TB/s), backward from them 205 to 222 us for
 // 1082 MB (4.9 to 5.3 TB/s; 41 vector instructions an element are 140 us of
-// it). One token of 5120 channels takes 4.8 us.
+// it). One token of 5120 channels takes 4.8 us. Furthest from that is the
+// backward pass without a gate, which needs the statistics before it has dv and
+// so takes one more sum after the others: 8192 tokens of one group of 5120
+// channels 90 us in bf16 (252 MB, 2.8 TB/s; vector instructions 42% of the
+// waves' time, waits 33%) and 117 us centred, with three sums in turn (34% and
+// 46%); in fp32 (503 MB) 116 and 128 us.
 #include "norm.h"
 
 namespace ssd {
@@ -243,8 +249,14 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormArgs a) {
   const Place<WIDE, R> at(a);
   // With 4 parts a lane there are no registers for a second row, and in fp32
   // or with a bias none for the weights either: those are read again, from
-  // L2, for each row (4096 tokens of 16384 channels, fp32 with a bias: 516 us;
-  // held, and spilled, 803).
+  // L2, for each row. 4096 tokens of 16384 channels, with a bias, from tensors
+  // and from 8 bits, against the weights held: fp32 gate first 327 and 244 us
+  // (held 427 and 262), gate last 336 and 259 (552 and 481), no gate 241 and 212
+  // (236 and 206); bf16 gate first 158 and 145 (152 and 140), gate last 181 and
+  // 167 (175 and 173), no gate 167 and 163 (152 and 151). In fp32 with a bias
+  // three of these kernels still spill some registers (60 bytes a lane gate
+  // first from tensors, 136 gate last, 120 gate last from 8 bits), which the
+  // times above include.
   constexpr bool kAhead = R < 4, kRoom = R < 4 || (sizeof(T) == 2 && !BIAS);
   float dw[R][8], db[R][BIAS ? 8 : 1];
   float ws[kRoom ? R : 1][8], bs[kRoom && BIAS ? R : 1][8];
@@ -524,10 +536,15 @@ Team team_of(const NormArgs &a, int r_wide, int threads_wide) {
 }
 
 // Forward: 4 waves of 3 or 4 parts. Backward: 8 waves of 2 parts; from 8-bit
-// checkpoints, whose loads are shorter, 4 waves of 3 up to 768 lanes (140 us
-// at the shape above against 168 us with 8 waves of 2; 8192 tokens of 5632
-// channels 80 against 84; past 768 lanes 4 waves of 4 lose, 115 us against 111
-// at 8192 x 8192).
+// checkpoints, whose loads are shorter, 4 waves of 3 up to 768 lanes (bf16, gate
+// first: 140 us at the shape above against 168 us with 8 waves of 2; 8192 tokens
+// of 5632 channels 80 against 84; past 768 lanes 4 waves of 4 lose, 115 us
+// against 111 at 8192 x 8192). In fp32 neither wins everywhere: 8192 tokens of
+// 5120 channels, without and with a bias, no gate 92 and 108 us with 4 waves of
+// 3, 117 and 125 with 8 of 2; gate first 127 and 136 against 132 and 124; gate
+// last, whose 4 waves of 3 need so many registers that one wave a SIMD is
+// resident, 137 and 151 against 130 and 136 (4104 channels: gated 111 to 142
+// against 103 to 123, no gate 87 and 101 against 114 and 121).
 Team forward_team(const NormArgs &a) { return team_of(a, 3, 256); }
 Team backward_team(const NormArgs &a) {
   const int lanes = a.gs / 8;
@@ -567,8 +584,10 @@ int forward_blocks(const NormArgs &a, const Team &t) {
 // 113 to 117 us; 12 waves 119 to 125), from checkpoints of bf16, with half the
 // bytes a load, 16 (110 to 111 us; 8 waves 125 to 135; of fp32, whose gradients
 // are as wide as ever, 8: 8192 tokens of 8 groups of 512 97 us against 110).
-// Lanes of several parts hold twice the loads: 8. No lane adds up more than 256
-// rows in fp32 (up to 16 million tokens).
+// Lanes of several parts hold twice the loads: 8 (also where the registers leave
+// room for 4 only, and the rest wait their turn). No lane adds up more than 256
+// rows in fp32 (up to 16 million tokens); where a workgroup takes rows side by
+// side, up to 255 more sums are added to a lane's in turn.
 int backward_blocks(const NormArgs &a, const Team &t) {
   return row_blocks(a, t, a.xk.q && a.bf16_io && t.r == 1 ? 16 : 8, 2048, 256);
 }
