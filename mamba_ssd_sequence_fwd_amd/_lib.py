@@ -953,8 +953,8 @@ def conv1d_silu_backward(xbc, weight, bias, dx, dB, dC, history=None, cu_seqlens
 
     xbc, weight, bias, history and cu_seqlens as given to :func:`conv1d_silu`
     (xbc may be a :class:`Checkpoint` of it). dx, dB and dC are the gradients
-    of its outputs, as :func:`backward` returns them or with their channels
-    flattened; dhistory_out that of history_out, or None. dxbc (optional
+    of its outputs, as :func:`backward` returns them (packed, with its batch
+    axis of 1) or with their channels flattened; dhistory_out that of history_out, or None. dxbc (optional
     output, shaped like xbc) may be a slice of wider rows and must not overlap
     the inputs. dbias without a bias is the gradient at zero.
     """
@@ -1044,8 +1044,11 @@ def _conv_backward_bytes(*sizes):
 
 
 def _channels_after(lead, name, t, dtype):
-    """Channels of a gradient shaped ``lead`` + one or more axes of them."""
+    """Channels of a gradient shaped ``lead`` + one or more axes of them; packed
+    (``lead`` the tokens alone), a batch axis of 1 may stand before the tokens."""
     shape, n = t.shape, len(lead)
+    if n == 1 and len(shape) > 2 and shape[0] == 1 and shape[1] == lead[0]:
+        shape = shape[1:]
     if len(shape) <= n or shape[:n] != lead or t.dtype != dtype:
         raise ValueError("%s must be %s + channels, %s" % (name, lead, dtype))
     return shape[n] if len(shape) == n + 1 else shape[n:].numel()

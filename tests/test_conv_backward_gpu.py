@@ -241,3 +241,27 @@ def test_conv_backward_offsets_that_are_no_partition():
     with pytest.raises(ValueError, match="cu_seqlens"):
         ssd.conv1d_silu_backward(xbc, w, None, dx, dB, dC, None,
                                  torch.tensor([0, 300, 200], dtype=torch.int32, device="cuda"))
+
+
+def test_conv_backward_of_the_packed_layer():
+    """Packed input, the layer's gradients as ssd.backward returns them (a batch
+    axis of 1): what their flattened form gives, from xbc and from 8 bits."""
+    H, P, G, N, K, lens = 4, 64, 1, 64, 4, [5, 0, 90, 1, 31]
+    X, BC, T = H * P, G * N, sum(lens)
+    inp = si.make_conv_inputs(1, 0, X, BC, K, "bf16", seed=4950, seq_lens=lens)
+    xbc, w, b, cu = (inp[k].cuda() for k in ("xbc", "weight", "bias", "cu_seqlens"))
+    g = torch.Generator().manual_seed(4951)
+    dt = torch.rand(1, T, H, generator=g).to(torch.bfloat16).cuda()
+    A, dy = -torch.rand(H, generator=g).cuda(), torch.randn(1, T, H, P, generator=g)
+    print("[gpu] conv backward of the packed layer", flush=True)
+    x, B, C, _, kept_ = ssd.conv1d_silu(xbc, w, b, X, BC, None, cu, checkpoint=True)
+    gs = ssd.backward(x.view(1, T, H, P), dt, A, B.view(1, T, G, N), C.view(1, T, G, N), None, None,
+                      dy.to(torch.bfloat16).cuda(), cu_seqlens=cu)
+    assert gs["dx"].shape == (1, T, H, P) and gs["dB"].shape == (1, T, G, N)
+    flat = [gs[k].reshape(T, -1) for k in ("dx", "dB", "dC")]
+    for src in (xbc, kept_):
+        got = ssd.conv1d_silu_backward(src, w, b, gs["dx"], gs["dB"], gs["dC"], None, cu)
+        want = ssd.conv1d_silu_backward(src, w, b, *flat, None, cu)
+        torch.cuda.synchronize()
+        for k in ("dxbc", "dweight", "dbias"):
+            assert got[k].shape == want[k].shape and torch.equal(got[k], want[k]), k

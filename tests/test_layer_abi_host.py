@@ -454,3 +454,17 @@ def test_a_checkpoint_where_a_tensor_belongs_is_refused(monkeypatch):
                      dC=_meta(2, 32, 16))
             a[name] = k
             refused(name, ssd.conv1d_silu_backward, xbc, **a)
+
+
+def test_conv_backward_takes_packed_gradients_as_the_layer_returns_them():
+    """Packed: the layer's gradients have a batch axis of 1 before the tokens,
+    which the packed input has not."""
+    after = lambda lead, *shape: _lib._channels_after(lead, "dx", _meta(*shape), torch.bfloat16)
+    for T in (1, 37):
+        assert after((T,), 1, T, 4, 16) == 64 and after((T,), 1, T, 64) == 64
+        assert after((T,), T, 4, 16) == 64 and after((T,), T, 64) == 64
+    assert after((0,), 1, 0, 4, 16) == 64 and after((1, 37), 1, 37, 4, 16) == 64
+    for lead, shape in (((37,), (2, 37, 64)), ((37,), (1, 36, 64)), ((37,), (1, 37)),
+                        ((1, 37), (37, 64)), ((2, 37), (1, 2, 37, 64))):
+        with pytest.raises(ValueError, match="dx must be"):
+            after(lead, *shape)
