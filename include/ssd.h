@@ -634,6 +634,140 @@ ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *prob, const void
                                         float *dbias, void *workspace, size_t workspace_bytes,
                                         void *stream);
 
+/* The gated delta rule: the layer's recurrence with a write that replaces what
+ * the state holds for a key instead of adding to it. Per sequence s and head h,
+ * with group g = h / (H / G):
+ *
+ *   state <- initial_state[s, h]  (headdim x dstate, fp32), or zeros
+ *   for each token t of s:
+ *     state <- exp(g[t, h]) * state
+ *     e[p]   = beta[t, h] * (x[t, h, p] - sum_n state[p, n] * B[t, g, n])
+ *     state[p, n] <- state[p, n] + e[p] * B[t, g, n]
+ *     y[t, h, p]   = sum_n C[t, g, n] * state[p, n]
+ *   final_state[s, h] <- state
+ *
+ * that is state_t = exp(g_t) state_{t-1} (I - beta_t B_t B_t^T) + beta_t x_t B_t^T.
+ * It stays bounded for |B| <= 1, 0 <= beta <= 2 and g <= 0 (expected, not
+ * required; ssd_bc_norm makes unit keys). The sequence is evaluated in chunks
+ * of 64 tokens: a triangular system inside a chunk, the state between them.
+ *
+ * Problem: as for ssd_forward with batch, seqlen >= 0 (0 = nothing to do but
+ * the states), headdim in {16, 32, 64, 128}, dstate a multiple of 16 up to 256,
+ * flags 0; chunk_size is ignored. num_seqs > 0 packs sequences (batch 1).
+ * Arguments (device pointers, 16-byte aligned but for g and beta):
+ *   x              (batch, seqlen, H, P)  dtype: the values
+ *   g              (batch, seqlen, H)     dtype: logarithm of the decay; -inf
+ *                                         (anything under -103) resets the state
+ *   beta           (batch, seqlen, H)     dtype: write strength
+ *   B, C           (batch, seqlen, G, N)  dtype: keys and queries
+ *   initial_state  (batch | num_seqs, H, P, N) fp32, NULL = zeros
+ *   cu_seqlens     (num_seqs + 1) int32 device array, packed only, as for
+ *                  ssd_forward (invalid values never cause an out-of-bounds
+ *                  access, but the outputs are then unspecified)
+ *   y              (batch, seqlen, H, P)  dtype (out)
+ *   final_state    (batch | num_seqs, H, P, N) fp32 (out), NULL = not written
+ *   workspace      at least ssd_delta_workspace_size() bytes, 256-byte aligned;
+ *                  contents on entry do not matter
+ *   stream         a hipStream_t (NULL = the default stream)
+ * Inputs and outputs must not overlap. Equal calls give equal bits. Errors as
+ * for ssd_forward; nothing is enqueued on error. No allocation, no
+ * synchronisation. */
+ssd_status ssd_delta_workspace_size(const ssd_problem *prob, size_t *bytes);
+ssd_status ssd_delta_forward(const ssd_problem *prob, const void *x, const void *g,
+                             const void *beta, const void *B, const void *C,
+                             const float *initial_state, const int32_t *cu_seqlens, void *y,
+                             float *final_state, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* One decode step of the gated delta rule: every sequence of a dense batch
+ * advances by one token, its fp32 state updated in place. Shapes and errors as
+ * for ssd_step (seqlen 1, num_seqs 0): x, y (batch, H, P); g, beta (batch, H);
+ * B, C (batch, G, N) dtype; state (batch, H, P, N) fp32. One kernel, no
+ * workspace. */
+ssd_status ssd_delta_step(const ssd_problem *prob, const void *x, const void *g, const void *beta,
+                          const void *B, const void *C, float *state, void *y, void *stream);
+
+/* The gated delta rule backwards: gradients of a loss with respect to every
+ * input of ssd_delta_forward, given those with respect to y and the final
+ * state. The states are recomputed. With G = dL/dstate walked backwards from
+ * dfinal_state, d the decayed old state and e as above, per token and head:
+ *   G += dy C^T;  dC += state^T dy;  de = beta G B;  dx = de
+ *   dbeta = (G B) . (x - d B);  dB += G^T e - d^T de;  G -= de B^T
+ *   dg = <G, d>;  G <- exp(g) G
+ * (dB, dC summed over the heads of a group, in a fixed order; equal calls give
+ * equal bits.) Problem and errors as above. dy like y; dfinal_state NULL =
+ * zero; dx, dg, dbeta, dB, dC like x, g, beta, B, C (out; dx, dB, dC 16-byte
+ * aligned); dinitial_state (batch | num_seqs, H, P, N) fp32 (out), NULL = not
+ * written, without an initial state the gradient at zeros. workspace: at least
+ * ssd_delta_backward_workspace_size() bytes, 256-byte aligned. Outputs must not
+ * overlap inputs or each other. */
+ssd_status ssd_delta_backward_workspace_size(const ssd_problem *prob, size_t *bytes);
+ssd_status ssd_delta_backward(const ssd_problem *prob, const void *x, const void *g,
+                              const void *beta, const void *B, const void *C,
+                              const float *initial_state, const int32_t *cu_seqlens,
+                              const void *dy, const float *dfinal_state, void *dx, void *dg,
+                              void *dbeta, void *dB, void *dC, float *dinitial_state,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* B and C (a recurrence's keys and queries) normalised per head and rotated by
+ * their positions, in one pass over both. Per token and head, with n = dim, or 1
+ * with SSD_BC_NORM_UNIT:
+ *   h   = x / sqrt(sum of x^2 / n + eps),  v = h * weight
+ *   out = v, where the pair (u, w) number i of the first rotary_dim channels
+ *         becomes (u cos a - w sin a, u sin a + w cos a),
+ *         a = positions[t mod period] * freqs[i]  (the exact product, reduced
+ *         in 64 bits)
+ * Pair i holds channels i and i + rotary_dim / 2, or with
+ * SSD_BC_NORM_INTERLEAVED channels 2i and 2i + 1.
+ *
+ * Problem: tokens >= 0 (below 2^30); b_heads, c_heads >= 1 heads of B and C; dim
+ * a multiple of 8 up to 256; rotary_dim a multiple of 8 up to dim, 0 = no
+ * rotation; period >= 1 positions that repeat over the tokens (a dense batch's
+ * sequence length, or the token count; not looked at without rotation); dtype F32
+ * or BF16 of B, C, the outputs and their gradients; flags 0 or SSD_BC_NORM_*
+ * bits; eps finite and >= 0; strides in elements between token rows, each at
+ * least heads * dim, a multiple of 16 bytes and at most 2^31 - 1 (a token's heads
+ * are contiguous).
+ * Arguments (device pointers; tensors 16-byte aligned):
+ *   B, C               rows at b_stride, c_stride          dtype
+ *   b_weight, c_weight (dim) fp32, NULL = ones
+ *   positions          (period) int32, freqs (rotary_dim / 2) fp32 radians per
+ *                      position; both NULL without rotation
+ *   b_out, c_out       rows at b_out_stride, c_out_stride  dtype (out)
+ *   stream             a hipStream_t (NULL = the default stream)
+ * Arithmetic is fp32; bf16 outputs are rounded once. Outputs must not overlap
+ * inputs or each other. One kernel, no allocation, no workspace. Errors as for
+ * ssd_group_norm_silu. */
+#define SSD_BC_NORM_UNIT 1u        /* divide by the root of the sum of squares */
+#define SSD_BC_NORM_INTERLEAVED 2u /* pairs of neighbouring channels */
+typedef struct ssd_bc_norm_problem {
+  int64_t b_stride, c_stride, b_out_stride, c_out_stride, db_stride, dc_stride;
+  int32_t tokens, b_heads, c_heads, dim, rotary_dim, period;
+  int32_t dtype;      /* an ssd_dtype value */
+  uint32_t flags;
+  float eps;
+} ssd_bc_norm_problem;
+ssd_status ssd_bc_norm(const ssd_bc_norm_problem *prob, const void *B, const void *C,
+                       const float *b_weight, const float *c_weight, const int32_t *positions,
+                       const float *freqs, void *b_out, void *c_out, void *stream);
+
+/* Its backward pass. With dv = the output's gradient rotated back:
+ *   dweight = sum over tokens and heads of dv * h,  dh = dv * weight
+ *   dx = (dh - h * (sum of dh * h) / n) / sqrt(... + eps)
+ * db_out, dc_out have rows at b_out_stride, c_out_stride; dB, dC (out) at
+ * db_stride, dc_stride. db_weight, dc_weight are (dim) fp32 (out), NULL = not
+ * written; without a weight they are the gradient at ones, without tokens zero.
+ * workspace: at least ssd_bc_norm_backward_workspace_size() bytes, 256-byte
+ * aligned (needed with db_weight or dc_weight only). Sums are taken in a fixed
+ * order: equal calls give equal bits. Errors as above, and SSD_ERR_WORKSPACE. */
+ssd_status ssd_bc_norm_backward_workspace_size(const ssd_bc_norm_problem *prob, size_t *bytes);
+ssd_status ssd_bc_norm_backward(const ssd_bc_norm_problem *prob, const void *db_out,
+                                const void *dc_out, const void *B, const void *C,
+                                const float *b_weight, const float *c_weight,
+                                const int32_t *positions, const float *freqs, void *dB, void *dC,
+                                float *db_weight, float *dc_weight, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *ssd_status_string(ssd_status status);
 

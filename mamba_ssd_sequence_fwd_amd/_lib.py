@@ -24,6 +24,7 @@ SSD_FLAG_GENERIC_KERNELS = 1
 SSD_FLAG_UNFUSED = 2
 SSD_FLAG_PER_SEQUENCE = 4
 SSD_NORM_CENTER, SSD_NORM_BEFORE_GATE = 1, 2
+SSD_BC_NORM_UNIT, SSD_BC_NORM_INTERLEAVED = 1, 2
 CHECKPOINT_BLOCK = 32   # channels that share a scale in an 8-bit checkpoint
 
 
@@ -81,6 +82,17 @@ class CheckpointProblem(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class BcNormProblem(ctypes.Structure):
+    _fields_ = [("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+                ("b_out_stride", ctypes.c_int64), ("c_out_stride", ctypes.c_int64),
+                ("db_stride", ctypes.c_int64), ("dc_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int32), ("b_heads", ctypes.c_int32),
+                ("c_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("period", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("eps", ctypes.c_float)]
+
+
 class CheckpointArg(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("exponents", ctypes.c_void_p)]
 
@@ -110,6 +122,9 @@ EXPORTED = ("ssd_validate", "ssd_validate_cu_seqlens", "ssd_workspace_size",
             "ssd_conv1d_silu_backward", "ssd_group_norm_silu",
             "ssd_group_norm_silu_backward_workspace_size", "ssd_group_norm_silu_backward",
             "ssd_checkpoint_save", "ssd_checkpoint_load",
+            "ssd_delta_workspace_size", "ssd_delta_forward", "ssd_delta_step",
+            "ssd_delta_backward_workspace_size", "ssd_delta_backward",
+            "ssd_bc_norm", "ssd_bc_norm_backward_workspace_size", "ssd_bc_norm_backward",
             "ssd_get_workspace_layout",
             "ssd_status_string", "ssd_last_error_detail")
 
@@ -157,6 +172,15 @@ def load(path: str = LIB_PATH):
                                                      + [ctypes.c_size_t, vp])
         lib.ssd_checkpoint_save.argtypes = [KP, vp, KA, vp]
         lib.ssd_checkpoint_load.argtypes = [KP, KA, vp, vp]
+        lib.ssd_delta_workspace_size.argtypes = [P, szp]
+        lib.ssd_delta_forward.argtypes = [P] + [vp] * 10 + [ctypes.c_size_t, vp]
+        lib.ssd_delta_step.argtypes = [P] + [vp] * 8
+        lib.ssd_delta_backward_workspace_size.argtypes = [P, szp]
+        lib.ssd_delta_backward.argtypes = [P] + [vp] * 16 + [ctypes.c_size_t, vp]
+        BN = ctypes.POINTER(BcNormProblem)
+        lib.ssd_bc_norm.argtypes = [BN] + [vp] * 9
+        lib.ssd_bc_norm_backward_workspace_size.argtypes = [BN, szp]
+        lib.ssd_bc_norm_backward.argtypes = [BN] + [vp] * 13 + [ctypes.c_size_t, vp]
         lib.ssd_backward_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
         lib.ssd_backward.argtypes = [P] + [vp] * 18 + [ctypes.c_size_t, vp]
         lib.ssd_backward_timed.argtypes = ([P] + [vp] * 18 + [ctypes.c_size_t, vp,
@@ -1215,3 +1239,343 @@ def group_norm_silu_backward(dout, x, weight=None, bias=None, z=None, *, groups=
             _addr(weight), _addr(bias), dx.data_ptr(), _addr(dz), _addr(dweight), _addr(dbias),
             _addr(ws), n, handle), "ssd_group_norm_silu_backward")
     return dict(dx=dx, dz=dz, dweight=dweight, dbias=dbias)
+
+
+def _delta_tensors(x, g, beta, B, C, dim, **like):
+    """Checks of a delta-rule call: x (..., H, P) with ``dim`` axes, g and beta
+    (..., H), B and C (..., G, N), all of x's dtype and on its device; ``like``
+    (name -> tensor or None) are shaped like x. Returns the leading shape and
+    (H, P, N, G)."""
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if len(shape) != dim:
+        raise ValueError("x must be (batch, nheads, headdim)" if dim == 3 else
+                         "x must be (batch, seqlen, nheads, headdim)")
+    if B.dim() != dim:
+        raise ValueError("B must be (batch, ngroups, dstate)" if dim == 3 else
+                         "B must be (batch, seqlen, ngroups, dstate)")
+    lead, rows, bc = shape[:-2], shape[:-1], B.shape
+    if dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float32")
+    for name, t, want in (("g", g, rows), ("beta", beta, rows), ("B", B, lead + bc[-2:]),
+                          ("C", C, bc)):
+        if t.device != dev or isinstance(t, Checkpoint):
+            _same_device(dev, **{name: t})
+        if t.shape != want or t.dtype != dtype:
+            raise ValueError("%s must be %s %s" % (name, tuple(want), dtype))
+    for name, t in like.items():
+        if t is not None:
+            _same_device(dev, **{name: t})
+            if t.shape != shape or t.dtype != dtype:
+                raise ValueError("%s must be %s %s" % (name, tuple(shape), dtype))
+    _on_gpu(dev)
+    if shape.numel() // max(shape[-1] * shape[-2], 1) >= _MOST_TOKENS:
+        raise ValueError("%d tokens are more than one call takes"
+                         % (shape.numel() // (shape[-1] * shape[-2])))
+    return lead, (shape[-2], shape[-1], bc[-1], bc[-2])
+
+
+def _delta_states(dev, shape, **states):
+    for name, t in states.items():
+        if t is not None:
+            _same_device(dev, **{name: t})
+            if t.shape != shape or t.dtype != torch.float32:
+                raise ValueError("%s must be %s float32" % (name, tuple(shape)))
+
+
+def _delta_packed(cu_seqlens, lead, check):
+    """Sequences of a packed call (0: dense), with the host's check of the offsets."""
+    if cu_seqlens is None:
+        return 0
+    if lead[0] != 1:
+        raise ValueError("cu_seqlens needs batch == 1")
+    num_seqs = cu_seqlens.numel() - 1
+    if num_seqs < 1 or num_seqs >= _MOST_TOKENS:
+        raise ValueError("cu_seqlens must hold at least two offsets")
+    if check or cu_seqlens.device.type == "cpu":
+        _check_offsets(cu_seqlens, lead[1])
+    return num_seqs
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_problem(what, *sizes):
+    """The problem (read only) and workspace bytes of a delta-rule call, by its sizes."""
+    prob, n = make_problem(*sizes), ctypes.c_size_t(0)
+    name = "ssd_delta_workspace_size" if what == "forward" else "ssd_delta_backward_workspace_size"
+    _check(getattr(load(), name)(prob, ctypes.byref(n)), name)
+    return prob, n.value
+
+
+def delta_forward(x, g, beta, B, C, initial_state=None, cu_seqlens=None, *,
+                  want_final_state=True, y=None, final_state=None, check_cu_seqlens=True,
+                  stream=None):
+    """The gated delta rule (ssd_delta_forward): returns (y, final_state).
+
+    Per token and head the state (P, N) decays by exp(g), then the value x
+    replaces what the state holds for the key B, by the part beta; y is read
+    with the query C:
+
+        h = exp(g) h;  h += beta (x - h B) B^T;  y = h C
+
+    Shapes as for :func:`forward`: x (batch, L, H, P); g, beta (batch, L, H);
+    B, C (batch, L, G, N); initial_state (batch | num_seqs, H, P, N) float32
+    or None; cu_seqlens for packed sequences (batch 1). x, g, beta, B and C
+    share the dtype (bfloat16 or float32); P in {16, 32, 64, 128}, N a multiple
+    of 16 up to 256. Keys should have at most unit length (:func:`bc_norm`
+    with ``unit=True``), g <= 0 and 0 <= beta <= 2, or the state may grow.
+    y and final_state are optional outputs (contiguous).
+    """
+    lead, (H, P, N, G) = _delta_tensors(x, g, beta, B, C, 4, y=y)
+    dev, dtype = x.device, x.dtype
+    num_seqs = _delta_packed(cu_seqlens, lead, check_cu_seqlens)
+    sshape = (num_seqs or lead[0], H, P, N)
+    _delta_states(dev, sshape, initial_state=initial_state, final_state=final_state)
+    for name, t in (("y", y), ("final_state", final_state)):
+        if t is not None and (not t.is_contiguous() or t.data_ptr() & 15):
+            raise ValueError("%s must be contiguous and 16-byte aligned" % name)
+    prob, n = _delta_problem("forward", lead[0], lead[1], H, P, N, G, 0, num_seqs, _DTYPES[dtype])
+    context, handle = _stream_of(dev, stream)
+    # copies, outputs and the workspace are made on the stream the kernels run on
+    with context:
+        cu = cu_seqlens.to(device=dev, dtype=torch.int32).contiguous() if num_seqs else None
+        if y is None:
+            y = x.new_empty(x.shape)
+        if final_state is None and want_final_state:
+            final_state = x.new_empty(sshape, dtype=torch.float32)
+        x, B, C, h0 = _dense(x), _dense(B), _dense(C), _dense(initial_state)
+        g, beta = g.contiguous(), beta.contiguous()
+        ws = x.new_empty(n, dtype=torch.uint8) if n else None
+        _check(load().ssd_delta_forward(
+            prob, x.data_ptr(), g.data_ptr(), beta.data_ptr(), B.data_ptr(), C.data_ptr(),
+            _addr(h0), _addr(cu), y.data_ptr(), _addr(final_state), _addr(ws), n, handle),
+            "ssd_delta_forward")
+    return y, final_state
+
+
+def delta_step(x, g, beta, B, C, state, *, y=None, stream=None):
+    """One decode step of the gated delta rule (ssd_delta_step): every sequence
+    advances by one token and ``state`` is updated IN PLACE; returns y.
+
+    Shapes: x (batch, H, P); g, beta (batch, H); B, C (batch, G, N); state
+    (batch, H, P, N) float32, contiguous; y (optional output) like x. Types and
+    sizes as for :func:`delta_forward`.
+    """
+    lead, (H, P, N, G) = _delta_tensors(x, g, beta, B, C, 3, y=y)
+    dev = x.device
+    if state is None:
+        raise ValueError("state is required")
+    _delta_states(dev, (lead[0], H, P, N), state=state)
+    for name, t in (("y", y), ("state", state)):
+        if t is not None and (not t.is_contiguous() or t.data_ptr() & 15):
+            raise ValueError("%s must be contiguous and 16-byte aligned" % name)
+    context, handle = _stream_of(dev, stream)
+    with context:
+        if y is None:
+            y = x.new_empty(x.shape)
+        x, B, C = _dense(x), _dense(B), _dense(C)
+        g, beta = g.contiguous(), beta.contiguous()
+        prob = Problem(lead[0], 1, H, P, N, G, 0, 0, _DTYPES[x.dtype], 0)
+        _check(load().ssd_delta_step(prob, x.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                     B.data_ptr(), C.data_ptr(), state.data_ptr(), y.data_ptr(),
+                                     handle), "ssd_delta_step")
+    return y
+
+
+def delta_backward(x, g, beta, B, C, initial_state, dy, dfinal_state=None, cu_seqlens=None, *,
+                   check_cu_seqlens=True, stream=None):
+    """The gated delta rule backwards (ssd_delta_backward): a dict with dx, dg,
+    dbeta, dB, dC and dinitial_state (without an initial state the gradient at
+    zeros). The forward inputs as given to :func:`delta_forward`; dy like x;
+    dfinal_state (batch | num_seqs, H, P, N) float32 or None. The states are
+    recomputed."""
+    if dy is None:
+        raise ValueError("dy is required")
+    lead, (H, P, N, G) = _delta_tensors(x, g, beta, B, C, 4, dy=dy)
+    dev, dtype = x.device, x.dtype
+    num_seqs = _delta_packed(cu_seqlens, lead, check_cu_seqlens)
+    sshape = (num_seqs or lead[0], H, P, N)
+    _delta_states(dev, sshape, initial_state=initial_state, dfinal_state=dfinal_state)
+    prob, n = _delta_problem("backward", lead[0], lead[1], H, P, N, G, 0, num_seqs, _DTYPES[dtype])
+    context, handle = _stream_of(dev, stream)
+    # copies, outputs and the workspace are made on the stream the kernels run on
+    with context:
+        cu = cu_seqlens.to(device=dev, dtype=torch.int32).contiguous() if num_seqs else None
+        x, B, C, dy = _dense(x), _dense(B), _dense(C), _dense(dy)
+        h0, dhT = _dense(initial_state), _dense(dfinal_state)
+        g, beta = g.contiguous(), beta.contiguous()
+        d = dict(dx=x.new_empty(x.shape), dg=x.new_empty(g.shape), dbeta=x.new_empty(g.shape),
+                 dB=x.new_empty(B.shape), dC=x.new_empty(B.shape),
+                 dinitial_state=x.new_empty(sshape, dtype=torch.float32))
+        ws = x.new_empty(n, dtype=torch.uint8) if n else None
+        _check(load().ssd_delta_backward(
+            prob, x.data_ptr(), g.data_ptr(), beta.data_ptr(), B.data_ptr(), C.data_ptr(),
+            _addr(h0), _addr(cu), dy.data_ptr(), _addr(dhT),
+            *(t.data_ptr() for t in d.values()), _addr(ws), n, handle), "ssd_delta_backward")
+    return d
+
+
+def _head_rows(t):
+    """Elements between the token rows of ``t`` (..., heads, dim), a row's heads
+    contiguous, or None where they cannot be addressed like that."""
+    if t.data_ptr() & 15:
+        return None
+    if t.is_contiguous():
+        return t.shape[-1] * t.shape[-2]
+    if t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+        return None
+    return _row_stride(t.flatten(-2))
+
+
+def _head_rows_in(t):
+    stride = _head_rows(t)
+    if stride is not None:
+        return t, stride
+    t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.shape[-1] * t.shape[-2]
+
+
+def _head_rows_out(t, like, name):
+    """A new output shaped like ``like``, or the caller's; and its row stride."""
+    if t is None:
+        return like.new_empty(like.shape), like.shape[-1] * like.shape[-2]
+    stride = _head_rows(t)
+    if stride is None:
+        raise ValueError("the token rows of %s must be evenly spaced, with contiguous heads, "
+                         "16-byte aligned" % name)
+    return t, stride
+
+
+def _bc_norm_checks(B, C, B_weight, C_weight, positions, freqs, unit, interleaved, eps, **like):
+    """Checks of a norm of B and C; ``like``: name -> (tensor or None, B or C).
+    Returns the sizes of a BcNormProblem behind its strides."""
+    shape, dtype, dev = B.shape, B.dtype, B.device
+    _same_device(dev, B=B, C=C, B_weight=B_weight, C_weight=C_weight, positions=positions,
+                 freqs=freqs)
+    if len(shape) < 2 or dtype not in _DTYPES:
+        raise ValueError("B must be bfloat16 or float32, (..., heads, dim)")
+    lead, N = shape[:-2], shape[-1]
+    if C.dim() != len(shape) or C.shape[:-2] != lead or C.shape[-1] != N or C.dtype != dtype:
+        raise ValueError("C must be %s + (heads, %d) %s" % (tuple(lead), N, dtype))
+    for name, (t, of) in like.items():
+        if t is not None:
+            _same_device(dev, **{name: t})
+            if t.shape != of.shape or t.dtype != dtype:
+                raise ValueError("%s must be %s %s" % (name, tuple(of.shape), dtype))
+    for name, t in (("B_weight", B_weight), ("C_weight", C_weight)):
+        if t is not None and (t.shape != (N,) or t.dtype != torch.float32):
+            raise ValueError("%s must be (%d,) float32" % (name, N))
+    _on_gpu(dev)
+    tokens = lead.numel()
+    if tokens >= _MOST_TOKENS or max(shape[-2], C.shape[-2]) >= 1 << 20:
+        raise ValueError("%d tokens are more than one call takes" % tokens)
+    rotary = period = 0
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs go together")
+    if freqs is not None:
+        if freqs.dim() != 1 or freqs.dtype != torch.float32:
+            raise ValueError("freqs must be (rotary_dim / 2,) float32")
+        if positions.dtype not in (torch.int32, torch.int64) or not (
+                positions.shape == lead or (len(lead) > 1 and positions.shape == lead[-1:])):
+            raise ValueError("positions must be int32 or int64, %s or %s"
+                             % (tuple(lead), tuple(lead[-1:])))
+        rotary, period = 2 * freqs.shape[0], positions.numel()
+        if rotary == 0:
+            period = 0
+    flags = (SSD_BC_NORM_UNIT if unit else 0) | (SSD_BC_NORM_INTERLEAVED if interleaved else 0)
+    return tokens, shape[-2], C.shape[-2], N, rotary, period, _DTYPES[dtype], flags, eps
+
+
+def bc_norm(B, C, B_weight=None, C_weight=None, positions=None, freqs=None, *, eps=1e-6,
+            unit=False, interleaved=False, B_out=None, C_out=None, stream=None):
+    """B and C (keys and queries) normalised per head and rotated by their
+    positions in one pass (ssd_bc_norm). Returns (B_out, C_out).
+
+    B (..., heads, dim), C (..., other heads, dim), bfloat16 or float32, dim a
+    multiple of 8 up to 256. Every head of every token is divided by its root
+    mean square (with ``unit`` by its length), sqrt(... + eps), and multiplied
+    by the side's weight (dim,) float32, or ones. With ``positions`` (shaped like
+    the token axes, or the last of them; int32, or int64 below 2^31) and ``freqs``
+    (rotary_dim / 2,) float32 radians per position, the first rotary_dim
+    channels turn by positions * freqs: channel i with i + rotary_dim / 2, or with
+    ``interleaved`` 2i with 2i + 1. Inputs and the optional outputs may be
+    slices of wider rows; outputs must not overlap inputs.
+    """
+    sizes = _bc_norm_checks(B, C, B_weight, C_weight, positions, freqs, unit, interleaved, eps,
+                            B_out=(B_out, B), C_out=(C_out, C))
+    context, handle = _stream_of(B.device, stream)
+    # copies and outputs are made on the stream the kernel runs on
+    with context:
+        B_out, bo = _head_rows_out(B_out, B, "B_out")
+        C_out, co = _head_rows_out(C_out, C, "C_out")
+        B, bs = _head_rows_in(B)
+        C, cs = _head_rows_in(C)
+        bw = B_weight.contiguous() if B_weight is not None else None
+        cw = C_weight.contiguous() if C_weight is not None else None
+        pos, freqs = _rotation(positions, freqs, sizes[4])
+        _check(load().ssd_bc_norm(
+            BcNormProblem(bs, cs, bo, co, 0, 0, *sizes), B.data_ptr(), C.data_ptr(), _addr(bw),
+            _addr(cw), _addr(pos), _addr(freqs), B_out.data_ptr(), C_out.data_ptr(), handle),
+            "ssd_bc_norm")
+    return B_out, C_out
+
+
+def _rotation(positions, freqs, rotary):
+    if not rotary:
+        return None, None
+    if positions.dtype != torch.int32:
+        positions = positions.to(torch.int32)
+    return positions.contiguous(), freqs.contiguous()
+
+
+@functools.lru_cache(maxsize=256)
+def _bc_norm_backward_bytes(*sizes):
+    """Workspace bytes of a norm's backward pass, by its sizes."""
+    n = ctypes.c_size_t(0)
+    row = [sizes[1] * sizes[3], sizes[2] * sizes[3]] * 3
+    _check(load().ssd_bc_norm_backward_workspace_size(BcNormProblem(*row, *sizes),
+                                                      ctypes.byref(n)),
+           "ssd_bc_norm_backward_workspace_size")
+    return n.value
+
+
+def bc_norm_backward(dB_out, dC_out, B, C, B_weight=None, C_weight=None, positions=None,
+                     freqs=None, *, eps=1e-6, unit=False, interleaved=False, dB=None, dC=None,
+                     stream=None):
+    """:func:`bc_norm` backwards (ssd_bc_norm_backward): a dict with dB, dC,
+    dB_weight and dC_weight (each None without the weight).
+
+    The forward inputs and options as given there; dB_out, dC_out and the
+    optional outputs dB, dC are shaped like B and C and may be slices of wider
+    rows. Outputs must not overlap inputs.
+    """
+    if dB_out is None or dC_out is None:
+        raise ValueError("dB_out and dC_out are required")
+    sizes = _bc_norm_checks(B, C, B_weight, C_weight, positions, freqs, unit, interleaved, eps,
+                            dB_out=(dB_out, B), dC_out=(dC_out, C), dB=(dB, B), dC=(dC, C))
+    dev = B.device
+    context, handle = _stream_of(dev, stream)
+    # copies, outputs and the workspace are made on the stream the kernels run on
+    with context:
+        dB, dbs = _head_rows_out(dB, B, "dB")
+        dC, dcs = _head_rows_out(dC, C, "dC")
+        dB_out, bo = _head_rows_in(dB_out)
+        dC_out, co = _head_rows_in(dC_out)
+        B, bs = _head_rows_in(B)
+        C, cs = _head_rows_in(C)
+        pos, freqs = _rotation(positions, freqs, sizes[4])
+        bw = cw = dbw = dcw = ws = None
+        n = 0
+        if B_weight is not None:
+            bw = B_weight.contiguous()
+            dbw = bw.new_empty(sizes[3])
+        if C_weight is not None:
+            cw = C_weight.contiguous()
+            dcw = cw.new_empty(sizes[3])
+        if dbw is not None or dcw is not None:
+            n = _bc_norm_backward_bytes(*sizes)
+            ws = B.new_empty(n, dtype=torch.uint8) if n else None
+        _check(load().ssd_bc_norm_backward(
+            BcNormProblem(bs, cs, bo, co, dbs, dcs, *sizes), dB_out.data_ptr(),
+            dC_out.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(bw), _addr(cw), _addr(pos),
+            _addr(freqs), dB.data_ptr(), dC.data_ptr(), _addr(dbw), _addr(dcw), _addr(ws), n,
+            handle), "ssd_bc_norm_backward")
+    return dict(dB=dB, dC=dC, dB_weight=dbw, dC_weight=dcw)

@@ -1,0 +1,527 @@
+// k_delta_f32.hip -- the gated delta rule's chunks in fp32 arithmetic
+// (delta.h has the formulas): the walk over a sequence's chunks, the same
+// walk backwards, and the gradients of each chunk.
+//
+// The columns of the state (one per value channel) never mix, so a wave takes
+// 16 of them through all chunks with the state in registers: S is a stack of
+// 16 x 16 result tiles (rows: state channels n), and every product of the walk
+// contracts over the rows of tiles that the wave holds already (S, R, U),
+// which makes them right operands as they are. The left operands, rows of K
+// and Q, are staged in LDS for the workgroup's waves; T and M come from
+// k_delta_prep through the caches. The bound is the fp32 matrix rate (1/16 of
+// the bf16 rate).
+#include "delta_tiles.h"
+
+namespace ssd {
+
+// Left operand from staged rows: K^T (row n0 + lr, tokens t0 + 4 lg + r).
+template <int W>
+__device__ __forceinline__ f32x4 column_operand(const float *rows, int t0, int n0) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const float *p = rows + (t0 + 4 * lg) * W + n0 + lr;
+  return f32x4{p[0], p[W], p[2 * W], p[3 * W]};
+}
+template <int W>
+__device__ __forceinline__ f32x4 row_operand(const float *rows, int t0, int n0) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  return ldf4(rows + (t0 + lr) * W + n0 + 4 * lg);
+}
+
+// 16 columns from p0 of 4 token rows (t0 + 4 lg + r), zeros past len.
+template <typename T>
+__device__ __forceinline__ f32x4 value_tile(const T *v, size_t ld, int t0, int len) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  f32x4 o;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int t = t0 + 4 * lg + r;
+    o[r] = t < len ? to_f32(v[t * ld + lr]) : 0.f;
+  }
+  return o;
+}
+
+// Forward (kStates false): y and the final state. For the backward pass
+// (kStates true): the state entering each chunk, as (P, N), and U.
+template <typename T, int NT, bool kStates>
+__global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
+  constexpr int W = 16 * NT + 4;
+  extern __shared__ float lds[];
+  float *sG = lds, *sB = lds + kDeltaChunk, *sK = lds + 2 * kDeltaChunk, *sQ = sK + kDeltaChunk * W;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int waves = blockDim.x >> 6, blocks = a.P / (16 * waves);
+  int unit = blockIdx.x;
+  const int p0 = ((unit % blocks) * waves + (threadIdx.x >> 6)) * 16;
+  unit /= blocks;
+  const int h = unit % a.H, seq = unit / a.H, grp = h / a.hpg;
+  int64_t lo, hi;
+  delta_seq(a, seq, lo, hi);
+  const int slot0 = delta_slot0(a, seq, lo);
+  const size_t srow = (((size_t)seq * a.H + h) * a.P + p0 + lr) * a.N + 4 * lg;
+
+  f32x4 S[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    S[n] = a.h0 && 16 * n < a.N ? ldf4(a.h0 + srow + 16 * n) : kZero4;
+
+  const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
+  int c = 0;
+  for (int64_t at = lo; at < hi; at += kDeltaChunk, ++c) {
+    const int len = (int)min((int64_t)kDeltaChunk, hi - at);
+    const size_t sh = (size_t)(slot0 + c) * a.H + h;
+    __syncthreads();
+    stage_rows_f32<W>(sK, (const T *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
+    if (!kStates) stage_rows_f32<W>(sQ, (const T *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
+    stage_gates<T>(sG, sB, a, at, h, len);
+    __syncthreads();
+    const float *tri = (const float *)a.tri + sh * ((kStates ? 3 : 2) * 4096);
+    const T *x = (const T *)a.x + ((size_t)at * a.H + h) * a.P + p0;
+
+    f32x4 R[4], O[4], U[4], e[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f32x4 ks = kZero4, qs = kZero4;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        ks = mfma16(row_operand<W>(sK, 16 * t, 16 * n), S[n], ks);
+        if (!kStates) qs = mfma16(row_operand<W>(sQ, 16 * t, 16 * n), S[n], qs);
+      }
+      const f32x4 gm = ldf4(sG + 16 * t + 4 * lg), b = ldf4(sB + 16 * t + 4 * lg);
+      const f32x4 v = value_tile<T>(x, ldx, 16 * t, len);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        e[t][r] = exp2_fast(gm[r]);
+        R[t][r] = b[r] * (v[r] - e[t][r] * ks[r]);
+        O[t][r] = e[t][r] * qs[r];
+      }
+    }
+    const float gc = sG[kDeltaChunk - 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      U[i] = kZero4;
+#pragma unroll
+      for (int j = 0; j <= i; ++j)
+        U[i] = mfma16(ldf4(tri + (16 * i + lr) * kDeltaChunk + 16 * j + 4 * lg), R[j], U[i]);
+    }
+    if (!kStates) {
+      T *y = (T *)a.y + ((size_t)at * a.H + h) * a.P + p0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j <= i; ++j)
+          O[i] = mfma16(ldf4(tri + 4096 + (16 * i + lr) * kDeltaChunk + 16 * j + 4 * lg), U[j], O[i]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * lg + r;
+          if (t < len) y[t * ldx + lr] = from_f32<T>(O[i][r]);
+        }
+      }
+    } else {
+      float *st = (float *)a.st0 + (sh * a.P + p0 + lr) * a.N + 4 * lg;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (16 * n < a.N) stf4(st + 16 * n, S[n]);
+      float *u = (float *)a.u + sh * kDeltaChunk * a.P + p0 + lr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[(16 * i + 4 * lg + r) * a.P] = U[i][r];
+    }
+    const float ec = exp2_fast(gc);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const f32x4 gm = ldf4(sG + 16 * t + 4 * lg);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) U[t][r] *= exp2_fast(gc - gm[r]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      S[n] *= ec;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) S[n] = mfma16(column_operand<W>(sK, 16 * t, 16 * n), U[t], S[n]);
+    }
+  }
+  if (a.hT && !kStates) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (16 * n < a.N) stf4(a.hT + srow + 16 * n, S[n]);
+  }
+}
+
+// Backwards: dL/dS entering from behind each chunk, as (P, N), dL/dR, and the
+// gradient of the initial state.
+//   dU = M^T dY + e^{gam_c - gam} (K dS),  dR = T^T dU
+//   dS <- e^{gam_c} dS + Q^T (e^gam dY) - K^T (beta e^gam dR)
+template <typename T, int NT>
+__global__ __launch_bounds__(256) void k_delta_reverse_f32(DeltaArgs a) {
+  constexpr int W = 16 * NT + 4;
+  extern __shared__ float lds[];
+  float *sG = lds, *sB = lds + kDeltaChunk, *sK = lds + 2 * kDeltaChunk, *sQ = sK + kDeltaChunk * W;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int waves = blockDim.x >> 6, blocks = a.P / (16 * waves);
+  int unit = blockIdx.x;
+  const int p0 = ((unit % blocks) * waves + (threadIdx.x >> 6)) * 16;
+  unit /= blocks;
+  const int h = unit % a.H, seq = unit / a.H, grp = h / a.hpg;
+  int64_t lo, hi;
+  delta_seq(a, seq, lo, hi);
+  const int slot0 = delta_slot0(a, seq, lo);
+  const size_t srow = (((size_t)seq * a.H + h) * a.P + p0 + lr) * a.N + 4 * lg;
+
+  f32x4 S[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    S[n] = a.dhT && 16 * n < a.N ? ldf4(a.dhT + srow + 16 * n) : kZero4;
+
+  const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
+  const int chunks = (int)((hi - lo + kDeltaChunk - 1) / kDeltaChunk);
+  for (int c = chunks - 1; c >= 0; --c) {
+    const int64_t at = lo + (int64_t)c * kDeltaChunk;
+    const int len = (int)min((int64_t)kDeltaChunk, hi - at);
+    const size_t sh = (size_t)(slot0 + c) * a.H + h;
+    __syncthreads();
+    stage_rows_f32<W>(sK, (const T *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
+    stage_rows_f32<W>(sQ, (const T *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
+    stage_gates<T>(sG, sB, a, at, h, len);
+    __syncthreads();
+    const float *tri = (const float *)a.tri + sh * (3 * 4096);
+    const T *dy = (const T *)a.dy + ((size_t)at * a.H + h) * a.P + p0;
+    const float gc = sG[kDeltaChunk - 1];
+
+    float *st = (float *)a.st1 + (sh * a.P + p0 + lr) * a.N + 4 * lg;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (16 * n < a.N) stf4(st + 16 * n, S[n]);
+
+    f32x4 Y[4], U[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      Y[t] = value_tile<T>(dy, ldx, 16 * t, len);
+      f32x4 ks = kZero4;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) ks = mfma16(row_operand<W>(sK, 16 * t, 16 * n), S[n], ks);
+      const f32x4 gm = ldf4(sG + 16 * t + 4 * lg);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) U[t][r] = exp2_fast(gc - gm[r]) * ks[r];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = j; i < 4; ++i)
+        U[j] = mfma16(ldf4(tri + 8192 + (16 * j + lr) * kDeltaChunk + 16 * i + 4 * lg), Y[i], U[j]);
+    f32x4 R[4];
+    float *dr = (float *)a.dr + sh * kDeltaChunk * a.P + p0 + lr;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      R[j] = kZero4;
+#pragma unroll
+      for (int i = j; i < 4; ++i)
+        R[j] = mfma16(ldf4(tri + 4096 + (16 * j + lr) * kDeltaChunk + 16 * i + 4 * lg), U[i], R[j]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dr[(16 * j + 4 * lg + r) * a.P] = R[j][r];
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const f32x4 gm = ldf4(sG + 16 * t + 4 * lg), b = ldf4(sB + 16 * t + 4 * lg);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float e = exp2_fast(gm[r]);
+        Y[t][r] *= e;
+        R[t][r] *= -b[r] * e;
+      }
+    }
+    const float ec = exp2_fast(gc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      S[n] *= ec;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        S[n] = mfma16(column_operand<W>(sQ, 16 * t, 16 * n), Y[t], S[n]);
+        S[n] = mfma16(column_operand<W>(sK, 16 * t, 16 * n), R[t], S[n]);
+      }
+    }
+  }
+  if (a.dh0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (16 * n < a.N) stf4(a.dh0 + srow + 16 * n, S[n]);
+  }
+}
+
+// Sum over the 16 lanes that share lg (columns of a result tile).
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// The gradients of one (chunk, head), a wave per 16 tokens. With D the decay
+// factors e^{gam_i - gam_j}, dM = dY U^T (i >= j), dL = -dR U^T (i > j):
+//   dx = beta dR
+//   dQ = e^gam dY S^T + (dM D) K
+//   dK = -beta e^gam dR S^T + e^{gam_c - gam} U dS^T + (dM D)^T Q + (dL beta D) K + (dL beta D)^T K
+//   dbeta = dR . V - e^gam K . (dR S^T) + sum_j dL (K K^T) D
+//   dg_t = sum_{i >= t} [e^gam Q . (dY S^T) - beta e^gam K . (dR S^T)]_i
+//        + sum_{i < t} [e^{gam_c - gam} K . (U dS^T)]_i
+//        + sum_{i >= t > j} (dM M + dL L)_ij + e^{gam_c} <S, dS>
+// The pair sum is taken as suffix sums of row sums less column sums of one
+// matrix, so that pairs on one side of t cancel to fp32 rounding.
+template <typename T>
+__global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
+  constexpr int W1 = kDeltaChunk + 4;
+  __shared__ float sG[kDeltaChunk], sB[kDeltaChunk];
+  __shared__ float sM[kDeltaChunk * W1], sL[kDeltaChunk * W1];  // dM D, dL beta D
+  __shared__ float sZ[kDeltaChunk], sP[kDeltaChunk], sC[4][kDeltaChunk], sS[4];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, w = threadIdx.x >> 6;
+  const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, grp = h / a.hpg;
+  int64_t start;
+  int len;
+  if (!delta_chunk(a, slot, start, len)) return;
+  const size_t sh = (size_t)slot * a.H + h;
+  const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
+  const T *K = (const T *)a.B + ((size_t)start * a.G + grp) * a.N;
+  const T *Q = (const T *)a.C + ((size_t)start * a.G + grp) * a.N;
+  const T *X = (const T *)a.x + ((size_t)start * a.H + h) * a.P;
+  const T *dY = (const T *)a.dy + ((size_t)start * a.H + h) * a.P;
+  const float *U = (const float *)a.u + sh * kDeltaChunk * a.P;
+  const float *dR = (const float *)a.dr + sh * kDeltaChunk * a.P;
+  const float *S0 = (const float *)a.st0 + sh * a.P * a.N;
+  const float *S1 = (const float *)a.st1 + sh * a.P * a.N;
+  stage_gates<T>(sG, sB, a, start, h, len);
+  for (int e = threadIdx.x; e < 4 * kDeltaChunk; e += 256) (&sC[0][0])[e] = 0.f;
+  __syncthreads();
+
+  const int ti = 16 * w + lr;                    // this lane's token as a row of a left operand
+  const int tr = min(ti, len - 1);
+  const bool live = ti < len;
+  const f32x4 gm = ldf4(sG + 16 * w + 4 * lg), bt = ldf4(sB + 16 * w + 4 * lg);
+  const float gi = sG[ti], bi = sB[ti], gc = sG[kDeltaChunk - 1];
+
+  // pairs: rows i of this wave's tile, columns j of tiles up to it (lane: row
+  // i, 4 columns j)
+  float rowsum = 0.f, betasum = 0.f;
+  for (int j = 0; j <= w; ++j) {
+    f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4;
+    const int tj = min(16 * j + lr, len - 1);
+    for (int n = 4 * lg; n < a.N; n += 16) {
+      const f32x4 kj = widen4(K + tj * ldk + n);
+      kk = mfma16(kj, widen4(K + tr * ldk + n), kk);
+      qk = mfma16(kj, widen4(Q + tr * ldk + n), qk);
+    }
+    for (int p = 4 * lg; p < a.P; p += 16) {
+      const f32x4 u = ldf4(U + (16 * j + lr) * a.P + p);
+      const f32x4 y = widen4(dY + tr * ldx + p);
+      dm = mfma16(u, live ? y : kZero4, dm);
+      dl = mfma16(u, ldf4(dR + ti * a.P + p), dl);
+    }
+    const f32x4 gj = ldf4(sG + 16 * j + 4 * lg);
+    f32x4 m, l, both;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int d = ti - (16 * j + 4 * lg + r);
+      const float e = d >= 0 ? exp2_fast(gi - gj[r]) : 0.f;
+      m[r] = d >= 0 ? dm[r] * e : 0.f;
+      const float lk = d > 0 ? -dl[r] * e : 0.f;
+      l[r] = lk * bi;
+      betasum += lk * kk[r];
+      both[r] = m[r] * qk[r] + l[r] * kk[r];
+      rowsum += both[r];
+    }
+    stf4(sM + ti * W1 + 16 * j + 4 * lg, m);
+    stf4(sL + ti * W1 + 16 * j + 4 * lg, l);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float cs = sum16(both[r]);
+      if (lr == 0) sC[w][16 * j + 4 * lg + r] = cs;
+    }
+  }
+  rowsum += __shfl_xor(rowsum, 16);
+  rowsum += __shfl_xor(rowsum, 32);
+  betasum += __shfl_xor(betasum, 16);
+  betasum += __shfl_xor(betasum, 32);
+
+  // dx, and dR . V
+  float rv = 0.f;
+  for (int p = 4 * lg; p < a.P; p += 16) {
+    const f32x4 r = ldf4(dR + ti * a.P + p), v = widen4(X + tr * ldx + p);
+    T *dx = (T *)a.dx + ((size_t)(start + tr) * a.H + h) * a.P + p;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (live) {
+        rv += r[q] * v[q];
+        dx[q] = from_f32<T>(bi * r[q]);
+      }
+    }
+  }
+  rv += __shfl_xor(rv, 16);
+  rv += __shfl_xor(rv, 32);
+  __syncthreads();
+
+  // dQ, dK of this wave's tokens, 16 state channels at a time (result tiles:
+  // lane: channel n, 4 tokens)
+  f32x4 za = kZero4, zb = kZero4, zk = kZero4;
+  float ss = 0.f;
+  float *dKo = a.part + (size_t)h * a.N, *dQo = dKo + (size_t)a.T * a.H * a.N;
+  for (int n0 = 0; n0 < a.N; n0 += 16) {
+    f32x4 ys = kZero4, rs = kZero4, us = kZero4;
+    for (int p = 4 * lg; p < a.P; p += 16) {
+      f32x4 s0, s1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s0[r] = S0[(size_t)(p + r) * a.N + n0 + lr];
+        s1[r] = S1[(size_t)(p + r) * a.N + n0 + lr];
+        if (w == (n0 >> 4) % 4) ss += s0[r] * s1[r];
+      }
+      const f32x4 y = widen4(dY + tr * ldx + p);
+      ys = mfma16(live ? y : kZero4, s0, ys);
+      rs = mfma16(ldf4(dR + ti * a.P + p), s0, rs);
+      us = mfma16(ldf4(U + ti * a.P + p), s1, us);
+    }
+    f32x4 k, q, dq, dk;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = min(16 * w + 4 * lg + r, len - 1);
+      k[r] = to_f32(K[t * ldk + n0 + lr]);
+      q[r] = to_f32(Q[t * ldk + n0 + lr]);
+      const float e = exp2_fast(gm[r]);
+      dq[r] = e * ys[r];
+      const float rk = -e * rs[r], uk = exp2_fast(gc - gm[r]) * us[r];
+      dk[r] = bt[r] * rk + uk;
+      za[r] += q[r] * dq[r] + bt[r] * k[r] * rk;
+      zk[r] += k[r] * rk;
+      zb[r] += k[r] * uk;
+    }
+    for (int j = 0; j < 4; ++j) {
+      // columns n of K and Q rows of tile j as right operands
+      f32x4 kj, qj;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = min(16 * j + 4 * lg + r, len - 1);
+        kj[r] = to_f32(K[t * ldk + n0 + lr]);
+        qj[r] = to_f32(Q[t * ldk + n0 + lr]);
+      }
+      if (j <= w) {
+        dq = mfma16(ldf4(sM + ti * W1 + 16 * j + 4 * lg), kj, dq);
+        dk = mfma16(ldf4(sL + ti * W1 + 16 * j + 4 * lg), kj, dk);
+      }
+      if (j >= w) {
+        f32x4 mt, lt;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          mt[r] = sM[(16 * j + 4 * lg + r) * W1 + ti];
+          lt[r] = sL[(16 * j + 4 * lg + r) * W1 + ti];
+        }
+        dk = mfma16(mt, qj, dk);
+        dk = mfma16(lt, kj, dk);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * w + 4 * lg + r;
+      if (t < len) {
+        const size_t to = (size_t)(start + t) * a.H * a.N + n0 + lr;
+        dKo[to] = dk[r];
+        dQo[to] = dq[r];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    za[r] = sum16(za[r]);
+    zb[r] = sum16(zb[r]);
+    zk[r] = sum16(zk[r]);
+    if (lr == 0) {
+      sZ[16 * w + 4 * lg + r] = za[r];
+      sP[16 * w + 4 * lg + r] = zb[r];
+    }
+  }
+  // dbeta: rv and betasum are per row i (lanes lr), zk per row 4 lg + r
+  __shared__ float sK2[kDeltaChunk], sR[kDeltaChunk];
+  if (lr == 0)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sK2[16 * w + 4 * lg + r] = zk[r];
+  if (lg == 0) sR[ti] = rowsum;
+  ss = sum16(ss);
+  ss += __shfl_xor(ss, 16);
+  ss += __shfl_xor(ss, 32);
+  if (lane == 0) sS[w] = ss;
+  __syncthreads();
+  if (lg == 0 && live)
+    ((T *)a.dbeta)[(size_t)(start + ti) * a.H + h] = from_f32<T>(rv + betasum + sK2[ti]);
+  if (w == 0) {
+    const float zed = sZ[lane] + sR[lane] -
+                      (sC[0][lane] + sC[1][lane] + sC[2][lane] + sC[3][lane]);
+    const float zp = sP[lane];
+    const float pre = wave_inclusive_sum(zed), all = __shfl(pre, 63);
+    const float prefix = wave_inclusive_sum(zp) - zp;
+    const float ends = exp2_fast(sG[kDeltaChunk - 1]) * (sS[0] + sS[1] + sS[2] + sS[3]);
+    if (lane < len)
+      ((T *)a.dg)[(size_t)(start + lane) * a.H + h] =
+          from_f32<T>(all - (pre - zed) + prefix + ends);
+  }
+}
+
+// dB, dC of a group: the sum over its heads, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_delta_heads_sum(const float *part, T *dB, T *dC, int64_t n4,
+                                                         int N4, int G, int hpg, int64_t all4) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * n4) return;
+  const bool q = i >= n4;
+  const int64_t e = q ? i - n4 : i;
+  const int64_t row = e / N4;                    // token * G + group
+  const f32x4 *p = reinterpret_cast<const f32x4 *>(part) + (q ? all4 : 0) + row * hpg * N4 + e % N4;
+  f32x4 v = kZero4;
+  for (int k = 0; k < hpg; ++k) v += p[(int64_t)k * N4];
+  T *to = (q ? dC : dB) + 4 * e;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) to[r] = from_f32<T>(v[r]);
+}
+
+template <typename T, int NT>
+hipError_t chain_f32(const DeltaArgs &a, int what, hipStream_t s) {
+  constexpr int W = 16 * NT + 4;
+  const int waves = min(4, a.P / 16);
+  const dim3 grid((unsigned)((int64_t)a.nseq * a.H * (a.P / (16 * waves)))), block(64 * waves);
+  const size_t lds = (2 * kDeltaChunk + (what == 1 ? 1 : 2) * kDeltaChunk * W) * sizeof(float);
+  const void *f = what == 0   ? (const void *)k_delta_chain_f32<T, NT, false>
+                  : what == 1 ? (const void *)k_delta_chain_f32<T, NT, true>
+                              : (const void *)k_delta_reverse_f32<T, NT>;
+  if (hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
+    return e;
+  DeltaArgs b = a;
+  void *args[] = {&b};
+  return hipLaunchKernel(f, grid, block, args, lds, s);
+}
+
+template <typename T>
+hipError_t chain_f32_n(const DeltaArgs &a, int what, hipStream_t s) {
+  if (a.nseq == 0) return hipSuccess;
+  if (a.N <= 64) return chain_f32<T, 4>(a, what, s);
+  if (a.N <= 128) return chain_f32<T, 8>(a, what, s);
+  return chain_f32<T, 16>(a, what, s);
+}
+
+hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool bf16_io, bool states, hipStream_t s) {
+  return bf16_io ? chain_f32_n<bf16>(a, states ? 1 : 0, s) : chain_f32_n<float>(a, states ? 1 : 0, s);
+}
+
+hipError_t launch_delta_reverse_f32(const DeltaArgs &a, bool bf16_io, hipStream_t s) {
+  return bf16_io ? chain_f32_n<bf16>(a, 2, s) : chain_f32_n<float>(a, 2, s);
+}
+
+template <typename T>
+hipError_t grad_f32(const DeltaArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL(k_delta_grad_f32<T>, dim3((unsigned)((int64_t)a.nslots * a.H)), dim3(256), 0,
+                     s, a);
+  const int64_t n4 = a.T * a.G * (a.N / 4);
+  hipLaunchKernelGGL(k_delta_heads_sum<T>, dim3((unsigned)((2 * n4 + 255) / 256)), dim3(256), 0, s,
+                     a.part, (T *)a.dB, (T *)a.dC, n4, a.N / 4, a.G, a.hpg, a.T * a.H * (a.N / 4));
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_grad_f32(const DeltaArgs &a, bool bf16_io, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  return bf16_io ? grad_f32<bf16>(a, s) : grad_f32<float>(a, s);
+}
+
+}  // namespace ssd
