@@ -35,12 +35,20 @@ struct DeltaArgs {
   float *dh0;          // (S, H, P, N) or null
   // workspace, per (chunk slot, head)
   void *tri;           // triangular matrices, tri_bytes each
-  void *st0, *st1;     // backward: S and dL/dS at the chunk's start and end
-  void *u, *dr;        // backward: U and dL/dR, (64, P)
-  float *part;         // backward: per-head dK, dQ of fp32 calls, (2, T, H, N)
+  void *st0, *st1;     // backward: S and dL/dS at the chunk's start and end, (P, N)
+  void *u, *dr;        // backward: U and dL/dR, (64, P); on the bf16 path (P, 64)
+  float *part;         // backward: dK, dQ of parts of a group's heads, (2, T, G parts, N)
+  // workspace, per (segment, head)
+  float *span;         // rows (P + N, N): first its own state and then the one at
+                       // its start; and the columns of its transition
+  float *dspan;        // backward: (P, N), the same for dL/dS at its end
   int64_t T;           // tokens
   int32_t L, H, P, N, G, hpg;
   int32_t nseq, nc_per, nslots;
+  int32_t seg, nseg_per, nsegs;  // chunks of a segment (0: whole sequences), segments of a
+                       // dense sequence, segment slots
+  int32_t hparts;      // backward: parts a group's heads are taken in
+  int32_t tri_stride;  // bf16 path: elements of a (slot, head)'s triangular matrices
 };
 
 // Triangular matrices of a (slot, head): what the chunks' own products need.
@@ -73,21 +81,57 @@ __device__ __forceinline__ int delta_slot0(const DeltaArgs &a, int s, int64_t lo
   return a.cu ? (int)(lo / kDeltaChunk) + s : s * a.nc_per;
 }
 
+// The sequence that a unit (a chunk slot, or with `step` chunks a segment) of a
+// packed call belongs to: the last whose first unit is not past it.
+__device__ __forceinline__ int delta_owner(const DeltaArgs &a, int unit, int64_t step) {
+  int l = 0, r = a.nseq - 1;
+  while (l < r) {
+    const int m = (l + r + 1) / 2;
+    const int64_t lo = min(max((int64_t)a.cu[m], (int64_t)0), a.T);
+    if (lo / (kDeltaChunk * step) + m <= unit) l = m; else r = m - 1;
+  }
+  return l;
+}
+
+// What a walk over chunks covers: tokens [lo, hi) of sequence s, from chunk
+// slot `slot` on; all of a sequence, or one segment of it.
+struct DeltaWalk {
+  int64_t lo, hi;
+  int s, slot;
+  bool first, last;  // of its sequence
+};
+__device__ __forceinline__ bool delta_walk(const DeltaArgs &a, int unit, DeltaWalk &w) {
+  int k = 0;
+  if (!a.seg) {
+    w.s = unit;
+  } else if (!a.cu) {
+    w.s = unit / a.nseg_per;
+    k = unit - w.s * a.nseg_per;
+  } else {
+    w.s = delta_owner(a, unit, a.seg);
+    const int64_t lo = min(max((int64_t)a.cu[w.s], (int64_t)0), a.T);
+    k = unit - (int)(lo / (kDeltaChunk * (int64_t)a.seg)) - w.s;
+    if (k < 0) return false;
+  }
+  delta_seq(a, w.s, w.lo, w.hi);
+  w.slot = delta_slot0(a, w.s, w.lo);
+  w.first = k == 0;
+  w.last = true;
+  if (a.seg) {
+    const int64_t n = (int64_t)kDeltaChunk * a.seg, at = k * n;
+    if (k > 0 && at >= w.hi - w.lo) return false;
+    w.last = w.hi - w.lo <= at + n;
+    w.hi = min(w.hi, w.lo + at + n);
+    w.lo += at;
+    w.slot += k * a.seg;
+  }
+  return true;
+}
+
 // First token and length of the chunk in a slot; false if the slot has none.
 __device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int64_t &start,
                                             int &len) {
-  int s;
-  if (!a.cu) {
-    s = slot / a.nc_per;
-  } else {
-    int l = 0, r = a.nseq - 1;  // the last sequence whose first slot is not past this one
-    while (l < r) {
-      const int m = (l + r + 1) / 2;
-      const int64_t lo = min(max((int64_t)a.cu[m], (int64_t)0), a.T);
-      if (delta_slot0(a, m, lo) <= slot) l = m; else r = m - 1;
-    }
-    s = l;
-  }
+  const int s = a.cu ? delta_owner(a, slot, 1) : slot / a.nc_per;
   int64_t lo, hi;
   delta_seq(a, s, lo, hi);
   const int64_t at = (int64_t)(slot - delta_slot0(a, s, lo)) * kDeltaChunk;
@@ -97,13 +141,33 @@ __device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int64_
   return true;
 }
 
+// A workgroup's place in the order of units: workgroups go round-robin over the
+// eight XCDs, and each takes an eighth of the units in a row, so that heads that
+// read the same rows of B and C find them in one L2.
+__device__ __forceinline__ int xcd_unit() {
+  const int n = (int)gridDim.x, b = (int)blockIdx.x, q = n / 8, r = n % 8, x = b % 8;
+  return x * q + min(x, r) + b / 8;
+}
+
 // Bytes of one (slot, head)'s triangular matrices.
-size_t delta_tri_bytes(bool bf16_path, DeltaTri which);
+size_t delta_tri_bytes(bool tiles, DeltaTri which);
 
 hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16_io, DeltaTri which, hipStream_t s);
-hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool bf16_io, bool states, hipStream_t s);
-hipError_t launch_delta_reverse_f32(const DeltaArgs &a, bool bf16_io, hipStream_t s);
-hipError_t launch_delta_grad_f32(const DeltaArgs &a, bool bf16_io, hipStream_t s);
+// The bf16 path: segments (sets a.seg, a.nseg_per, a.nsegs), the forward call
+// (triangular matrices in place), and the backward call's steps.
+void delta_segments(DeltaArgs &a, bool packed);
+hipError_t launch_delta_forward(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_states(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_reverse(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_grad(const DeltaArgs &a, hipStream_t s);
+// Parts that a group's heads are taken in by the gradients (1: dB and dC are
+// written at once).
+int delta_grad_parts(const DeltaArgs &a);
+hipError_t launch_delta_heads_sum(const DeltaArgs &a, bool bf16_io, hipStream_t s);
+// The same in fp32.
+hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool states, hipStream_t s);
+hipError_t launch_delta_reverse_f32(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_grad_f32(const DeltaArgs &a, hipStream_t s);
 
 struct DeltaStepArgs {
   const void *x, *g, *beta, *B, *C;

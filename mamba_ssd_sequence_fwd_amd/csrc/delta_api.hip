@@ -55,7 +55,8 @@ ssd_status check_delta(const ssd_problem *p, bool step, ssd::DeltaArgs *a) {
                                                                              : p->dstate) / 4);
   if (T >= kMostTokens || slots > kMostBlocks || nseq > kMostBlocks ||
       slots * p->nheads > kMostBlocks || nseq * p->nheads * (p->headdim / 16) > kMostBlocks ||
-      elements > kMostBlocks * 256)
+      elements > kMostBlocks * 256 || (int64_t)p->ngroups * p->dstate > (1 << 24) ||
+      (int64_t)p->nheads * p->headdim > (1 << 24))
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences x %d heads too large for one "
                 "launch", (long long)T, (long long)nseq, p->nheads);
   a->T = T;
@@ -86,27 +87,54 @@ ssd_status check_workspace(const void *ws, size_t have, size_t need) {
   return SSD_OK;
 }
 
-size_t forward_bytes(const ssd::DeltaArgs &a, bool bf) {
-  return (size_t)a.nslots * a.H * ssd::delta_tri_bytes(bf, ssd::kTriForward);
-}
-
-// The backward pass's workspace; with a base, its parts are set.
-size_t backward_bytes(ssd::DeltaArgs *a, bool bf, void *ws) {
-  char *base = static_cast<char *>(ws);
+// Parts of a workspace in turn; with a base, their addresses.
+struct Carver {
+  char *base;
   size_t at = 0;
-  const auto take = [&](size_t n) {
+  void *take(size_t n) {
     void *p = base ? base + at : nullptr;
     at += padded(n);
     return p;
-  };
-  const size_t sh = (size_t)a->nslots * a->H;
-  a->tri = take(sh * ssd::delta_tri_bytes(bf, ssd::kTriBackward));
-  a->st0 = take(sh * a->P * a->N * sizeof(float));
-  a->st1 = take(sh * a->P * a->N * sizeof(float));
-  a->u = take(sh * ssd::kDeltaChunk * a->P * sizeof(float));
-  a->dr = take(sh * ssd::kDeltaChunk * a->P * sizeof(float));
-  a->part = static_cast<float *>(take(2 * (size_t)a->T * a->H * a->N * sizeof(float)));
-  return at;
+  }
+};
+
+// The forward pass's workspace; with a base, its parts are set.
+size_t forward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
+  const bool bf = p->dtype == SSD_DTYPE_BF16;
+  if (bf) ssd::delta_segments(*a, p->num_seqs > 0);
+  Carver c{static_cast<char *>(ws)};
+  const size_t tri = ssd::delta_tri_bytes(bf, ssd::kTriForward);
+  a->tri = c.take((size_t)a->nslots * a->H * tri);
+  a->tri_stride = (int32_t)(tri / 2);
+  if (a->seg)
+    a->span = static_cast<float *>(
+        c.take((size_t)a->nsegs * a->H * (a->P + a->N) * a->N * sizeof(float)));
+  return c.at;
+}
+
+// The backward pass's.
+size_t backward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
+  const bool bf = p->dtype == SSD_DTYPE_BF16;
+  const size_t es = bf ? 2 : sizeof(float), sh = (size_t)a->nslots * a->H;
+  if (bf) ssd::delta_segments(*a, p->num_seqs > 0);
+  a->hparts = bf ? ssd::delta_grad_parts(*a) : a->hpg;
+  Carver c{static_cast<char *>(ws)};
+  const size_t tri = ssd::delta_tri_bytes(bf, ssd::kTriBackward);
+  a->tri = c.take(sh * tri);
+  a->tri_stride = (int32_t)(tri / 2);
+  a->st0 = c.take(sh * a->P * a->N * es);
+  a->st1 = c.take(sh * a->P * a->N * es);
+  a->u = c.take(sh * ssd::kDeltaChunk * a->P * es);
+  a->dr = c.take(sh * ssd::kDeltaChunk * a->P * es);
+  if (!bf || a->hparts > 1)
+    a->part = static_cast<float *>(
+        c.take(2 * (size_t)a->T * a->G * a->hparts * a->N * sizeof(float)));
+  if (a->seg) {
+    const size_t seg = (size_t)a->nsegs * a->H * a->N * sizeof(float);
+    a->span = static_cast<float *>(c.take(seg * (a->P + a->N)));
+    a->dspan = static_cast<float *>(c.take(seg * a->P));
+  }
+  return c.at;
 }
 
 ssd_status hip_result(hipError_t e, const char *what) {
@@ -186,7 +214,7 @@ ssd_status ssd_delta_workspace_size(const ssd_problem *p, size_t *bytes) {
   ssd_status st = check_delta(p, false, &a);
   if (st != SSD_OK) return st;
   if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = forward_bytes(a, p->dtype == SSD_DTYPE_BF16);
+  *bytes = forward_bytes(&a, p, nullptr);
   return SSD_OK;
 }
 
@@ -205,7 +233,8 @@ ssd_status ssd_delta_forward(const ssd_problem *p, const void *x, const void *g,
       !aligned16(initial_state) || !aligned16(final_state))
     return fail(SSD_ERR_INVALID_ARG, "x, B, C, y and the states must be 16-byte aligned");
   const bool bf = p->dtype == SSD_DTYPE_BF16;
-  if ((st = check_workspace(workspace, workspace_bytes, forward_bytes(a, bf))) != SSD_OK) return st;
+  const size_t need = forward_bytes(&a, p, workspace);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != SSD_OK) return st;
   a.x = x;
   a.g = g;
   a.beta = beta;
@@ -215,12 +244,12 @@ ssd_status ssd_delta_forward(const ssd_problem *p, const void *x, const void *g,
   a.cu = p->num_seqs > 0 ? cu_seqlens : nullptr;
   a.y = y;
   a.hT = final_state;
-  a.tri = workspace;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = hip_result(ssd::launch_delta_prep(a, bf, ssd::kTriForward, s), "delta rule prep")) !=
       SSD_OK)
     return st;
-  return hip_result(ssd::launch_delta_chain_f32(a, bf, false, s), "delta rule");
+  return hip_result(bf ? ssd::launch_delta_forward(a, s)
+                       : ssd::launch_delta_chain_f32(a, false, s), "delta rule");
 }
 
 ssd_status ssd_delta_step(const ssd_problem *p, const void *x, const void *g, const void *beta,
@@ -258,7 +287,7 @@ ssd_status ssd_delta_backward_workspace_size(const ssd_problem *p, size_t *bytes
   ssd_status st = check_delta(p, false, &a);
   if (st != SSD_OK) return st;
   if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = backward_bytes(&a, p->dtype == SSD_DTYPE_BF16, nullptr);
+  *bytes = backward_bytes(&a, p, nullptr);
   return SSD_OK;
 }
 
@@ -282,7 +311,7 @@ ssd_status ssd_delta_backward(const ssd_problem *p, const void *x, const void *g
     return fail(SSD_ERR_INVALID_ARG,
                 "x, B, C, dy, dx, dB, dC and the states must be 16-byte aligned");
   const bool bf = p->dtype == SSD_DTYPE_BF16;
-  const size_t need = backward_bytes(&a, bf, workspace);
+  const size_t need = backward_bytes(&a, p, workspace);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != SSD_OK) return st;
   a.x = x;
   a.g = g;
@@ -303,12 +332,15 @@ ssd_status ssd_delta_backward(const ssd_problem *p, const void *x, const void *g
   if ((st = hip_result(ssd::launch_delta_prep(a, bf, ssd::kTriBackward, s), "delta rule prep")) !=
       SSD_OK)
     return st;
-  if (a.T > 0 &&
-      (st = hip_result(ssd::launch_delta_chain_f32(a, bf, true, s), "delta rule states")) != SSD_OK)
+  if (a.T > 0 && (st = hip_result(bf ? ssd::launch_delta_states(a, s)
+                                     : ssd::launch_delta_chain_f32(a, true, s),
+                                  "delta rule states")) != SSD_OK)
     return st;
-  if ((st = hip_result(ssd::launch_delta_reverse_f32(a, bf, s), "delta rule reverse")) != SSD_OK)
+  if ((st = hip_result(bf ? ssd::launch_delta_reverse(a, s) : ssd::launch_delta_reverse_f32(a, s),
+                       "delta rule reverse")) != SSD_OK)
     return st;
-  return hip_result(ssd::launch_delta_grad_f32(a, bf, s), "delta rule gradients");
+  return hip_result(bf ? ssd::launch_delta_grad(a, s) : ssd::launch_delta_grad_f32(a, s),
+                    "delta rule gradients");
 }
 
 ssd_status ssd_bc_norm(const ssd_bc_norm_problem *p, const void *B, const void *C,

@@ -1,0 +1,689 @@
+// k_delta.hip -- the gated delta rule in bf16 (delta.h has the formulas): the
+// walks over a sequence's chunks, forwards and backwards, on the bf16 matrix
+// instructions.
+//
+// The state's columns (value channels) never mix, so a wave takes 16 of them
+// through all chunks with the state in fp32 result tiles and no exchange with
+// other waves: each product contracts over rows of tiles that the wave holds
+// (S, R, U), whose registers are right operands as they are, once rounded to
+// bf16. A result tile's rows stand for state channels
+// n = 32 ks + 8 (row / 4) + 4 par + row % 4, so that two tiles make an operand
+// with 8 channels in a row, as the rows of K and Q lie in LDS; R and U pair
+// tiles of 16 tokens, in which order k_delta_prep writes its matrices.
+//
+// Rounding. K, Q, V and dY are bf16 as they are. What enters a state is held in
+// two bf16 (the value, and what rounding left of it: 2^-17 off), so that the
+// fp32 states stay fp32: S in K S, R and T in T R (the three large products of
+// four), U in K^T U, and the same backwards. y is rounded to bf16 anyway: S
+// enters it whole, U and M once rounded.
+//
+// Segments. A walk's length is its chunks' latencies one after the other, and
+// few sequences and heads leave most of the card idle. Then each sequence is
+// cut: a first walk takes every segment at once from a state of zeros, together
+// with its transition (the N unit vectors walked through it, without values);
+// k_delta_join passes the states through the transitions; and the walk proper
+// starts every segment from its own state.
+#include "delta_tiles.h"
+
+namespace ssd {
+
+// 64 token rows of W columns (row stride ld, columns past n and rows past len
+// read as others of the tensor) into a swizzled LDS tile, asynchronously.
+template <int W, int WV>
+__device__ __forceinline__ void stage_async(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
+  constexpr int R = 512 / W, NI = kDeltaChunk / R;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane / (W / 8), pc = lane % (W / 8);
+  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
+  const char *base = reinterpret_cast<const char *>(src);
+#pragma unroll
+  for (int k = 0; k < (NI + WV - 1) / WV; ++k) {
+    const int m = wave + WV * k;
+    if (NI % WV != 0 && m >= NI) break;
+    const int s = m * R + rl;
+    const int c = min(pc ^ (s & kMask), n / 8 - 1);
+    const uint32_t off = (uint32_t)min(s, len - 1) * (uint32_t)(ld * 2) + 16u * (uint32_t)c;
+    __builtin_amdgcn_global_load_lds(base + off, (lds_void *)(tile + m * 512), 16, 0, 0);
+  }
+}
+// `n` KiB in a row.
+template <int WV>
+__device__ __forceinline__ void stage_block(bf16 *to, const void *src, int n) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const char *base = static_cast<const char *>(src);
+  for (int m = wave; m < n; m += WV)
+    __builtin_amdgcn_global_load_lds(base + m * 1024 + lane * 16, (lds_void *)(to + m * 512), 16, 0,
+                                     0);
+}
+
+// Staged values (64 tokens x W columns): 16 columns from c0 of tokens
+// t0 + 4 lg + r, as a result tile has them.
+template <int W>
+__device__ __forceinline__ f32x4 value_tile(const bf16 *v, int t0, int c0) {
+  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int row = t0 + 4 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
+  const bf16x4 w = ds_tr4(v, row * W + (((col >> 3) ^ (row & kMask)) << 3) + (col & 7));
+  return f32x4{(float)w[0], (float)w[1], (float)w[2], (float)w[3]};
+}
+
+__device__ __forceinline__ float bits_to_f32(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
+
+// Tables of a chunk, one entry a token: beta, beta e^gam, e^{gam_c - gam},
+// e^gam; zeros in the first two past the end. Filled by one wave.
+struct Gates {
+  float b[kDeltaChunk], be[kDeltaChunk], lf[kDeltaChunk], ef[kDeltaChunk];
+};
+__device__ __forceinline__ void fill_gates(Gates &G, float g, float beta, bool live) {
+  const int lane = threadIdx.x & 63;
+  const float gam = wave_inclusive_sum(live ? delta_log2_decay(g) : 0.f);
+  const float gc = __shfl(gam, 63), e = exp2_fast(gam);
+  G.b[lane] = live ? beta : 0.f;
+  G.be[lane] = live ? beta * e : 0.f;
+  G.lf[lane] = exp2_fast(gc - gam);
+  G.ef[lane] = e;
+}
+
+// Left operand K^T: rows n (as the state's tiles have them), tokens
+// 32 kt + 16 (e / 4) + 4 lg + e % 4.
+template <int N>
+__device__ __forceinline__ bf16x8 state_operand(const bf16 *rows, int kt, int ks, int par) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int row = 32 * kt + 4 * lg + (lr >> 2), col = 32 * ks + 8 * (lr & 3) + 4 * par;
+  const bf16x4 a = ds_tr4(rows, rswz<N>(row, col));
+  const bf16x4 b = ds_tr4(rows, rswz<N>(row + 16, col));
+  return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// The two operands (values 32 kt + 16 (e / 4) + 4 lg + e % 4) of staged values
+// as they are.
+template <int W>
+__device__ __forceinline__ bf16x8 value_operand(const bf16 *v, int kt, int c0) {
+  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int row = 32 * kt + 4 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
+  const int at = row * W + (((col >> 3) ^ (row & kMask)) << 3) + (col & 7);
+  const bf16x4 a = ds_tr4(v, at), b = ds_tr4(v, at + 16 * W);  // (16 rows on: the same swizzle)
+  return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// What a walk writes.
+enum WalkMode : int {
+  kWalkY = 0,      // y, and the final state
+  kWalkSave = 1,   // backward pass: the state entering each chunk, and U
+  kWalkLocal = 2   // a segment's own final state and its transition's columns
+};
+
+// Three workgroups of four waves to a compute unit: 168 registers and 53 KB of
+// LDS each, which is why M's tiles come straight from the cache.
+template <int NK, int WV, bool kPad, WalkMode kMode>
+__global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(DeltaArgs a) {
+  constexpr int N = 32 * NK, W = 16 * WV;  // state channels, the workgroup's columns
+  constexpr bool kY = kMode == kWalkY, kLocal = kMode == kWalkLocal;
+  constexpr int kT = 2 * kTriTiles * kTileElems;
+  // One array for each of what is staged: the compiler then sees which reads do
+  // not meet the loads under way, and does not wait for those.
+  __shared__ bf16 sK[kDeltaChunk * N], sQ[kY ? kDeltaChunk * N : 8], sT[kT], sV[kDeltaChunk * W];
+  __shared__ Gates G;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wave = threadIdx.x >> 6;
+  const int tiles = (kLocal ? a.P + a.N : a.P) / 16, blocks = (tiles + WV - 1) / WV;
+  int unit = xcd_unit();
+  const int tile0 = (unit % blocks) * WV, tile = min(tile0 + wave, tiles - 1);
+  const bool on = tile0 + wave < tiles;     // (a wave past the last tile repeats it)
+  unit /= blocks;
+  const int h = unit % a.H, sg = unit / a.H, grp = h / a.hpg;
+  DeltaWalk w;
+  if (!delta_walk(a, sg, w)) return;
+  if (kLocal && w.last && !a.dspan) return;  // forward, nothing starts from its end
+  const int p0 = 16 * tile, p = p0 + lr;
+  const bool valued = !kLocal || tile0 * 16 < a.P;  // (P / 16 is a multiple of WV)
+
+  f32x4 S[NK][2];
+  {
+    const float *from = nullptr;
+    if (!kLocal && a.seg)
+      from = a.span + (((size_t)sg * a.H + h) * (a.P + a.N) + p) * a.N;
+    else if (!kLocal && a.h0)
+      from = a.h0 + (((size_t)w.s * a.H + h) * a.P + p) * a.N;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const int n = 32 * ks + 8 * lg + 4 * par;
+        S[ks][par] = from && n < a.N ? ldf4(from + n) : kZero4;
+        if (kLocal)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[ks][par][r] = n + r == p - a.P ? 1.f : 0.f;
+      }
+  }
+
+  const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
+  const int chunks = (int)((w.hi - w.lo + kDeltaChunk - 1) / kDeltaChunk);
+  const auto length = [&](int c) {
+    return (int)min((int64_t)kDeltaChunk, w.hi - w.lo - (int64_t)c * kDeltaChunk);
+  };
+  const auto rows_at = [&](int c) { return (w.lo + (int64_t)c * kDeltaChunk); };
+  const auto tri_at = [&](int c) {
+    return (const bf16 *)a.tri + ((size_t)(w.slot + c) * a.H + h) * a.tri_stride;
+  };
+  uint16_t g = 0, bt = 0;  // (bits: a conversion here would wait for the loads)
+  const auto fetch_keys = [&](int c) __attribute__((always_inline)) {
+    stage_async<N, WV>(sK, (const bf16 *)a.B + (rows_at(c) * a.G + grp) * a.N, ldk, a.N, length(c));
+  };
+  const auto fetch_rest = [&](int c) __attribute__((always_inline)) {
+    const int64_t at = rows_at(c);
+    const int len = length(c);
+    if (wave == 0) {
+      const size_t ga = (size_t)(at + min(lane, len - 1)) * a.H + h;
+      g = ((const uint16_t *)a.g)[ga];
+      bt = ((const uint16_t *)a.beta)[ga];
+    }
+    if (kY)
+      stage_async<N, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
+    if (valued)
+      stage_async<W, WV>(sV, (const bf16 *)a.x + ((size_t)at * a.H + h) * a.P + 16 * tile0, ldx, W,
+                         len);
+    stage_block<WV>(sT, tri_at(c), 2 * kTriTiles);
+  };
+  if (chunks > 0) {
+    fetch_keys(0);
+    fetch_rest(0);
+  }
+  for (int c = 0; c < chunks; ++c) {
+    const int64_t at = rows_at(c);
+    const int len = length(c);
+    wait_vmem_all();
+    if (wave == 0) fill_gates(G, bits_to_f32(g), bits_to_f32(bt), lane < len);
+    __syncthreads();
+    bf16x8 M[kTriTiles];
+    if (kY) {
+      const bf16 *m = tri_at(c) + kT + 8 * lane;
+#pragma unroll
+      for (int k = 0; k < kTriTiles; ++k) M[k] = ldg8(m + k * kTileElems);
+    }
+
+    // K S, and Q S transposed (lane: token lr of its tile, rows p)
+    f32x4 A[4], O[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) A[t] = O[t] = kZero4;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      const Split s = split8(S[ks][0], S[ks][1]);
+      if (kMode == kWalkSave && 32 * ks + 8 * lg < a.N)
+        *reinterpret_cast<bf16x8 *>((bf16 *)a.st0 +
+                                    (((size_t)(w.slot + c) * a.H + h) * a.P + p) * a.N + 32 * ks +
+                                    8 * lg) = s.hi;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int e = rswz<N>(16 * t + lr, 32 * ks + 8 * lg);
+        const bf16x8 k = *reinterpret_cast<const bf16x8 *>(sK + e);
+        A[t] = mfma(k, s.hi, A[t]);
+        A[t] = mfma(k, s.lo, A[t]);
+        if (kY) {
+          const bf16x8 q = *reinterpret_cast<const bf16x8 *>(sQ + e);
+          O[t] = mfma(s.hi, q, O[t]);
+          O[t] = mfma(s.lo, q, O[t]);
+        }
+      }
+    }
+    // R, as operands
+    Split R[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      f32x4 v[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = 2 * kt + u;
+        const f32x4 b = ldf4(G.b + 16 * t + 4 * lg), be = ldf4(G.be + 16 * t + 4 * lg);
+        v[u] = -be * A[t];
+        if (valued) v[u] += b * value_tile<W>(sV, 16 * t, p0 - 16 * tile0);
+      }
+      R[kt] = split8(v[0], v[1]);
+    }
+    // U = T R
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      A[i] = kZero4;
+#pragma unroll
+      for (int kt = 0; kt <= i / 2; ++kt) {
+        const bf16 *t = sT + (lower_tile(i, kt) * 2) * kTileElems + 8 * lane;
+        const bf16x8 th = lower_operand(*reinterpret_cast<const bf16x8 *>(t), i, kt);
+        const bf16x8 tl = lower_operand(*reinterpret_cast<const bf16x8 *>(t + kTileElems), i, kt);
+        A[i] = mfma(th, R[kt].hi, A[i]);
+        A[i] = mfma(th, R[kt].lo, A[i]);
+        A[i] = mfma(tl, R[kt].hi, A[i]);
+      }
+    }
+    if (c + 1 < chunks) {
+      __syncthreads();
+      fetch_rest(c + 1);
+    }
+    const float ec = G.ef[kDeltaChunk - 1];
+    bf16x8 U[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) U[kt] = pack8(A[2 * kt], A[2 * kt + 1]);
+    if (kY) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        O[t] *= G.ef[16 * t + lr];
+#pragma unroll
+        for (int kt = 0; kt <= t / 2; ++kt)
+          O[t] = mfma(U[kt], lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
+      }
+    }
+    // the state: rows of U fall by e^{gam_c - gam}
+    Split D[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+      D[kt] = split8(A[2 * kt] * ldf4(G.lf + 32 * kt + 4 * lg),
+                     A[2 * kt + 1] * ldf4(G.lf + 32 * kt + 16 + 4 * lg));
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        S[ks][par] *= ec;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          const bf16x8 k = state_operand<N>(sK, kt, ks, par);
+          S[ks][par] = mfma(k, D[kt].hi, S[ks][par]);
+          S[ks][par] = mfma(k, D[kt].lo, S[ks][par]);
+        }
+        if (kPad && 32 * ks + 8 * lg >= a.N)  // columns past N were staged from others
+          S[ks][par] = kZero4;
+      }
+    if (kY) {
+      bf16 *y = (bf16 *)a.y + ((size_t)at * a.H + h) * a.P + p0 + 4 * lg;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (16 * t + lr < len)
+          *reinterpret_cast<uint2 *>(y + (size_t)(16 * t + lr) * ldx) =
+              make_uint2(pack2(O[t][0], O[t][1]), pack2(O[t][2], O[t][3]));
+    } else if (!kLocal) {
+      bf16 *u = (bf16 *)a.u + (((size_t)(w.slot + c) * a.H + h) * a.P + p) * kDeltaChunk + 4 * lg;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const u32x4 v = __builtin_bit_cast(u32x4, U[kt]);
+        *reinterpret_cast<uint2 *>(u + 32 * kt) = make_uint2(v[0], v[1]);
+        *reinterpret_cast<uint2 *>(u + 32 * kt + 16) = make_uint2(v[2], v[3]);
+      }
+    }
+    if (c + 1 < chunks) {
+      __syncthreads();
+      fetch_keys(c + 1);
+    }
+  }
+  float *to = nullptr;
+  if (kLocal && on)
+    to = a.span + (((size_t)sg * a.H + h) * (a.P + a.N) + p) * a.N;
+  else if (kY && a.hT && w.last)
+    to = a.hT + (((size_t)w.s * a.H + h) * a.P + p) * a.N;
+  if (to)
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const int n = 32 * ks + 8 * lg + 4 * par;
+        if (n < a.N) stf4(to + n, S[ks][par]);
+      }
+}
+
+// Backwards, from the last chunk to the first:
+//   dU = M^T dY + e^{gam_c - gam} (K dS),  dR = T^T dU
+//   dS <- e^{gam_c} dS + Q^T (e^gam dY) - K^T (beta e^gam dR)
+// Writes dS behind each chunk, dR, and the initial state's gradient; or
+// (kLocal) a segment's dS at its start from zeros at its end.
+template <int NK, int WV, bool kPad, bool kLocal>
+__global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(DeltaArgs a) {
+  constexpr int N = 32 * NK, W = 16 * WV;
+  constexpr int kT = 2 * kTriTiles * kTileElems;
+  __shared__ bf16 sK[kDeltaChunk * N], sQ[kDeltaChunk * N], sT[kT], sV[kDeltaChunk * W];
+  __shared__ Gates G;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wave = threadIdx.x >> 6;
+  const int blocks = a.P / W;
+  int unit = xcd_unit();
+  const int pw = (unit % blocks) * W, p0 = pw + 16 * wave, p = p0 + lr;
+  unit /= blocks;
+  const int h = unit % a.H, sg = unit / a.H, grp = h / a.hpg;
+  DeltaWalk w;
+  if (!delta_walk(a, sg, w)) return;
+  if (kLocal && w.first) return;            // nothing ends at its start
+
+  f32x4 S[NK][2];
+  {
+    const float *from = nullptr;
+    if (!kLocal && a.seg)
+      from = a.dspan + (((size_t)sg * a.H + h) * a.P + p) * a.N;
+    else if (!kLocal && a.dhT)
+      from = a.dhT + (((size_t)w.s * a.H + h) * a.P + p) * a.N;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const int n = 32 * ks + 8 * lg + 4 * par;
+        S[ks][par] = from && n < a.N ? ldf4(from + n) : kZero4;
+      }
+  }
+
+  const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
+  const int chunks = (int)((w.hi - w.lo + kDeltaChunk - 1) / kDeltaChunk);
+  const auto length = [&](int c) {
+    return (int)min((int64_t)kDeltaChunk, w.hi - w.lo - (int64_t)c * kDeltaChunk);
+  };
+  const auto rows_at = [&](int c) { return (w.lo + (int64_t)c * kDeltaChunk); };
+  const auto tri_at = [&](int c) {
+    return (const bf16 *)a.tri + ((size_t)(w.slot + c) * a.H + h) * a.tri_stride;
+  };
+  uint16_t g = 0, bt = 0;
+  const auto fetch_rows = [&](int c) __attribute__((always_inline)) {
+    const int64_t at = rows_at(c);
+    const int len = length(c);
+    stage_async<N, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
+    stage_async<N, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
+  };
+  const auto fetch_rest = [&](int c) __attribute__((always_inline)) {
+    const int64_t at = rows_at(c);
+    const int len = length(c);
+    if (wave == 0) {
+      const size_t ga = (size_t)(at + min(lane, len - 1)) * a.H + h;
+      g = ((const uint16_t *)a.g)[ga];
+      bt = ((const uint16_t *)a.beta)[ga];
+    }
+    stage_async<W, WV>(sV, (const bf16 *)a.dy + ((size_t)at * a.H + h) * a.P + pw, ldx, W, len);
+    stage_block<WV>(sT, tri_at(c) + kT, 2 * kTriTiles);
+  };
+  if (chunks > 0) {
+    fetch_rows(chunks - 1);
+    fetch_rest(chunks - 1);
+  }
+  for (int c = chunks - 1; c >= 0; --c) {
+    const int len = length(c);
+    wait_vmem_all();
+    if (wave == 0) fill_gates(G, bits_to_f32(g), bits_to_f32(bt), lane < len);
+    __syncthreads();
+    const bf16 *m = tri_at(c) + 2 * kT + 8 * lane;
+    bf16x8 Mh[kTriTiles], Ml[kTriTiles];
+#pragma unroll
+    for (int k = 0; k < kTriTiles; ++k) {
+      Mh[k] = ldg8(m + 2 * k * kTileElems);
+      Ml[k] = ldg8(m + (2 * k + 1) * kTileElems);
+    }
+    // dY as it is, rows past the end as zeros
+    bf16x8 Y[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      Y[kt] = value_operand<W>(sV, kt, p0 - pw);
+      if (len < kDeltaChunk)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (32 * kt + 16 * (e >> 2) + 4 * lg + (e & 3) >= len) Y[kt][e] = (bf16)0.f;
+    }
+    f32x4 A[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) A[t] = kZero4;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      const Split s = split8(S[ks][0], S[ks][1]);
+      if (!kLocal && 32 * ks + 8 * lg < a.N)
+        *reinterpret_cast<bf16x8 *>((bf16 *)a.st1 +
+                                    (((size_t)(w.slot + c) * a.H + h) * a.P + p) * a.N + 32 * ks +
+                                    8 * lg) = s.hi;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const bf16x8 k =
+            *reinterpret_cast<const bf16x8 *>(sK + rswz<N>(16 * t + lr, 32 * ks + 8 * lg));
+        A[t] = mfma(k, s.hi, A[t]);
+        A[t] = mfma(k, s.lo, A[t]);
+      }
+    }
+    Split U[2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
+#pragma unroll
+      for (int kt = t / 2; kt < 2; ++kt) {
+        const int k = upper_tile(t, kt);
+        A[t] = mfma(upper_operand(Mh[k], t, kt), Y[kt], A[t]);
+        A[t] = mfma(upper_operand(Ml[k], t, kt), Y[kt], A[t]);
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      A[t] = kZero4;
+#pragma unroll
+      for (int kt = t / 2; kt < 2; ++kt) {
+        const bf16 *q = sT + (upper_tile(t, kt) * 2) * kTileElems + 8 * lane;
+        const bf16x8 th = upper_operand(*reinterpret_cast<const bf16x8 *>(q), t, kt);
+        const bf16x8 tl = upper_operand(*reinterpret_cast<const bf16x8 *>(q + kTileElems), t, kt);
+        A[t] = mfma(th, U[kt].hi, A[t]);
+        A[t] = mfma(th, U[kt].lo, A[t]);
+        A[t] = mfma(tl, U[kt].hi, A[t]);
+      }
+    }
+    if (c > 0) {
+      __syncthreads();
+      fetch_rest(c - 1);
+    }
+    if (!kLocal) {
+      bf16 *dr = (bf16 *)a.dr + (((size_t)(w.slot + c) * a.H + h) * a.P + p) * kDeltaChunk + 4 * lg;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<uint2 *>(dr + 16 * t) =
+            make_uint2(pack2(A[t][0], A[t][1]), pack2(A[t][2], A[t][3]));
+    }
+    Split E[2], D[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      f32x4 e[2], d[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = 32 * kt + 16 * u + 4 * lg;
+        const f32x4 ef = ldf4(G.ef + t), be = ldf4(G.be + t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) e[u][r] = ef[r] * (float)Y[kt][4 * u + r];
+        d[u] = -be * A[2 * kt + u];
+      }
+      E[kt] = split8(e[0], e[1]);
+      D[kt] = split8(d[0], d[1]);
+    }
+    const float ec = G.ef[kDeltaChunk - 1];
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        S[ks][par] *= ec;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          const bf16x8 q = state_operand<N>(sQ, kt, ks, par);
+          S[ks][par] = mfma(q, E[kt].hi, S[ks][par]);
+          S[ks][par] = mfma(q, E[kt].lo, S[ks][par]);
+          const bf16x8 k = state_operand<N>(sK, kt, ks, par);
+          S[ks][par] = mfma(k, D[kt].hi, S[ks][par]);
+          S[ks][par] = mfma(k, D[kt].lo, S[ks][par]);
+        }
+        if (kPad && 32 * ks + 8 * lg >= a.N) S[ks][par] = kZero4;
+      }
+    if (c > 0) {
+      __syncthreads();
+      fetch_rows(c - 1);
+    }
+  }
+  float *to = nullptr;
+  if (kLocal)
+    to = a.dspan + (((size_t)sg * a.H + h) * a.P + p) * a.N;
+  else if (a.dh0 && w.first)
+    to = a.dh0 + (((size_t)w.s * a.H + h) * a.P + p) * a.N;
+  if (to)
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const int n = 32 * ks + 8 * lg + 4 * par;
+        if (n < a.N) stf4(to + n, S[ks][par]);
+      }
+}
+
+// The states at the segments' starts, in place of their own final states: with
+// F a segment's transition, S <- F S + (its own). kBack: dL/dS at the segments'
+// ends, dS <- F^T dS + (its own), from the last to the first. Per (sequence,
+// head) and 16 columns a workgroup; wave w holds the state channels of tiles
+// w, w + 4, ...; the state goes round through LDS, in fp32 throughout. `span`
+// has a transition's columns as rows: span[P + j][n] = F[n][j].
+template <bool kBack>
+__global__ __launch_bounds__(256) void k_delta_join(DeltaArgs a) {
+  constexpr int kMost = 4;  // tiles of a wave, N <= 256
+  __shared__ float sS[2][256][17];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wave = threadIdx.x >> 6;
+  const int blocks = a.P / 16, tiles = a.N / 16;
+  int unit = blockIdx.x;
+  const int p = (unit % blocks) * 16 + lr;
+  unit /= blocks;
+  const int h = unit % a.H, seq = unit / a.H;
+  int64_t lo, hi;
+  delta_seq(a, seq, lo, hi);
+  const int64_t len = (int64_t)kDeltaChunk * a.seg;
+  const int first = a.cu ? (int)(lo / len) + seq : seq * a.nseg_per;
+  const int n = max(1, (int)((hi - lo + len - 1) / len));
+  const float *init = kBack ? a.dhT : a.h0;
+  f32x4 S[kMost];
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int t = wave + 4 * k;
+    if (t >= tiles) break;
+    S[k] = init ? ldf4(init + (((size_t)seq * a.H + h) * a.P + p) * a.N + 16 * t + 4 * lg) : kZero4;
+  }
+  for (int c = 0; c < n; ++c) {
+    const int sg = first + (kBack ? n - 1 - c : c);
+    const size_t at = (size_t)sg * a.H + h;
+    float *own = kBack ? a.dspan + (at * a.P + p) * a.N : a.span + (at * (a.P + a.N) + p) * a.N;
+    const float *F = a.span + (at * (a.P + a.N) + a.P) * a.N;
+    float (*s)[17] = sS[c & 1];
+    f32x4 next[kMost];
+    const bool more = c + 1 < n;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int t = wave + 4 * k;
+      if (t >= tiles) break;
+      if (more) next[k] = ldf4(own + 16 * t + 4 * lg);
+      stf4(own + 16 * t + 4 * lg, S[k]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[16 * t + 4 * lg + r][lr] = S[k][r];
+    }
+    if (!more) break;
+    __syncthreads();
+    for (int j = 0; j < tiles; ++j) {
+      f32x4 b;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = s[16 * j + 4 * lg + r][lr];
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        const int t = wave + 4 * k;
+        if (t >= tiles) break;
+        f32x4 f;
+        if (kBack) {
+          f = ldf4(F + (size_t)(16 * t + lr) * a.N + 16 * j + 4 * lg);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) f[r] = F[(size_t)(16 * j + 4 * lg + r) * a.N + 16 * t + lr];
+        }
+        next[k] = mfma16(f, b, next[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) S[k] = next[k];
+  }
+}
+
+enum Walk : int { kY, kSave, kLocal, kBack, kBackLocal };
+
+template <int NK, int WV, bool kPad>
+hipError_t walk_launch(const DeltaArgs &a, Walk what, hipStream_t s) {
+  const int tiles = (what == kLocal ? a.P + a.N : a.P) / 16;
+  const int64_t units = (int64_t)(a.seg ? a.nsegs : a.nseq) * a.H;
+  const dim3 grid((unsigned)(units * ((tiles + WV - 1) / WV))), block(64 * WV);
+  switch (what) {
+    case kY: hipLaunchKernelGGL((k_delta_walk<NK, WV, kPad, kWalkY>), grid, block, 0, s, a); break;
+    case kSave:
+      hipLaunchKernelGGL((k_delta_walk<NK, WV, kPad, kWalkSave>), grid, block, 0, s, a);
+      break;
+    case kLocal:
+      hipLaunchKernelGGL((k_delta_walk<NK, WV, kPad, kWalkLocal>), grid, block, 0, s, a);
+      break;
+    case kBack:
+      hipLaunchKernelGGL((k_delta_back<NK, WV, kPad, false>), grid, block, 0, s, a);
+      break;
+    case kBackLocal:
+      hipLaunchKernelGGL((k_delta_back<NK, WV, kPad, true>), grid, block, 0, s, a);
+      break;
+  }
+  return hipGetLastError();
+}
+
+template <int NK>
+hipError_t walk_n(const DeltaArgs &a, Walk what, hipStream_t s) {
+  const bool pad = a.N != 32 * NK;
+  if (a.P == 16)
+    return pad ? walk_launch<NK, 1, true>(a, what, s) : walk_launch<NK, 1, false>(a, what, s);
+  if (a.P == 32)
+    return pad ? walk_launch<NK, 2, true>(a, what, s) : walk_launch<NK, 2, false>(a, what, s);
+  return pad ? walk_launch<NK, 4, true>(a, what, s) : walk_launch<NK, 4, false>(a, what, s);
+}
+
+hipError_t walk(const DeltaArgs &a, Walk what, hipStream_t s) {
+  if (a.nseq == 0) return hipSuccess;
+  if (a.N <= 64) return walk_n<2>(a, what, s);
+  if (a.N <= 128) return walk_n<4>(a, what, s);
+  return walk_n<8>(a, what, s);
+}
+
+hipError_t join(const DeltaArgs &a, bool back, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.nseq * a.H * (a.P / 16))), block(256);
+  if (back)
+    hipLaunchKernelGGL(k_delta_join<true>, grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL(k_delta_join<false>, grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+void delta_segments(DeltaArgs &a, bool packed) {
+  a.seg = a.nseg_per = a.nsegs = 0;
+  static const char *v = getenv("DELTA_SEG");
+  const int m = v ? atoi(v) : 0;
+  if (!m || a.T == 0) return;
+  a.seg = m;
+  a.nseg_per = (a.nc_per + m - 1) / m;
+  a.nsegs = packed ? (int)(a.T / ((int64_t)kDeltaChunk * m)) + a.nseq : a.nseq * a.nseg_per;
+}
+
+hipError_t launch_delta_forward(const DeltaArgs &a, hipStream_t s) {
+  if (a.seg) {
+    hipError_t e = walk(a, kLocal, s);
+    if (e == hipSuccess) e = join(a, false, s);
+    if (e != hipSuccess) return e;
+  }
+  return walk(a, kY, s);
+}
+
+hipError_t launch_delta_states(const DeltaArgs &a, hipStream_t s) {
+  if (a.seg) {
+    hipError_t e = walk(a, kLocal, s);
+    if (e == hipSuccess) e = join(a, false, s);
+    if (e != hipSuccess) return e;
+  }
+  return walk(a, kSave, s);
+}
+
+hipError_t launch_delta_reverse(const DeltaArgs &a, hipStream_t s) {
+  if (a.seg) {
+    hipError_t e = walk(a, kBackLocal, s);
+    if (e == hipSuccess) e = join(a, true, s);
+    if (e != hipSuccess) return e;
+  }
+  return walk(a, kBack, s);
+}
+
+}  // namespace ssd

@@ -460,18 +460,18 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   }
 }
 
-// dB, dC of a group: the sum over its heads, in order.
+// dB, dC of a group: the sum over the parts of its heads, in order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_delta_heads_sum(const float *part, T *dB, T *dC, int64_t n4,
-                                                         int N4, int G, int hpg, int64_t all4) {
+                                                         int N4, int parts, int64_t all4) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= 2 * n4) return;
   const bool q = i >= n4;
   const int64_t e = q ? i - n4 : i;
   const int64_t row = e / N4;                    // token * G + group
-  const f32x4 *p = reinterpret_cast<const f32x4 *>(part) + (q ? all4 : 0) + row * hpg * N4 + e % N4;
+  const f32x4 *p = reinterpret_cast<const f32x4 *>(part) + (q ? all4 : 0) + row * parts * N4 + e % N4;
   f32x4 v = kZero4;
-  for (int k = 0; k < hpg; ++k) v += p[(int64_t)k * N4];
+  for (int k = 0; k < parts; ++k) v += p[(int64_t)k * N4];
   T *to = (q ? dC : dB) + 4 * e;
 #pragma unroll
   for (int r = 0; r < 4; ++r) to[r] = from_f32<T>(v[r]);
@@ -501,27 +501,35 @@ hipError_t chain_f32_n(const DeltaArgs &a, int what, hipStream_t s) {
   return chain_f32<T, 16>(a, what, s);
 }
 
-hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool bf16_io, bool states, hipStream_t s) {
-  return bf16_io ? chain_f32_n<bf16>(a, states ? 1 : 0, s) : chain_f32_n<float>(a, states ? 1 : 0, s);
+hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool states, hipStream_t s) {
+  return chain_f32_n<float>(a, states ? 1 : 0, s);
 }
 
-hipError_t launch_delta_reverse_f32(const DeltaArgs &a, bool bf16_io, hipStream_t s) {
-  return bf16_io ? chain_f32_n<bf16>(a, 2, s) : chain_f32_n<float>(a, 2, s);
+hipError_t launch_delta_reverse_f32(const DeltaArgs &a, hipStream_t s) {
+  return chain_f32_n<float>(a, 2, s);
+}
+
+template <typename T>
+hipError_t heads_sum(const DeltaArgs &a, hipStream_t s) {
+  const int64_t n4 = a.T * a.G * (a.N / 4);
+  hipLaunchKernelGGL(k_delta_heads_sum<T>, dim3((unsigned)((2 * n4 + 255) / 256)), dim3(256), 0, s,
+                     a.part, (T *)a.dB, (T *)a.dC, n4, a.N / 4, a.hparts, n4 * a.hparts);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_heads_sum(const DeltaArgs &a, bool bf16_io, hipStream_t s) {
+  return bf16_io ? heads_sum<bf16>(a, s) : heads_sum<float>(a, s);
 }
 
 template <typename T>
 hipError_t grad_f32(const DeltaArgs &a, hipStream_t s) {
   hipLaunchKernelGGL(k_delta_grad_f32<T>, dim3((unsigned)((int64_t)a.nslots * a.H)), dim3(256), 0,
                      s, a);
-  const int64_t n4 = a.T * a.G * (a.N / 4);
-  hipLaunchKernelGGL(k_delta_heads_sum<T>, dim3((unsigned)((2 * n4 + 255) / 256)), dim3(256), 0, s,
-                     a.part, (T *)a.dB, (T *)a.dC, n4, a.N / 4, a.G, a.hpg, a.T * a.H * (a.N / 4));
-  return hipGetLastError();
+  return heads_sum<T>(a, s);
 }
 
-hipError_t launch_delta_grad_f32(const DeltaArgs &a, bool bf16_io, hipStream_t s) {
-  if (a.T == 0) return hipSuccess;
-  return bf16_io ? grad_f32<bf16>(a, s) : grad_f32<float>(a, s);
+hipError_t launch_delta_grad_f32(const DeltaArgs &a, hipStream_t s) {
+  return a.T == 0 ? hipSuccess : grad_f32<float>(a, s);
 }
 
 }  // namespace ssd

@@ -1,0 +1,374 @@
+// k_delta_grad.hip -- the gradients of the gated delta rule's chunks in bf16.
+//
+// One workgroup takes a chunk and a part of the heads of one group, head by
+// head; wave w owns tokens 16 w .. 16 w + 15 and keeps their dQ and dK (fp32,
+// all state channels) in registers over the heads. With D the decay factors
+// e^{gam_i - gam_j}, dM = dY U^T (i >= j), dL = -dR U^T (i > j):
+//   dx = beta dR
+//   dQ = e^gam dY S^T + (dM D) K
+//   dK = -beta e^gam dR S^T + e^{gam_c - gam} U dS^T + (dM D)^T Q + (dL beta D) K + (dL beta D)^T K
+//   dbeta = dR . V - e^gam K . (dR S^T) + sum_j dL (K K^T) D
+//   dg_t = sum_{i >= t} [e^gam Q . (dY S^T) - beta e^gam K . (dR S^T)]_i
+//        + sum_{i < t} [e^{gam_c - gam} K . (U dS^T)]_i
+//        + sum_{i >= t > j} (dM M + dL L)_ij + e^{gam_c} <S, dS>
+// Results are taken transposed (lane: token, 4 state channels), so that the
+// pair matrices' result tiles are right operands as they are: once as rows j of
+// a column i for dQ and (dL beta D) K, once as rows i of a column j for the
+// transposed products. The pair sum of dg is taken as suffix sums of row sums
+// less column sums of the same fp32 products, so that pairs on one side of t
+// cancel. All operands are bf16 (S, dS, U and dR come rounded from the walks);
+// every sum is fp32. The states pass through LDS 32 channels at a time, the next
+// block under way while one is used.
+#include "delta_tiles.h"
+
+namespace ssd {
+namespace {
+
+// Swizzled place of (row, col) in rows of W elements.
+template <int W>
+__device__ __forceinline__ int place(int row, int col) {
+  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
+  return row * W + (((col >> 3) ^ (row & kMask)) << 3) + (col & 7);
+}
+
+// ROWS rows of W columns (columns past n and rows past len read as others).
+template <int W, int ROWS>
+__device__ __forceinline__ void stage(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
+  constexpr int R = 512 / W, NI = ROWS / R, kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane / (W / 8), pc = lane % (W / 8);
+  const char *base = reinterpret_cast<const char *>(src);
+#pragma unroll
+  for (int k = 0; k < (NI + 3) / 4; ++k) {
+    const int m = wave + 4 * k;
+    if (NI % 4 != 0 && m >= NI) break;
+    const int s = m * R + rl, c = min(pc ^ (s & kMask), n / 8 - 1);
+    const uint32_t off = (uint32_t)min(s, len - 1) * (uint32_t)(ld * 2) + 16u * (uint32_t)c;
+    __builtin_amdgcn_global_load_lds(base + off, (lds_void *)(tile + m * 512), 16, 0, 0);
+  }
+}
+
+// Eight of a row, and a column's rows r0 + 8 lg + e (natural order) or
+// r0 + 16 (e / 4) + 4 lg + e % 4 (the order of result tiles).
+template <int W>
+__device__ __forceinline__ bf16x8 row8(const bf16 *t, int row, int col) {
+  return *reinterpret_cast<const bf16x8 *>(t + place<W>(row, col));
+}
+template <int W>
+__device__ __forceinline__ bf16x8 column8(const bf16 *t, int r0, int c0) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int row = r0 + 8 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
+  const bf16x4 a = ds_tr4(t, place<W>(row, col)), b = ds_tr4(t, place<W>(row + 4, col));
+  return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+template <int W>
+__device__ __forceinline__ bf16x8 column8_tiles(const bf16 *t, int r0, int c0) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int row = r0 + 4 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
+  const bf16x4 a = ds_tr4(t, place<W>(row, col)), b = ds_tr4(t, place<W>(row + 16, col));
+  return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+__device__ __forceinline__ float dot8(bf16x8 a, bf16x8 b) {
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s += (float)a[e] * (float)b[e];
+  return s;
+}
+// Sum over the four lanes that share lr.
+__device__ __forceinline__ float sum_lg(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// Result tiles 2 kt and 2 kt + 1 of an operand, one at a time.
+__device__ __forceinline__ void set_half(bf16x8 &to, int half, f32x4 v) {
+  const uint32_t a = pack2(v[0], v[1]), b = pack2(v[2], v[3]);
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w = __builtin_bit_cast(u32x4, to);
+  w[2 * half] = a;
+  w[2 * half + 1] = b;
+  to = __builtin_bit_cast(bf16x8, w);
+}
+
+template <int NK, int PK>
+__global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
+  constexpr int N = 32 * NK, P = 32 * PK, C = kDeltaChunk;
+  __shared__ bf16 sK[C * N], sQ[C * N], sY[C * P], sU[P * C], sR[P * C];
+  __shared__ bf16 sA0[P * 32], sB0[P * 32], sA1[P * 32], sB1[P * 32];  // blocks of S, dS
+  __shared__ float sG[C], sBt[C], sZ[C], sP[C], sS[4];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int unit = xcd_unit();
+  const int part = unit % a.hparts;
+  unit /= a.hparts;
+  const int grp = unit % a.G, slot = unit / a.G;
+  int64_t start;
+  int len;
+  if (!delta_chunk(a, slot, start, len)) return;
+  const int per = (a.hpg + a.hparts - 1) / a.hparts;
+  const int h0 = grp * a.hpg + part * per, h1 = min(h0 + per, (grp + 1) * a.hpg);
+  const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
+  const int own = 16 * w + lr;              // this lane's token
+  const bool live = own < len;
+  const size_t tok = (size_t)(start + min(own, len - 1));
+
+  f32x4 dQ[NK][2], dK[NK][2];
+#pragma unroll
+  for (int nb = 0; nb < NK; ++nb)
+#pragma unroll
+    for (int par = 0; par < 2; ++par) dQ[nb][par] = dK[nb][par] = kZero4;
+  stage<N, C>(sK, (const bf16 *)a.B + ((size_t)start * a.G + grp) * a.N, ldk, a.N, len);
+  stage<N, C>(sQ, (const bf16 *)a.C + ((size_t)start * a.G + grp) * a.N, ldk, a.N, len);
+
+  for (int h = h0; h < h1; ++h) {
+    const size_t sh = (size_t)slot * a.H + h;
+    const bf16 *S0 = (const bf16 *)a.st0 + sh * a.P * a.N, *S1 = (const bf16 *)a.st1 + sh * a.P * a.N;
+    const auto fetch = [&](int nb, bf16 *A, bf16 *B) __attribute__((always_inline)) {
+      stage<32, P>(A, S0 + 32 * nb, a.N, min(32, a.N - 32 * nb), a.P);
+      stage<32, P>(B, S1 + 32 * nb, a.N, min(32, a.N - 32 * nb), a.P);
+    };
+    if (h > h0) __syncthreads();
+    stage<P, C>(sY, (const bf16 *)a.dy + ((size_t)start * a.H + h) * a.P, ldx, a.P, len);
+    stage<C, P>(sU, (const bf16 *)a.u + sh * a.P * C, C, C, a.P);
+    stage<C, P>(sR, (const bf16 *)a.dr + sh * a.P * C, C, C, a.P);
+    fetch(0, sA0, sB0);
+    if (w == 0) {
+      const size_t ga = (size_t)(start + min(lane, len - 1)) * a.H + h;
+      sG[lane] = wave_inclusive_sum(
+          lane < len ? delta_log2_decay((float)((const bf16 *)a.g)[ga]) : 0.f);
+      sBt[lane] = lane < len ? (float)((const bf16 *)a.beta)[ga] : 0.f;
+    }
+    wait_vmem_all();
+    __syncthreads();
+
+    // this token's rows of dY, dR, U (zeros past the end and past P)
+    bf16x8 yo[PK], ro[PK], uo[PK];
+    const float bi = sBt[own], gi = sG[own], gc = sG[C - 1];
+    const float ef = exp2_fast(gi), lf = exp2_fast(gc - gi), be = bi * ef;
+    float rv = 0.f;
+#pragma unroll
+    for (int ps = 0; ps < PK; ++ps) {
+      const bool in = 32 * ps + 8 * lg < a.P;
+      yo[ps] = row8<P>(sY, own, 32 * ps + 8 * lg);
+      ro[ps] = column8<C>(sR, 32 * ps, 16 * w);
+      uo[ps] = column8<C>(sU, 32 * ps, 16 * w);
+      if (!in || !live) yo[ps] = zero8();
+      if (!in) ro[ps] = uo[ps] = zero8();
+      if (in && live) {
+        const size_t at = (tok * a.H + h) * a.P + 32 * ps + 8 * lg;
+        rv += dot8(ro[ps], ldg8((const bf16 *)a.x + at));
+        f32x4 p, q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = bi * (float)ro[ps][e];
+          q[e] = bi * (float)ro[ps][4 + e];
+        }
+        *reinterpret_cast<bf16x8 *>((bf16 *)a.dx + at) = pack8(p, q);
+      }
+    }
+    // the pair matrices
+    bf16x8 m1[2], l1[2], m2[2], l2[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) m1[kt] = l1[kt] = m2[kt] = l2[kt] = zero8();
+    float pairs = 0.f, betas = 0.f;         // row sums less column sums; for dbeta
+    {
+      bf16x8 ko[NK], qo[NK];
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        ko[ks] = row8<N>(sK, own, 32 * ks + 8 * lg);
+        qo[ks] = row8<N>(sQ, own, 32 * ks + 8 * lg);
+        if (32 * ks + 8 * lg >= a.N) ko[ks] = qo[ks] = zero8();
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 gt = ldf4(sG + 16 * t + 4 * lg);
+        if (t <= w) {                        // rows j of tile t, column i = own
+          f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4, m, l;
+#pragma unroll
+          for (int ks = 0; ks < NK; ++ks) {
+            const bf16x8 k = row8<N>(sK, 16 * t + lr, 32 * ks + 8 * lg);
+            kk = mfma(k, ko[ks], kk);
+            qk = mfma(k, qo[ks], qk);
+          }
+#pragma unroll
+          for (int ps = 0; ps < PK; ++ps) {
+            const bf16x8 u = column8<C>(sU, 32 * ps, 16 * t);
+            dm = mfma(u, yo[ps], dm);
+            dl = mfma(u, ro[ps], dl);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int d = own - (16 * t + 4 * lg + r);
+            const float e = d >= 0 ? exp2_fast(gi - gt[r]) : 0.f;
+            m[r] = d >= 0 ? dm[r] * e : 0.f;
+            const float lk = d > 0 ? -dl[r] * e : 0.f;
+            l[r] = bi * lk;
+            betas += lk * kk[r];
+            pairs += m[r] * qk[r] + l[r] * kk[r];
+          }
+          set_half(m1[t >> 1], t & 1, m);
+          set_half(l1[t >> 1], t & 1, l);
+        }
+        if (t >= w) {                        // rows i of tile t, column j = own
+          f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4, m, l;
+#pragma unroll
+          for (int ks = 0; ks < NK; ++ks) {
+            kk = mfma(row8<N>(sK, 16 * t + lr, 32 * ks + 8 * lg), ko[ks], kk);
+            qk = mfma(row8<N>(sQ, 16 * t + lr, 32 * ks + 8 * lg), ko[ks], qk);
+          }
+#pragma unroll
+          for (int ps = 0; ps < PK; ++ps) {
+            dm = mfma(row8<P>(sY, 16 * t + lr, 32 * ps + 8 * lg), uo[ps], dm);
+            dl = mfma(column8<C>(sR, 32 * ps, 16 * t), uo[ps], dl);
+          }
+          const f32x4 bt = ldf4(sBt + 16 * t + 4 * lg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * t + 4 * lg + r, d = i - own;
+            const bool in = d >= 0 && i < len;
+            const float e = in ? exp2_fast(gt[r] - gi) : 0.f;
+            m[r] = in ? dm[r] * e : 0.f;
+            l[r] = in && d > 0 ? -bt[r] * dl[r] * e : 0.f;
+            pairs -= m[r] * qk[r] + l[r] * kk[r];
+          }
+          set_half(m2[t >> 1], t & 1, m);
+          set_half(l2[t >> 1], t & 1, l);
+        }
+      }
+    }
+    // the states, 32 channels at a time
+    float zq = 0.f, zk = 0.f, zu = 0.f, ss = 0.f;
+    const auto block = [&](int nb, const bf16 *A, const bf16 *B) __attribute__((always_inline)) {
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const int n0 = 32 * nb + 16 * par;
+        f32x4 ys = kZero4, rs = kZero4, us = kZero4;
+#pragma unroll
+        for (int ps = 0; ps < PK; ++ps) {
+          const bf16x8 s0 = column8<32>(A, 32 * ps, 16 * par), s1 = column8<32>(B, 32 * ps, 16 * par);
+          ys = mfma(s0, yo[ps], ys);
+          rs = mfma(s0, ro[ps], rs);
+          us = mfma(s1, uo[ps], us);
+          if (((2 * nb + par) & 3) == w && n0 < a.N && 32 * ps + 8 * lg < a.P) ss += dot8(s0, s1);
+        }
+        const bf16x4 k4 = *reinterpret_cast<const bf16x4 *>(sK + place<N>(own, n0 + 4 * lg));
+        const bf16x4 q4 = *reinterpret_cast<const bf16x4 *>(sQ + place<N>(own, n0 + 4 * lg));
+        if (n0 < a.N)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            zq += (float)q4[r] * ys[r];
+            zk += (float)k4[r] * rs[r];
+            zu += (float)k4[r] * us[r];
+          }
+        f32x4 q = dQ[nb][par] + ef * ys, k = dK[nb][par] - be * rs + lf * us;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          const bf16x8 kT = column8_tiles<N>(sK, 32 * kt, n0);
+          if (kt <= w / 2) {                 // tokens up to this wave's
+            q = mfma(kT, m1[kt], q);
+            k = mfma(kT, l1[kt], k);
+          }
+          if (kt >= w / 2) {                 // and from them on
+            k = mfma(kT, l2[kt], k);
+            k = mfma(column8_tiles<N>(sQ, 32 * kt, n0), m2[kt], k);
+          }
+        }
+        dQ[nb][par] = q;
+        dK[nb][par] = k;
+      }
+    };
+#pragma unroll
+    for (int nb = 0; nb < NK; ++nb) {
+      if (nb + 1 < NK) {
+        if (nb & 1)
+          fetch(min(nb + 1, (a.N - 1) / 32), sA0, sB0);
+        else
+          fetch(min(nb + 1, (a.N - 1) / 32), sA1, sB1);
+      }
+      if (nb & 1)
+        block(nb, sA1, sB1);
+      else
+        block(nb, sA0, sB0);
+      if (nb + 1 < NK) {
+        wait_vmem_all();
+        __syncthreads();
+      }
+    }
+    // dbeta and dg
+    rv = sum_lg(rv);
+    betas = sum_lg(betas);
+    pairs = sum_lg(pairs);
+    zq = sum_lg(zq);
+    zk = sum_lg(zk);
+    zu = sum_lg(zu);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) ss += __shfl_xor(ss, o);
+    if (lg == 0) {
+      sZ[own] = live ? ef * zq - be * zk + pairs : 0.f;  // (dR past the end is not zero)
+      sP[own] = lf * zu;
+      if (live) ((bf16 *)a.dbeta)[tok * a.H + h] = (bf16)(rv + betas - ef * zk);
+    }
+    if (lane == 0) sS[w] = ss;
+    __syncthreads();
+    if (w == 0) {
+      const float z = sZ[lane], p = sP[lane];
+      const float upto = wave_inclusive_sum(z), all = __shfl(upto, 63);
+      const float before = wave_inclusive_sum(p) - p;
+      const float ends = exp2_fast(gc) * (sS[0] + sS[1] + sS[2] + sS[3]);
+      if (lane < len)
+        ((bf16 *)a.dg)[(size_t)(start + lane) * a.H + h] = (bf16)(all - (upto - z) + before + ends);
+    }
+  }
+  if (!live) return;
+#pragma unroll
+  for (int nb = 0; nb < NK; ++nb)
+#pragma unroll
+    for (int par = 0; par < 2; ++par) {
+      const int n = 32 * nb + 16 * par + 4 * lg;
+      if (n >= a.N) continue;
+      const f32x4 k = dK[nb][par], q = dQ[nb][par];
+      if (a.hparts == 1) {
+        const size_t at = (tok * a.G + grp) * a.N + n;
+        *reinterpret_cast<uint2 *>((bf16 *)a.dB + at) = make_uint2(pack2(k[0], k[1]), pack2(k[2], k[3]));
+        *reinterpret_cast<uint2 *>((bf16 *)a.dC + at) = make_uint2(pack2(q[0], q[1]), pack2(q[2], q[3]));
+      } else {
+        const size_t at = ((tok * a.G + grp) * a.hparts + part) * a.N + n;
+        stf4(a.part + at, k);
+        stf4(a.part + (size_t)a.T * a.G * a.hparts * a.N + at, q);
+      }
+    }
+}
+
+template <int NK, int PK>
+hipError_t grad(const DeltaArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.nslots * a.G * a.hparts)), block(256);
+  hipLaunchKernelGGL((k_delta_grad<NK, PK>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <int NK>
+hipError_t grad_p(const DeltaArgs &a, hipStream_t s) {
+  if (a.P <= 32) return grad<NK, 1>(a, s);
+  if (a.P == 64) return grad<NK, 2>(a, s);
+  return grad<NK, 4>(a, s);
+}
+
+}  // namespace
+
+int delta_grad_parts(const DeltaArgs &a) {
+  // workgroups for the card before a workgroup takes more heads of a group
+  int64_t parts = a.nslots ? 1024 / ((int64_t)a.nslots * a.G) : 1;
+  parts = parts < 1 ? 1 : parts > a.hpg ? a.hpg : parts;
+  const int per = (int)((a.hpg + parts - 1) / parts);
+  return (a.hpg + per - 1) / per;
+}
+
+hipError_t launch_delta_grad(const DeltaArgs &a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  const hipError_t e = a.N <= 64 ? grad_p<2>(a, s) : a.N <= 128 ? grad_p<4>(a, s) : grad_p<8>(a, s);
+  if (e != hipSuccess || a.hparts == 1) return e;
+  return launch_delta_heads_sum(a, true, s);
+}
+
+}  // namespace ssd

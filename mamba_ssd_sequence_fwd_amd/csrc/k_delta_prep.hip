@@ -1,10 +1,9 @@
 // k_delta_prep.hip -- the triangular matrices of each chunk of the gated delta
 // rule: T = (I + L)^-1 and M (delta.h), or T, T^T and M^T for the backward pass.
 //
-// One wave takes one chunk and a few heads of one group. K K^T and Q K^T are
-// products of the group's rows, kept in registers for its heads as 16 x 16
-// tiles on and below the diagonal, transposed: a lane holds 4 consecutive
-// columns j of one row i. In that layout a tile of L is the left operand of
+// One wave takes one chunk and head. Q K^T and K K^T are kept in registers as
+// 16 x 16 tiles on and below the diagonal, transposed: a lane holds 4
+// consecutive columns j of one row i. In that layout a tile of L is the left operand of
 // the fp32 matrix instruction (lane l: row l % 16, columns 4 (l / 16) + r at
 // step r) and a result tile its right operand, so the block inversion
 //   T_ij = -T_ii sum_{j <= k < i} L_ik T_kj
@@ -14,6 +13,8 @@
 // lane. (Substitution, not powers of L: with equal keys the powers of a
 // 16 x 16 block reach 6435 and cancel, the substitution's values stay within
 // those of the inverse.)
+#include <type_traits>
+
 #include "delta_tiles.h"
 
 namespace ssd {
@@ -22,123 +23,154 @@ namespace ssd {
 __host__ __device__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
 
 // acc[tri(i, j)] = rows j of X against rows i of Y (lane: row i % 16, 4
-// columns j): 64 rows each, `ld` apart, N columns, rows past len read as the
-// last one. Both products that share the rows K are taken in one walk.
-template <typename T>
-__device__ __forceinline__ void tri_products(const T *K, const T *Q, size_t ld, int N, int len,
-                                             f32x4 (&kk)[10], f32x4 (&qk)[10], bool transposed_q) {
+// columns j), or with kSwap the other way round (lane: row j % 16, 4 columns
+// i). 64 rows each, `ld` apart, N columns, rows past len read as the last one.
+template <bool kSwap, typename T>
+__device__ __forceinline__ void tri_product(const T *X, const T *Y, size_t ld, int N, int len,
+                                            f32x4 (&acc)[10]) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
 #pragma unroll
-  for (int e = 0; e < 10; ++e) kk[e] = qk[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int e = 0; e < 10; ++e) acc[e] = kZero4;
+  size_t row[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) row[t] = (size_t)min(16 * t + lr, len - 1) * ld;
   if constexpr (sizeof(T) == 2) {
+#pragma unroll 2
     for (int n0 = 0; n0 < N; n0 += 32) {
-      bf16x8 k[4], q[4];
+      bf16x8 x[4], y[4];
       const int col = n0 + 8 * lg;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const size_t row = (size_t)min(16 * t + lr, len - 1) * ld + min(col, N - 8);
-        k[t] = ldg8((const bf16 *)K + row);
-        q[t] = ldg8((const bf16 *)Q + row);
-        if (col >= N) k[t] = q[t] = zero8();
+        x[t] = ldg8((const bf16 *)X + row[t] + min(col, N - 8));
+        y[t] = X == Y ? x[t] : ldg8((const bf16 *)Y + row[t] + min(col, N - 8));
       }
+      if (n0 + 32 > N && col >= N)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = y[t] = zero8();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j <= i; ++j) {
-          kk[tri(i, j)] = mfma(k[j], k[i], kk[tri(i, j)]);
-          qk[tri(i, j)] = transposed_q ? mfma(q[i], k[j], qk[tri(i, j)])
-                                       : mfma(k[j], q[i], qk[tri(i, j)]);
-        }
+        for (int j = 0; j <= i; ++j)
+          acc[tri(i, j)] = kSwap ? mfma(y[i], x[j], acc[tri(i, j)]) : mfma(x[j], y[i], acc[tri(i, j)]);
     }
   } else {
+#pragma unroll 2
     for (int n0 = 0; n0 < N; n0 += 16) {
-      f32x4 k[4], q[4];
+      f32x4 x[4], y[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const size_t row = (size_t)min(16 * t + lr, len - 1) * ld + n0 + 4 * lg;
-        k[t] = *reinterpret_cast<const f32x4 *>(K + row);
-        q[t] = *reinterpret_cast<const f32x4 *>(Q + row);
+        x[t] = ldf4((const float *)X + row[t] + n0 + 4 * lg);
+        y[t] = X == Y ? x[t] : ldf4((const float *)Y + row[t] + n0 + 4 * lg);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j <= i; ++j) {
-          kk[tri(i, j)] = mfma16(k[j], k[i], kk[tri(i, j)]);
-          qk[tri(i, j)] = transposed_q ? mfma16(q[i], k[j], qk[tri(i, j)])
-                                       : mfma16(k[j], q[i], qk[tri(i, j)]);
-        }
+        for (int j = 0; j <= i; ++j)
+          acc[tri(i, j)] =
+              kSwap ? mfma16(y[i], x[j], acc[tri(i, j)]) : mfma16(x[j], y[i], acc[tri(i, j)]);
     }
   }
 }
 
-// T (64, 64) fp32 rows, tiles above the diagonal not written.
-__device__ __forceinline__ void store_rows_f32(float *to, int i, int j, f32x4 v) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  *reinterpret_cast<f32x4 *>(to + (16 * i + lr) * kDeltaChunk + 16 * j + 4 * lg) = v;
-}
+// Where a chunk's matrices go. v: the ten tiles (lane: row 16 i + l % 16, columns
+// 16 j + 4 (l / 16) + r) of a lower matrix, tile (i, j) at tri(i, j), or of an
+// upper one, tile (j, i) at tri(i, j). As fp32 rows of 64 (tiles that are zero
+// not written), or as operand tiles of the bf16 matrix instruction (a row's 8 of
+// k are 4 of each tile of a pair), rounded, with what rounding left behind them
+// where kSplit.
+struct RowsOut {
+  float *p;
+  template <int kMatrix, bool kSplit, bool kUpper>
+  __device__ __forceinline__ void put(const f32x4 (&v)[10]) const {
+    const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j <= i; ++j)
+        stf4(p + kMatrix * 4096 + (16 * (kUpper ? j : i) + lr) * kDeltaChunk +
+                 16 * (kUpper ? i : j) + 4 * lg, v[tri(i, j)]);
+  }
+};
+struct TilesOut {
+  bf16 *p;
+  template <int kMatrix, bool kSplit, bool kUpper>
+  __device__ __forceinline__ void put(const f32x4 (&v)[10]) const {
+    bf16 *to = p + kMatrix * 2 * kTriTiles * kTileElems + 8 * (threadIdx.x & 63);
+    const auto tile = [&](int t, f32x4 a, f32x4 b) {
+      if (kSplit) {
+        const Split s = split8(a, b);
+        *reinterpret_cast<bf16x8 *>(to + 2 * t * kTileElems) = s.hi;
+        *reinterpret_cast<bf16x8 *>(to + (2 * t + 1) * kTileElems) = s.lo;
+      } else {
+        *reinterpret_cast<bf16x8 *>(to + t * kTileElems) = pack8(a, b);
+      }
+    };
+    if (!kUpper) {
+      tile(lower_tile(1, 0), v[tri(1, 0)], v[tri(1, 1)]);
+      tile(lower_tile(2, 0), v[tri(2, 0)], v[tri(2, 1)]);
+      tile(lower_tile(3, 0), v[tri(3, 0)], v[tri(3, 1)]);
+      tile(lower_tile(3, 1), v[tri(3, 2)], v[tri(3, 3)]);
+      tile(4, v[tri(0, 0)], v[tri(2, 2)]);
+    } else {
+      tile(upper_tile(0, 0), v[tri(0, 0)], v[tri(1, 0)]);
+      tile(upper_tile(0, 1), v[tri(2, 0)], v[tri(3, 0)]);
+      tile(upper_tile(1, 1), v[tri(2, 1)], v[tri(3, 1)]);
+      tile(upper_tile(2, 1), v[tri(2, 2)], v[tri(3, 2)]);
+      tile(4, v[tri(1, 1)], v[tri(3, 3)]);
+    }
+  }
+};
 
-template <typename T, DeltaTri W>
-__global__ __launch_bounds__(64) void k_delta_prep_f32(DeltaArgs a, int per) {
+template <typename T, DeltaTri W, typename Out>
+__global__ __launch_bounds__(64, 4) void k_delta_prep(DeltaArgs a, int64_t bytes) {
   __shared__ float sG[kDeltaChunk], sB[kDeltaChunk];
   __shared__ f32x4 sD[4][16][5];  // diagonal blocks: rows of L, then columns of T
   const int lane = threadIdx.x, lr = lane & 15, lg = lane >> 4;
-  const int parts = (a.hpg + per - 1) / per;
-  int unit = blockIdx.x;
-  const int hp = unit % parts;
-  unit /= parts;
-  const int grp = unit % a.G, slot = unit / a.G;
+  const int unit = xcd_unit(), h = unit % a.H, slot = unit / a.H, grp = h / a.hpg;
   int64_t start;
   int len;
   if (!delta_chunk(a, slot, start, len)) return;
+  stage_gates<T>(sG, sB, a, start, h, len);
+  const size_t row0 = ((size_t)start * a.G + grp) * a.N, ld = (size_t)a.G * a.N;
+  const T *K = (const T *)a.B + row0, *Q = (const T *)a.C + row0;
+  Out out;
+  out.p = reinterpret_cast<decltype(out.p)>((char *)a.tri + ((int64_t)slot * a.H + h) * bytes);
 
-  f32x4 kk[10], qk[10];
-  const size_t row0 = ((size_t)start * a.G + grp) * a.N;
-  tri_products<T>((const T *)a.B + row0, (const T *)a.C + row0, (size_t)a.G * a.N, a.N, len, kk,
-                  qk, W == kTriBackward);
-
-  const int h1 = grp * a.hpg + min(a.hpg, (hp + 1) * per);
-  for (int h = grp * a.hpg + hp * per; h < h1; ++h) {
-    {
-      const size_t at = (size_t)(start + min(lane, len - 1)) * a.H + h;
-      const float gl = lane < len ? delta_log2_decay(ld<T>(a.g, at)) : 0.f;
-      sG[lane] = wave_inclusive_sum(gl);
-      sB[lane] = lane < len ? ld<T>(a.beta, at) : 0.f;
-    }
+  {  // M, or M^T (lane holds column j, 4 rows i)
+    f32x4 qk[10];
+    tri_product<W == kTriBackward, T>(K, Q, ld, a.N, len, qk);
     __syncthreads();
-    f32x4 gr[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) gr[t] = *reinterpret_cast<const f32x4 *>(sG + 16 * t + 4 * lg);
-    float *out = (float *)a.tri + ((size_t)slot * a.H + h) * ((W == kTriForward ? 2 : 3) * 4096);
-
-    // L, and M beside it
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j <= i; ++j) {
+        const float ga = sG[16 * (W == kTriForward ? i : j) + lr];
+        const f32x4 gb = ldf4(sG + 16 * (W == kTriForward ? j : i) + 4 * lg);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool below = j < i || (W == kTriForward ? 4 * lg + r <= lr : lr <= 4 * lg + r);
+          const float e = exp2_fast(W == kTriForward ? ga - gb[r] : gb[r] - ga);
+          qk[tri(i, j)][r] = below ? qk[tri(i, j)][r] * e : 0.f;
+        }
+      }
+    if (W == kTriForward)
+      out.template put<1, false, false>(qk);
+    else
+      out.template put<2, true, true>(qk);
+  }
+  {
     f32x4 Lt[10];
+    tri_product<false, T>(K, K, ld, a.N, len, Lt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float gi = sG[16 * i + lr], bi = sB[16 * i + lr];
 #pragma unroll
       for (int j = 0; j <= i; ++j) {
-        f32x4 m;
+        const f32x4 gj = ldf4(sG + 16 * j + 4 * lg);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const bool below = j < i || 4 * lg + r < lr;
-          const float e = exp2_fast(gi - gr[j][r]);
-          Lt[tri(i, j)][r] = below ? bi * kk[tri(i, j)][r] * e : 0.f;
-          if (W == kTriForward) m[r] = below || 4 * lg + r == lr ? qk[tri(i, j)][r] * e : 0.f;
-        }
-        if (W == kTriForward) store_rows_f32(out + 4096, i, j, m);
-      }
-    }
-    if (W == kTriBackward) {  // M^T: lane holds column j, 4 rows i
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float gj = sG[16 * j + lr];
-#pragma unroll
-        for (int i = j; i < 4; ++i) {
-          f32x4 m;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            m[r] = j < i || lr <= 4 * lg + r ? qk[tri(i, j)][r] * exp2_fast(gr[i][r] - gj) : 0.f;
-          store_rows_f32(out + 8192, j, i, m);
+          Lt[tri(i, j)][r] = below ? bi * Lt[tri(i, j)][r] * exp2_fast(gi - gj[r]) : 0.f;
         }
       }
     }
@@ -165,15 +197,14 @@ __global__ __launch_bounds__(64) void k_delta_prep_f32(DeltaArgs a, int per) {
     for (int q = 0; q < 4; ++q)
       sD[lg][lr][q] = f32x4{t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]};
     __syncthreads();
-    f32x4 Tt[10], Ta[4];  // Tt: lane column j, 4 rows i; Ta: lane row i, 4 columns
+    // T: lane column j, 4 rows i; and lane row i, 4 columns j
+    f32x4 Tt[10], Ta[10];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       Tt[tri(b, b)] = sD[b][lr][lg];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        Ta[b][r] = reinterpret_cast<const float *>(&sD[b][4 * lg + r][0])[lr];
-      store_rows_f32(out, b, b, Ta[b]);
-      if (W == kTriBackward) store_rows_f32(out + 4096, b, b, Tt[tri(b, b)]);
+        Ta[tri(b, b)][r] = reinterpret_cast<const float *>(&sD[b][4 * lg + r][0])[lr];
     }
 #pragma unroll
     for (int d = 1; d < 4; ++d)
@@ -184,35 +215,34 @@ __global__ __launch_bounds__(64) void k_delta_prep_f32(DeltaArgs a, int per) {
 #pragma unroll
         for (int k = j; k < i; ++k) x = mfma16(Lt[tri(i, k)], Tt[tri(k, j)], x);
         x = -x;
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        Tt[tri(i, j)] = mfma16(Ta[i], x, zero);
-        store_rows_f32(out, i, j, mfma16(x, Ta[i], zero));
-        if (W == kTriBackward) store_rows_f32(out + 4096, j, i, Tt[tri(i, j)]);
+        Tt[tri(i, j)] = mfma16(Ta[tri(i, i)], x, kZero4);
+        Ta[tri(i, j)] = mfma16(x, Ta[tri(i, i)], kZero4);
       }
-    __syncthreads();
+    out.template put<0, true, false>(Ta);
+    if (W == kTriBackward) out.template put<1, true, true>(Tt);
   }
 }
 
-size_t delta_tri_bytes(bool bf16_path, DeltaTri which) {
+size_t delta_tri_bytes(bool tiles, DeltaTri which) {
+  if (tiles) return (size_t)(which == kTriForward ? 3 : 6) * kTriTiles * kTileElems * sizeof(bf16);
   return (size_t)(which == kTriForward ? 2 : 3) * 4096 * sizeof(float);
+}
+
+template <typename T, DeltaTri W, typename Out>
+hipError_t prep(const DeltaArgs &a, hipStream_t s) {
+  const int64_t bytes = delta_tri_bytes(std::is_same<Out, TilesOut>::value, W);
+  const dim3 grid((unsigned)((int64_t)a.nslots * a.H)), block(64);
+  hipLaunchKernelGGL((k_delta_prep<T, W, Out>), grid, block, 0, s, a, bytes);
+  return hipGetLastError();
 }
 
 hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16_io, DeltaTri which, hipStream_t s) {
   if (a.nslots == 0) return hipSuccess;
-  const int per = 1;
-  const dim3 grid((unsigned)((int64_t)a.nslots * a.G * ((a.hpg + per - 1) / per))), block(64);
-  if (bf16_io) {
-    if (which == kTriForward)
-      hipLaunchKernelGGL((k_delta_prep_f32<bf16, kTriForward>), grid, block, 0, s, a, per);
-    else
-      hipLaunchKernelGGL((k_delta_prep_f32<bf16, kTriBackward>), grid, block, 0, s, a, per);
-  } else {
-    if (which == kTriForward)
-      hipLaunchKernelGGL((k_delta_prep_f32<float, kTriForward>), grid, block, 0, s, a, per);
-    else
-      hipLaunchKernelGGL((k_delta_prep_f32<float, kTriBackward>), grid, block, 0, s, a, per);
-  }
-  return hipGetLastError();
+  if (bf16_io)
+    return which == kTriForward ? prep<bf16, kTriForward, TilesOut>(a, s)
+                                : prep<bf16, kTriBackward, TilesOut>(a, s);
+  return which == kTriForward ? prep<float, kTriForward, RowsOut>(a, s)
+                              : prep<float, kTriBackward, RowsOut>(a, s);
 }
 
 }  // namespace ssd
