@@ -55,6 +55,75 @@ __device__ __forceinline__ f32x4 widen4(const bf16 *p) {
   return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
 }
 
+// Place (in elements) of (row, col) in a staged tile with rows of W bf16: the
+// 16-byte pieces of a row are permuted so that the 256 bytes which LDS gives at
+// once hold 16 rows of one piece (a row operand), and two neighbouring pieces of
+// 8 rows, 0 to 7 or 0 to 3 and 8 to 11 (a transposed read).
+template <int W>
+__device__ __forceinline__ int tile_swizzle(int row) {
+  if (W >= 128) {
+    const int h = (row & 3) | ((((row >> 2) ^ (row >> 3)) & 1) << 2);
+    return 2 * h + ((row >> 3) & 1);
+  }
+  if (W == 64) return 2 * (((row >> 1) & 1) | ((((row >> 2) ^ (row >> 3)) & 1) << 1)) + ((row >> 3) & 1);
+  if (W == 32) return 2 * (((row >> 2) ^ (row >> 3)) & 1) + ((row >> 3) & 1);
+  return (row >> 3) & 1;
+}
+template <int W>
+__device__ __forceinline__ int place(int row, int col) {
+  return row * W + (((col >> 3) ^ tile_swizzle<W>(row)) << 3) + (col & 7);
+}
+
+// ROWS rows of W columns (row stride ld; zeros from column n and row len on) into
+// such a tile, asynchronously, by WV waves; and `n` KiB in a row.
+template <int W, int ROWS, int WV>
+__device__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len);
+template <int WV>
+__device__ void stage_block(bf16 *to, const void *src, int n);
+
+#ifdef __HIP_DEVICE_COMPILE__  // (the host pass has no type for buffer descriptors)
+// Buffer descriptor of `bytes` from p: loads past them give zeros.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void *p, uint32_t bytes) {
+  constexpr int kRaw = 0x00027000;  // untyped dwords
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, kRaw);
+}
+
+// Only the descriptor changes from call to call: a lane's offset stays in one
+// register.
+template <int W, int ROWS, int WV>
+__device__ __forceinline__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
+  constexpr int R = 512 / W, NI = ROWS / R;  // rows of an instruction, instructions
+  constexpr int kSame = WV * R % 16 == 0 ? 1 : 16 / (WV * R);  // until the swizzle repeats
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane / (W / 8), pc = lane % (W / 8);
+  const Buffer rows = buffer_of(src, (uint32_t)(len - 1) * (uint32_t)(ld * 2) + 2u * (uint32_t)n);
+  uint32_t off[kSame];
+#pragma unroll
+  for (int k = 0; k < kSame; ++k) {
+    const int s = (wave + WV * k) * R + rl, c = pc ^ tile_swizzle<W>(s);
+    off[k] = 8 * c < n ? (uint32_t)s * (uint32_t)(ld * 2) + 16u * (uint32_t)c : 0x80000000u;
+  }
+#pragma unroll
+  for (int k = 0; k < (NI + WV - 1) / WV; ++k) {
+    if (NI % WV != 0 && wave + WV * k >= NI) break;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rows, (lds_void *)(tile + (wave + WV * k) * 512), 16,
+        off[k % kSame] + (uint32_t)(k / kSame * kSame * WV * R) * (uint32_t)(ld * 2), 0, 0, 0);
+  }
+}
+template <int WV>
+__device__ __forceinline__ void stage_block(bf16 *to, const void *src, int n) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Buffer block = buffer_of(src, (uint32_t)n * 1024u);
+  for (int m = wave; m < n; m += WV)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(block, (lds_void *)(to + m * 512), 16,
+                                             lane * 16 + m * 1024, 0, 0, 0);
+}
+#endif
+
 // Eight values of an operand in two bf16 each.
 struct Split {
   bf16x8 hi, lo;

@@ -14,8 +14,9 @@
 // Rounding. K, Q, V and dY are bf16 as they are. What enters a state is held in
 // two bf16 (the value, and what rounding left of it: 2^-17 off), so that the
 // fp32 states stay fp32: S in K S, R and T in T R (the three large products of
-// four), U in K^T U, and the same backwards. y is rounded to bf16 anyway: S
-// enters it whole, U and M once rounded.
+// four), U in K^T U, and the same backwards. y is rounded to bf16 anyway: S and M
+// enter it once rounded, U in two (it adds 6 products to 104 and takes y's error
+// from 2.97e-3 to the figure in the file's last paragraph).
 //
 // Segments. A walk's length is its chunks' latencies one after the other, and
 // few sequences and heads leave most of the card idle. Then each sequence is
@@ -27,45 +28,12 @@
 
 namespace ssd {
 
-// 64 token rows of W columns (row stride ld, columns past n and rows past len
-// read as others of the tensor) into a swizzled LDS tile, asynchronously.
-template <int W, int WV>
-__device__ __forceinline__ void stage_async(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
-  constexpr int R = 512 / W, NI = kDeltaChunk / R;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rl = lane / (W / 8), pc = lane % (W / 8);
-  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
-  const char *base = reinterpret_cast<const char *>(src);
-#pragma unroll
-  for (int k = 0; k < (NI + WV - 1) / WV; ++k) {
-    const int m = wave + WV * k;
-    if (NI % WV != 0 && m >= NI) break;
-    const int s = m * R + rl;
-    const int c = min(pc ^ (s & kMask), n / 8 - 1);
-    const uint32_t off = (uint32_t)min(s, len - 1) * (uint32_t)(ld * 2) + 16u * (uint32_t)c;
-    __builtin_amdgcn_global_load_lds(base + off, (lds_void *)(tile + m * 512), 16, 0, 0);
-  }
-}
-// `n` KiB in a row.
-template <int WV>
-__device__ __forceinline__ void stage_block(bf16 *to, const void *src, int n) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const char *base = static_cast<const char *>(src);
-  for (int m = wave; m < n; m += WV)
-    __builtin_amdgcn_global_load_lds(base + m * 1024 + lane * 16, (lds_void *)(to + m * 512), 16, 0,
-                                     0);
-}
-
 // Staged values (64 tokens x W columns): 16 columns from c0 of tokens
 // t0 + 4 lg + r, as a result tile has them.
 template <int W>
 __device__ __forceinline__ f32x4 value_tile(const bf16 *v, int t0, int c0) {
-  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  const int row = t0 + 4 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
-  const bf16x4 w = ds_tr4(v, row * W + (((col >> 3) ^ (row & kMask)) << 3) + (col & 7));
+  const bf16x4 w = ds_tr4(v, place<W>(t0 + 4 * lg + (lr >> 2), c0 + 4 * (lr & 3)));
   return f32x4{(float)w[0], (float)w[1], (float)w[2], (float)w[3]};
 }
 
@@ -92,8 +60,8 @@ template <int N>
 __device__ __forceinline__ bf16x8 state_operand(const bf16 *rows, int kt, int ks, int par) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int row = 32 * kt + 4 * lg + (lr >> 2), col = 32 * ks + 8 * (lr & 3) + 4 * par;
-  const bf16x4 a = ds_tr4(rows, rswz<N>(row, col));
-  const bf16x4 b = ds_tr4(rows, rswz<N>(row + 16, col));
+  const bf16x4 a = ds_tr4(rows, place<N>(row, col));
+  const bf16x4 b = ds_tr4(rows, place<N>(row + 16, col));
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
@@ -101,12 +69,16 @@ __device__ __forceinline__ bf16x8 state_operand(const bf16 *rows, int kt, int ks
 // as they are.
 template <int W>
 __device__ __forceinline__ bf16x8 value_operand(const bf16 *v, int kt, int c0) {
-  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  const int row = 32 * kt + 4 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
-  const int at = row * W + (((col >> 3) ^ (row & kMask)) << 3) + (col & 7);
+  const int at = place<W>(32 * kt + 4 * lg + (lr >> 2), c0 + 4 * (lr & 3));
   const bf16x4 a = ds_tr4(v, at), b = ds_tr4(v, at + 16 * W);  // (16 rows on: the same swizzle)
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// A store at a lane's 32-bit byte offset from an address that the wave shares.
+template <typename V>
+__device__ __forceinline__ void store_at(void *base, uint32_t off, V v) {
+  *reinterpret_cast<V *>(static_cast<char *>(base) + off) = v;
 }
 
 // What a walk writes.
@@ -118,7 +90,7 @@ enum WalkMode : int {
 
 // Three workgroups of four waves to a compute unit: 168 registers and 53 KB of
 // LDS each, which is why M's tiles come straight from the cache.
-template <int NK, int WV, bool kPad, WalkMode kMode>
+template <int NK, int WV, WalkMode kMode>
 __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(DeltaArgs a) {
   constexpr int N = 32 * NK, W = 16 * WV;  // state channels, the workgroup's columns
   constexpr bool kY = kMode == kWalkY, kLocal = kMode == kWalkLocal;
@@ -127,7 +99,8 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
   // not meet the loads under way, and does not wait for those.
   __shared__ bf16 sK[kDeltaChunk * N], sQ[kY ? kDeltaChunk * N : 8], sT[kT], sV[kDeltaChunk * W];
   __shared__ Gates G;
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (kLocal ? a.P + a.N : a.P) / 16, blocks = (tiles + WV - 1) / WV;
   int unit = xcd_unit();
   const int tile0 = (unit % blocks) * WV, tile = min(tile0 + wave, tiles - 1);
@@ -170,7 +143,7 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
   };
   uint16_t g = 0, bt = 0;  // (bits: a conversion here would wait for the loads)
   const auto fetch_keys = [&](int c) __attribute__((always_inline)) {
-    stage_async<N, WV>(sK, (const bf16 *)a.B + (rows_at(c) * a.G + grp) * a.N, ldk, a.N, length(c));
+    stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (rows_at(c) * a.G + grp) * a.N, ldk, a.N, length(c));
   };
   const auto fetch_rest = [&](int c) __attribute__((always_inline)) {
     const int64_t at = rows_at(c);
@@ -181,9 +154,9 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
       bt = ((const uint16_t *)a.beta)[ga];
     }
     if (kY)
-      stage_async<N, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
+      stage_tile<N, kDeltaChunk, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
     if (valued)
-      stage_async<W, WV>(sV, (const bf16 *)a.x + ((size_t)at * a.H + h) * a.P + 16 * tile0, ldx, W,
+      stage_tile<W, kDeltaChunk, WV>(sV, (const bf16 *)a.x + ((size_t)at * a.H + h) * a.P + 16 * tile0, ldx, W,
                          len);
     stage_block<WV>(sT, tri_at(c), 2 * kTriTiles);
   };
@@ -197,37 +170,53 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
     wait_vmem_all();
     if (wave == 0) fill_gates(G, bits_to_f32(g), bits_to_f32(bt), lane < len);
     __syncthreads();
-    bf16x8 M[kTriTiles];
-    if (kY) {
-      const bf16 *m = tri_at(c) + kT + 8 * lane;
-#pragma unroll
-      for (int k = 0; k < kTriTiles; ++k) M[k] = ldg8(m + k * kTileElems);
-    }
 
-    // K S, and Q S transposed (lane: token lr of its tile, rows p)
+    // K S, and Q S transposed (lane: token lr of its tile, rows p); two tiles'
+    // operands at a time, the next ones under way
     f32x4 A[4], O[4];
+    {
+      bf16x8 kb[2][2], qb[2][2];
+      const auto keys = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) A[t] = O[t] = kZero4;
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      const Split s = split8(S[ks][0], S[ks][1]);
-      if (kMode == kWalkSave && 32 * ks + 8 * lg < a.N)
-        *reinterpret_cast<bf16x8 *>((bf16 *)a.st0 +
-                                    (((size_t)(w.slot + c) * a.H + h) * a.P + p) * a.N + 32 * ks +
-                                    8 * lg) = s.hi;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int e = rswz<N>(16 * t + lr, 32 * ks + 8 * lg);
-        const bf16x8 k = *reinterpret_cast<const bf16x8 *>(sK + e);
-        A[t] = mfma(k, s.hi, A[t]);
-        A[t] = mfma(k, s.lo, A[t]);
-        if (kY) {
-          const bf16x8 q = *reinterpret_cast<const bf16x8 *>(sQ + e);
-          O[t] = mfma(s.hi, q, O[t]);
-          O[t] = mfma(s.lo, q, O[t]);
+        for (int u = 0; u < 2; ++u) {
+          const int e = place<N>(32 * (b & 1) + 16 * u + lr, 32 * (b >> 1) + 8 * lg);
+          kb[b & 1][u] = *reinterpret_cast<const bf16x8 *>(sK + e);
+          if (kY) qb[b & 1][u] = *reinterpret_cast<const bf16x8 *>(sQ + e);
         }
+      };
+      keys(0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) A[t] = O[t] = kZero4;
+      Split s;
+#pragma unroll
+      for (int b = 0; b < 2 * NK; ++b) {
+        const int ks = b >> 1, t = 2 * (b & 1);
+        if (b + 1 < 2 * NK) keys(b + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if ((b & 1) == 0) {
+          s = split8(S[ks][0], S[ks][1]);
+          if (kMode == kWalkSave && 32 * ks + 8 * lg < a.N)
+            store_at((bf16 *)a.st0 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks,
+                     (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.hi, A[t + u]);
+        if (kY)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) O[t + u] = mfma(s.hi, qb[b & 1][u], O[t + u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.lo, A[t + u]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    const auto tri_tiles = [&](int lo, bf16x8 (&to)[kTriTiles]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < kTriTiles; ++k)
+        to[k] = *reinterpret_cast<const bf16x8 *>(sT + (2 * k + lo) * kTileElems + 8 * lane);
+    };
+    bf16x8 Th[kTriTiles], Tl[kTriTiles];
+    tri_tiles(0, Th);
+    __builtin_amdgcn_sched_barrier(0);
     // R, as operands
     Split R[2];
 #pragma unroll
@@ -242,72 +231,95 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
       }
       R[kt] = split8(v[0], v[1]);
     }
-    // U = T R
+    // U = T R; M's tiles come straight from the cache
+    __builtin_amdgcn_sched_barrier(0);
+    tri_tiles(1, Tl);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      A[i] = kZero4;
+    for (int i = 0; i < 4; ++i) A[i] = kZero4;
 #pragma unroll
-      for (int kt = 0; kt <= i / 2; ++kt) {
-        const bf16 *t = sT + (lower_tile(i, kt) * 2) * kTileElems + 8 * lane;
-        const bf16x8 th = lower_operand(*reinterpret_cast<const bf16x8 *>(t), i, kt);
-        const bf16x8 tl = lower_operand(*reinterpret_cast<const bf16x8 *>(t + kTileElems), i, kt);
-        A[i] = mfma(th, R[kt].hi, A[i]);
-        A[i] = mfma(th, R[kt].lo, A[i]);
-        A[i] = mfma(tl, R[kt].hi, A[i]);
-      }
+    for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int i = 2 * kt; i < 4; ++i)
+          A[i] = mfma(lower_operand(Th[lower_tile(i, kt)], i, kt), lo ? R[kt].lo : R[kt].hi, A[i]);
+    __builtin_amdgcn_sched_barrier(0);
+    bf16x8 M[kTriTiles];
+    if (kY) {
+      const bf16 *m = tri_at(c) + kT + 8 * lane;
+#pragma unroll
+      for (int k = 0; k < kTriTiles; ++k) M[k] = ldg8(m + k * kTileElems);
     }
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int i = 2 * kt; i < 4; ++i)
+        A[i] = mfma(lower_operand(Tl[lower_tile(i, kt)], i, kt), R[kt].hi, A[i]);
     if (c + 1 < chunks) {
       __syncthreads();
       fetch_rest(c + 1);
     }
     const float ec = G.ef[kDeltaChunk - 1];
+    bf16x8 kT[2][2];  // of a block of 16 channels, the next one's under way
+    const auto columns = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) kT[b & 1][kt] = state_operand<N>(sK, kt, b >> 1, b & 1);
+    };
     bf16x8 U[2];
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) U[kt] = pack8(A[2 * kt], A[2 * kt + 1]);
     if (kY) {
+      Split u[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        O[t] *= G.ef[16 * t + lr];
-#pragma unroll
-        for (int kt = 0; kt <= t / 2; ++kt)
-          O[t] = mfma(U[kt], lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
+      for (int kt = 0; kt < 2; ++kt) {
+        u[kt] = split8(A[2 * kt], A[2 * kt + 1]);
+        U[kt] = u[kt].hi;
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) O[t] *= G.ef[16 * t + lr];
+#pragma unroll
+      for (int step = 0; step < 2; ++step)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int t = 2 * kt; t < 4; ++t)
+            O[t] = mfma(step ? u[kt].lo : u[kt].hi, lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
+    } else {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) U[kt] = pack8(A[2 * kt], A[2 * kt + 1]);
     }
     // the state: rows of U fall by e^{gam_c - gam}
+    columns(0);
     Split D[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
       D[kt] = split8(A[2 * kt] * ldf4(G.lf + 32 * kt + 4 * lg),
                      A[2 * kt + 1] * ldf4(G.lf + 32 * kt + 16 + 4 * lg));
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        S[ks][par] *= ec;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const bf16x8 k = state_operand<N>(sK, kt, ks, par);
-          S[ks][par] = mfma(k, D[kt].hi, S[ks][par]);
-          S[ks][par] = mfma(k, D[kt].lo, S[ks][par]);
-        }
-        if (kPad && 32 * ks + 8 * lg >= a.N)  // columns past N were staged from others
-          S[ks][par] = kZero4;
-      }
+    for (int b = 0; b < 2 * NK; ++b) {
+      if (b + 1 < 2 * NK) columns(b + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 s = S[b >> 1][b & 1] * ec;
+      s = mfma(kT[b & 1][0], D[0].hi, s);
+      s = mfma(kT[b & 1][0], D[0].lo, s);
+      s = mfma(kT[b & 1][1], D[1].hi, s);
+      S[b >> 1][b & 1] = mfma(kT[b & 1][1], D[1].lo, s);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if (kY) {
-      bf16 *y = (bf16 *)a.y + ((size_t)at * a.H + h) * a.P + p0 + 4 * lg;
+      bf16 *y = (bf16 *)a.y + ((size_t)at * a.H + h) * a.P + p0;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         if (16 * t + lr < len)
-          *reinterpret_cast<uint2 *>(y + (size_t)(16 * t + lr) * ldx) =
-              make_uint2(pack2(O[t][0], O[t][1]), pack2(O[t][2], O[t][3]));
+          store_at(y + 16 * t * ldx, (uint32_t)(lr * (int)ldx + 4 * lg) * 2u,
+                   make_uint2(pack2(O[t][0], O[t][1]), pack2(O[t][2], O[t][3])));
     } else if (!kLocal) {
-      bf16 *u = (bf16 *)a.u + (((size_t)(w.slot + c) * a.H + h) * a.P + p) * kDeltaChunk + 4 * lg;
+      bf16 *u = (bf16 *)a.u + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
         const u32x4 v = __builtin_bit_cast(u32x4, U[kt]);
-        *reinterpret_cast<uint2 *>(u + 32 * kt) = make_uint2(v[0], v[1]);
-        *reinterpret_cast<uint2 *>(u + 32 * kt + 16) = make_uint2(v[2], v[3]);
+        const uint32_t off = (uint32_t)(lr * kDeltaChunk + 4 * lg) * 2u;
+        store_at(u + 32 * kt, off, make_uint2(v[0], v[1]));
+        store_at(u + 32 * kt + 16, off, make_uint2(v[2], v[3]));
       }
     }
     if (c + 1 < chunks) {
@@ -335,13 +347,14 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
 //   dS <- e^{gam_c} dS + Q^T (e^gam dY) - K^T (beta e^gam dR)
 // Writes dS behind each chunk, dR, and the initial state's gradient; or
 // (kLocal) a segment's dS at its start from zeros at its end.
-template <int NK, int WV, bool kPad, bool kLocal>
+template <int NK, int WV, bool kLocal>
 __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(DeltaArgs a) {
   constexpr int N = 32 * NK, W = 16 * WV;
   constexpr int kT = 2 * kTriTiles * kTileElems;
   __shared__ bf16 sK[kDeltaChunk * N], sQ[kDeltaChunk * N], sT[kT], sV[kDeltaChunk * W];
   __shared__ Gates G;
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = a.P / W;
   int unit = xcd_unit();
   const int pw = (unit % blocks) * W, p0 = pw + 16 * wave, p = p0 + lr;
@@ -380,8 +393,8 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
   const auto fetch_rows = [&](int c) __attribute__((always_inline)) {
     const int64_t at = rows_at(c);
     const int len = length(c);
-    stage_async<N, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
-    stage_async<N, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
+    stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
+    stage_tile<N, kDeltaChunk, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
   };
   const auto fetch_rest = [&](int c) __attribute__((always_inline)) {
     const int64_t at = rows_at(c);
@@ -391,7 +404,7 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
       g = ((const uint16_t *)a.g)[ga];
       bt = ((const uint16_t *)a.beta)[ga];
     }
-    stage_async<W, WV>(sV, (const bf16 *)a.dy + ((size_t)at * a.H + h) * a.P + pw, ldx, W, len);
+    stage_tile<W, kDeltaChunk, WV>(sV, (const bf16 *)a.dy + ((size_t)at * a.H + h) * a.P + pw, ldx, W, len);
     stage_block<WV>(sT, tri_at(c) + kT, 2 * kTriTiles);
   };
   if (chunks > 0) {
@@ -403,77 +416,93 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
     wait_vmem_all();
     if (wave == 0) fill_gates(G, bits_to_f32(g), bits_to_f32(bt), lane < len);
     __syncthreads();
-    const bf16 *m = tri_at(c) + 2 * kT + 8 * lane;
-    bf16x8 Mh[kTriTiles], Ml[kTriTiles];
-#pragma unroll
-    for (int k = 0; k < kTriTiles; ++k) {
-      Mh[k] = ldg8(m + 2 * k * kTileElems);
-      Ml[k] = ldg8(m + (2 * k + 1) * kTileElems);
-    }
-    // dY as it is, rows past the end as zeros
+    // dY as it is (rows past the end are zeros)
     bf16x8 Y[2];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      Y[kt] = value_operand<W>(sV, kt, p0 - pw);
-      if (len < kDeltaChunk)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (32 * kt + 16 * (e >> 2) + 4 * lg + (e & 3) >= len) Y[kt][e] = (bf16)0.f;
-    }
+    for (int kt = 0; kt < 2; ++kt) Y[kt] = value_operand<W>(sV, kt, p0 - pw);
     f32x4 A[4];
+    {
+      bf16x8 kb[2][2];
+      const auto keys = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) A[t] = kZero4;
+        for (int u = 0; u < 2; ++u)
+          kb[b & 1][u] = *reinterpret_cast<const bf16x8 *>(
+              sK + place<N>(32 * (b & 1) + 16 * u + lr, 32 * (b >> 1) + 8 * lg));
+      };
+      keys(0);
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      const Split s = split8(S[ks][0], S[ks][1]);
-      if (!kLocal && 32 * ks + 8 * lg < a.N)
-        *reinterpret_cast<bf16x8 *>((bf16 *)a.st1 +
-                                    (((size_t)(w.slot + c) * a.H + h) * a.P + p) * a.N + 32 * ks +
-                                    8 * lg) = s.hi;
+      for (int t = 0; t < 4; ++t) A[t] = kZero4;
+      Split s;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const bf16x8 k =
-            *reinterpret_cast<const bf16x8 *>(sK + rswz<N>(16 * t + lr, 32 * ks + 8 * lg));
-        A[t] = mfma(k, s.hi, A[t]);
-        A[t] = mfma(k, s.lo, A[t]);
+      for (int b = 0; b < 2 * NK; ++b) {
+        const int ks = b >> 1, t = 2 * (b & 1);
+        if (b + 1 < 2 * NK) keys(b + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if ((b & 1) == 0) {
+          s = split8(S[ks][0], S[ks][1]);
+          if (!kLocal && 32 * ks + 8 * lg < a.N)
+            store_at((bf16 *)a.st1 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks,
+                     (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.hi, A[t + u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.lo, A[t + u]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    bf16x8 Mh[kTriTiles], Ml[kTriTiles];
+    {
+      const bf16 *m = tri_at(c) + 2 * kT + 8 * lane;
+#pragma unroll
+      for (int k = 0; k < kTriTiles; ++k) {
+        Mh[k] = ldg8(m + 2 * k * kTileElems);
+        Ml[k] = ldg8(m + (2 * k + 1) * kTileElems);
       }
     }
     Split U[2];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
+    for (int t = 0; t < 4; ++t) A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
 #pragma unroll
-      for (int kt = t / 2; kt < 2; ++kt) {
-        const int k = upper_tile(t, kt);
-        A[t] = mfma(upper_operand(Mh[k], t, kt), Y[kt], A[t]);
-        A[t] = mfma(upper_operand(Ml[k], t, kt), Y[kt], A[t]);
-      }
-    }
+    for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int t = 0; t < 2 * kt + 2; ++t)
+          A[t] = mfma(upper_operand(lo ? Ml[upper_tile(t, kt)] : Mh[upper_tile(t, kt)], t, kt),
+                      Y[kt], A[t]);
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
+    __builtin_amdgcn_sched_barrier(0);
+    bf16x8 Th[kTriTiles], Tl[kTriTiles];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      A[t] = kZero4;
+    for (int k = 0; k < kTriTiles; ++k)
+      Th[k] = *reinterpret_cast<const bf16x8 *>(sT + 2 * k * kTileElems + 8 * lane);
 #pragma unroll
-      for (int kt = t / 2; kt < 2; ++kt) {
-        const bf16 *q = sT + (upper_tile(t, kt) * 2) * kTileElems + 8 * lane;
-        const bf16x8 th = upper_operand(*reinterpret_cast<const bf16x8 *>(q), t, kt);
-        const bf16x8 tl = upper_operand(*reinterpret_cast<const bf16x8 *>(q + kTileElems), t, kt);
-        A[t] = mfma(th, U[kt].hi, A[t]);
-        A[t] = mfma(th, U[kt].lo, A[t]);
-        A[t] = mfma(tl, U[kt].hi, A[t]);
-      }
-    }
+    for (int k = 0; k < kTriTiles; ++k)
+      Tl[k] = *reinterpret_cast<const bf16x8 *>(sT + (2 * k + 1) * kTileElems + 8 * lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) A[t] = kZero4;
+#pragma unroll
+    for (int step = 0; step < 3; ++step)
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int t = 0; t < 2 * kt + 2; ++t) {
+          const int k = upper_tile(t, kt);
+          A[t] = mfma(upper_operand(step == 2 ? Tl[k] : Th[k], t, kt),
+                      step == 1 ? U[kt].lo : U[kt].hi, A[t]);
+        }
     if (c > 0) {
       __syncthreads();
       fetch_rest(c - 1);
     }
     if (!kLocal) {
-      bf16 *dr = (bf16 *)a.dr + (((size_t)(w.slot + c) * a.H + h) * a.P + p) * kDeltaChunk + 4 * lg;
+      bf16 *dr = (bf16 *)a.dr + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        *reinterpret_cast<uint2 *>(dr + 16 * t) =
-            make_uint2(pack2(A[t][0], A[t][1]), pack2(A[t][2], A[t][3]));
+        store_at(dr + 16 * t, (uint32_t)(lr * kDeltaChunk + 4 * lg) * 2u,
+                 make_uint2(pack2(A[t][0], A[t][1]), pack2(A[t][2], A[t][3])));
     }
     Split E[2], D[2];
 #pragma unroll
@@ -491,22 +520,30 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
       D[kt] = split8(d[0], d[1]);
     }
     const float ec = G.ef[kDeltaChunk - 1];
+    bf16x8 kT[2][2], qT[2][2];  // of a block of 16 channels, the next one's under way
+    const auto columns = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        S[ks][par] *= ec;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const bf16x8 q = state_operand<N>(sQ, kt, ks, par);
-          S[ks][par] = mfma(q, E[kt].hi, S[ks][par]);
-          S[ks][par] = mfma(q, E[kt].lo, S[ks][par]);
-          const bf16x8 k = state_operand<N>(sK, kt, ks, par);
-          S[ks][par] = mfma(k, D[kt].hi, S[ks][par]);
-          S[ks][par] = mfma(k, D[kt].lo, S[ks][par]);
-        }
-        if (kPad && 32 * ks + 8 * lg >= a.N) S[ks][par] = kZero4;
+      for (int kt = 0; kt < 2; ++kt) {
+        kT[b & 1][kt] = state_operand<N>(sK, kt, b >> 1, b & 1);
+        qT[b & 1][kt] = state_operand<N>(sQ, kt, b >> 1, b & 1);
       }
+    };
+    columns(0);
+#pragma unroll
+    for (int b = 0; b < 2 * NK; ++b) {
+      if (b + 1 < 2 * NK) columns(b + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 s = S[b >> 1][b & 1] * ec;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        s = mfma(qT[b & 1][kt], E[kt].hi, s);
+        s = mfma(kT[b & 1][kt], D[kt].hi, s);
+        s = mfma(qT[b & 1][kt], E[kt].lo, s);
+        s = mfma(kT[b & 1][kt], D[kt].lo, s);
+      }
+      S[b >> 1][b & 1] = s;
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if (c > 0) {
       __syncthreads();
       fetch_rows(c - 1);
@@ -530,15 +567,18 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
 // The states at the segments' starts, in place of their own final states: with
 // F a segment's transition, S <- F S + (its own). kBack: dL/dS at the segments'
 // ends, dS <- F^T dS + (its own), from the last to the first. Per (sequence,
-// head) and 16 columns a workgroup; wave w holds the state channels of tiles
-// w, w + 4, ...; the state goes round through LDS, in fp32 throughout. `span`
-// has a transition's columns as rows: span[P + j][n] = F[n][j].
-template <bool kBack>
-__global__ __launch_bounds__(256) void k_delta_join(DeltaArgs a) {
-  constexpr int kMost = 4;  // tiles of a wave, N <= 256
-  __shared__ float sS[2][256][17];
+// head) and 16 columns a workgroup of WV waves, in fp32 throughout; wave w holds
+// the state channels of tiles w, w + WV, ...; the state goes round through LDS.
+// A transition does not depend on the state: the next one is on its way into
+// registers while one is used (without that, 16 segments of 32 heads took 130 us
+// instead of the figure beside launch_delta_forward). `span` has a transition's
+// columns as rows: span[P + j][n] = F[n][j].
+template <int NT, int WV, bool kBack>
+__global__ __launch_bounds__(64 * WV) void k_delta_join(DeltaArgs a) {
+  constexpr int kOwn = NT / WV;  // tiles of a wave
+  __shared__ float sS[2][16 * NT][17];
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wave = threadIdx.x >> 6;
-  const int blocks = a.P / 16, tiles = a.N / 16;
+  const int blocks = a.P / 16;
   int unit = blockIdx.x;
   const int p = (unit % blocks) * 16 + lr;
   unit /= blocks;
@@ -549,88 +589,92 @@ __global__ __launch_bounds__(256) void k_delta_join(DeltaArgs a) {
   const int first = a.cu ? (int)(lo / len) + seq : seq * a.nseg_per;
   const int n = max(1, (int)((hi - lo + len - 1) / len));
   const float *init = kBack ? a.dhT : a.h0;
-  f32x4 S[kMost];
+  const auto place_of = [&](int c) { return (size_t)(first + (kBack ? n - 1 - c : c)) * a.H + h; };
+  f32x4 S[kOwn], F[kOwn][NT], own[kOwn];
+  const auto fetch = [&](int c) __attribute__((always_inline)) {
+    const size_t at = place_of(c);
+    const float *from = kBack ? a.dspan + (at * a.P + p) * a.N : a.span + (at * (a.P + a.N) + p) * a.N;
+    const float *f = a.span + (at * (a.P + a.N) + a.P) * a.N;
 #pragma unroll
-  for (int k = 0; k < kMost; ++k) {
-    const int t = wave + 4 * k;
-    if (t >= tiles) break;
-    S[k] = init ? ldf4(init + (((size_t)seq * a.H + h) * a.P + p) * a.N + 16 * t + 4 * lg) : kZero4;
-  }
-  for (int c = 0; c < n; ++c) {
-    const int sg = first + (kBack ? n - 1 - c : c);
-    const size_t at = (size_t)sg * a.H + h;
-    float *own = kBack ? a.dspan + (at * a.P + p) * a.N : a.span + (at * (a.P + a.N) + p) * a.N;
-    const float *F = a.span + (at * (a.P + a.N) + a.P) * a.N;
-    float (*s)[17] = sS[c & 1];
-    f32x4 next[kMost];
-    const bool more = c + 1 < n;
+    for (int k = 0; k < kOwn; ++k) {
+      const int t = 16 * (wave + WV * k);
+      if (t >= a.N) continue;
+      own[k] = ldf4(from + t + 4 * lg);
 #pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-      const int t = wave + 4 * k;
-      if (t >= tiles) break;
-      if (more) next[k] = ldf4(own + 16 * t + 4 * lg);
-      stf4(own + 16 * t + 4 * lg, S[k]);
+      for (int j = 0; j < NT; ++j) {
+        if (16 * j >= a.N) continue;
+        if (kBack) {
+          F[k][j] = ldf4(f + (size_t)(t + lr) * a.N + 16 * j + 4 * lg);
+        } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[16 * t + 4 * lg + r][lr] = S[k][r];
+          for (int r = 0; r < 4; ++r) F[k][j][r] = f[(size_t)(16 * j + 4 * lg + r) * a.N + t + lr];
+        }
+      }
     }
-    if (!more) break;
+  };
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int t = 16 * (wave + WV * k);
+    S[k] = init && t < a.N ? ldf4(init + (((size_t)seq * a.H + h) * a.P + p) * a.N + t + 4 * lg)
+                           : kZero4;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) F[k][j] = kZero4;
+    own[k] = kZero4;
+  }
+  if (n > 1) fetch(0);
+  for (int c = 0; c < n; ++c) {
+    const size_t at = place_of(c);
+    float *to = kBack ? a.dspan + (at * a.P + p) * a.N : a.span + (at * (a.P + a.N) + p) * a.N;
+    float (*s)[17] = sS[c & 1];
+    f32x4 next[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int t = 16 * (wave + WV * k);
+      next[k] = own[k];
+      if (t < a.N) stf4(to + t + 4 * lg, S[k]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[t + 4 * lg + r][lr] = S[k][r];
+    }
+    if (c + 1 == n) break;
     __syncthreads();
-    for (int j = 0; j < tiles; ++j) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
       f32x4 b;
 #pragma unroll
       for (int r = 0; r < 4; ++r) b[r] = s[16 * j + 4 * lg + r][lr];
 #pragma unroll
-      for (int k = 0; k < kMost; ++k) {
-        const int t = wave + 4 * k;
-        if (t >= tiles) break;
-        f32x4 f;
-        if (kBack) {
-          f = ldf4(F + (size_t)(16 * t + lr) * a.N + 16 * j + 4 * lg);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) f[r] = F[(size_t)(16 * j + 4 * lg + r) * a.N + 16 * t + lr];
-        }
-        next[k] = mfma16(f, b, next[k]);
-      }
+      for (int k = 0; k < kOwn; ++k) next[k] = mfma16(F[k][j], b, next[k]);
     }
+    if (c + 2 < n) fetch(c + 1);
 #pragma unroll
-    for (int k = 0; k < kMost; ++k) S[k] = next[k];
+    for (int k = 0; k < kOwn; ++k) S[k] = next[k];
   }
 }
 
 enum Walk : int { kY, kSave, kLocal, kBack, kBackLocal };
 
-template <int NK, int WV, bool kPad>
+template <int NK, int WV>
 hipError_t walk_launch(const DeltaArgs &a, Walk what, hipStream_t s) {
   const int tiles = (what == kLocal ? a.P + a.N : a.P) / 16;
   const int64_t units = (int64_t)(a.seg ? a.nsegs : a.nseq) * a.H;
   const dim3 grid((unsigned)(units * ((tiles + WV - 1) / WV))), block(64 * WV);
   switch (what) {
-    case kY: hipLaunchKernelGGL((k_delta_walk<NK, WV, kPad, kWalkY>), grid, block, 0, s, a); break;
-    case kSave:
-      hipLaunchKernelGGL((k_delta_walk<NK, WV, kPad, kWalkSave>), grid, block, 0, s, a);
-      break;
+    case kY: hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkY>), grid, block, 0, s, a); break;
+    case kSave: hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkSave>), grid, block, 0, s, a); break;
     case kLocal:
-      hipLaunchKernelGGL((k_delta_walk<NK, WV, kPad, kWalkLocal>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkLocal>), grid, block, 0, s, a);
       break;
-    case kBack:
-      hipLaunchKernelGGL((k_delta_back<NK, WV, kPad, false>), grid, block, 0, s, a);
-      break;
-    case kBackLocal:
-      hipLaunchKernelGGL((k_delta_back<NK, WV, kPad, true>), grid, block, 0, s, a);
-      break;
+    case kBack: hipLaunchKernelGGL((k_delta_back<NK, WV, false>), grid, block, 0, s, a); break;
+    case kBackLocal: hipLaunchKernelGGL((k_delta_back<NK, WV, true>), grid, block, 0, s, a); break;
   }
   return hipGetLastError();
 }
 
 template <int NK>
 hipError_t walk_n(const DeltaArgs &a, Walk what, hipStream_t s) {
-  const bool pad = a.N != 32 * NK;
-  if (a.P == 16)
-    return pad ? walk_launch<NK, 1, true>(a, what, s) : walk_launch<NK, 1, false>(a, what, s);
-  if (a.P == 32)
-    return pad ? walk_launch<NK, 2, true>(a, what, s) : walk_launch<NK, 2, false>(a, what, s);
-  return pad ? walk_launch<NK, 4, true>(a, what, s) : walk_launch<NK, 4, false>(a, what, s);
+  if (a.P == 16) return walk_launch<NK, 1>(a, what, s);
+  if (a.P == 32) return walk_launch<NK, 2>(a, what, s);
+  return walk_launch<NK, 4>(a, what, s);
 }
 
 hipError_t walk(const DeltaArgs &a, Walk what, hipStream_t s) {
@@ -640,13 +684,20 @@ hipError_t walk(const DeltaArgs &a, Walk what, hipStream_t s) {
   return walk_n<8>(a, what, s);
 }
 
-hipError_t join(const DeltaArgs &a, bool back, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.nseq * a.H * (a.P / 16))), block(256);
+template <int NT, int WV>
+hipError_t join_n(const DeltaArgs &a, bool back, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.nseq * a.H * (a.P / 16))), block(64 * WV);
   if (back)
-    hipLaunchKernelGGL(k_delta_join<true>, grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_delta_join<NT, WV, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL(k_delta_join<false>, grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_delta_join<NT, WV, false>), grid, block, 0, s, a);
   return hipGetLastError();
+}
+
+hipError_t join(const DeltaArgs &a, bool back, hipStream_t s) {
+  if (a.N <= 64) return join_n<4, 4>(a, back, s);
+  if (a.N <= 128) return join_n<8, 4>(a, back, s);
+  return join_n<16, 8>(a, back, s);
 }
 
 void delta_segments(DeltaArgs &a, bool packed) {

@@ -24,31 +24,6 @@
 namespace ssd {
 namespace {
 
-// Swizzled place of (row, col) in rows of W elements.
-template <int W>
-__device__ __forceinline__ int place(int row, int col) {
-  constexpr int kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
-  return row * W + (((col >> 3) ^ (row & kMask)) << 3) + (col & 7);
-}
-
-// ROWS rows of W columns (columns past n and rows past len read as others).
-template <int W, int ROWS>
-__device__ __forceinline__ void stage(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
-  constexpr int R = 512 / W, NI = ROWS / R, kMask = W / 8 - 1 < 7 ? W / 8 - 1 : 7;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rl = lane / (W / 8), pc = lane % (W / 8);
-  const char *base = reinterpret_cast<const char *>(src);
-#pragma unroll
-  for (int k = 0; k < (NI + 3) / 4; ++k) {
-    const int m = wave + 4 * k;
-    if (NI % 4 != 0 && m >= NI) break;
-    const int s = m * R + rl, c = min(pc ^ (s & kMask), n / 8 - 1);
-    const uint32_t off = (uint32_t)min(s, len - 1) * (uint32_t)(ld * 2) + 16u * (uint32_t)c;
-    __builtin_amdgcn_global_load_lds(base + off, (lds_void *)(tile + m * 512), 16, 0, 0);
-  }
-}
-
 // Eight of a row, and a column's rows r0 + 8 lg + e (natural order) or
 // r0 + 16 (e / 4) + 4 lg + e % 4 (the order of result tiles).
 template <int W>
@@ -118,20 +93,21 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
   for (int nb = 0; nb < NK; ++nb)
 #pragma unroll
     for (int par = 0; par < 2; ++par) dQ[nb][par] = dK[nb][par] = kZero4;
-  stage<N, C>(sK, (const bf16 *)a.B + ((size_t)start * a.G + grp) * a.N, ldk, a.N, len);
-  stage<N, C>(sQ, (const bf16 *)a.C + ((size_t)start * a.G + grp) * a.N, ldk, a.N, len);
+  stage_tile<N, C, 4>(sK, (const bf16 *)a.B + ((size_t)start * a.G + grp) * a.N, ldk, a.N, len);
+  stage_tile<N, C, 4>(sQ, (const bf16 *)a.C + ((size_t)start * a.G + grp) * a.N, ldk, a.N, len);
 
   for (int h = h0; h < h1; ++h) {
     const size_t sh = (size_t)slot * a.H + h;
     const bf16 *S0 = (const bf16 *)a.st0 + sh * a.P * a.N, *S1 = (const bf16 *)a.st1 + sh * a.P * a.N;
     const auto fetch = [&](int nb, bf16 *A, bf16 *B) __attribute__((always_inline)) {
-      stage<32, P>(A, S0 + 32 * nb, a.N, min(32, a.N - 32 * nb), a.P);
-      stage<32, P>(B, S1 + 32 * nb, a.N, min(32, a.N - 32 * nb), a.P);
+      const int n = max(min(32, a.N - 32 * nb), 0);
+      stage_tile<32, P, 4>(A, S0 + 32 * nb, a.N, n, a.P);
+      stage_tile<32, P, 4>(B, S1 + 32 * nb, a.N, n, a.P);
     };
     if (h > h0) __syncthreads();
-    stage<P, C>(sY, (const bf16 *)a.dy + ((size_t)start * a.H + h) * a.P, ldx, a.P, len);
-    stage<C, P>(sU, (const bf16 *)a.u + sh * a.P * C, C, C, a.P);
-    stage<C, P>(sR, (const bf16 *)a.dr + sh * a.P * C, C, C, a.P);
+    stage_tile<P, C, 4>(sY, (const bf16 *)a.dy + ((size_t)start * a.H + h) * a.P, ldx, a.P, len);
+    stage_tile<C, P, 4>(sU, (const bf16 *)a.u + sh * a.P * C, C, C, a.P);
+    stage_tile<C, P, 4>(sR, (const bf16 *)a.dr + sh * a.P * C, C, C, a.P);
     fetch(0, sA0, sB0);
     if (w == 0) {
       const size_t ga = (size_t)(start + min(lane, len - 1)) * a.H + h;
@@ -142,7 +118,7 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
     wait_vmem_all();
     __syncthreads();
 
-    // this token's rows of dY, dR, U (zeros past the end and past P)
+    // this token's rows of dY, dR, U (what is staged past the end and past P is zeros)
     bf16x8 yo[PK], ro[PK], uo[PK];
     const float bi = sBt[own], gi = sG[own], gc = sG[C - 1];
     const float ef = exp2_fast(gi), lf = exp2_fast(gc - gi), be = bi * ef;
@@ -153,8 +129,6 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
       yo[ps] = row8<P>(sY, own, 32 * ps + 8 * lg);
       ro[ps] = column8<C>(sR, 32 * ps, 16 * w);
       uo[ps] = column8<C>(sU, 32 * ps, 16 * w);
-      if (!in || !live) yo[ps] = zero8();
-      if (!in) ro[ps] = uo[ps] = zero8();
       if (in && live) {
         const size_t at = (tok * a.H + h) * a.P + 32 * ps + 8 * lg;
         rv += dot8(ro[ps], ldg8((const bf16 *)a.x + at));
@@ -178,7 +152,6 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
       for (int ks = 0; ks < NK; ++ks) {
         ko[ks] = row8<N>(sK, own, 32 * ks + 8 * lg);
         qo[ks] = row8<N>(sQ, own, 32 * ks + 8 * lg);
-        if (32 * ks + 8 * lg >= a.N) ko[ks] = qo[ks] = zero8();
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -250,11 +223,10 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
           ys = mfma(s0, yo[ps], ys);
           rs = mfma(s0, ro[ps], rs);
           us = mfma(s1, uo[ps], us);
-          if (((2 * nb + par) & 3) == w && n0 < a.N && 32 * ps + 8 * lg < a.P) ss += dot8(s0, s1);
+          if (((2 * nb + par) & 3) == w) ss += dot8(s0, s1);
         }
         const bf16x4 k4 = *reinterpret_cast<const bf16x4 *>(sK + place<N>(own, n0 + 4 * lg));
         const bf16x4 q4 = *reinterpret_cast<const bf16x4 *>(sQ + place<N>(own, n0 + 4 * lg));
-        if (n0 < a.N)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             zq += (float)q4[r] * ys[r];
@@ -282,9 +254,9 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
     for (int nb = 0; nb < NK; ++nb) {
       if (nb + 1 < NK) {
         if (nb & 1)
-          fetch(min(nb + 1, (a.N - 1) / 32), sA0, sB0);
+          fetch(nb + 1, sA0, sB0);
         else
-          fetch(min(nb + 1, (a.N - 1) / 32), sA1, sB1);
+          fetch(nb + 1, sA1, sB1);
       }
       if (nb & 1)
         block(nb, sA1, sB1);

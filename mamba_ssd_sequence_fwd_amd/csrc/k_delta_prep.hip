@@ -1,9 +1,10 @@
 // k_delta_prep.hip -- the triangular matrices of each chunk of the gated delta
 // rule: T = (I + L)^-1 and M (delta.h), or T, T^T and M^T for the backward pass.
 //
-// One wave takes one chunk and head. Q K^T and K K^T are kept in registers as
-// 16 x 16 tiles on and below the diagonal, transposed: a lane holds 4
-// consecutive columns j of one row i. In that layout a tile of L is the left operand of
+// A workgroup takes one chunk and some heads of one group. Q K^T and K K^T, which
+// those share, are computed once, as 16 x 16 tiles on and below the diagonal,
+// transposed: a lane holds 4 consecutive columns j of one row i. Each wave then
+// takes heads in turn. In that layout a tile of L is the left operand of
 // the fp32 matrix instruction (lane l: row l % 16, columns 4 (l / 16) + r at
 // step r) and a result tile its right operand, so the block inversion
 //   T_ij = -T_ii sum_{j <= k < i} L_ik T_kj
@@ -19,56 +20,64 @@
 
 namespace ssd {
 
+// LDS accesses of one wave before and after stay in order (they run in order).
+__device__ __forceinline__ void wave_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Index of lower tile (i, j), j <= i.
 __host__ __device__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
 
-// acc[tri(i, j)] = rows j of X against rows i of Y (lane: row i % 16, 4
-// columns j), or with kSwap the other way round (lane: row j % 16, 4 columns
-// i). 64 rows each, `ld` apart, N columns, rows past len read as the last one.
-template <bool kSwap, typename T>
-__device__ __forceinline__ void tri_product(const T *X, const T *Y, size_t ld, int N, int len,
-                                            f32x4 (&acc)[10]) {
+// Tiles (i, j), j <= i, of one product: rows j of X against rows i of Y (lane:
+// row i % 16, 4 columns j), or with kSwap the other way round (lane: row j % 16,
+// 4 columns i). 64 rows each, `ld` apart, N columns, rows past len read as the
+// last one. The tiles go to LDS in lane order, tile (i, j) at tri(i, j).
+template <bool kSwap, int I, typename T>
+__device__ __forceinline__ void tile_row(const T *X, const T *Y, size_t ld, int N, int len,
+                                         f32x4 (*out)[64]) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  f32x4 acc[I + 1];
 #pragma unroll
-  for (int e = 0; e < 10; ++e) acc[e] = kZero4;
-  size_t row[4];
+  for (int j = 0; j <= I; ++j) acc[j] = kZero4;
+  size_t row[I + 1];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) row[t] = (size_t)min(16 * t + lr, len - 1) * ld;
+  for (int j = 0; j <= I; ++j) row[j] = (size_t)min(16 * j + lr, len - 1) * ld;
   if constexpr (sizeof(T) == 2) {
-#pragma unroll 2
+#pragma unroll 4
     for (int n0 = 0; n0 < N; n0 += 32) {
-      bf16x8 x[4], y[4];
-      const int col = n0 + 8 * lg;
+      const int col = n0 + 8 * lg, at = min(col, N - 8);
+      bf16x8 y = ldg8((const bf16 *)Y + row[I] + at);
+      if (col >= N) y = zero8();
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        x[t] = ldg8((const bf16 *)X + row[t] + min(col, N - 8));
-        y[t] = X == Y ? x[t] : ldg8((const bf16 *)Y + row[t] + min(col, N - 8));
+      for (int j = 0; j <= I; ++j) {
+        const bf16x8 x = ldg8((const bf16 *)X + row[j] + at);
+        acc[j] = kSwap ? mfma(y, x, acc[j]) : mfma(x, y, acc[j]);
       }
-      if (n0 + 32 > N && col >= N)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) x[t] = y[t] = zero8();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i; ++j)
-          acc[tri(i, j)] = kSwap ? mfma(y[i], x[j], acc[tri(i, j)]) : mfma(x[j], y[i], acc[tri(i, j)]);
     }
   } else {
-#pragma unroll 2
+#pragma unroll 4
     for (int n0 = 0; n0 < N; n0 += 16) {
-      f32x4 x[4], y[4];
+      const f32x4 y = ldf4((const float *)Y + row[I] + n0 + 4 * lg);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        x[t] = ldf4((const float *)X + row[t] + n0 + 4 * lg);
-        y[t] = X == Y ? x[t] : ldf4((const float *)Y + row[t] + n0 + 4 * lg);
+      for (int j = 0; j <= I; ++j) {
+        const f32x4 x = ldf4((const float *)X + row[j] + n0 + 4 * lg);
+        acc[j] = kSwap ? mfma16(y, x, acc[j]) : mfma16(x, y, acc[j]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i; ++j)
-          acc[tri(i, j)] =
-              kSwap ? mfma16(y[i], x[j], acc[tri(i, j)]) : mfma16(x[j], y[i], acc[tri(i, j)]);
     }
+  }
+#pragma unroll
+  for (int j = 0; j <= I; ++j) out[tri(I, j)][lane] = acc[j];
+}
+template <bool kSwap, typename T>
+__device__ __forceinline__ void tile_row(int i, const T *X, const T *Y, size_t ld, int N, int len,
+                                         f32x4 (*out)[64]) {
+  switch (i) {
+    case 0: return tile_row<kSwap, 0>(X, Y, ld, N, len, out);
+    case 1: return tile_row<kSwap, 1>(X, Y, ld, N, len, out);
+    case 2: return tile_row<kSwap, 2>(X, Y, ld, N, len, out);
+    default: return tile_row<kSwap, 3>(X, Y, ld, N, len, out);
   }
 }
 
@@ -121,56 +130,75 @@ struct TilesOut {
   }
 };
 
-template <typename T, DeltaTri W, typename Out>
-__global__ __launch_bounds__(64, 4) void k_delta_prep(DeltaArgs a, int64_t bytes) {
-  __shared__ float sG[kDeltaChunk], sB[kDeltaChunk];
-  __shared__ f32x4 sD[4][16][5];  // diagonal blocks: rows of L, then columns of T
-  const int lane = threadIdx.x, lr = lane & 15, lg = lane >> 4;
-  const int unit = xcd_unit(), h = unit % a.H, slot = unit / a.H, grp = h / a.hpg;
+template <typename T, DeltaTri W, int WV, typename Out>
+__global__ __launch_bounds__(64 * WV, 4) void k_delta_prep(DeltaArgs a, int64_t bytes, int per) {
+  __shared__ f32x4 sKK[10][64], sQK[10][64];
+  __shared__ float sGate[WV][2][kDeltaChunk];
+  __shared__ f32x4 sDiag[WV][4][16][5];  // diagonal blocks: rows of L, then columns of T
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int parts = (a.hpg + WV * per - 1) / (WV * per);
+  int unit = xcd_unit();
+  const int part = unit % parts;
+  unit /= parts;
+  const int grp = unit % a.G, slot = unit / a.G;
   int64_t start;
   int len;
   if (!delta_chunk(a, slot, start, len)) return;
-  stage_gates<T>(sG, sB, a, start, h, len);
   const size_t row0 = ((size_t)start * a.G + grp) * a.N, ld = (size_t)a.G * a.N;
   const T *K = (const T *)a.B + row0, *Q = (const T *)a.C + row0;
-  Out out;
-  out.p = reinterpret_cast<decltype(out.p)>((char *)a.tri + ((int64_t)slot * a.H + h) * bytes);
-
-  {  // M, or M^T (lane holds column j, 4 rows i)
-    f32x4 qk[10];
-    tri_product<W == kTriBackward, T>(K, Q, ld, a.N, len, qk);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j <= i; ++j) {
-        const float ga = sG[16 * (W == kTriForward ? i : j) + lr];
-        const f32x4 gb = ldf4(sG + 16 * (W == kTriForward ? j : i) + 4 * lg);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool below = j < i || (W == kTriForward ? 4 * lg + r <= lr : lr <= 4 * lg + r);
-          const float e = exp2_fast(W == kTriForward ? ga - gb[r] : gb[r] - ga);
-          qk[tri(i, j)][r] = below ? qk[tri(i, j)][r] * e : 0.f;
-        }
-      }
-    if (W == kTriForward)
-      out.template put<1, false, false>(qk);
-    else
-      out.template put<2, true, true>(qk);
+  // the group's products, a row of one and a row of the other (five tiles) at a time
+  for (int v = wave * 4 / WV; v < (wave + 1) * 4 / WV; ++v) {
+    tile_row<false>(3 - v, K, K, ld, a.N, len, sKK);
+    tile_row<W == kTriBackward>(v, K, Q, ld, a.N, len, sQK);
   }
-  {
+  __syncthreads();
+  float *sG = sGate[wave][0], *sB = sGate[wave][1];
+  f32x4 (*sD)[16][5] = sDiag[wave];
+  const int h1 = min((part + 1) * WV * per, a.hpg);
+  for (int hh = part * WV * per + wave; hh < h1; hh += WV) {
+    const int h = grp * a.hpg + hh;
+    {
+      const size_t at = (size_t)(start + min(lane, len - 1)) * a.H + h;
+      const float gl = lane < len ? delta_log2_decay(ssd::ld<T>(a.g, at)) : 0.f;
+      sG[lane] = wave_inclusive_sum(gl);
+      sB[lane] = lane < len ? ssd::ld<T>(a.beta, at) : 0.f;
+    }
+    wave_order();
+    Out out;
+    out.p = reinterpret_cast<decltype(out.p)>((char *)a.tri + ((int64_t)slot * a.H + h) * bytes);
+    {  // M, or M^T (lane holds column j, 4 rows i)
+      f32x4 qk[10];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) {
+          qk[tri(i, j)] = sQK[tri(i, j)][lane];
+          const float ga = sG[16 * (W == kTriForward ? i : j) + lr];
+          const f32x4 gb = ldf4(sG + 16 * (W == kTriForward ? j : i) + 4 * lg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const bool below = j < i || (W == kTriForward ? 4 * lg + r <= lr : lr <= 4 * lg + r);
+            const float e = exp2_fast(W == kTriForward ? ga - gb[r] : gb[r] - ga);
+            qk[tri(i, j)][r] = below ? qk[tri(i, j)][r] * e : 0.f;
+          }
+        }
+      if (W == kTriForward)
+        out.template put<1, false, false>(qk);
+      else
+        out.template put<2, true, true>(qk);
+    }
     f32x4 Lt[10];
-    tri_product<false, T>(K, K, ld, a.N, len, Lt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float gi = sG[16 * i + lr], bi = sB[16 * i + lr];
 #pragma unroll
       for (int j = 0; j <= i; ++j) {
-        const f32x4 gj = ldf4(sG + 16 * j + 4 * lg);
+        const f32x4 gj = ldf4(sG + 16 * j + 4 * lg), kk = sKK[tri(i, j)][lane];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const bool below = j < i || 4 * lg + r < lr;
-          Lt[tri(i, j)][r] = below ? bi * Lt[tri(i, j)][r] * exp2_fast(gi - gj[r]) : 0.f;
+          Lt[tri(i, j)][r] = below ? bi * kk[r] * exp2_fast(gi - gj[r]) : 0.f;
         }
       }
     }
@@ -178,7 +206,7 @@ __global__ __launch_bounds__(64, 4) void k_delta_prep(DeltaArgs a, int64_t bytes
     // diagonal blocks: lane (b, j) = (lg, lr) takes column j of block b
 #pragma unroll
     for (int b = 0; b < 4; ++b) sD[b][lr][lg] = Lt[tri(b, b)];
-    __syncthreads();
+    wave_order();
     float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -192,11 +220,11 @@ __global__ __launch_bounds__(64, 4) void k_delta_prep(DeltaArgs a, int64_t bytes
       }
       t[i] = v;
     }
-    __syncthreads();
+    wave_order();
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       sD[lg][lr][q] = f32x4{t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]};
-    __syncthreads();
+    wave_order();
     // T: lane column j, 4 rows i; and lane row i, 4 columns j
     f32x4 Tt[10], Ta[10];
 #pragma unroll
@@ -228,12 +256,25 @@ size_t delta_tri_bytes(bool tiles, DeltaTri which) {
   return (size_t)(which == kTriForward ? 2 : 3) * 4096 * sizeof(float);
 }
 
+template <typename T, DeltaTri W, int WV, typename Out>
+hipError_t prep_wv(const DeltaArgs &a, hipStream_t s) {
+  const int64_t bytes = delta_tri_bytes(std::is_same<Out, TilesOut>::value, W);
+  // heads a wave takes in turn: more where waves are left for the card
+  const int64_t waves = (int64_t)a.nslots * a.H;
+  int per = (int)(waves / 4096);
+  const int most = (a.hpg + WV - 1) / WV;
+  per = per < 1 ? 1 : per > most ? most : per;
+  const int64_t parts = (a.hpg + WV * per - 1) / (WV * per);
+  const dim3 grid((unsigned)((int64_t)a.nslots * a.G * parts)), block(64 * WV);
+  hipLaunchKernelGGL((k_delta_prep<T, W, WV, Out>), grid, block, 0, s, a, bytes, per);
+  return hipGetLastError();
+}
+
 template <typename T, DeltaTri W, typename Out>
 hipError_t prep(const DeltaArgs &a, hipStream_t s) {
-  const int64_t bytes = delta_tri_bytes(std::is_same<Out, TilesOut>::value, W);
-  const dim3 grid((unsigned)((int64_t)a.nslots * a.H)), block(64);
-  hipLaunchKernelGGL((k_delta_prep<T, W, Out>), grid, block, 0, s, a, bytes);
-  return hipGetLastError();
+  if (a.hpg == 1) return prep_wv<T, W, 1, Out>(a, s);
+  if (a.hpg <= 3) return prep_wv<T, W, 2, Out>(a, s);
+  return prep_wv<T, W, 4, Out>(a, s);
 }
 
 hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16_io, DeltaTri which, hipStream_t s) {
