@@ -36,7 +36,8 @@ struct DeltaArgs {
   // workspace, per (chunk slot, head)
   void *tri;           // triangular matrices, tri_bytes each
   void *st0, *st1;     // backward: S and dL/dS at the chunk's start and end, (P, N)
-  void *u, *dr;        // backward: U and dL/dR, (64, P); on the bf16 path (P, 64)
+  void *u, *dr;        // backward: U and dL/dR, (64, P); on the bf16 path (P, 64),
+                       // tokens in the order of the operand tiles
   float *part;         // backward: dK, dQ of parts of a group's heads, (2, T, G parts, N)
   // workspace, per (segment, head)
   float *span;         // rows (P + N, N): first its own state and then the one at

@@ -76,7 +76,7 @@ __device__ __forceinline__ int place(int row, int col) {
 
 // ROWS rows of W columns (row stride ld; zeros from column n and row len on) into
 // such a tile, asynchronously, by WV waves; and `n` KiB in a row.
-template <int W, int ROWS, int WV>
+template <int W, int ROWS, int WV, bool kAnew = false>
 __device__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len);
 template <int WV>
 __device__ void stage_block(bf16 *to, const void *src, int n);
@@ -90,12 +90,13 @@ __device__ __forceinline__ Buffer buffer_of(const void *p, uint32_t bytes) {
 }
 
 // Only the descriptor changes from call to call: a lane's offset stays in one
-// register.
-template <int W, int ROWS, int WV>
+// register (kAnew: in none, it is worked out again).
+template <int W, int ROWS, int WV, bool kAnew>
 __device__ __forceinline__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
   constexpr int R = 512 / W, NI = ROWS / R;  // rows of an instruction, instructions
   constexpr int kSame = WV * R % 16 == 0 ? 1 : 16 / (WV * R);  // until the swizzle repeats
-  const int lane = threadIdx.x & 63;
+  int lane = threadIdx.x & 63;
+  if (kAnew) asm volatile("" : "+v"(lane));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane / (W / 8), pc = lane % (W / 8);
   const Buffer rows = buffer_of(src, (uint32_t)(len - 1) * (uint32_t)(ld * 2) + 2u * (uint32_t)n);

@@ -16,7 +16,7 @@
 // fp32 states stay fp32: S in K S, R and T in T R (the three large products of
 // four), U in K^T U, and the same backwards. y is rounded to bf16 anyway: S and M
 // enter it once rounded, U in two (it adds 6 products to 104 and takes y's error
-// from 2.97e-3 to the figure in the file's last paragraph).
+// from 2.97e-3 to 2.44e-3, where the rounding of y alone makes 1.66e-3).
 //
 // Segments. A walk's length is its chunks' latencies one after the other, and
 // few sequences and heads leave most of the card idle. Then each sequence is
@@ -89,7 +89,7 @@ enum WalkMode : int {
 };
 
 // Three workgroups of four waves to a compute unit: 168 registers and 53 KB of
-// LDS each, which is why M's tiles come straight from the cache.
+// LDS each.
 template <int NK, int WV, WalkMode kMode>
 __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(DeltaArgs a) {
   constexpr int N = 32 * NK, W = 16 * WV;  // state channels, the workgroup's columns
@@ -97,8 +97,10 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
   constexpr int kT = 2 * kTriTiles * kTileElems;
   // One array for each of what is staged: the compiler then sees which reads do
   // not meet the loads under way, and does not wait for those.
+  // M takes Q's place once Q S is done, y that of the values.
   __shared__ bf16 sK[kDeltaChunk * N], sQ[kY ? kDeltaChunk * N : 8], sT[kT], sV[kDeltaChunk * W];
   __shared__ Gates G;
+  static_assert(!kY || kDeltaChunk * N >= kTriTiles * kTileElems, "M must fit where Q was");
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (kLocal ? a.P + a.N : a.P) / 16, blocks = (tiles + WV - 1) / WV;
@@ -142,27 +144,25 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
     return (const bf16 *)a.tri + ((size_t)(w.slot + c) * a.H + h) * a.tri_stride;
   };
   uint16_t g = 0, bt = 0;  // (bits: a conversion here would wait for the loads)
-  const auto fetch_keys = [&](int c) __attribute__((always_inline)) {
-    stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (rows_at(c) * a.G + grp) * a.N, ldk, a.N, length(c));
-  };
-  const auto fetch_rest = [&](int c) __attribute__((always_inline)) {
+  const auto fetch_rows = [&](int c) __attribute__((always_inline)) {
     const int64_t at = rows_at(c);
-    const int len = length(c);
+    stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N,
+                                   length(c));
+    if (kY)
+      stage_tile<N, kDeltaChunk, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N,
+                                     length(c));
+  };
+  const auto fetch_tri = [&](int c) __attribute__((always_inline)) {
     if (wave == 0) {
-      const size_t ga = (size_t)(at + min(lane, len - 1)) * a.H + h;
+      const size_t ga = (size_t)(rows_at(c) + min(lane, length(c) - 1)) * a.H + h;
       g = ((const uint16_t *)a.g)[ga];
       bt = ((const uint16_t *)a.beta)[ga];
     }
-    if (kY)
-      stage_tile<N, kDeltaChunk, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
-    if (valued)
-      stage_tile<W, kDeltaChunk, WV>(sV, (const bf16 *)a.x + ((size_t)at * a.H + h) * a.P + 16 * tile0, ldx, W,
-                         len);
     stage_block<WV>(sT, tri_at(c), 2 * kTriTiles);
   };
   if (chunks > 0) {
-    fetch_keys(0);
-    fetch_rest(0);
+    fetch_rows(0);
+    fetch_tri(0);
   }
   for (int c = 0; c < chunks; ++c) {
     const int64_t at = rows_at(c);
@@ -170,6 +170,9 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
     wait_vmem_all();
     if (wave == 0) fill_gates(G, bits_to_f32(g), bits_to_f32(bt), lane < len);
     __syncthreads();
+    if (valued)
+      stage_tile<W, kDeltaChunk, WV>(
+          sV, (const bf16 *)a.x + ((size_t)at * a.H + h) * a.P + 16 * tile0, ldx, W, len);
 
     // K S, and Q S transposed (lane: token lr of its tile, rows p); two tiles'
     // operands at a time, the next ones under way
@@ -216,6 +219,9 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
     };
     bf16x8 Th[kTriTiles], Tl[kTriTiles];
     tri_tiles(0, Th);
+    wait_vmem_all();
+    __syncthreads();
+    if (kY) stage_block<WV>(sQ, tri_at(c) + kT, kTriTiles);
     __builtin_amdgcn_sched_barrier(0);
     // R, as operands
     Split R[2];
@@ -231,7 +237,7 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
       }
       R[kt] = split8(v[0], v[1]);
     }
-    // U = T R; M's tiles come straight from the cache
+    // U = T R
     __builtin_amdgcn_sched_barrier(0);
     tri_tiles(1, Tl);
 #pragma unroll
@@ -243,22 +249,14 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
 #pragma unroll
         for (int i = 2 * kt; i < 4; ++i)
           A[i] = mfma(lower_operand(Th[lower_tile(i, kt)], i, kt), lo ? R[kt].lo : R[kt].hi, A[i]);
-    __builtin_amdgcn_sched_barrier(0);
-    bf16x8 M[kTriTiles];
-    if (kY) {
-      const bf16 *m = tri_at(c) + kT + 8 * lane;
-#pragma unroll
-      for (int k = 0; k < kTriTiles; ++k) M[k] = ldg8(m + k * kTileElems);
-    }
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
       for (int i = 2 * kt; i < 4; ++i)
         A[i] = mfma(lower_operand(Tl[lower_tile(i, kt)], i, kt), R[kt].hi, A[i]);
-    if (c + 1 < chunks) {
-      __syncthreads();
-      fetch_rest(c + 1);
-    }
+    wait_vmem_all();
+    __syncthreads();
+    if (c + 1 < chunks) fetch_tri(c + 1);
     const float ec = G.ef[kDeltaChunk - 1];
     bf16x8 kT[2][2];  // of a block of 16 channels, the next one's under way
     const auto columns = [&](int b) __attribute__((always_inline)) {
@@ -268,6 +266,10 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
     bf16x8 U[2];
     if (kY) {
       Split u[2];
+      bf16x8 M[kTriTiles];
+#pragma unroll
+      for (int k = 0; k < kTriTiles; ++k)
+        M[k] = *reinterpret_cast<const bf16x8 *>(sQ + k * kTileElems + 8 * lane);
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         u[kt] = split8(A[2 * kt], A[2 * kt + 1]);
@@ -305,26 +307,30 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
       __builtin_amdgcn_sched_barrier(0);
     }
     if (kY) {
-      bf16 *y = (bf16 *)a.y + ((size_t)at * a.H + h) * a.P + p0;
+      // y by whole rows of the workgroup's columns: 16 bytes a lane
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        if (16 * t + lr < len)
-          store_at(y + 16 * t * ldx, (uint32_t)(lr * (int)ldx + 4 * lg) * 2u,
-                   make_uint2(pack2(O[t][0], O[t][1]), pack2(O[t][2], O[t][3])));
+        *reinterpret_cast<uint2 *>(sV + place<W>(16 * t + lr, p0 - 16 * tile0 + 4 * lg)) =
+            make_uint2(pack2(O[t][0], O[t][1]), pack2(O[t][2], O[t][3]));
     } else if (!kLocal) {
+      // (tokens in the order of the operands: 16 bytes a lane)
       bf16 *u = (bf16 *)a.u + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-        const u32x4 v = __builtin_bit_cast(u32x4, U[kt]);
-        const uint32_t off = (uint32_t)(lr * kDeltaChunk + 4 * lg) * 2u;
-        store_at(u + 32 * kt, off, make_uint2(v[0], v[1]));
-        store_at(u + 32 * kt + 16, off, make_uint2(v[2], v[3]));
-      }
+      for (int kt = 0; kt < 2; ++kt)
+        store_at(u + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u, U[kt]);
     }
-    if (c + 1 < chunks) {
-      __syncthreads();
-      fetch_keys(c + 1);
+    __syncthreads();
+    if (c + 1 < chunks) fetch_rows(c + 1);
+    if (kY) {
+      constexpr int kPer = 64 * 8 / W;  // rows of an instruction
+      bf16 *y = (bf16 *)a.y + ((size_t)at * a.H + h) * a.P + 16 * tile0;
+      const int row = lane / (W / 8), col = 8 * (lane % (W / 8));
+#pragma unroll
+      for (int k = 0; k < kDeltaChunk / (kPer * WV); ++k) {
+        const int t = (k * WV + wave) * kPer;
+        const bf16x8 v = *reinterpret_cast<const bf16x8 *>(sV + place<W>(t + row, col));
+        if (t + row < len) store_at(y + t * ldx, (uint32_t)(row * (int)ldx + col) * 2u, v);
+      }
     }
   }
   float *to = nullptr;
@@ -390,26 +396,34 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
     return (const bf16 *)a.tri + ((size_t)(w.slot + c) * a.H + h) * a.tri_stride;
   };
   uint16_t g = 0, bt = 0;
-  const auto fetch_rows = [&](int c) __attribute__((always_inline)) {
+  // K and M^T, and what is free earlier in a chunk: Q and dY (T^T takes M^T's
+  // place once dU is done)
+  const auto fetch_keys = [&](int c) __attribute__((always_inline)) {
     const int64_t at = rows_at(c);
-    const int len = length(c);
-    stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
-    stage_tile<N, kDeltaChunk, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
-  };
-  const auto fetch_rest = [&](int c) __attribute__((always_inline)) {
-    const int64_t at = rows_at(c);
-    const int len = length(c);
     if (wave == 0) {
-      const size_t ga = (size_t)(at + min(lane, len - 1)) * a.H + h;
+      const size_t ga = (size_t)(at + min(lane, length(c) - 1)) * a.H + h;
       g = ((const uint16_t *)a.g)[ga];
       bt = ((const uint16_t *)a.beta)[ga];
     }
-    stage_tile<W, kDeltaChunk, WV>(sV, (const bf16 *)a.dy + ((size_t)at * a.H + h) * a.P + pw, ldx, W, len);
-    stage_block<WV>(sT, tri_at(c) + kT, 2 * kTriTiles);
+    stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N,
+                                   length(c));
+    stage_block<WV>(sT, tri_at(c) + 2 * kT, 2 * kTriTiles);
+  };
+  const auto fetch_rows = [&](int c) __attribute__((always_inline)) {
+    const int64_t at = rows_at(c);
+    stage_tile<N, kDeltaChunk, WV>(sQ, (const bf16 *)a.C + (at * a.G + grp) * a.N, ldk, a.N,
+                                   length(c));
+    stage_tile<W, kDeltaChunk, WV>(sV, (const bf16 *)a.dy + ((size_t)at * a.H + h) * a.P + pw, ldx,
+                                   W, length(c));
+  };
+  const auto tri_tiles = [&](int lo, bf16x8 (&to)[kTriTiles]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kTriTiles; ++k)
+      to[k] = *reinterpret_cast<const bf16x8 *>(sT + (2 * k + lo) * kTileElems + 8 * lane);
   };
   if (chunks > 0) {
+    fetch_keys(chunks - 1);
     fetch_rows(chunks - 1);
-    fetch_rest(chunks - 1);
   }
   for (int c = chunks - 1; c >= 0; --c) {
     const int len = length(c);
@@ -451,102 +465,107 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    bf16x8 Mh[kTriTiles], Ml[kTriTiles];
+    Split U[2];
     {
-      const bf16 *m = tri_at(c) + 2 * kT + 8 * lane;
+      bf16x8 Mh[kTriTiles], Ml[kTriTiles];
+      tri_tiles(0, Mh);
+      tri_tiles(1, Ml);
 #pragma unroll
-      for (int k = 0; k < kTriTiles; ++k) {
-        Mh[k] = ldg8(m + 2 * k * kTileElems);
-        Ml[k] = ldg8(m + (2 * k + 1) * kTileElems);
+      for (int t = 0; t < 4; ++t) A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
+#pragma unroll
+      for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int t = 0; t < 2 * kt + 2; ++t)
+            A[t] = mfma(upper_operand(lo ? Ml[upper_tile(t, kt)] : Mh[upper_tile(t, kt)], t, kt),
+                        Y[kt], A[t]);
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
+    }
+    __syncthreads();
+    stage_block<WV>(sT, tri_at(c) + kT, 2 * kTriTiles);
+    // dS <- e^{gam_c} dS + Q^T (e^gam dY), while T^T comes
+    const float ec = G.ef[kDeltaChunk - 1];
+    bf16x8 kT[2][2];  // of a block of 16 channels, the next one's under way
+    const auto columns = [&](const bf16 *rows, int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) kT[b & 1][kt] = state_operand<N>(rows, kt, b >> 1, b & 1);
+    };
+    columns(sQ, 0);
+    {
+      Split E[2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        f32x4 e[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const f32x4 ef = ldf4(G.ef + 32 * kt + 16 * u + 4 * lg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) e[u][r] = ef[r] * (float)Y[kt][4 * u + r];
+        }
+        E[kt] = split8(e[0], e[1]);
+      }
+#pragma unroll
+      for (int b = 0; b < 2 * NK; ++b) {
+        if (b + 1 < 2 * NK) columns(sQ, b + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 s = S[b >> 1][b & 1] * ec;
+        s = mfma(kT[b & 1][0], E[0].hi, s);
+        s = mfma(kT[b & 1][0], E[0].lo, s);
+        s = mfma(kT[b & 1][1], E[1].hi, s);
+        S[b >> 1][b & 1] = mfma(kT[b & 1][1], E[1].lo, s);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    Split U[2];
+    wait_vmem_all();
+    __syncthreads();
+    if (c > 0) fetch_rows(c - 1);
+    // dR = T^T dU
+    {
+      bf16x8 Th[kTriTiles], Tl[kTriTiles];
+      tri_tiles(0, Th);
+      tri_tiles(1, Tl);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
+      for (int t = 0; t < 4; ++t) A[t] = kZero4;
 #pragma unroll
-    for (int lo = 0; lo < 2; ++lo)
+      for (int step = 0; step < 3; ++step)
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-        for (int t = 0; t < 2 * kt + 2; ++t)
-          A[t] = mfma(upper_operand(lo ? Ml[upper_tile(t, kt)] : Mh[upper_tile(t, kt)], t, kt),
-                      Y[kt], A[t]);
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
-    __builtin_amdgcn_sched_barrier(0);
-    bf16x8 Th[kTriTiles], Tl[kTriTiles];
-#pragma unroll
-    for (int k = 0; k < kTriTiles; ++k)
-      Th[k] = *reinterpret_cast<const bf16x8 *>(sT + 2 * k * kTileElems + 8 * lane);
-#pragma unroll
-    for (int k = 0; k < kTriTiles; ++k)
-      Tl[k] = *reinterpret_cast<const bf16x8 *>(sT + (2 * k + 1) * kTileElems + 8 * lane);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) A[t] = kZero4;
-#pragma unroll
-    for (int step = 0; step < 3; ++step)
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int t = 0; t < 2 * kt + 2; ++t) {
-          const int k = upper_tile(t, kt);
-          A[t] = mfma(upper_operand(step == 2 ? Tl[k] : Th[k], t, kt),
-                      step == 1 ? U[kt].lo : U[kt].hi, A[t]);
-        }
-    if (c > 0) {
-      __syncthreads();
-      fetch_rest(c - 1);
+          for (int t = 0; t < 2 * kt + 2; ++t) {
+            const int k = upper_tile(t, kt);
+            A[t] = mfma(upper_operand(step == 2 ? Tl[k] : Th[k], t, kt),
+                        step == 1 ? U[kt].lo : U[kt].hi, A[t]);
+          }
     }
     if (!kLocal) {
       bf16 *dr = (bf16 *)a.dr + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        store_at(dr + 16 * t, (uint32_t)(lr * kDeltaChunk + 4 * lg) * 2u,
-                 make_uint2(pack2(A[t][0], A[t][1]), pack2(A[t][2], A[t][3])));
+      for (int kt = 0; kt < 2; ++kt)
+        store_at(dr + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u,
+                 pack8(A[2 * kt], A[2 * kt + 1]));
     }
-    Split E[2], D[2];
+    // dS <- dS - K^T (beta e^gam dR)
+    columns(sK, 0);
+    Split D[2];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      f32x4 e[2], d[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = 32 * kt + 16 * u + 4 * lg;
-        const f32x4 ef = ldf4(G.ef + t), be = ldf4(G.be + t);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) e[u][r] = ef[r] * (float)Y[kt][4 * u + r];
-        d[u] = -be * A[2 * kt + u];
-      }
-      E[kt] = split8(e[0], e[1]);
-      D[kt] = split8(d[0], d[1]);
-    }
-    const float ec = G.ef[kDeltaChunk - 1];
-    bf16x8 kT[2][2], qT[2][2];  // of a block of 16 channels, the next one's under way
-    const auto columns = [&](int b) __attribute__((always_inline)) {
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        kT[b & 1][kt] = state_operand<N>(sK, kt, b >> 1, b & 1);
-        qT[b & 1][kt] = state_operand<N>(sQ, kt, b >> 1, b & 1);
-      }
-    };
-    columns(0);
+    for (int kt = 0; kt < 2; ++kt)
+      D[kt] = split8(-ldf4(G.be + 32 * kt + 4 * lg) * A[2 * kt],
+                     -ldf4(G.be + 32 * kt + 16 + 4 * lg) * A[2 * kt + 1]);
 #pragma unroll
     for (int b = 0; b < 2 * NK; ++b) {
-      if (b + 1 < 2 * NK) columns(b + 1);
+      if (b + 1 < 2 * NK) columns(sK, b + 1);
       __builtin_amdgcn_sched_barrier(0);
-      f32x4 s = S[b >> 1][b & 1] * ec;
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        s = mfma(qT[b & 1][kt], E[kt].hi, s);
-        s = mfma(kT[b & 1][kt], D[kt].hi, s);
-        s = mfma(qT[b & 1][kt], E[kt].lo, s);
-        s = mfma(kT[b & 1][kt], D[kt].lo, s);
-      }
-      S[b >> 1][b & 1] = s;
+      f32x4 s = mfma(kT[b & 1][0], D[0].hi, S[b >> 1][b & 1]);
+      s = mfma(kT[b & 1][0], D[0].lo, s);
+      s = mfma(kT[b & 1][1], D[1].hi, s);
+      S[b >> 1][b & 1] = mfma(kT[b & 1][1], D[1].lo, s);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (c > 0) {
       __syncthreads();
-      fetch_rows(c - 1);
+      fetch_keys(c - 1);
     }
   }
   float *to = nullptr;
@@ -570,8 +589,8 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
 // head) and 16 columns a workgroup of WV waves, in fp32 throughout; wave w holds
 // the state channels of tiles w, w + WV, ...; the state goes round through LDS.
 // A transition does not depend on the state: the next one is on its way into
-// registers while one is used (without that, 16 segments of 32 heads took 130 us
-// instead of the figure beside launch_delta_forward). `span` has a transition's
+// registers while one is used (without that, 16 segments of 32 heads of 128 x 128
+// took 130 us, not 56). `span` has a transition's
 // columns as rows: span[P + j][n] = F[n][j].
 template <int NT, int WV, bool kBack>
 __global__ __launch_bounds__(64 * WV) void k_delta_join(DeltaArgs a) {
@@ -700,14 +719,32 @@ hipError_t join(const DeltaArgs &a, bool back, hipStream_t s) {
   return join_n<16, 8>(a, back, s);
 }
 
+// Whether and where sequences are cut. Cut, a call walks every segment twice and
+// the N columns of its transition once, 2 + N / P times the work, so the card has
+// to be that empty without: a workgroup on each compute unit is close to all that
+// the units give (three there take 2.3 times as long as one). And it has to be a
+// shorter way: two walks through a segment, the join's step for each segment (about
+// a chunk's time) and two more launches. sqrt(chunks) of them make a segment, or
+// as many as leave two workgroups for each unit. Measured in us, whole and cut:
+//   32 heads of 128, 1 x 16384 tokens    978, 484    backward 2243, 1277
+//   24 heads of 64, 1 x 4096 tokens      212, 100    backward  452,  261
+//   24 heads of 64, 1 x 1024 tokens       63,  57    backward  140,  131
+//   32 heads of 64, 4 x 2048 tokens      107,  99 (N = 64; just not cut)
+//   32 heads of 64, 2 x 2048 tokens      176, 252 (N = 256; not cut)
+//   24 heads of 64, 3 sequences <= 1536   56,  67 (not cut)
+constexpr int kComputeUnits = 256;
 void delta_segments(DeltaArgs &a, bool packed) {
   a.seg = a.nseg_per = a.nsegs = 0;
-  static const char *v = getenv("DELTA_SEG");
-  const int m = v ? atoi(v) : 0;
-  if (!m || a.T == 0) return;
-  a.seg = m;
-  a.nseg_per = (a.nc_per + m - 1) / m;
-  a.nsegs = packed ? (int)(a.T / ((int64_t)kDeltaChunk * m)) + a.nseq : a.nseq * a.nseg_per;
+  if (a.nseq == 0 || a.T == 0) return;
+  const int64_t chunks = (a.T / a.nseq + kDeltaChunk - 1) / kDeltaChunk;  // (packed: on average)
+  const int64_t groups = (int64_t)a.nseq * a.H * ((a.P + 63) / 64);
+  if (groups * (2 * a.P + a.N) > (int64_t)kComputeUnits * a.P) return;
+  int64_t m = chunks * groups / (2 * kComputeUnits);
+  while (m * m < chunks) ++m;
+  if (2 * m + chunks / m + 4 > chunks) return;
+  a.seg = (int)m;
+  a.nseg_per = (int)((a.nc_per + m - 1) / m);
+  a.nsegs = packed ? (int)(a.T / (kDeltaChunk * m)) + a.nseq : a.nseq * a.nseg_per;
 }
 
 hipError_t launch_delta_forward(const DeltaArgs &a, hipStream_t s) {

@@ -24,26 +24,63 @@
 namespace ssd {
 namespace {
 
-// Eight of a row, and a column's rows r0 + 8 lg + e (natural order) or
-// r0 + 16 (e / 4) + 4 lg + e % 4 (the order of result tiles).
-template <int W>
-__device__ __forceinline__ bf16x8 row8(const bf16 *t, int row, int col) {
-  return *reinterpret_cast<const bf16x8 *>(t + place<W>(row, col));
+// Eight consecutive elements, and four rows of one column (transposed read).
+__device__ __forceinline__ bf16x8 read8(const bf16 *t, int at) {
+  return *reinterpret_cast<const bf16x8 *>(t + at);
 }
-template <int W>
-__device__ __forceinline__ bf16x8 column8(const bf16 *t, int r0, int c0) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  const int row = r0 + 8 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
-  const bf16x4 a = ds_tr4(t, place<W>(row, col)), b = ds_tr4(t, place<W>(row + 4, col));
+__device__ __forceinline__ bf16x8 read4x2(const bf16 *t, int at, int at2) {
+  const bf16x4 a = ds_tr4(t, at), b = ds_tr4(t, at2);
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-template <int W>
-__device__ __forceinline__ bf16x8 column8_tiles(const bf16 *t, int r0, int c0) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  const int row = r0 + 4 * lg + (lr >> 2), col = c0 + 4 * (lr & 3);
-  const bf16x4 a = ds_tr4(t, place<W>(row, col)), b = ds_tr4(t, place<W>(row + 16, col));
-  return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
+
+// A lane's places in the staged tiles, of which all others follow by an XOR of
+// the column and an added row: W is a power of two, the swizzle an XOR and the
+// same for rows 16 apart. (Made anew for each use of the tiles: kept over the
+// heads, the places themselves would fill the registers.)
+template <int N, int P>
+struct Places {
+  int row, own4, yrow;   // row lr: columns 8 lg of K and Q, 4 lg, and 8 lg of dY
+  int tile;              // transposed, result-tile order: rows 4 lg + lr / 4 of K, Q
+  int tok0, tok1;        // transposed: rows 8 lg + lr / 4 (+ 4) of U, dR, tokens 8 (lr % 4)
+  int st0, st1;          // the same of a block of S, columns 4 (lr % 4)
+  __device__ __forceinline__ Places() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int lr = lane & 15, lg = lane >> 4, r8 = 8 * lg + (lr >> 2);
+    row = place<N>(lr, 8 * lg);
+    own4 = place<N>(lr, 4 * lg);
+    yrow = place<P>(lr, 8 * lg);
+    tile = place<N>(4 * lg + (lr >> 2), 4 * (lr & 3));
+    tok0 = place<kDeltaChunk>(r8, 8 * (lr & 3));
+    tok1 = place<kDeltaChunk>(r8 + 4, 8 * (lr & 3));
+    st0 = place<32>(r8, 4 * (lr & 3));
+    st1 = place<32>(r8 + 4, 4 * (lr & 3));
+  }
+  // K or Q: eight of row 16 t + lr from column 32 ks + 8 lg
+  __device__ __forceinline__ bf16x8 keys(const bf16 *s, int t, int ks) const {
+    return read8(s, (row ^ (32 * ks)) + 16 * t * N);
+  }
+  // dY: the same
+  __device__ __forceinline__ bf16x8 values(const bf16 *s, int t, int ps) const {
+    return read8(s, (yrow ^ (32 * ps)) + 16 * t * P);
+  }
+  // K or Q transposed: tokens 32 kt + 16 (e / 4) + 4 lg + e % 4 of column n0 + lr
+  __device__ __forceinline__ bf16x8 columns(const bf16 *s, int kt, int n0) const {
+    const int at = (tile ^ n0) + 32 * kt * N;
+    return read4x2(s, at, at + 16 * N);
+  }
+  // U or dR (rows of value channels, a pair of tiles' tokens in the order of the
+  // operands: 32 kt + 8 lg + e for token 32 kt + 16 (e / 4) + 4 lg + e % 4):
+  // channels 32 ps + 8 lg + e of token 16 t + lr
+  __device__ __forceinline__ bf16x8 tokens(const bf16 *s, int ps, int t) const {
+    const int x = 32 * (t >> 1), d = 4 * (t & 1) + 32 * ps * kDeltaChunk;
+    return read4x2(s, (tok0 ^ x) + d, (tok1 ^ x) + d);
+  }
+  // a block of S: channels 32 ps + 8 lg + e of column 16 par + lr
+  __device__ __forceinline__ bf16x8 state(const bf16 *s, int ps, int par) const {
+    return read4x2(s, (st0 ^ (16 * par)) + 32 * ps * 32, (st1 ^ (16 * par)) + 32 * ps * 32);
+  }
+};
 
 __device__ __forceinline__ float dot8(bf16x8 a, bf16x8 b) {
   float s = 0.f;
@@ -56,6 +93,10 @@ __device__ __forceinline__ float sum_lg(float v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
+// A sum that is added up where it is written: left to the end, with all that it is
+// the sum of, it fills the registers.
+__device__ __forceinline__ void keep_here(float &v) { asm volatile("" : "+v"(v)); }
+
 // Result tiles 2 kt and 2 kt + 1 of an operand, one at a time.
 __device__ __forceinline__ void set_half(bf16x8 &to, int half, f32x4 v) {
   const uint32_t a = pack2(v[0], v[1]), b = pack2(v[2], v[3]);
@@ -66,8 +107,11 @@ __device__ __forceinline__ void set_half(bf16x8 &to, int half, f32x4 v) {
   to = __builtin_bit_cast(bf16x8, w);
 }
 
+// Heads wider than 64 channels are taken 64 at a time: every result is a sum
+// over them. (That is what lets two workgroups share a compute unit: 75 KB of LDS
+// and 256 registers up to 128 state channels.)
 template <int NK, int PK>
-__global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
+__global__ __launch_bounds__(256, (NK <= 4 ? 2 : 1)) void k_delta_grad(DeltaArgs a) {
   constexpr int N = 32 * NK, P = 32 * PK, C = kDeltaChunk;
   __shared__ bf16 sK[C * N], sQ[C * N], sY[C * P], sU[P * C], sR[P * C];
   __shared__ bf16 sA0[P * 32], sB0[P * 32], sA1[P * 32], sB1[P * 32];  // blocks of S, dS
@@ -98,173 +142,186 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
 
   for (int h = h0; h < h1; ++h) {
     const size_t sh = (size_t)slot * a.H + h;
-    const bf16 *S0 = (const bf16 *)a.st0 + sh * a.P * a.N, *S1 = (const bf16 *)a.st1 + sh * a.P * a.N;
-    const auto fetch = [&](int nb, bf16 *A, bf16 *B) __attribute__((always_inline)) {
-      const int n = max(min(32, a.N - 32 * nb), 0);
-      stage_tile<32, P, 4>(A, S0 + 32 * nb, a.N, n, a.P);
-      stage_tile<32, P, 4>(B, S1 + 32 * nb, a.N, n, a.P);
-    };
-    if (h > h0) __syncthreads();
-    stage_tile<P, C, 4>(sY, (const bf16 *)a.dy + ((size_t)start * a.H + h) * a.P, ldx, a.P, len);
-    stage_tile<C, P, 4>(sU, (const bf16 *)a.u + sh * a.P * C, C, C, a.P);
-    stage_tile<C, P, 4>(sR, (const bf16 *)a.dr + sh * a.P * C, C, C, a.P);
-    fetch(0, sA0, sB0);
-    if (w == 0) {
-      const size_t ga = (size_t)(start + min(lane, len - 1)) * a.H + h;
-      sG[lane] = wave_inclusive_sum(
-          lane < len ? delta_log2_decay((float)((const bf16 *)a.g)[ga]) : 0.f);
-      sBt[lane] = lane < len ? (float)((const bf16 *)a.beta)[ga] : 0.f;
-    }
-    wait_vmem_all();
-    __syncthreads();
-
-    // this token's rows of dY, dR, U (what is staged past the end and past P is zeros)
-    bf16x8 yo[PK], ro[PK], uo[PK];
-    const float bi = sBt[own], gi = sG[own], gc = sG[C - 1];
-    const float ef = exp2_fast(gi), lf = exp2_fast(gc - gi), be = bi * ef;
-    float rv = 0.f;
-#pragma unroll
-    for (int ps = 0; ps < PK; ++ps) {
-      const bool in = 32 * ps + 8 * lg < a.P;
-      yo[ps] = row8<P>(sY, own, 32 * ps + 8 * lg);
-      ro[ps] = column8<C>(sR, 32 * ps, 16 * w);
-      uo[ps] = column8<C>(sU, 32 * ps, 16 * w);
-      if (in && live) {
-        const size_t at = (tok * a.H + h) * a.P + 32 * ps + 8 * lg;
-        rv += dot8(ro[ps], ldg8((const bf16 *)a.x + at));
-        f32x4 p, q;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = bi * (float)ro[ps][e];
-          q[e] = bi * (float)ro[ps][4 + e];
-        }
-        *reinterpret_cast<bf16x8 *>((bf16 *)a.dx + at) = pack8(p, q);
-      }
-    }
-    // the pair matrices
-    bf16x8 m1[2], l1[2], m2[2], l2[2];
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) m1[kt] = l1[kt] = m2[kt] = l2[kt] = zero8();
-    float pairs = 0.f, betas = 0.f;         // row sums less column sums; for dbeta
-    {
-      bf16x8 ko[NK], qo[NK];
-#pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        ko[ks] = row8<N>(sK, own, 32 * ks + 8 * lg);
-        qo[ks] = row8<N>(sQ, own, 32 * ks + 8 * lg);
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f32x4 gt = ldf4(sG + 16 * t + 4 * lg);
-        if (t <= w) {                        // rows j of tile t, column i = own
-          f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4, m, l;
-#pragma unroll
-          for (int ks = 0; ks < NK; ++ks) {
-            const bf16x8 k = row8<N>(sK, 16 * t + lr, 32 * ks + 8 * lg);
-            kk = mfma(k, ko[ks], kk);
-            qk = mfma(k, qo[ks], qk);
-          }
-#pragma unroll
-          for (int ps = 0; ps < PK; ++ps) {
-            const bf16x8 u = column8<C>(sU, 32 * ps, 16 * t);
-            dm = mfma(u, yo[ps], dm);
-            dl = mfma(u, ro[ps], dl);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int d = own - (16 * t + 4 * lg + r);
-            const float e = d >= 0 ? exp2_fast(gi - gt[r]) : 0.f;
-            m[r] = d >= 0 ? dm[r] * e : 0.f;
-            const float lk = d > 0 ? -dl[r] * e : 0.f;
-            l[r] = bi * lk;
-            betas += lk * kk[r];
-            pairs += m[r] * qk[r] + l[r] * kk[r];
-          }
-          set_half(m1[t >> 1], t & 1, m);
-          set_half(l1[t >> 1], t & 1, l);
-        }
-        if (t >= w) {                        // rows i of tile t, column j = own
-          f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4, m, l;
-#pragma unroll
-          for (int ks = 0; ks < NK; ++ks) {
-            kk = mfma(row8<N>(sK, 16 * t + lr, 32 * ks + 8 * lg), ko[ks], kk);
-            qk = mfma(row8<N>(sQ, 16 * t + lr, 32 * ks + 8 * lg), ko[ks], qk);
-          }
-#pragma unroll
-          for (int ps = 0; ps < PK; ++ps) {
-            dm = mfma(row8<P>(sY, 16 * t + lr, 32 * ps + 8 * lg), uo[ps], dm);
-            dl = mfma(column8<C>(sR, 32 * ps, 16 * t), uo[ps], dl);
-          }
-          const f32x4 bt = ldf4(sBt + 16 * t + 4 * lg);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * t + 4 * lg + r, d = i - own;
-            const bool in = d >= 0 && i < len;
-            const float e = in ? exp2_fast(gt[r] - gi) : 0.f;
-            m[r] = in ? dm[r] * e : 0.f;
-            l[r] = in && d > 0 ? -bt[r] * dl[r] * e : 0.f;
-            pairs -= m[r] * qk[r] + l[r] * kk[r];
-          }
-          set_half(m2[t >> 1], t & 1, m);
-          set_half(l2[t >> 1], t & 1, l);
-        }
-      }
-    }
-    // the states, 32 channels at a time
+    float rv = 0.f, pairs = 0.f, betas = 0.f;  // for dbeta; row sums less column sums; for dbeta
     float zq = 0.f, zk = 0.f, zu = 0.f, ss = 0.f;
-    const auto block = [&](int nb, const bf16 *A, const bf16 *B) __attribute__((always_inline)) {
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const int n0 = 32 * nb + 16 * par;
-        f32x4 ys = kZero4, rs = kZero4, us = kZero4;
-#pragma unroll
-        for (int ps = 0; ps < PK; ++ps) {
-          const bf16x8 s0 = column8<32>(A, 32 * ps, 16 * par), s1 = column8<32>(B, 32 * ps, 16 * par);
-          ys = mfma(s0, yo[ps], ys);
-          rs = mfma(s0, ro[ps], rs);
-          us = mfma(s1, uo[ps], us);
-          if (((2 * nb + par) & 3) == w) ss += dot8(s0, s1);
+    float bi, gi, gc, ef, lf, be;
+    for (int pb = 0; pb < a.P; pb += P) {
+      const int pn = min(P, a.P - pb);         // value channels of this pass
+      const bf16 *S0 = (const bf16 *)a.st0 + (sh * a.P + pb) * a.N;
+      const bf16 *S1 = (const bf16 *)a.st1 + (sh * a.P + pb) * a.N;
+      const auto fetch = [&](int nb, bf16 *A, bf16 *B) __attribute__((always_inline)) {
+        const int n = max(min(32, a.N - 32 * nb), 0);
+        stage_tile<32, P, 4, true>(A, S0 + 32 * nb, a.N, n, pn);
+        stage_tile<32, P, 4, true>(B, S1 + 32 * nb, a.N, n, pn);
+      };
+      if (h > h0 || pb > 0) __syncthreads();
+      stage_tile<P, C, 4, true>(sY, (const bf16 *)a.dy + ((size_t)start * a.H + h) * a.P + pb, ldx, pn, len);
+      stage_tile<C, P, 4, true>(sU, (const bf16 *)a.u + (sh * a.P + pb) * C, C, C, pn);
+      stage_tile<C, P, 4, true>(sR, (const bf16 *)a.dr + (sh * a.P + pb) * C, C, C, pn);
+      fetch(0, sA0, sB0);
+      if (w == 0) {
+        const size_t ga = (size_t)(start + min(lane, len - 1)) * a.H + h;
+        sG[lane] = wave_inclusive_sum(
+            lane < len ? delta_log2_decay((float)((const bf16 *)a.g)[ga]) : 0.f);
+        sBt[lane] = lane < len ? (float)((const bf16 *)a.beta)[ga] : 0.f;
+      }
+      wait_vmem_all();
+      __syncthreads();
+
+      // this token's rows of dY, dR, U (what is staged past the end and past P is zeros)
+      const Places<N, P> at;
+      bf16x8 yo[PK], ro[PK], uo[PK];
+      bi = sBt[own], gi = sG[own], gc = sG[C - 1];
+      ef = exp2_fast(gi), lf = exp2_fast(gc - gi), be = bi * ef;
+  #pragma unroll
+      for (int ps = 0; ps < PK; ++ps) {
+        const bool in = 32 * ps + 8 * lg < pn;
+        yo[ps] = at.values(sY, w, ps);
+        ro[ps] = at.tokens(sR, ps, w);
+        uo[ps] = at.tokens(sU, ps, w);
+        if (in && live) {
+          const size_t xa = (tok * a.H + h) * a.P + pb + 32 * ps + 8 * lg;
+          rv += dot8(ro[ps], ldg8((const bf16 *)a.x + xa));
+          f32x4 p, q;
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = bi * (float)ro[ps][e];
+            q[e] = bi * (float)ro[ps][4 + e];
+          }
+          *reinterpret_cast<bf16x8 *>((bf16 *)a.dx + xa) = pack8(p, q);
         }
-        const bf16x4 k4 = *reinterpret_cast<const bf16x4 *>(sK + place<N>(own, n0 + 4 * lg));
-        const bf16x4 q4 = *reinterpret_cast<const bf16x4 *>(sQ + place<N>(own, n0 + 4 * lg));
-#pragma unroll
+      }
+      // the pair matrices
+      bf16x8 m1[2], l1[2], m2[2], l2[2];
+  #pragma unroll
+      for (int kt = 0; kt < 2; ++kt) m1[kt] = l1[kt] = m2[kt] = l2[kt] = zero8();
+      {
+        bf16x8 ko[NK], qo[NK];
+  #pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+          ko[ks] = at.keys(sK, w, ks);
+          qo[ks] = at.keys(sQ, w, ks);
+        }
+  #pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          __builtin_amdgcn_sched_barrier(0);
+          const f32x4 gt = ldf4(sG + 16 * t + 4 * lg);
+          if (t <= w) {                        // rows j of tile t, column i = own
+            f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4, m, l;
+  #pragma unroll
+            for (int ks = 0; ks < NK; ++ks) {
+              const bf16x8 k = at.keys(sK, t, ks);
+              kk = mfma(k, ko[ks], kk);
+              qk = mfma(k, qo[ks], qk);
+            }
+  #pragma unroll
+            for (int ps = 0; ps < PK; ++ps) {
+              const bf16x8 u = at.tokens(sU, ps, t);
+              dm = mfma(u, yo[ps], dm);
+              dl = mfma(u, ro[ps], dl);
+            }
+  #pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int d = own - (16 * t + 4 * lg + r);
+              const float e = d >= 0 ? exp2_fast(gi - gt[r]) : 0.f;
+              m[r] = d >= 0 ? dm[r] * e : 0.f;
+              const float lk = d > 0 ? -dl[r] * e : 0.f;
+              l[r] = bi * lk;
+              betas += lk * kk[r];
+              pairs += m[r] * qk[r] + l[r] * kk[r];
+            }
+            keep_here(betas), keep_here(pairs);
+            set_half(m1[t >> 1], t & 1, m);
+            set_half(l1[t >> 1], t & 1, l);
+          }
+          if (t >= w) {                        // rows i of tile t, column j = own
+            f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4, m, l;
+  #pragma unroll
+            for (int ks = 0; ks < NK; ++ks) {
+              kk = mfma(at.keys(sK, t, ks), ko[ks], kk);
+              qk = mfma(at.keys(sQ, t, ks), ko[ks], qk);
+            }
+  #pragma unroll
+            for (int ps = 0; ps < PK; ++ps) {
+              dm = mfma(at.values(sY, t, ps), uo[ps], dm);
+              dl = mfma(at.tokens(sR, ps, t), uo[ps], dl);
+            }
+            const f32x4 bt = ldf4(sBt + 16 * t + 4 * lg);
+  #pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int i = 16 * t + 4 * lg + r, d = i - own;
+              const bool in = d >= 0 && i < len;
+              const float e = in ? exp2_fast(gt[r] - gi) : 0.f;
+              m[r] = in ? dm[r] * e : 0.f;
+              l[r] = in && d > 0 ? -bt[r] * dl[r] * e : 0.f;
+              pairs -= m[r] * qk[r] + l[r] * kk[r];
+            }
+            keep_here(pairs);
+            set_half(m2[t >> 1], t & 1, m);
+            set_half(l2[t >> 1], t & 1, l);
+          }
+        }
+      }
+      // the states, 32 channels at a time
+      const auto block = [&](int nb, const bf16 *A, const bf16 *B) __attribute__((always_inline)) {
+        const Places<N, P> at;
+  #pragma unroll
+        for (int par = 0; par < 2; ++par) {
+          __builtin_amdgcn_sched_barrier(0);
+          const int n0 = 32 * nb + 16 * par;
+          f32x4 ys = kZero4, rs = kZero4, us = kZero4;
+  #pragma unroll
+          for (int ps = 0; ps < PK; ++ps) {
+            const bf16x8 s0 = at.state(A, ps, par), s1 = at.state(B, ps, par);
+            ys = mfma(s0, yo[ps], ys);
+            rs = mfma(s0, ro[ps], rs);
+            us = mfma(s1, uo[ps], us);
+            if (((2 * nb + par) & 3) == w) ss += dot8(s0, s1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          const int o = (at.own4 ^ n0) + 16 * w * N;
+          const bf16x4 k4 = *reinterpret_cast<const bf16x4 *>(sK + o);
+          const bf16x4 q4 = *reinterpret_cast<const bf16x4 *>(sQ + o);
+  #pragma unroll
           for (int r = 0; r < 4; ++r) {
             zq += (float)q4[r] * ys[r];
             zk += (float)k4[r] * rs[r];
             zu += (float)k4[r] * us[r];
           }
-        f32x4 q = dQ[nb][par] + ef * ys, k = dK[nb][par] - be * rs + lf * us;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const bf16x8 kT = column8_tiles<N>(sK, 32 * kt, n0);
-          if (kt <= w / 2) {                 // tokens up to this wave's
-            q = mfma(kT, m1[kt], q);
-            k = mfma(kT, l1[kt], k);
+          keep_here(zq), keep_here(zk), keep_here(zu), keep_here(ss);
+          f32x4 q = dQ[nb][par] + ef * ys, k = dK[nb][par] - be * rs + lf * us;
+  #pragma unroll
+          for (int kt = 0; kt < 2; ++kt) {
+            const bf16x8 kT = at.columns(sK, kt, n0);
+            if (kt <= w / 2) {                 // tokens up to this wave's
+              q = mfma(kT, m1[kt], q);
+              k = mfma(kT, l1[kt], k);
+            }
+            if (kt >= w / 2) {                 // and from them on
+              k = mfma(kT, l2[kt], k);
+              k = mfma(at.columns(sQ, kt, n0), m2[kt], k);
+            }
           }
-          if (kt >= w / 2) {                 // and from them on
-            k = mfma(kT, l2[kt], k);
-            k = mfma(column8_tiles<N>(sQ, 32 * kt, n0), m2[kt], k);
-          }
+          dQ[nb][par] = q;
+          dK[nb][par] = k;
         }
-        dQ[nb][par] = q;
-        dK[nb][par] = k;
-      }
-    };
-#pragma unroll
-    for (int nb = 0; nb < NK; ++nb) {
-      if (nb + 1 < NK) {
+      };
+  #pragma unroll
+      for (int nb = 0; nb < NK; ++nb) {
+        if (nb + 1 < NK) {
+          if (nb & 1)
+            fetch(nb + 1, sA0, sB0);
+          else
+            fetch(nb + 1, sA1, sB1);
+        }
         if (nb & 1)
-          fetch(nb + 1, sA0, sB0);
+          block(nb, sA1, sB1);
         else
-          fetch(nb + 1, sA1, sB1);
-      }
-      if (nb & 1)
-        block(nb, sA1, sB1);
-      else
-        block(nb, sA0, sB0);
-      if (nb + 1 < NK) {
-        wait_vmem_all();
-        __syncthreads();
+          block(nb, sA0, sB0);
+        if (nb + 1 < NK) {
+          wait_vmem_all();
+          __syncthreads();
+        }
       }
     }
     // dbeta and dg
@@ -277,7 +334,7 @@ __global__ __launch_bounds__(256) void k_delta_grad(DeltaArgs a) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) ss += __shfl_xor(ss, o);
     if (lg == 0) {
-      sZ[own] = live ? ef * zq - be * zk + pairs : 0.f;  // (dR past the end is not zero)
+      sZ[own] = live ? ef * zq - be * zk + pairs : 0.f;
       sP[own] = lf * zu;
       if (live) ((bf16 *)a.dbeta)[tok * a.H + h] = (bf16)(rv + betas - ef * zk);
     }
@@ -321,9 +378,7 @@ hipError_t grad(const DeltaArgs &a, hipStream_t s) {
 
 template <int NK>
 hipError_t grad_p(const DeltaArgs &a, hipStream_t s) {
-  if (a.P <= 32) return grad<NK, 1>(a, s);
-  if (a.P == 64) return grad<NK, 2>(a, s);
-  return grad<NK, 4>(a, s);
+  return a.P <= 32 ? grad<NK, 1>(a, s) : grad<NK, 2>(a, s);
 }
 
 }  // namespace
