@@ -24,13 +24,19 @@ namespace {
 
 typedef bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ void load4(const float *p, float *v) {
-  const f32x4_t q = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t *>(p));
+// Four channels as they lie in memory, and their values: the rows of several
+// heads are on their way before the first is used.
+__device__ __forceinline__ f32x4_t fetch4(const float *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t *>(p));
+}
+__device__ __forceinline__ u32x2_t fetch4(const bf16 *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(p));
+}
+__device__ __forceinline__ void values4(f32x4_t q, float *v) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = q[k];
 }
-__device__ __forceinline__ void load4(const bf16 *p, float *v) {
-  const u32x2_t q = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(p));
+__device__ __forceinline__ void values4(u32x2_t q, float *v) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     v[2 * k] = __uint_as_float(q[k] << 16);
@@ -65,31 +71,26 @@ __device__ __forceinline__ float team_sum(float v) {
 }
 
 // Four pairs of a lane's channels v[0..7] turned by (c, s).
+__device__ __forceinline__ void turn2(float &x, float &y, float c, float s) {
+  const float u = x * c - y * s;
+  y = x * s + y * c;
+  x = u;
+}
 __device__ __forceinline__ void turn(float (&v)[8], const float (&c)[4], const float (&s)[4],
                                      bool side_by_side) {
-  // (selects, not indexes that depend on the layout: v stays in registers)
-  float a[4], b[4];
+  // (the layout is the same for all lanes: a branch, no selects)
+  if (side_by_side) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    a[p] = side_by_side ? v[2 * p] : v[p];
-    b[p] = side_by_side ? v[2 * p + 1] : v[p + 4];
-  }
-  float x[4], y[4];
+    for (int p = 0; p < 4; ++p) turn2(v[2 * p], v[2 * p + 1], c[p], s[p]);
+  } else {
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    x[p] = a[p] * c[p] - b[p] * s[p];
-    y[p] = a[p] * s[p] + b[p] * c[p];
-  }
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    v[p] = side_by_side ? (p & 1 ? y[p / 2] : x[p / 2]) : x[p];
-    v[p + 4] = side_by_side ? (p & 1 ? y[2 + p / 2] : x[2 + p / 2]) : y[p];
+    for (int p = 0; p < 4; ++p) turn2(v[p], v[p + 4], c[p], s[p]);
   }
 }
 
 template <typename T, int TEAM, bool kBackward>
 __global__ __launch_bounds__(256) void k_bc_norm(BcNormArgs a) {
-  constexpr int kTeams = 256 / TEAM;
+  constexpr int kTeams = 256 / TEAM, kBatch = kBackward ? 2 : 4;  // heads under way
   const int j = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
   const bool on = 8 * j < a.N;
   const bool rotated = a.pos && 8 * j < a.rot;
@@ -110,7 +111,6 @@ __global__ __launch_bounds__(256) void k_bc_norm(BcNormArgs a) {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
       f[p] = (double)a.freqs[4 * j + p] * 0.15915494309189533577;  // turns a position
-  const int all = a.heads[0] + a.heads[1];
   const int64_t units = (int64_t)a.tokens * a.parts;
   for (int64_t u = (int64_t)blockIdx.x * kTeams + team; u < units;
        u += (int64_t)gridDim.x * kTeams) {
@@ -126,52 +126,68 @@ __global__ __launch_bounds__(256) void k_bc_norm(BcNormArgs a) {
         if (kBackward) sn[q] = -sn[q];
       }
     }
-    for (int hh = part; hh < all; hh += a.parts) {
-      const int side = hh >= a.heads[0];
-      const int head = side ? hh - a.heads[0] : hh;
-      const T *x = (const T *)a.in[side] + t * a.in_stride[side] + (int64_t)head * a.N;
-      float v[8], d[8];
-      load4(x + c0, v);
-      load4(x + c1, v + 4);
-      if (kBackward) {
-        const T *g = (const T *)a.dout[side] + t * a.out_stride[side] + (int64_t)head * a.N;
-        load4(g + c0, d);
-        load4(g + c1, d + 4);
-      }
-      float ss = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
-      ss = team_sum<TEAM>(on ? ss : 0.f);
-      const float m = ss * a.inv_n + a.eps;
-      const float r = 1.f / sqrtf(m);
-      if (!kBackward) {
+    for (int side = 0; side < 2; ++side) {
+      // (the sides' heads in a row, every parts-th of them from the part's own)
+      const int heads = a.heads[side];
+      int h = side ? part - a.heads[0] % a.parts : part;
+      if (h < 0) h += a.parts;
+      const T *x = (const T *)a.in[side] + t * a.in_stride[side];
+      const T *g = (const T *)a.dout[side] + t * a.out_stride[side];
+      T *o = kBackward ? (T *)a.out[side] + t * a.dx_stride[side]
+                       : (T *)a.out[side] + t * a.out_stride[side];
+      for (; h < heads; h += kBatch * a.parts) {
+        decltype(fetch4((const T *)nullptr)) raw[kBatch][kBackward ? 4 : 2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= r * (side ? w[1][k] : w[0][k]);
-        if (rotated) turn(v, cs, sn, a.interleaved);
-        if (on) {
-          T *o = (T *)a.out[side] + t * a.out_stride[side] + (int64_t)head * a.N;
-          store4(o + c0, v);
-          store4(o + c1, v + 4);
+        for (int b = 0; b < kBatch; ++b) {
+          const int64_t at = (int64_t)min(h + b * a.parts, heads - 1) * a.N;
+          raw[b][0] = fetch4(x + at + c0);
+          raw[b][1] = fetch4(x + at + c1);
+          if (kBackward) {
+            raw[b][2] = fetch4(g + at + c0);
+            raw[b][3] = fetch4(g + at + c1);
+          }
         }
-      } else {
-        if (rotated) turn(d, cs, sn, a.interleaved);
-        float dot = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[k] *= r;
-          const float dv = d[k] * v[k];
-          dw[0][k] += side ? 0.f : dv;
-          dw[1][k] += side ? dv : 0.f;
-          d[k] *= side ? w[1][k] : w[0][k];
-          dot += d[k] * v[k];
-        }
-        dot = team_sum<TEAM>(on ? dot : 0.f) * a.inv_n;
+        for (int b = 0; b < kBatch; ++b) {
+          if (h + b * a.parts >= heads) break;
+          const int64_t at = (int64_t)(h + b * a.parts) * a.N;
+          float v[8], d[8];
+          values4(raw[b][0], v);
+          values4(raw[b][1], v + 4);
+          float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = r * (d[k] - v[k] * dot);
-        if (on) {
-          T *o = (T *)a.out[side] + t * a.dx_stride[side] + (int64_t)head * a.N;
-          store4(o + c0, d);
-          store4(o + c1, d + 4);
+          for (int k = 0; k < 8; ++k) ss += v[k] * v[k];
+          ss = team_sum<TEAM>(on ? ss : 0.f);
+          const float r = rsqrtf(ss * a.inv_n + a.eps);
+          if (!kBackward) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= r * w[side][k];
+            if (rotated) turn(v, cs, sn, a.interleaved);
+            if (on) {
+              store4(o + at + c0, v);
+              store4(o + at + c1, v + 4);
+            }
+          } else {
+            values4(raw[b][2], d);
+            values4(raw[b][3], d + 4);
+            if (rotated) turn(d, cs, sn, a.interleaved);
+            float dot = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              v[k] *= r;
+              dw[side][k] += d[k] * v[k];
+              d[k] *= w[side][k];
+              dot += d[k] * v[k];
+            }
+            dot = team_sum<TEAM>(on ? dot : 0.f) * a.inv_n;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = r * (d[k] - v[k] * dot);
+            if (on) {
+              store4(o + at + c0, d);
+              store4(o + at + c1, d + 4);
+            }
+          }
         }
       }
     }

@@ -30,55 +30,81 @@ __device__ __forceinline__ void wave_order() {
 // Index of lower tile (i, j), j <= i.
 __host__ __device__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
 
-// Tiles (i, j), j <= i, of one product: rows j of X against rows i of Y (lane:
-// row i % 16, 4 columns j), or with kSwap the other way round (lane: row j % 16,
-// 4 columns i). 64 rows each, `ld` apart, N columns, rows past len read as the
-// last one. The tiles go to LDS in lane order, tile (i, j) at tri(i, j).
-template <bool kSwap, int I, typename T>
-__device__ __forceinline__ void tile_row(const T *X, const T *Y, size_t ld, int N, int len,
-                                         f32x4 (*out)[64]) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  f32x4 acc[I + 1];
-#pragma unroll
-  for (int j = 0; j <= I; ++j) acc[j] = kZero4;
-  size_t row[I + 1];
-#pragma unroll
-  for (int j = 0; j <= I; ++j) row[j] = (size_t)min(16 * j + lr, len - 1) * ld;
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll 4
-    for (int n0 = 0; n0 < N; n0 += 32) {
-      const int col = n0 + 8 * lg, at = min(col, N - 8);
-      bf16x8 y = ldg8((const bf16 *)Y + row[I] + at);
-      if (col >= N) y = zero8();
-#pragma unroll
-      for (int j = 0; j <= I; ++j) {
-        const bf16x8 x = ldg8((const bf16 *)X + row[j] + at);
-        acc[j] = kSwap ? mfma(y, x, acc[j]) : mfma(x, y, acc[j]);
-      }
-    }
-  } else {
-#pragma unroll 4
-    for (int n0 = 0; n0 < N; n0 += 16) {
-      const f32x4 y = ldf4((const float *)Y + row[I] + n0 + 4 * lg);
-#pragma unroll
-      for (int j = 0; j <= I; ++j) {
-        const f32x4 x = ldf4((const float *)X + row[j] + n0 + 4 * lg);
-        acc[j] = kSwap ? mfma16(y, x, acc[j]) : mfma16(x, y, acc[j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j <= I; ++j) out[tri(I, j)][lane] = acc[j];
+// Row r, columns n.. of a tile's rows as an operand: 8 of 32 columns in bf16, 4 of
+// 16 in fp32; zeros from column N on.
+__device__ __forceinline__ bf16x8 operand(const bf16 *row, int n, int N) {
+  const int col = n + 8 * ((threadIdx.x & 63) >> 4);
+  bf16x8 v = ldg8(row + min(col, N - 8));
+  return col < N ? v : zero8();
 }
-template <bool kSwap, typename T>
-__device__ __forceinline__ void tile_row(int i, const T *X, const T *Y, size_t ld, int N, int len,
-                                         f32x4 (*out)[64]) {
-  switch (i) {
-    case 0: return tile_row<kSwap, 0>(X, Y, ld, N, len, out);
-    case 1: return tile_row<kSwap, 1>(X, Y, ld, N, len, out);
-    case 2: return tile_row<kSwap, 2>(X, Y, ld, N, len, out);
-    default: return tile_row<kSwap, 3>(X, Y, ld, N, len, out);
+__device__ __forceinline__ f32x4 operand(const float *row, int n, int N) {
+  const f32x4 v = ldf4(row + min(n, N - 16) + 4 * ((threadIdx.x & 63) >> 4));
+  return n < N ? v : kZero4;
+}
+__device__ __forceinline__ f32x4 product(bf16x8 a, bf16x8 b, f32x4 c) { return mfma(a, b, c); }
+__device__ __forceinline__ f32x4 product(f32x4 a, f32x4 b, f32x4 c) { return mfma16(a, b, c); }
+
+// Tile rows 3 - v of K K^T and v of Q K^T (five tiles on and below the diagonal)
+// for v from LO to HI: rows j of K against rows i (lane: row i % 16, 4 columns j),
+// or with kSwap Q K^T the other way round (lane: row j % 16, 4 columns i). Rows past
+// len are read as the last one. NB operands' columns are on their way at once; a
+// wave reads the rows of K once. The tiles go to LDS in lane order, tile (i, j) at
+// tri(i, j).
+template <int LO, int HI, int NB, bool kSwap, typename T>
+__device__ __forceinline__ void tile_rows(const T *K, const T *Q, size_t ld, int N, int len,
+                                          f32x4 (*kk)[64], f32x4 (*qk)[64]) {
+  constexpr int kCols = sizeof(T) == 2 ? 32 : 16;
+  constexpr int kRows = (3 - LO > HI - 1 ? 3 - LO : HI - 1) + 1;  // of K's tiles
+  const int lane = threadIdx.x & 63, lr = lane & 15;
+  f32x4 k[HI - LO][4], q[HI - LO][4];
+#pragma unroll
+  for (int v = LO; v < HI; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[v - LO][j] = q[v - LO][j] = kZero4;
+  for (int n0 = 0; n0 < N; n0 += NB * kCols) {
+    decltype(operand(K, 0, 0)) x[kRows][NB], y[HI - LO][NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        x[j][b] = operand(K + (size_t)min(16 * j + lr, len - 1) * ld, n0 + kCols * b, N);
+#pragma unroll
+      for (int v = LO; v < HI; ++v)
+        y[v - LO][b] = operand(Q + (size_t)min(16 * v + lr, len - 1) * ld, n0 + kCols * b, N);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int v = LO; v < HI; ++v) {
+#pragma unroll
+        for (int j = 0; j <= 3 - v; ++j)
+          k[v - LO][j] = product(x[j][b], x[3 - v][b], k[v - LO][j]);
+#pragma unroll
+        for (int j = 0; j <= v; ++j)
+          q[v - LO][j] = kSwap ? product(y[v - LO][b], x[j][b], q[v - LO][j])
+                               : product(x[j][b], y[v - LO][b], q[v - LO][j]);
+      }
   }
+#pragma unroll
+  for (int v = LO; v < HI; ++v) {
+#pragma unroll
+    for (int j = 0; j <= 3 - v; ++j) kk[tri(3 - v, j)][lane] = k[v - LO][j];
+#pragma unroll
+    for (int j = 0; j <= v; ++j) qk[tri(v, j)][lane] = q[v - LO][j];
+  }
+}
+template <int WV, int NB, bool kSwap, typename T>
+__device__ __forceinline__ void group_tiles(int wave, const T *K, const T *Q, size_t ld, int N,
+                                            int len, f32x4 (*kk)[64], f32x4 (*qk)[64]) {
+  constexpr int R = 4 / WV;
+  if (wave == 0)
+    tile_rows<0, R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+  else if (wave == 1)
+    tile_rows<R % 4, R % 4 + R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+  else if (wave == 2)
+    tile_rows<2 * R % 4, 2 * R % 4 + R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+  else
+    tile_rows<3 * R % 4, 3 * R % 4 + R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
 }
 
 // Where a chunk's matrices go. v: the ten tiles (lane: row 16 i + l % 16, columns
@@ -131,7 +157,7 @@ struct TilesOut {
 };
 
 template <typename T, DeltaTri W, int WV, typename Out>
-__global__ __launch_bounds__(64 * WV, 4) void k_delta_prep(DeltaArgs a, int64_t bytes, int per) {
+__global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaArgs a, int64_t bytes, int per) {
   __shared__ f32x4 sKK[10][64], sQK[10][64];
   __shared__ float sGate[WV][2][kDeltaChunk];
   __shared__ f32x4 sDiag[WV][4][16][5];  // diagonal blocks: rows of L, then columns of T
@@ -147,11 +173,13 @@ __global__ __launch_bounds__(64 * WV, 4) void k_delta_prep(DeltaArgs a, int64_t 
   if (!delta_chunk(a, slot, start, len)) return;
   const size_t row0 = ((size_t)start * a.G + grp) * a.N, ld = (size_t)a.G * a.N;
   const T *K = (const T *)a.B + row0, *Q = (const T *)a.C + row0;
-  // the group's products, a row of one and a row of the other (five tiles) at a time
-  for (int v = wave * 4 / WV; v < (wave + 1) * 4 / WV; ++v) {
-    tile_row<false>(3 - v, K, K, ld, a.N, len, sKK);
-    tile_row<W == kTriBackward>(v, K, Q, ld, a.N, len, sQK);
-  }
+  // the group's products
+  constexpr bool kSwap = W == kTriBackward;
+  constexpr int kFew = sizeof(T) == 2 ? 2 : 4;  // operands of 64 columns
+  if (a.N <= 64)
+    group_tiles<WV, kFew, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
+  else
+    group_tiles<WV, 4, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
   __syncthreads();
   float *sG = sGate[wave][0], *sB = sGate[wave][1];
   f32x4 (*sD)[16][5] = sDiag[wave];
