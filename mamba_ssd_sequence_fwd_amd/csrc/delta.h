@@ -59,9 +59,37 @@ enum DeltaTri : int {
 };
 
 // The log decay in base 2, at least -150: 2^-150 is 0 in fp32, so a decay of
-// e^-inf resets the state and no difference of two sums is inf - inf.
+// e^-inf resets the state and no difference of two sums is inf - inf. (A NaN
+// stays one.)
 __device__ __forceinline__ float delta_log2_decay(float g) {
-  return fmaxf(g * 1.4426950408889634f, -150.f);
+  const float v = g * 1.4426950408889634f;
+  return v < -150.f ? -150.f : v;
+}
+
+// Sums of a chunk's log decays, each lane's up to and including its own, in two
+// floats: the decay between two tokens is e^(difference of two sums), and behind
+// a reset the sums are large and the difference is not (one float at -150 is off
+// by 2^-17, 5e-6 of every decay behind it; with the residuals only the difference
+// itself is rounded).
+struct DecaySum {
+  float hi, lo;
+};
+template <int Ctrl, int RowMask>
+__device__ __forceinline__ void decay_sum_step(DecaySum &v) {
+  const float h = dpp_or_zero<Ctrl, RowMask>(v.hi), l = dpp_or_zero<Ctrl, RowMask>(v.lo);
+  const float sum = v.hi + h, part = sum - v.hi;
+  v.lo += l + ((v.hi - (sum - part)) + (h - part));  // what rounding left
+  v.hi = sum;
+}
+__device__ __forceinline__ DecaySum decay_sums(float g) {
+  DecaySum v = {g, 0.f};
+  decay_sum_step<kDppRowShr1, 0xf>(v);
+  decay_sum_step<kDppRowShr2, 0xf>(v);
+  decay_sum_step<kDppRowShr4, 0xf>(v);
+  decay_sum_step<kDppRowShr8, 0xf>(v);
+  decay_sum_step<kDppRowBcast15, 0xa>(v);
+  decay_sum_step<kDppRowBcast31, 0xc>(v);
+  return v;
 }
 
 // Tokens [lo, hi) of sequence s, within the stream whatever cu holds.

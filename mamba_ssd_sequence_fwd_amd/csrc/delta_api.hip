@@ -55,7 +55,7 @@ ssd_status check_delta(const ssd_problem *p, bool step, ssd::DeltaArgs *a) {
                                                                              : p->dstate) / 4);
   if (T >= kMostTokens || slots > kMostBlocks || nseq > kMostBlocks ||
       slots * p->nheads > kMostBlocks || nseq * p->nheads * (p->headdim / 16) > kMostBlocks ||
-      elements > kMostBlocks * 256 || (int64_t)p->ngroups * p->dstate > (1 << 24) ||
+      elements > kMostBlocks * 128 || (int64_t)p->ngroups * p->dstate > (1 << 24) ||
       (int64_t)p->nheads * p->headdim > (1 << 24))
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences x %d heads too large for one "
                 "launch", (long long)T, (long long)nseq, p->nheads);

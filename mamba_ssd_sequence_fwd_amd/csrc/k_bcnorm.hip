@@ -133,7 +133,7 @@ __global__ __launch_bounds__(256) void k_bc_norm(BcNormArgs a) {
       int h = side ? part - a.heads[0] % a.parts : part;
       if (h < 0) h += a.parts;
       const T *x = (const T *)a.in[side] + t * a.in_stride[side];
-      const T *g = (const T *)a.dout[side] + t * a.out_stride[side];
+      const T *g = kBackward ? (const T *)a.dout[side] + t * a.out_stride[side] : nullptr;
       T *o = kBackward ? (T *)a.out[side] + t * a.dx_stride[side]
                        : (T *)a.out[side] + t * a.out_stride[side];
       for (; h < heads; h += kBatch * a.parts) {

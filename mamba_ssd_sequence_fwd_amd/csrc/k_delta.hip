@@ -46,11 +46,11 @@ struct Gates {
 };
 __device__ __forceinline__ void fill_gates(Gates &G, float g, float beta, bool live) {
   const int lane = threadIdx.x & 63;
-  const float gam = wave_inclusive_sum(live ? delta_log2_decay(g) : 0.f);
-  const float gc = __shfl(gam, 63), e = exp2_fast(gam);
+  const DecaySum gam = decay_sums(live ? delta_log2_decay(g) : 0.f);
+  const float e = exp2_fast(gam.hi);
   G.b[lane] = live ? beta : 0.f;
   G.be[lane] = live ? beta * e : 0.f;
-  G.lf[lane] = exp2_fast(gc - gam);
+  G.lf[lane] = exp2_fast((__shfl(gam.hi, 63) - gam.hi) + (__shfl(gam.lo, 63) - gam.lo));
   G.ef[lane] = e;
 }
 

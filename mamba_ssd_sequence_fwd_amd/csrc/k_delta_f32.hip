@@ -7,12 +7,53 @@
 // 16 x 16 result tiles (rows: state channels n), and every product of the walk
 // contracts over the rows of tiles that the wave holds already (S, R, U),
 // which makes them right operands as they are. The left operands, rows of K
-// and Q, are staged in LDS for the workgroup's waves; T and M come from
-// k_delta_prep through the caches. The bound is the fp32 matrix rate (1/16 of
+// and Q, are staged in LDS for the workgroup's waves; T and M (k_delta_prep's)
+// come through the caches into registers. The bound is the fp32 matrix rate (1/16 of
 // the bf16 rate).
 #include "delta_tiles.h"
 
 namespace ssd {
+
+// `len` of 64 token rows of K and Q (or of K alone: null), N columns each, as rows
+// of W floats in LDS; the rest is zero. Four of a thread's loads are on their way
+// at once (one after the other they took as long as the chunk's products).
+template <int W>
+__device__ __forceinline__ void stage_rows(float *toK, float *toQ, const float *K, const float *Q,
+                                           size_t ld, int N, int len) {
+  constexpr int kAll = kDeltaChunk * (W / 4), kAtOnce = 4;
+  for (int e0 = threadIdx.x; e0 < kAll; e0 += kAtOnce * (int)blockDim.x) {
+    f32x4 k[kAtOnce], q[kAtOnce];
+#pragma unroll
+    for (int b = 0; b < kAtOnce; ++b) {
+      const int e = e0 + b * (int)blockDim.x, t = e / (W / 4), c = 4 * (e % (W / 4));
+      const size_t at = (size_t)min(t, len - 1) * ld + min(c, N - 4);
+      k[b] = ldf4(K + at);
+      if (Q) q[b] = ldf4(Q + at);
+    }
+#pragma unroll
+    for (int b = 0; b < kAtOnce; ++b) {
+      const int e = e0 + b * (int)blockDim.x, t = e / (W / 4), c = 4 * (e % (W / 4));
+      if (e >= kAll) break;
+      const bool in = t < len && c < N;
+      stf4(toK + t * W + c, in ? k[b] : kZero4);
+      if (Q) stf4(toQ + t * W + c, in ? q[b] : kZero4);
+    }
+  }
+}
+
+// decay_sums (sG and sE) and write strengths of a chunk, by the first wave.
+__device__ __forceinline__ void stage_gates(float *sG, float *sE, float *sB, const DeltaArgs &a, int64_t start,
+                                            int h, int len) {
+  if (threadIdx.x < kDeltaChunk) {
+    const int t = threadIdx.x;
+    const size_t at = (size_t)(start + min(t, len - 1)) * a.H + h;
+    const float gl = t < len ? delta_log2_decay(((const float *)a.g)[at]) : 0.f;
+    const DecaySum gam = decay_sums(gl);
+    sG[t] = gam.hi;
+    sE[t] = gam.lo;
+    sB[t] = t < len ? ((const float *)a.beta)[at] : 0.f;
+  }
+}
 
 // Left operand from staged rows: K^T (row n0 + lr, tokens t0 + 4 lg + r).
 template <int W>
@@ -28,25 +69,26 @@ __device__ __forceinline__ f32x4 row_operand(const float *rows, int t0, int n0) 
 }
 
 // 16 columns from p0 of 4 token rows (t0 + 4 lg + r), zeros past len.
-template <typename T>
-__device__ __forceinline__ f32x4 value_tile(const T *v, size_t ld, int t0, int len) {
+__device__ __forceinline__ f32x4 value_tile(const float *v, size_t ld, int t0, int len) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   f32x4 o;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int t = t0 + 4 * lg + r;
-    o[r] = t < len ? to_f32(v[t * ld + lr]) : 0.f;
+    const float x = v[min(t, len - 1) * ld + lr];
+    o[r] = t < len ? x : 0.f;
   }
   return o;
 }
 
 // Forward (kStates false): y and the final state. For the backward pass
 // (kStates true): the state entering each chunk, as (P, N), and U.
-template <typename T, int NT, bool kStates>
+template <int NT, bool kStates>
 __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
   constexpr int W = 16 * NT + 4;
   extern __shared__ float lds[];
-  float *sG = lds, *sB = lds + kDeltaChunk, *sK = lds + 2 * kDeltaChunk, *sQ = sK + kDeltaChunk * W;
+  float *sG = lds, *sE = sG + kDeltaChunk, *sB = sE + kDeltaChunk, *sK = sB + kDeltaChunk;
+  float *sQ = sK + kDeltaChunk * W;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int waves = blockDim.x >> 6, blocks = a.P / (16 * waves);
   int unit = blockIdx.x;
@@ -69,12 +111,25 @@ __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
     const int len = (int)min((int64_t)kDeltaChunk, hi - at);
     const size_t sh = (size_t)(slot0 + c) * a.H + h;
     __syncthreads();
-    stage_rows_f32<W>(sK, (const T *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
-    if (!kStates) stage_rows_f32<W>(sQ, (const T *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
-    stage_gates<T>(sG, sB, a, at, h, len);
-    __syncthreads();
+    const size_t rows = (at * a.G + grp) * a.N;
+    stage_rows<W>(sK, sQ, (const float *)a.B + rows, kStates ? nullptr : (const float *)a.C + rows,
+                  ldk, a.N, len);
+    stage_gates(sG, sE, sB, a, at, h, len);
+    // (on their way while K S is computed)
     const float *tri = (const float *)a.tri + sh * ((kStates ? 3 : 2) * 4096);
-    const T *x = (const T *)a.x + ((size_t)at * a.H + h) * a.P + p0;
+    const float *x = (const float *)a.x + ((size_t)at * a.H + h) * a.P + p0;
+    f32x4 V[4], T[10], M[10];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      V[i] = value_tile(x, ldx, 16 * i, len);
+#pragma unroll
+      for (int j = 0; j <= i; ++j) {
+        const int e = (16 * i + lr) * kDeltaChunk + 16 * j + 4 * lg;
+        T[i * (i + 1) / 2 + j] = ldf4(tri + e);
+        if (!kStates) M[i * (i + 1) / 2 + j] = ldf4(tri + 4096 + e);
+      }
+    }
+    __syncthreads();
 
     f32x4 R[4], O[4], U[4], e[4];
 #pragma unroll
@@ -86,7 +141,7 @@ __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
         if (!kStates) qs = mfma16(row_operand<W>(sQ, 16 * t, 16 * n), S[n], qs);
       }
       const f32x4 gm = ldf4(sG + 16 * t + 4 * lg), b = ldf4(sB + 16 * t + 4 * lg);
-      const f32x4 v = value_tile<T>(x, ldx, 16 * t, len);
+      const f32x4 v = V[t];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         e[t][r] = exp2_fast(gm[r]);
@@ -94,25 +149,25 @@ __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
         O[t][r] = e[t][r] * qs[r];
       }
     }
-    const float gc = sG[kDeltaChunk - 1];
+    const float gc = sG[kDeltaChunk - 1], rc = sE[kDeltaChunk - 1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       U[i] = kZero4;
 #pragma unroll
       for (int j = 0; j <= i; ++j)
-        U[i] = mfma16(ldf4(tri + (16 * i + lr) * kDeltaChunk + 16 * j + 4 * lg), R[j], U[i]);
+        U[i] = mfma16(T[i * (i + 1) / 2 + j], R[j], U[i]);
     }
     if (!kStates) {
-      T *y = (T *)a.y + ((size_t)at * a.H + h) * a.P + p0;
+      float *y = (float *)a.y + ((size_t)at * a.H + h) * a.P + p0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int j = 0; j <= i; ++j)
-          O[i] = mfma16(ldf4(tri + 4096 + (16 * i + lr) * kDeltaChunk + 16 * j + 4 * lg), U[j], O[i]);
+          O[i] = mfma16(M[i * (i + 1) / 2 + j], U[j], O[i]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = 16 * i + 4 * lg + r;
-          if (t < len) y[t * ldx + lr] = from_f32<T>(O[i][r]);
+          if (t < len) y[t * ldx + lr] = (O[i][r]);
         }
       }
     } else {
@@ -129,9 +184,9 @@ __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
     const float ec = exp2_fast(gc);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const f32x4 gm = ldf4(sG + 16 * t + 4 * lg);
+      const f32x4 d = (gc - ldf4(sG + 16 * t + 4 * lg)) + (rc - ldf4(sE + 16 * t + 4 * lg));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) U[t][r] *= exp2_fast(gc - gm[r]);
+      for (int r = 0; r < 4; ++r) U[t][r] *= exp2_fast(d[r]);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -151,11 +206,12 @@ __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
 // gradient of the initial state.
 //   dU = M^T dY + e^{gam_c - gam} (K dS),  dR = T^T dU
 //   dS <- e^{gam_c} dS + Q^T (e^gam dY) - K^T (beta e^gam dR)
-template <typename T, int NT>
+template <int NT>
 __global__ __launch_bounds__(256) void k_delta_reverse_f32(DeltaArgs a) {
   constexpr int W = 16 * NT + 4;
   extern __shared__ float lds[];
-  float *sG = lds, *sB = lds + kDeltaChunk, *sK = lds + 2 * kDeltaChunk, *sQ = sK + kDeltaChunk * W;
+  float *sG = lds, *sE = sG + kDeltaChunk, *sB = sE + kDeltaChunk, *sK = sB + kDeltaChunk;
+  float *sQ = sK + kDeltaChunk * W;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int waves = blockDim.x >> 6, blocks = a.P / (16 * waves);
   int unit = blockIdx.x;
@@ -179,35 +235,46 @@ __global__ __launch_bounds__(256) void k_delta_reverse_f32(DeltaArgs a) {
     const int len = (int)min((int64_t)kDeltaChunk, hi - at);
     const size_t sh = (size_t)(slot0 + c) * a.H + h;
     __syncthreads();
-    stage_rows_f32<W>(sK, (const T *)a.B + (at * a.G + grp) * a.N, ldk, a.N, len);
-    stage_rows_f32<W>(sQ, (const T *)a.C + (at * a.G + grp) * a.N, ldk, a.N, len);
-    stage_gates<T>(sG, sB, a, at, h, len);
-    __syncthreads();
+    const size_t rows = (at * a.G + grp) * a.N;
+    stage_rows<W>(sK, sQ, (const float *)a.B + rows, (const float *)a.C + rows, ldk, a.N, len);
+    stage_gates(sG, sE, sB, a, at, h, len);
+    // (on their way while K dS is computed)
     const float *tri = (const float *)a.tri + sh * (3 * 4096);
-    const T *dy = (const T *)a.dy + ((size_t)at * a.H + h) * a.P + p0;
-    const float gc = sG[kDeltaChunk - 1];
+    const float *dy = (const float *)a.dy + ((size_t)at * a.H + h) * a.P + p0;
+    f32x4 Y[4], Tt[10], Mt[10];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Y[i] = value_tile(dy, ldx, 16 * i, len);
+#pragma unroll
+      for (int j = 0; j <= i; ++j) {
+        const int e = (16 * j + lr) * kDeltaChunk + 16 * i + 4 * lg;
+        Tt[i * (i + 1) / 2 + j] = ldf4(tri + 4096 + e);
+        Mt[i * (i + 1) / 2 + j] = ldf4(tri + 8192 + e);
+      }
+    }
+    __syncthreads();
+    const float gc = sG[kDeltaChunk - 1], rc = sE[kDeltaChunk - 1];
 
     float *st = (float *)a.st1 + (sh * a.P + p0 + lr) * a.N + 4 * lg;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       if (16 * n < a.N) stf4(st + 16 * n, S[n]);
 
-    f32x4 Y[4], U[4];
+    f32x4 U[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      Y[t] = value_tile<T>(dy, ldx, 16 * t, len);
       f32x4 ks = kZero4;
 #pragma unroll
       for (int n = 0; n < NT; ++n) ks = mfma16(row_operand<W>(sK, 16 * t, 16 * n), S[n], ks);
-      const f32x4 gm = ldf4(sG + 16 * t + 4 * lg);
+      const f32x4 d = (gc - ldf4(sG + 16 * t + 4 * lg)) + (rc - ldf4(sE + 16 * t + 4 * lg));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) U[t][r] = exp2_fast(gc - gm[r]) * ks[r];
+      for (int r = 0; r < 4; ++r) U[t][r] = exp2_fast(d[r]) * ks[r];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = j; i < 4; ++i)
-        U[j] = mfma16(ldf4(tri + 8192 + (16 * j + lr) * kDeltaChunk + 16 * i + 4 * lg), Y[i], U[j]);
+        U[j] = mfma16(Mt[i * (i + 1) / 2 + j], Y[i], U[j]);
     f32x4 R[4];
     float *dr = (float *)a.dr + sh * kDeltaChunk * a.P + p0 + lr;
 #pragma unroll
@@ -215,7 +282,7 @@ __global__ __launch_bounds__(256) void k_delta_reverse_f32(DeltaArgs a) {
       R[j] = kZero4;
 #pragma unroll
       for (int i = j; i < 4; ++i)
-        R[j] = mfma16(ldf4(tri + 4096 + (16 * j + lr) * kDeltaChunk + 16 * i + 4 * lg), U[i], R[j]);
+        R[j] = mfma16(Tt[i * (i + 1) / 2 + j], U[i], R[j]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) dr[(16 * j + 4 * lg + r) * a.P] = R[j][r];
     }
@@ -265,10 +332,9 @@ __device__ __forceinline__ float sum16(float v) {
 //        + sum_{i >= t > j} (dM M + dL L)_ij + e^{gam_c} <S, dS>
 // The pair sum is taken as suffix sums of row sums less column sums of one
 // matrix, so that pairs on one side of t cancel to fp32 rounding.
-template <typename T>
 __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   constexpr int W1 = kDeltaChunk + 4;
-  __shared__ float sG[kDeltaChunk], sB[kDeltaChunk];
+  __shared__ float sG[kDeltaChunk], sE[kDeltaChunk], sB[kDeltaChunk];
   __shared__ float sM[kDeltaChunk * W1], sL[kDeltaChunk * W1];  // dM D, dL beta D
   __shared__ float sZ[kDeltaChunk], sP[kDeltaChunk], sC[4][kDeltaChunk], sS[4];
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, w = threadIdx.x >> 6;
@@ -278,15 +344,15 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   if (!delta_chunk(a, slot, start, len)) return;
   const size_t sh = (size_t)slot * a.H + h;
   const size_t ldk = (size_t)a.G * a.N, ldx = (size_t)a.H * a.P;
-  const T *K = (const T *)a.B + ((size_t)start * a.G + grp) * a.N;
-  const T *Q = (const T *)a.C + ((size_t)start * a.G + grp) * a.N;
-  const T *X = (const T *)a.x + ((size_t)start * a.H + h) * a.P;
-  const T *dY = (const T *)a.dy + ((size_t)start * a.H + h) * a.P;
+  const float *K = (const float *)a.B + ((size_t)start * a.G + grp) * a.N;
+  const float *Q = (const float *)a.C + ((size_t)start * a.G + grp) * a.N;
+  const float *X = (const float *)a.x + ((size_t)start * a.H + h) * a.P;
+  const float *dY = (const float *)a.dy + ((size_t)start * a.H + h) * a.P;
   const float *U = (const float *)a.u + sh * kDeltaChunk * a.P;
   const float *dR = (const float *)a.dr + sh * kDeltaChunk * a.P;
   const float *S0 = (const float *)a.st0 + sh * a.P * a.N;
   const float *S1 = (const float *)a.st1 + sh * a.P * a.N;
-  stage_gates<T>(sG, sB, a, start, h, len);
+  stage_gates(sG, sE, sB, a, start, h, len);
   for (int e = threadIdx.x; e < 4 * kDeltaChunk; e += 256) (&sC[0][0])[e] = 0.f;
   __syncthreads();
 
@@ -294,7 +360,8 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   const int tr = min(ti, len - 1);
   const bool live = ti < len;
   const f32x4 gm = ldf4(sG + 16 * w + 4 * lg), bt = ldf4(sB + 16 * w + 4 * lg);
-  const float gi = sG[ti], bi = sB[ti], gc = sG[kDeltaChunk - 1];
+  const f32x4 toEnd = (sG[kDeltaChunk - 1] - gm) + (sE[kDeltaChunk - 1] - ldf4(sE + 16 * w + 4 * lg));
+  const float gi = sG[ti], ei = sE[ti], bi = sB[ti];
 
   // pairs: rows i of this wave's tile, columns j of tiles up to it (lane: row
   // i, 4 columns j)
@@ -303,22 +370,22 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
     f32x4 kk = kZero4, qk = kZero4, dm = kZero4, dl = kZero4;
     const int tj = min(16 * j + lr, len - 1);
     for (int n = 4 * lg; n < a.N; n += 16) {
-      const f32x4 kj = widen4(K + tj * ldk + n);
-      kk = mfma16(kj, widen4(K + tr * ldk + n), kk);
-      qk = mfma16(kj, widen4(Q + tr * ldk + n), qk);
+      const f32x4 kj = ldf4(K + tj * ldk + n);
+      kk = mfma16(kj, ldf4(K + tr * ldk + n), kk);
+      qk = mfma16(kj, ldf4(Q + tr * ldk + n), qk);
     }
     for (int p = 4 * lg; p < a.P; p += 16) {
       const f32x4 u = ldf4(U + (16 * j + lr) * a.P + p);
-      const f32x4 y = widen4(dY + tr * ldx + p);
+      const f32x4 y = ldf4(dY + tr * ldx + p);
       dm = mfma16(u, live ? y : kZero4, dm);
       dl = mfma16(u, ldf4(dR + ti * a.P + p), dl);
     }
-    const f32x4 gj = ldf4(sG + 16 * j + 4 * lg);
+    const f32x4 dg = (gi - ldf4(sG + 16 * j + 4 * lg)) + (ei - ldf4(sE + 16 * j + 4 * lg));
     f32x4 m, l, both;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = ti - (16 * j + 4 * lg + r);
-      const float e = d >= 0 ? exp2_fast(gi - gj[r]) : 0.f;
+      const float e = d >= 0 ? exp2_fast(dg[r]) : 0.f;
       m[r] = d >= 0 ? dm[r] * e : 0.f;
       const float lk = d > 0 ? -dl[r] * e : 0.f;
       l[r] = lk * bi;
@@ -342,13 +409,13 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   // dx, and dR . V
   float rv = 0.f;
   for (int p = 4 * lg; p < a.P; p += 16) {
-    const f32x4 r = ldf4(dR + ti * a.P + p), v = widen4(X + tr * ldx + p);
-    T *dx = (T *)a.dx + ((size_t)(start + tr) * a.H + h) * a.P + p;
+    const f32x4 r = ldf4(dR + ti * a.P + p), v = ldf4(X + tr * ldx + p);
+    float *dx = (float *)a.dx + ((size_t)(start + tr) * a.H + h) * a.P + p;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (live) {
         rv += r[q] * v[q];
-        dx[q] = from_f32<T>(bi * r[q]);
+        dx[q] = (bi * r[q]);
       }
     }
   }
@@ -371,7 +438,7 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
         s1[r] = S1[(size_t)(p + r) * a.N + n0 + lr];
         if (w == (n0 >> 4) % 4) ss += s0[r] * s1[r];
       }
-      const f32x4 y = widen4(dY + tr * ldx + p);
+      const f32x4 y = ldf4(dY + tr * ldx + p);
       ys = mfma16(live ? y : kZero4, s0, ys);
       rs = mfma16(ldf4(dR + ti * a.P + p), s0, rs);
       us = mfma16(ldf4(U + ti * a.P + p), s1, us);
@@ -380,11 +447,11 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = min(16 * w + 4 * lg + r, len - 1);
-      k[r] = to_f32(K[t * ldk + n0 + lr]);
-      q[r] = to_f32(Q[t * ldk + n0 + lr]);
+      k[r] = (K[t * ldk + n0 + lr]);
+      q[r] = (Q[t * ldk + n0 + lr]);
       const float e = exp2_fast(gm[r]);
       dq[r] = e * ys[r];
-      const float rk = -e * rs[r], uk = exp2_fast(gc - gm[r]) * us[r];
+      const float rk = -e * rs[r], uk = exp2_fast(toEnd[r]) * us[r];
       dk[r] = bt[r] * rk + uk;
       za[r] += q[r] * dq[r] + bt[r] * k[r] * rk;
       zk[r] += k[r] * rk;
@@ -396,8 +463,8 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = min(16 * j + 4 * lg + r, len - 1);
-        kj[r] = to_f32(K[t * ldk + n0 + lr]);
-        qj[r] = to_f32(Q[t * ldk + n0 + lr]);
+        kj[r] = (K[t * ldk + n0 + lr]);
+        qj[r] = (Q[t * ldk + n0 + lr]);
       }
       if (j <= w) {
         dq = mfma16(ldf4(sM + ti * W1 + 16 * j + 4 * lg), kj, dq);
@@ -446,7 +513,7 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   if (lane == 0) sS[w] = ss;
   __syncthreads();
   if (lg == 0 && live)
-    ((T *)a.dbeta)[(size_t)(start + ti) * a.H + h] = from_f32<T>(rv + betasum + sK2[ti]);
+    ((float *)a.dbeta)[(size_t)(start + ti) * a.H + h] = (rv + betasum + sK2[ti]);
   if (w == 0) {
     const float zed = sZ[lane] + sR[lane] -
                       (sC[0][lane] + sC[1][lane] + sC[2][lane] + sC[3][lane]);
@@ -455,8 +522,8 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
     const float prefix = wave_inclusive_sum(zp) - zp;
     const float ends = exp2_fast(sG[kDeltaChunk - 1]) * (sS[0] + sS[1] + sS[2] + sS[3]);
     if (lane < len)
-      ((T *)a.dg)[(size_t)(start + lane) * a.H + h] =
-          from_f32<T>(all - (pre - zed) + prefix + ends);
+      ((float *)a.dg)[(size_t)(start + lane) * a.H + h] =
+          (all - (pre - zed) + prefix + ends);
   }
 }
 
@@ -477,15 +544,15 @@ __global__ __launch_bounds__(256) void k_delta_heads_sum(const float *part, T *d
   for (int r = 0; r < 4; ++r) to[r] = from_f32<T>(v[r]);
 }
 
-template <typename T, int NT>
+template <int NT>
 hipError_t chain_f32(const DeltaArgs &a, int what, hipStream_t s) {
   constexpr int W = 16 * NT + 4;
   const int waves = min(4, a.P / 16);
   const dim3 grid((unsigned)((int64_t)a.nseq * a.H * (a.P / (16 * waves)))), block(64 * waves);
-  const size_t lds = (2 * kDeltaChunk + (what == 1 ? 1 : 2) * kDeltaChunk * W) * sizeof(float);
-  const void *f = what == 0   ? (const void *)k_delta_chain_f32<T, NT, false>
-                  : what == 1 ? (const void *)k_delta_chain_f32<T, NT, true>
-                              : (const void *)k_delta_reverse_f32<T, NT>;
+  const size_t lds = (3 * kDeltaChunk + (what == 1 ? 1 : 2) * kDeltaChunk * W) * sizeof(float);
+  const void *f = what == 0   ? (const void *)k_delta_chain_f32<NT, false>
+                  : what == 1 ? (const void *)k_delta_chain_f32<NT, true>
+                              : (const void *)k_delta_reverse_f32<NT>;
   if (hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
     return e;
   DeltaArgs b = a;
@@ -493,20 +560,19 @@ hipError_t chain_f32(const DeltaArgs &a, int what, hipStream_t s) {
   return hipLaunchKernel(f, grid, block, args, lds, s);
 }
 
-template <typename T>
 hipError_t chain_f32_n(const DeltaArgs &a, int what, hipStream_t s) {
   if (a.nseq == 0) return hipSuccess;
-  if (a.N <= 64) return chain_f32<T, 4>(a, what, s);
-  if (a.N <= 128) return chain_f32<T, 8>(a, what, s);
-  return chain_f32<T, 16>(a, what, s);
+  if (a.N <= 64) return chain_f32<4>(a, what, s);
+  if (a.N <= 128) return chain_f32<8>(a, what, s);
+  return chain_f32<16>(a, what, s);
 }
 
 hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool states, hipStream_t s) {
-  return chain_f32_n<float>(a, states ? 1 : 0, s);
+  return chain_f32_n(a, states ? 1 : 0, s);
 }
 
 hipError_t launch_delta_reverse_f32(const DeltaArgs &a, hipStream_t s) {
-  return chain_f32_n<float>(a, 2, s);
+  return chain_f32_n(a, 2, s);
 }
 
 template <typename T>
@@ -521,15 +587,10 @@ hipError_t launch_delta_heads_sum(const DeltaArgs &a, bool bf16_io, hipStream_t 
   return bf16_io ? heads_sum<bf16>(a, s) : heads_sum<float>(a, s);
 }
 
-template <typename T>
-hipError_t grad_f32(const DeltaArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(k_delta_grad_f32<T>, dim3((unsigned)((int64_t)a.nslots * a.H)), dim3(256), 0,
-                     s, a);
-  return heads_sum<T>(a, s);
-}
-
 hipError_t launch_delta_grad_f32(const DeltaArgs &a, hipStream_t s) {
-  return a.T == 0 ? hipSuccess : grad_f32<float>(a, s);
+  if (a.T == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_delta_grad_f32, dim3((unsigned)((int64_t)a.nslots * a.H)), dim3(256), 0, s, a);
+  return heads_sum<float>(a, s);
 }
 
 }  // namespace ssd

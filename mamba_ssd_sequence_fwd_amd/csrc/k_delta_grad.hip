@@ -161,6 +161,7 @@ __global__ __launch_bounds__(256, (NK <= 4 ? 2 : 1)) void k_delta_grad(DeltaArgs
       fetch(0, sA0, sB0);
       if (w == 0) {
         const size_t ga = (size_t)(start + min(lane, len - 1)) * a.H + h;
+        // (one float: all results are rounded to bf16)
         sG[lane] = wave_inclusive_sum(
             lane < len ? delta_log2_decay((float)((const bf16 *)a.g)[ga]) : 0.f);
         sBt[lane] = lane < len ? (float)((const bf16 *)a.beta)[ga] : 0.f;

@@ -159,7 +159,7 @@ struct TilesOut {
 template <typename T, DeltaTri W, int WV, typename Out>
 __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaArgs a, int64_t bytes, int per) {
   __shared__ f32x4 sKK[10][64], sQK[10][64];
-  __shared__ float sGate[WV][2][kDeltaChunk];
+  __shared__ float sGate[WV][2][kDeltaChunk];    // decay_sums
   __shared__ f32x4 sDiag[WV][4][16][5];  // diagonal blocks: rows of L, then columns of T
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -181,16 +181,20 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
   else
     group_tiles<WV, 4, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
   __syncthreads();
-  float *sG = sGate[wave][0], *sB = sGate[wave][1];
+  float *sG = sGate[wave][0], *sE = sGate[wave][1];
   f32x4 (*sD)[16][5] = sDiag[wave];
+  // (M enters nothing but y in bf16, rounded once)
+  constexpr bool kExactM = sizeof(T) == 4 || W == kTriBackward;
   const int h1 = min((part + 1) * WV * per, a.hpg);
   for (int hh = part * WV * per + wave; hh < h1; hh += WV) {
     const int h = grp * a.hpg + hh;
+    float beta;
     {
       const size_t at = (size_t)(start + min(lane, len - 1)) * a.H + h;
-      const float gl = lane < len ? delta_log2_decay(ssd::ld<T>(a.g, at)) : 0.f;
-      sG[lane] = wave_inclusive_sum(gl);
-      sB[lane] = lane < len ? ssd::ld<T>(a.beta, at) : 0.f;
+      const DecaySum gam = decay_sums(lane < len ? delta_log2_decay(ssd::ld<T>(a.g, at)) : 0.f);
+      sG[lane] = gam.hi;
+      sE[lane] = gam.lo;
+      beta = lane < len ? ssd::ld<T>(a.beta, at) : 0.f;
     }
     wave_order();
     Out out;
@@ -202,12 +206,14 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
 #pragma unroll
         for (int j = 0; j <= i; ++j) {
           qk[tri(i, j)] = sQK[tri(i, j)][lane];
-          const float ga = sG[16 * (W == kTriForward ? i : j) + lr];
-          const f32x4 gb = ldf4(sG + 16 * (W == kTriForward ? j : i) + 4 * lg);
+          const int row = 16 * (W == kTriForward ? i : j) + lr;
+          const int col = 16 * (W == kTriForward ? j : i) + 4 * lg;
+          f32x4 d = sG[row] - ldf4(sG + col);
+          if (kExactM) d += sE[row] - ldf4(sE + col);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const bool below = j < i || (W == kTriForward ? 4 * lg + r <= lr : lr <= 4 * lg + r);
-            const float e = exp2_fast(W == kTriForward ? ga - gb[r] : gb[r] - ga);
+            const float e = exp2_fast(W == kTriForward ? d[r] : -d[r]);
             qk[tri(i, j)][r] = below ? qk[tri(i, j)][r] * e : 0.f;
           }
         }
@@ -219,14 +225,15 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
     f32x4 Lt[10];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float gi = sG[16 * i + lr], bi = sB[16 * i + lr];
+      const float gi = sG[16 * i + lr], ei = sE[16 * i + lr], bi = __shfl(beta, 16 * i + lr);
 #pragma unroll
       for (int j = 0; j <= i; ++j) {
-        const f32x4 gj = ldf4(sG + 16 * j + 4 * lg), kk = sKK[tri(i, j)][lane];
+        const f32x4 kk = sKK[tri(i, j)][lane];
+        const f32x4 d = (gi - ldf4(sG + 16 * j + 4 * lg)) + (ei - ldf4(sE + 16 * j + 4 * lg));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const bool below = j < i || 4 * lg + r < lr;
-          Lt[tri(i, j)][r] = below ? bi * kk[r] * exp2_fast(gi - gj[r]) : 0.f;
+          Lt[tri(i, j)][r] = below ? bi * kk[r] * exp2_fast(d[r]) : 0.f;
         }
       }
     }
