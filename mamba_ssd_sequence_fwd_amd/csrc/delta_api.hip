@@ -51,11 +51,10 @@ ssd_status check_delta(const ssd_problem *p, bool step, ssd::DeltaArgs *a) {
   const int64_t nseq = packed ? p->num_seqs : p->batch;
   const int64_t per = ((int64_t)p->seqlen + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk;
   const int64_t slots = packed ? T / ssd::kDeltaChunk + nseq : nseq * per;
-  const int64_t elements = T * ((int64_t)p->nheads * (p->headdim > p->dstate ? p->headdim
-                                                                             : p->dstate) / 4);
+  const int64_t quads = T * p->ngroups * (p->dstate / 4);  // of dB and dC, each
   if (T >= kMostTokens || slots > kMostBlocks || nseq > kMostBlocks ||
       slots * p->nheads > kMostBlocks || nseq * p->nheads * (p->headdim / 16) > kMostBlocks ||
-      elements > kMostBlocks * 128 || (int64_t)p->ngroups * p->dstate > (1 << 24) ||
+      quads > kMostBlocks * 128 || (int64_t)p->ngroups * p->dstate > (1 << 24) ||
       (int64_t)p->nheads * p->headdim > (1 << 24))
     return fail(SSD_ERR_UNSUPPORTED, "%lld tokens in %lld sequences x %d heads too large for one "
                 "launch", (long long)T, (long long)nseq, p->nheads);
