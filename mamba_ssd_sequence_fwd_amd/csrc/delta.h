@@ -170,13 +170,14 @@ __device__ __forceinline__ bool delta_chunk(const DeltaArgs &a, int slot, int64_
   return true;
 }
 
-// A workgroup's place in the order of units: workgroups go round-robin over the
-// eight XCDs, and each takes an eighth of the units in a row, so that heads that
-// read the same rows of B and C find them in one L2.
-__device__ __forceinline__ int xcd_unit() {
-  const int n = (int)gridDim.x, b = (int)blockIdx.x, q = n / 8, r = n % 8, x = b % 8;
+// Workgroup b's place of n in the order of units: workgroups go round-robin over
+// the eight XCDs, and each takes an eighth of the units in a row, so that heads
+// that read the same rows of B and C find them in one L2.
+__device__ __forceinline__ int xcd_unit(int b, int n) {
+  const int q = n / 8, r = n % 8, x = b % 8;
   return x * q + min(x, r) + b / 8;
 }
+__device__ __forceinline__ int xcd_unit() { return xcd_unit((int)blockIdx.x, (int)gridDim.x); }
 
 // Bytes of one (slot, head)'s triangular matrices.
 size_t delta_tri_bytes(bool tiles, DeltaTri which);
@@ -184,10 +185,9 @@ size_t delta_tri_bytes(bool tiles, DeltaTri which);
 hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16_io, DeltaTri which, hipStream_t s);
 // The bf16 path: segments (sets a.seg, a.nseg_per, a.nsegs), the forward call
 // (triangular matrices in place), and the backward call's steps.
-void delta_segments(DeltaArgs &a, bool packed);
+void delta_segments(DeltaArgs &a, bool packed, bool backward);
 hipError_t launch_delta_forward(const DeltaArgs &a, hipStream_t s);
-hipError_t launch_delta_states(const DeltaArgs &a, hipStream_t s);
-hipError_t launch_delta_reverse(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_both_ways(const DeltaArgs &a, hipStream_t s);
 hipError_t launch_delta_grad(const DeltaArgs &a, hipStream_t s);
 // Parts that a group's heads are taken in by the gradients (1: dB and dC are
 // written at once).

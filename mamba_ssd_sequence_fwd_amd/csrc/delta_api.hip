@@ -100,7 +100,7 @@ struct Carver {
 // The forward pass's workspace; with a base, its parts are set.
 size_t forward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   const bool bf = p->dtype == SSD_DTYPE_BF16;
-  if (bf) ssd::delta_segments(*a, p->num_seqs > 0);
+  if (bf) ssd::delta_segments(*a, p->num_seqs > 0, false);
   Carver c{static_cast<char *>(ws)};
   const size_t tri = ssd::delta_tri_bytes(bf, ssd::kTriForward);
   a->tri = c.take((size_t)a->nslots * a->H * tri);
@@ -115,7 +115,7 @@ size_t forward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
 size_t backward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   const bool bf = p->dtype == SSD_DTYPE_BF16;
   const size_t es = bf ? 2 : sizeof(float), sh = (size_t)a->nslots * a->H;
-  if (bf) ssd::delta_segments(*a, p->num_seqs > 0);
+  if (bf) ssd::delta_segments(*a, p->num_seqs > 0, true);
   a->hparts = bf ? ssd::delta_grad_parts(*a) : a->hpg;
   Carver c{static_cast<char *>(ws)};
   const size_t tri = ssd::delta_tri_bytes(bf, ssd::kTriBackward);
@@ -331,13 +331,13 @@ ssd_status ssd_delta_backward(const ssd_problem *p, const void *x, const void *g
   if ((st = hip_result(ssd::launch_delta_prep(a, bf, ssd::kTriBackward, s), "delta rule prep")) !=
       SSD_OK)
     return st;
-  if (a.T > 0 && (st = hip_result(bf ? ssd::launch_delta_states(a, s)
-                                     : ssd::launch_delta_chain_f32(a, true, s),
-                                  "delta rule states")) != SSD_OK)
-    return st;
-  if ((st = hip_result(bf ? ssd::launch_delta_reverse(a, s) : ssd::launch_delta_reverse_f32(a, s),
-                       "delta rule reverse")) != SSD_OK)
-    return st;
+  if (bf) {
+    st = hip_result(ssd::launch_delta_both_ways(a, s), "delta rule walks");
+  } else {
+    if (a.T > 0) st = hip_result(ssd::launch_delta_chain_f32(a, true, s), "delta rule states");
+    if (st == SSD_OK) st = hip_result(ssd::launch_delta_reverse_f32(a, s), "delta rule reverse");
+  }
+  if (st != SSD_OK) return st;
   return hip_result(bf ? ssd::launch_delta_grad(a, s) : ssd::launch_delta_grad_f32(a, s),
                     "delta rule gradients");
 }

@@ -88,23 +88,23 @@ enum WalkMode : int {
   kWalkLocal = 2   // a segment's own final state and its transition's columns
 };
 
-// Three workgroups of four waves to a compute unit: 168 registers and 53 KB of
-// LDS each.
+// What the walks stage, one array for each: the compiler then sees which reads do
+// not meet the loads under way, and does not wait for those. (M takes Q's place
+// once Q S is done, y that of the values.)
+template <int NK>
+constexpr int kRowElems = kDeltaChunk * 32 * NK;
+constexpr int kTriElems = 2 * kTriTiles * kTileElems;
+
+// The walk forwards of unit `unit`: 16 WV columns of a sequence or segment.
 template <int NK, int WV, WalkMode kMode>
-__global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(DeltaArgs a) {
+__device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16 *sK, bf16 *sQ,
+                                              bf16 *sT, bf16 *sV, Gates &G) {
   constexpr int N = 32 * NK, W = 16 * WV;  // state channels, the workgroup's columns
   constexpr bool kY = kMode == kWalkY, kLocal = kMode == kWalkLocal;
-  constexpr int kT = 2 * kTriTiles * kTileElems;
-  // One array for each of what is staged: the compiler then sees which reads do
-  // not meet the loads under way, and does not wait for those.
-  // M takes Q's place once Q S is done, y that of the values.
-  __shared__ bf16 sK[kDeltaChunk * N], sQ[kY ? kDeltaChunk * N : 8], sT[kT], sV[kDeltaChunk * W];
-  __shared__ Gates G;
-  static_assert(!kY || kDeltaChunk * N >= kTriTiles * kTileElems, "M must fit where Q was");
+  constexpr int kT = kTriElems;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (kLocal ? a.P + a.N : a.P) / 16, blocks = (tiles + WV - 1) / WV;
-  int unit = xcd_unit();
   const int tile0 = (unit % blocks) * WV, tile = min(tile0 + wave, tiles - 1);
   const bool on = tile0 + wave < tiles;     // (a wave past the last tile repeats it)
   unit /= blocks;
@@ -354,15 +354,13 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
 // Writes dS behind each chunk, dR, and the initial state's gradient; or
 // (kLocal) a segment's dS at its start from zeros at its end.
 template <int NK, int WV, bool kLocal>
-__global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(DeltaArgs a) {
+__device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf16 *sK, bf16 *sQ,
+                                               bf16 *sT, bf16 *sV, Gates &G) {
   constexpr int N = 32 * NK, W = 16 * WV;
-  constexpr int kT = 2 * kTriTiles * kTileElems;
-  __shared__ bf16 sK[kDeltaChunk * N], sQ[kDeltaChunk * N], sT[kT], sV[kDeltaChunk * W];
-  __shared__ Gates G;
+  constexpr int kT = kTriElems;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = a.P / W;
-  int unit = xcd_unit();
   const int pw = (unit % blocks) * W, p0 = pw + 16 * wave, p = p0 + lr;
   unit /= blocks;
   const int h = unit % a.H, sg = unit / a.H, grp = h / a.hpg;
@@ -583,6 +581,34 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_back(Delta
       }
 }
 
+// Three workgroups of four waves to a compute unit: 168 registers and 53 KB of
+// LDS each.
+template <int NK, int WV, WalkMode kMode>
+__global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(DeltaArgs a) {
+  constexpr bool kY = kMode == kWalkY;
+  __shared__ bf16 sK[kRowElems<NK>], sQ[kY ? kRowElems<NK> : 8], sT[kTriElems];
+  __shared__ bf16 sV[kDeltaChunk * 16 * WV];
+  __shared__ Gates G;
+  static_assert(!kY || kRowElems<NK> >= kTriTiles * kTileElems, "M must fit where Q was");
+  walk_forwards<NK, WV, kMode>(a, xcd_unit(), sK, sQ, sT, sV, G);
+}
+
+// The backward pass's two walks at once: neither needs the other (dS goes without
+// S and U), and one alone leaves most of a compute unit idle while it waits for its
+// chunk's products. The first `back` workgroups walk backwards, the longer way.
+template <int NK, int WV, bool kLocal>
+__global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_both(DeltaArgs a, int back) {
+  __shared__ bf16 sK[kRowElems<NK>], sQ[kRowElems<NK>], sT[kTriElems];
+  __shared__ bf16 sV[kDeltaChunk * 16 * WV];
+  __shared__ Gates G;
+  const int b = (int)blockIdx.x;
+  if (b < back)
+    walk_backwards<NK, WV, kLocal>(a, xcd_unit(b, back), sK, sQ, sT, sV, G);
+  else
+    walk_forwards<NK, WV, kLocal ? kWalkLocal : kWalkSave>(
+        a, xcd_unit(b - back, (int)gridDim.x - back), sK, sQ, sT, sV, G);
+}
+
 // The states at the segments' starts, in place of their own final states: with
 // F a segment's transition, S <- F S + (its own). kBack: dL/dS at the segments'
 // ends, dS <- F^T dS + (its own), from the last to the first. Per (sequence,
@@ -670,21 +696,29 @@ __global__ __launch_bounds__(64 * WV) void k_delta_join(DeltaArgs a) {
   }
 }
 
-enum Walk : int { kY, kSave, kLocal, kBack, kBackLocal };
+enum Walk : int { kForward, kForwardLocal, kBoth, kBothLocal };
 
 template <int NK, int WV>
 hipError_t walk_launch(const DeltaArgs &a, Walk what, hipStream_t s) {
-  const int tiles = (what == kLocal ? a.P + a.N : a.P) / 16;
+  // (a segment's local walk forwards takes its transition's columns too)
+  const int tiles = a.P / 16, more = what == kForwardLocal || what == kBothLocal ? a.N / 16 : 0;
   const int64_t units = (int64_t)(a.seg ? a.nsegs : a.nseq) * a.H;
-  const dim3 grid((unsigned)(units * ((tiles + WV - 1) / WV))), block(64 * WV);
+  const unsigned ahead = (unsigned)(units * ((tiles + more + WV - 1) / WV));
+  const unsigned back = (unsigned)(units * (tiles / WV));
+  const dim3 block(64 * WV);
   switch (what) {
-    case kY: hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkY>), grid, block, 0, s, a); break;
-    case kSave: hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkSave>), grid, block, 0, s, a); break;
-    case kLocal:
-      hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkLocal>), grid, block, 0, s, a);
+    case kForward:
+      hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkY>), dim3(ahead), block, 0, s, a);
       break;
-    case kBack: hipLaunchKernelGGL((k_delta_back<NK, WV, false>), grid, block, 0, s, a); break;
-    case kBackLocal: hipLaunchKernelGGL((k_delta_back<NK, WV, true>), grid, block, 0, s, a); break;
+    case kForwardLocal:
+      hipLaunchKernelGGL((k_delta_walk<NK, WV, kWalkLocal>), dim3(ahead), block, 0, s, a);
+      break;
+    case kBoth:
+      hipLaunchKernelGGL((k_delta_both<NK, WV, false>), dim3(back + ahead), block, 0, s, a, (int)back);
+      break;
+    case kBothLocal:
+      hipLaunchKernelGGL((k_delta_both<NK, WV, true>), dim3(back + ahead), block, 0, s, a, (int)back);
+      break;
   }
   return hipGetLastError();
 }
@@ -719,29 +753,38 @@ hipError_t join(const DeltaArgs &a, bool back, hipStream_t s) {
   return join_n<16, 8>(a, back, s);
 }
 
-// Whether and where sequences are cut. Cut, a call walks every segment twice and
-// the N columns of its transition once, 2 + N / P times the work, so the card has
-// to be that empty without: a workgroup on each compute unit is close to all that
-// the units give (three there take 2.3 times as long as one). And it has to be a
-// shorter way: two walks through a segment, the join's step for each segment (about
-// a chunk's time) and two more launches. sqrt(chunks) of them make a segment, or
-// as many as leave two workgroups for each unit. Measured in us, whole and cut:
-//   32 heads of 128, 1 x 16384 tokens    978, 484    backward 2243, 1277
-//   24 heads of 64, 1 x 4096 tokens      212, 100    backward  452,  261
-//   24 heads of 64, 1 x 1024 tokens       63,  57    backward  140,  131
-//   32 heads of 64, 4 x 2048 tokens      107,  99 (N = 64; just not cut)
-//   32 heads of 64, 2 x 2048 tokens      176, 252 (N = 256; not cut)
-//   24 heads of 64, 3 sequences <= 1536   56,  67 (not cut)
-constexpr int kComputeUnits = 256;
-void delta_segments(DeltaArgs &a, bool packed) {
+// Whether and where sequences are cut. Whole, a call takes its sequences' chunks one
+// after the other, while a workgroup (64 columns) on each compute unit is close to
+// half of what the units give. Cut, every segment is walked twice, the N columns of
+// its transition come along, and each of its joins takes a time that goes with N.
+// In units of a walk's chunk (4 us at N = 128), with w walks (1, backward 2):
+//   whole: chunks
+//   cut:   the longer of two segments and the work, (2 w + N / P) of it, at 0.6 of
+//          a chunk a workgroup (three share a unit; 1 past N = 128, where one fills
+//          it), w N / 128 a segment for the joins, and w + 1 launches more
+// sqrt(chunks) of them make a segment, or as many as leave two workgroups for each
+// unit. Measured in us, whole and cut:
+//   32 heads of 128, 1 x 16384 tokens    978, 455    backward 1555, 1273
+//   24 heads of 64, 1 x 4096 tokens      212, 100    backward  307,  218
+//   24 heads of 64, 2 x 4096 tokens      216, 140    backward  371,  347
+//   24 heads of 64, 1 x 1024 tokens       63,  57    backward  102,  105 (not cut)
+//   16 heads of 128, N = 256, 1 x 4096   315, 264    backward  543,  653 (not cut)
+//   32 heads of 64, 2 x 2048, N = 256    176, 252 (not cut)
+//   80 heads of 64, 1 x 4096 tokens      230, 210 (not cut)
+//   32 heads of 128, 1 x 2048 tokens                 backward  213,  251 (not cut)
+void delta_segments(DeltaArgs &a, bool packed, bool backward) {
+  constexpr int kComputeUnits = 256;
   a.seg = a.nseg_per = a.nsegs = 0;
   if (a.nseq == 0 || a.T == 0) return;
   const int64_t chunks = (a.T / a.nseq + kDeltaChunk - 1) / kDeltaChunk;  // (packed: on average)
   const int64_t groups = (int64_t)a.nseq * a.H * ((a.P + 63) / 64);
-  if (groups * (2 * a.P + a.N) > (int64_t)kComputeUnits * a.P) return;
-  int64_t m = chunks * groups / (2 * kComputeUnits);
+  const int64_t w = backward ? 2 : 1;
+  int64_t m = chunks * groups * w / (2 * kComputeUnits);
   while (m * m < chunks) ++m;
-  if (2 * m + chunks / m + 4 > chunks) return;
+  const float fill = (float)groups * (float)chunks / kComputeUnits * (a.N <= 128 ? 0.6f : 1.f);
+  const float work = fill * (2.f * (float)w + (float)a.N / (float)a.P);
+  const float joins = (float)((chunks + m - 1) / m * w) * (float)a.N / 128.f;
+  if (fmaxf(2.f * (float)m, work) + joins + (float)(w + 1) >= (float)chunks) return;
   a.seg = (int)m;
   a.nseg_per = (int)((a.nc_per + m - 1) / m);
   a.nsegs = packed ? (int)(a.T / (kDeltaChunk * m)) + a.nseq : a.nseq * a.nseg_per;
@@ -749,29 +792,21 @@ void delta_segments(DeltaArgs &a, bool packed) {
 
 hipError_t launch_delta_forward(const DeltaArgs &a, hipStream_t s) {
   if (a.seg) {
-    hipError_t e = walk(a, kLocal, s);
+    hipError_t e = walk(a, kForwardLocal, s);
     if (e == hipSuccess) e = join(a, false, s);
     if (e != hipSuccess) return e;
   }
-  return walk(a, kY, s);
+  return walk(a, kForward, s);
 }
 
-hipError_t launch_delta_states(const DeltaArgs &a, hipStream_t s) {
+hipError_t launch_delta_both_ways(const DeltaArgs &a, hipStream_t s) {
   if (a.seg) {
-    hipError_t e = walk(a, kLocal, s);
+    hipError_t e = walk(a, kBothLocal, s);
     if (e == hipSuccess) e = join(a, false, s);
-    if (e != hipSuccess) return e;
-  }
-  return walk(a, kSave, s);
-}
-
-hipError_t launch_delta_reverse(const DeltaArgs &a, hipStream_t s) {
-  if (a.seg) {
-    hipError_t e = walk(a, kBackLocal, s);
     if (e == hipSuccess) e = join(a, true, s);
     if (e != hipSuccess) return e;
   }
-  return walk(a, kBack, s);
+  return walk(a, kBoth, s);
 }
 
 }  // namespace ssd

@@ -50,6 +50,9 @@ CASES = {
     "segments-N256": ([1200], False, 2, 128, 256, 1, "bf16", True),
     "segments-P16-N176": ([1250], False, 3, 16, 176, 3, "bf16", False),
     "segments-packed": ([2500, 0, 1999, 1], True, 2, 32, 48, 1, "bf16", True),
+    "long-N128": ([3000], False, 2, 128, 128, 1, "bf16", True),
+    "long-N256": ([3200], False, 1, 128, 256, 1, "bf16", True),
+    "long-P16-N176": ([3000], False, 2, 16, 176, 2, "bf16", False),
     "one-token-fp32": ([1, 1], False, 4, 64, 128, 1, "fp32", True),
     "one-chunk-and-one-fp32": ([65], False, 6, 32, 64, 2, "fp32", False),
     "P16-N48-fp32": ([100, 100], False, 5, 16, 48, 1, "fp32", True),
