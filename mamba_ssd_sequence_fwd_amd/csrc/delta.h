@@ -194,8 +194,7 @@ hipError_t launch_delta_grad(const DeltaArgs &a, hipStream_t s);
 int delta_grad_parts(const DeltaArgs &a);
 hipError_t launch_delta_heads_sum(const DeltaArgs &a, bool bf16_io, hipStream_t s);
 // The same in fp32.
-hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool states, hipStream_t s);
-hipError_t launch_delta_reverse_f32(const DeltaArgs &a, hipStream_t s);
+hipError_t launch_delta_walk_f32(const DeltaArgs &a, bool both, hipStream_t s);
 hipError_t launch_delta_grad_f32(const DeltaArgs &a, hipStream_t s);
 
 struct DeltaStepArgs {

@@ -248,7 +248,7 @@ ssd_status ssd_delta_forward(const ssd_problem *p, const void *x, const void *g,
       SSD_OK)
     return st;
   return hip_result(bf ? ssd::launch_delta_forward(a, s)
-                       : ssd::launch_delta_chain_f32(a, false, s), "delta rule");
+                       : ssd::launch_delta_walk_f32(a, false, s), "delta rule");
 }
 
 ssd_status ssd_delta_step(const ssd_problem *p, const void *x, const void *g, const void *beta,
@@ -331,13 +331,9 @@ ssd_status ssd_delta_backward(const ssd_problem *p, const void *x, const void *g
   if ((st = hip_result(ssd::launch_delta_prep(a, bf, ssd::kTriBackward, s), "delta rule prep")) !=
       SSD_OK)
     return st;
-  if (bf) {
-    st = hip_result(ssd::launch_delta_both_ways(a, s), "delta rule walks");
-  } else {
-    if (a.T > 0) st = hip_result(ssd::launch_delta_chain_f32(a, true, s), "delta rule states");
-    if (st == SSD_OK) st = hip_result(ssd::launch_delta_reverse_f32(a, s), "delta rule reverse");
-  }
-  if (st != SSD_OK) return st;
+  if ((st = hip_result(bf ? ssd::launch_delta_both_ways(a, s)
+                          : ssd::launch_delta_walk_f32(a, true, s), "delta rule walks")) != SSD_OK)
+    return st;
   return hip_result(bf ? ssd::launch_delta_grad(a, s) : ssd::launch_delta_grad_f32(a, s),
                     "delta rule gradients");
 }

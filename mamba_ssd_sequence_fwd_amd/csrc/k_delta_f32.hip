@@ -84,14 +84,12 @@ __device__ __forceinline__ f32x4 value_tile(const float *v, size_t ld, int t0, i
 // Forward (kStates false): y and the final state. For the backward pass
 // (kStates true): the state entering each chunk, as (P, N), and U.
 template <int NT, bool kStates>
-__global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
+__device__ __forceinline__ void chain_f32(const DeltaArgs &a, int unit, float *lds) {
   constexpr int W = 16 * NT + 4;
-  extern __shared__ float lds[];
   float *sG = lds, *sE = sG + kDeltaChunk, *sB = sE + kDeltaChunk, *sK = sB + kDeltaChunk;
   float *sQ = sK + kDeltaChunk * W;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int waves = blockDim.x >> 6, blocks = a.P / (16 * waves);
-  int unit = blockIdx.x;
   const int p0 = ((unit % blocks) * waves + (threadIdx.x >> 6)) * 16;
   unit /= blocks;
   const int h = unit % a.H, seq = unit / a.H, grp = h / a.hpg;
@@ -207,14 +205,12 @@ __global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
 //   dU = M^T dY + e^{gam_c - gam} (K dS),  dR = T^T dU
 //   dS <- e^{gam_c} dS + Q^T (e^gam dY) - K^T (beta e^gam dR)
 template <int NT>
-__global__ __launch_bounds__(256) void k_delta_reverse_f32(DeltaArgs a) {
+__device__ __forceinline__ void reverse_f32(const DeltaArgs &a, int unit, float *lds) {
   constexpr int W = 16 * NT + 4;
-  extern __shared__ float lds[];
   float *sG = lds, *sE = sG + kDeltaChunk, *sB = sE + kDeltaChunk, *sK = sB + kDeltaChunk;
   float *sQ = sK + kDeltaChunk * W;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int waves = blockDim.x >> 6, blocks = a.P / (16 * waves);
-  int unit = blockIdx.x;
   const int p0 = ((unit % blocks) * waves + (threadIdx.x >> 6)) * 16;
   unit /= blocks;
   const int h = unit % a.H, seq = unit / a.H, grp = h / a.hpg;
@@ -312,6 +308,24 @@ __global__ __launch_bounds__(256) void k_delta_reverse_f32(DeltaArgs a) {
     for (int n = 0; n < NT; ++n)
       if (16 * n < a.N) stf4(a.dh0 + srow + 16 * n, S[n]);
   }
+}
+
+template <int NT>
+__global__ __launch_bounds__(256) void k_delta_chain_f32(DeltaArgs a) {
+  extern __shared__ float lds[];
+  chain_f32<NT, false>(a, (int)blockIdx.x, lds);
+}
+
+// The backward pass's two walks, which do not need each other: half of the
+// workgroups each, the longer way first.
+template <int NT>
+__global__ __launch_bounds__(256) void k_delta_both_f32(DeltaArgs a) {
+  extern __shared__ float lds[];
+  const int half = (int)gridDim.x / 2, b = (int)blockIdx.x;
+  if (b < half)
+    reverse_f32<NT>(a, b, lds);
+  else
+    chain_f32<NT, true>(a, b - half, lds);
 }
 
 // Sum over the 16 lanes that share lg (columns of a result tile).
@@ -545,34 +559,24 @@ __global__ __launch_bounds__(256) void k_delta_heads_sum(const float *part, T *d
 }
 
 template <int NT>
-hipError_t chain_f32(const DeltaArgs &a, int what, hipStream_t s) {
+hipError_t walk_f32(const DeltaArgs &a, bool both, hipStream_t s) {
   constexpr int W = 16 * NT + 4;
   const int waves = min(4, a.P / 16);
-  const dim3 grid((unsigned)((int64_t)a.nseq * a.H * (a.P / (16 * waves)))), block(64 * waves);
-  const size_t lds = (3 * kDeltaChunk + (what == 1 ? 1 : 2) * kDeltaChunk * W) * sizeof(float);
-  const void *f = what == 0   ? (const void *)k_delta_chain_f32<NT, false>
-                  : what == 1 ? (const void *)k_delta_chain_f32<NT, true>
-                              : (const void *)k_delta_reverse_f32<NT>;
-  if (hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
+  const unsigned units = (unsigned)((int64_t)a.nseq * a.H * (a.P / (16 * waves)));
+  const size_t lds = (3 * kDeltaChunk + 2 * kDeltaChunk * W) * sizeof(float);
+  const auto f = both ? k_delta_both_f32<NT> : k_delta_chain_f32<NT>;
+  if (hipError_t e = hipFuncSetAttribute((const void *)f, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)lds))
     return e;
-  DeltaArgs b = a;
-  void *args[] = {&b};
-  return hipLaunchKernel(f, grid, block, args, lds, s);
+  hipLaunchKernelGGL(f, dim3(both ? 2 * units : units), dim3(64 * waves), lds, s, a);
+  return hipGetLastError();
 }
 
-hipError_t chain_f32_n(const DeltaArgs &a, int what, hipStream_t s) {
+hipError_t launch_delta_walk_f32(const DeltaArgs &a, bool both, hipStream_t s) {
   if (a.nseq == 0) return hipSuccess;
-  if (a.N <= 64) return chain_f32<4>(a, what, s);
-  if (a.N <= 128) return chain_f32<8>(a, what, s);
-  return chain_f32<16>(a, what, s);
-}
-
-hipError_t launch_delta_chain_f32(const DeltaArgs &a, bool states, hipStream_t s) {
-  return chain_f32_n(a, states ? 1 : 0, s);
-}
-
-hipError_t launch_delta_reverse_f32(const DeltaArgs &a, hipStream_t s) {
-  return chain_f32_n(a, 2, s);
+  if (a.N <= 64) return walk_f32<4>(a, both, s);
+  if (a.N <= 128) return walk_f32<8>(a, both, s);
+  return walk_f32<16>(a, both, s);
 }
 
 template <typename T>
