@@ -16,13 +16,17 @@
 // a team walks several heads with one set of sines. They come from the product
 // in 64 bits, in turns: a far position keeps its fraction (an fp32 product at
 // position 10^6 is off by up to 0.06 rad).
+//
+// A lone row's way is its memory's latency, so a team has four heads (backwards two)
+// on their way at a time. Measured (MI355X), bf16, 32 heads of 128: 16384 tokens 51
+// us, 5.3 TB/s (96 us head by head; 68 us with pieces of 8 bytes where 16 do), 16
+// tokens 5 us; backwards, 40 heads of 128, all turned, 16384 tokens: 96 us, 5.2 TB/s
+// (127 us head by head), and 5 us for the weights' column sums.
 #include "bcnorm.h"
 #include "rows.h"
 
 namespace ssd {
 namespace {
-
-typedef bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 // Four channels as they lie in memory, and their values: the rows of several
 // heads are on their way before the first is used.

@@ -9,7 +9,11 @@
 // which makes them right operands as they are. The left operands, rows of K
 // and Q, are staged in LDS for the workgroup's waves; T and M (k_delta_prep's)
 // come through the caches into registers. The bound is the fp32 matrix rate (1/16 of
-// the bf16 rate).
+// the bf16 rate): 68 products of 16 x 16 x 16 a chunk and wave at N = 64, 4.1 us.
+// Measured (MI355X), 36 sequences and heads of 64 x 64 and 5 chunks: 49 us, 36
+// workgroups on 36 compute units, a chunk every 9.8 us (its rows staged, its four
+// products one after the other); 48 and 9: the two walks of the backward pass 79 us
+// together (76 and 59 one after the other), the gradients 43 us.
 #include "delta_tiles.h"
 
 namespace ssd {

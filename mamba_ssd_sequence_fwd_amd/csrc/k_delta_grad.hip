@@ -19,6 +19,11 @@
 // cancel. All operands are bf16 (S, dS, U and dR come rounded from the walks);
 // every sum is fp32. The states pass through LDS 32 channels at a time, the next
 // block under way while one is used.
+//
+// Measured (MI355X), 32 heads of 128 x 128, 4 x 2048 tokens: 224 to 252 us. Its 860 MB
+// (S and dS are 268 of them) take 170 us at a copy's rate; matrix instructions are
+// busy for 40 us and vector instructions for 100, two workgroups a compute unit.
+// Heads 128 channels at once, which leaves one, took 264 us.
 #include "delta_tiles.h"
 
 namespace ssd {

@@ -7,6 +7,7 @@
 // and the row is read once). Every state element is read and written once for
 // 7 flops: HBM is the bound. R lanes hold a row, 4 columns each; a wave makes
 // two passes with all loads issued first, nontemporal, as in the layer's step.
+// Measured (MI355X), 80 heads of 64 x 128: 256 sequences 218 to 223 us, 6.1 TB/s.
 #include "delta.h"
 #include "mfma_common.h"
 

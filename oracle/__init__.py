@@ -21,7 +21,8 @@ recurrence per sequence, the state carried by the caller), a fourth,
 channel) that the SSD layer is compared with, and a fifth, :mod:`oracle.conv`,
 the causal depthwise convolution and activation that produce the layer's x,
 B and C, and a sixth, :mod:`oracle.backward`, the gradients of the recurrence
-(the backward pass), all in numpy.
+(the backward pass), all in numpy. :mod:`oracle.delta` has the gated delta rule and
+the norm and rotation of its keys and queries, in both directions.
 
 Every function here is plain and slow on purpose.
 """
