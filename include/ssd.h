@@ -649,7 +649,10 @@ ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *prob, const void
  * that is state_t = exp(g_t) state_{t-1} (I - beta_t B_t B_t^T) + beta_t x_t B_t^T.
  * It stays bounded for |B| <= 1, 0 <= beta <= 2 and g <= 0 (expected, not
  * required; ssd_bc_norm makes unit keys). The sequence is evaluated in chunks
- * of 64 tokens: a triangular system inside a chunk, the state between them.
+ * of 64 tokens: a triangular system inside a chunk, the state between them. A
+ * value, key, query or gate that is not finite reaches all that follows in its
+ * sequence, and may reach the up to 63 tokens before it in its chunk (never
+ * another sequence; a value only its own channel).
  *
  * Problem: as for ssd_forward with batch, seqlen >= 0 (0 = nothing to do but
  * the states), headdim in {16, 32, 64, 128}, dstate a multiple of 16 up to 256,

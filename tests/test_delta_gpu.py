@@ -347,3 +347,32 @@ def test_device_offsets_need_no_check():
     for c in (cu.cuda(), cu.long().cuda()):
         got = forward(t, c, check_cu_seqlens=False)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_values_that_are_not_finite(dtype):
+    """An infinite value stays in its channel and sequence and does not reach an
+    earlier chunk; a NaN gate or key makes all that follows NaN."""
+    case = ([200, 90, 90], True, 2, 32, 48, 1, dtype, False)
+    d = inputs(case, 1600)
+    t, cu = on_gpu(d, case)
+    want, hw = forward(t, cu)
+    s = dict(t, x=t["x"].clone())
+    s["x"][0, 150, 1, 5] = float("inf")
+    print("[gpu] delta not finite %s" % dtype, flush=True)
+    y, h = forward(s, cu)
+    assert not y[0, 150:200, 1, 5].isfinite().any()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[0, 128:200, 1, 5] = False
+    assert torch.equal(y[keep], want[keep])
+    hk = torch.ones_like(h, dtype=torch.bool)
+    hk[0, 1, 5] = False
+    assert torch.equal(h[hk], hw[hk])
+    for k in ("g", "B"):
+        s = dict(t)
+        s[k] = t[k].clone()
+        s[k][0, 70] = float("nan")
+        y, h = forward(s, cu)
+        assert y[0, 70:200].isnan().all() and h[0].isnan().all()
+        assert torch.equal(y[0, :64], want[0, :64]) and torch.equal(y[0, 200:], want[0, 200:])
+        assert torch.equal(h[1:], hw[1:])
