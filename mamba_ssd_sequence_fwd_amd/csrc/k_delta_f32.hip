@@ -10,34 +10,35 @@
 // and Q, are staged in LDS for the workgroup's waves; T and M (k_delta_prep's)
 // come through the caches into registers. The bound is the fp32 matrix rate (1/16 of
 // the bf16 rate): 68 products of 16 x 16 x 16 a chunk and wave at N = 64, 4.1 us.
-// Measured (MI355X), 36 sequences and heads of 64 x 64 and 5 chunks: 49 us, 36
-// workgroups on 36 compute units, a chunk every 9.8 us (its rows staged, its four
-// products one after the other); 48 and 9: the two walks of the backward pass 79 us
-// together (76 and 59 one after the other), the gradients 43 us.
+// Measured (MI355X), 36 sequences and heads of 64 x 64 and 5 chunks: 44 us, 36
+// workgroups on 36 compute units, a chunk every 8.8 us (its rows staged, its four
+// products one after the other); 48 and up to 8: the two walks of the backward pass 73
+// us together (about 135 one after the other), the gradients 43 us.
 #include "delta_tiles.h"
 
 namespace ssd {
 
 // `len` of 64 token rows of K and Q (or of K alone: null), N columns each, as rows
-// of W floats in LDS; the rest is zero. Four of a thread's loads are on their way
-// at once (one after the other they took as long as the chunk's products).
-template <int W>
+// of 16 NT + 4 floats in LDS (the last 4 are for the banks), the rest zero. All of a
+// thread's loads for up to 128 columns are on their way at once (one after the other
+// they took as long as the chunk's products).
+template <int NT>
 __device__ __forceinline__ void stage_rows(float *toK, float *toQ, const float *K, const float *Q,
                                            size_t ld, int N, int len) {
-  constexpr int kAll = kDeltaChunk * (W / 4), kAtOnce = 4;
+  constexpr int W = 16 * NT + 4, kRow = 4 * NT, kAll = kDeltaChunk * kRow;
+  constexpr int kAtOnce = NT < 8 ? NT : 8;
   for (int e0 = threadIdx.x; e0 < kAll; e0 += kAtOnce * (int)blockDim.x) {
     f32x4 k[kAtOnce], q[kAtOnce];
 #pragma unroll
     for (int b = 0; b < kAtOnce; ++b) {
-      const int e = e0 + b * (int)blockDim.x, t = e / (W / 4), c = 4 * (e % (W / 4));
+      const int e = e0 + b * (int)blockDim.x, t = e / kRow, c = 4 * (e % kRow);
       const size_t at = (size_t)min(t, len - 1) * ld + min(c, N - 4);
       k[b] = ldf4(K + at);
       if (Q) q[b] = ldf4(Q + at);
     }
 #pragma unroll
     for (int b = 0; b < kAtOnce; ++b) {
-      const int e = e0 + b * (int)blockDim.x, t = e / (W / 4), c = 4 * (e % (W / 4));
-      if (e >= kAll) break;
+      const int e = e0 + b * (int)blockDim.x, t = e / kRow, c = 4 * (e % kRow);
       const bool in = t < len && c < N;
       stf4(toK + t * W + c, in ? k[b] : kZero4);
       if (Q) stf4(toQ + t * W + c, in ? q[b] : kZero4);
@@ -114,7 +115,7 @@ __device__ __forceinline__ void chain_f32(const DeltaArgs &a, int unit, float *l
     const size_t sh = (size_t)(slot0 + c) * a.H + h;
     __syncthreads();
     const size_t rows = (at * a.G + grp) * a.N;
-    stage_rows<W>(sK, sQ, (const float *)a.B + rows, kStates ? nullptr : (const float *)a.C + rows,
+    stage_rows<NT>(sK, sQ, (const float *)a.B + rows, kStates ? nullptr : (const float *)a.C + rows,
                   ldk, a.N, len);
     stage_gates(sG, sE, sB, a, at, h, len);
     // (on their way while K S is computed)
@@ -169,7 +170,7 @@ __device__ __forceinline__ void chain_f32(const DeltaArgs &a, int unit, float *l
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = 16 * i + 4 * lg + r;
-          if (t < len) y[t * ldx + lr] = (O[i][r]);
+          if (t < len) y[t * ldx + lr] = O[i][r];
         }
       }
     } else {
@@ -236,7 +237,7 @@ __device__ __forceinline__ void reverse_f32(const DeltaArgs &a, int unit, float 
     const size_t sh = (size_t)(slot0 + c) * a.H + h;
     __syncthreads();
     const size_t rows = (at * a.G + grp) * a.N;
-    stage_rows<W>(sK, sQ, (const float *)a.B + rows, (const float *)a.C + rows, ldk, a.N, len);
+    stage_rows<NT>(sK, sQ, (const float *)a.B + rows, (const float *)a.C + rows, ldk, a.N, len);
     stage_gates(sG, sE, sB, a, at, h, len);
     // (on their way while K dS is computed)
     const float *tri = (const float *)a.tri + sh * (3 * 4096);
@@ -433,7 +434,7 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
     for (int q = 0; q < 4; ++q) {
       if (live) {
         rv += r[q] * v[q];
-        dx[q] = (bi * r[q]);
+        dx[q] = bi * r[q];
       }
     }
   }
@@ -465,8 +466,8 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = min(16 * w + 4 * lg + r, len - 1);
-      k[r] = (K[t * ldk + n0 + lr]);
-      q[r] = (Q[t * ldk + n0 + lr]);
+      k[r] = K[t * ldk + n0 + lr];
+      q[r] = Q[t * ldk + n0 + lr];
       const float e = exp2_fast(gm[r]);
       dq[r] = e * ys[r];
       const float rk = -e * rs[r], uk = exp2_fast(toEnd[r]) * us[r];
@@ -481,8 +482,8 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = min(16 * j + 4 * lg + r, len - 1);
-        kj[r] = (K[t * ldk + n0 + lr]);
-        qj[r] = (Q[t * ldk + n0 + lr]);
+        kj[r] = K[t * ldk + n0 + lr];
+        qj[r] = Q[t * ldk + n0 + lr];
       }
       if (j <= w) {
         dq = mfma16(ldf4(sM + ti * W1 + 16 * j + 4 * lg), kj, dq);
@@ -531,7 +532,7 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   if (lane == 0) sS[w] = ss;
   __syncthreads();
   if (lg == 0 && live)
-    ((float *)a.dbeta)[(size_t)(start + ti) * a.H + h] = (rv + betasum + sK2[ti]);
+    ((float *)a.dbeta)[(size_t)(start + ti) * a.H + h] = rv + betasum + sK2[ti];
   if (w == 0) {
     const float zed = sZ[lane] + sR[lane] -
                       (sC[0][lane] + sC[1][lane] + sC[2][lane] + sC[3][lane]);
@@ -541,7 +542,7 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
     const float ends = exp2_fast(sG[kDeltaChunk - 1]) * (sS[0] + sS[1] + sS[2] + sS[3]);
     if (lane < len)
       ((float *)a.dg)[(size_t)(start + lane) * a.H + h] =
-          (all - (pre - zed) + prefix + ends);
+          all - (pre - zed) + prefix + ends;
   }
 }
 
