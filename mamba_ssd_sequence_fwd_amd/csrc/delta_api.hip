@@ -105,6 +105,8 @@ size_t forward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   const size_t tri = ssd::delta_tri_bytes(bf, ssd::kTriForward);
   a->tri = c.take((size_t)a->nslots * a->H * tri);
   a->tri_stride = (int32_t)(tri / 2);
+  if (bf && ssd::delta_ordered(*a, p->num_seqs > 0))
+    a->order = static_cast<int32_t *>(c.take((size_t)a->nseq * sizeof(int32_t)));
   if (a->seg)
     a->span = static_cast<float *>(
         c.take((size_t)a->nsegs * a->H * (a->P + a->N) * a->N * sizeof(float)));
@@ -121,6 +123,8 @@ size_t backward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   const size_t tri = ssd::delta_tri_bytes(bf, ssd::kTriBackward);
   a->tri = c.take(sh * tri);
   a->tri_stride = (int32_t)(tri / 2);
+  if (bf && ssd::delta_ordered(*a, p->num_seqs > 0))
+    a->order = static_cast<int32_t *>(c.take((size_t)a->nseq * sizeof(int32_t)));
   a->st0 = c.take(sh * a->P * a->N * es);
   a->st1 = c.take(sh * a->P * a->N * es);
   a->u = c.take(sh * ssd::kDeltaChunk * a->P * es);

@@ -600,7 +600,10 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
   __shared__ bf16 sV[kDeltaChunk * 16 * WV];
   __shared__ Gates G;
   static_assert(!kY || kRowElems<NK> >= kTriTiles * kTileElems, "M must fit where Q was");
-  walk_forwards<NK, WV, kMode>(a, xcd_unit(), sK, sQ, sT, sV, G);
+  const int unit = kMode == kWalkLocal
+                       ? xcd_unit()
+                       : delta_unit(a, (int)blockIdx.x, (int)gridDim.x, a.H * (a.P / (16 * WV)));
+  if (unit >= 0) walk_forwards<NK, WV, kMode>(a, unit, sK, sQ, sT, sV, G);
 }
 
 // The backward pass's two walks at once: neither needs the other (dS goes without
@@ -611,12 +614,14 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_both(Delta
   __shared__ bf16 sK[kRowElems<NK>], sQ[kRowElems<NK>], sT[kTriElems];
   __shared__ bf16 sV[kDeltaChunk * 16 * WV];
   __shared__ Gates G;
-  const int b = (int)blockIdx.x;
+  const int per = a.H * (a.P / (16 * WV)), b = (int)blockIdx.x;
+  const int unit = b < back ? delta_unit(a, b, back, per)
+                            : delta_unit(a, b - back, (int)gridDim.x - back, per);
+  if (unit < 0) return;
   if (b < back)
-    walk_backwards<NK, WV, kLocal>(a, xcd_unit(b, back), sK, sQ, sT, sV, G);
+    walk_backwards<NK, WV, kLocal>(a, unit, sK, sQ, sT, sV, G);
   else
-    walk_forwards<NK, WV, kLocal ? kWalkLocal : kWalkSave>(
-        a, xcd_unit(b - back, (int)gridDim.x - back), sK, sQ, sT, sV, G);
+    walk_forwards<NK, WV, kLocal ? kWalkLocal : kWalkSave>(a, unit, sK, sQ, sT, sV, G);
 }
 
 // The states at the segments' starts, in place of their own final states: with
@@ -712,7 +717,8 @@ template <int NK, int WV>
 hipError_t walk_launch(const DeltaArgs &a, Walk what, hipStream_t s) {
   // (a segment's local walk forwards takes its transition's columns too)
   const int tiles = a.P / 16, more = what == kForwardLocal || what == kBothLocal ? a.N / 16 : 0;
-  const int64_t units = (int64_t)(a.seg ? a.nsegs : a.nseq) * a.H;
+  const int64_t seqs = a.seg ? a.nsegs : a.order ? (a.nseq + 7) / 8 * 8 : a.nseq;
+  const int64_t units = seqs * a.H;
   const unsigned ahead = (unsigned)(units * ((tiles + more + WV - 1) / WV));
   const unsigned back = (unsigned)(units * (tiles / WV));
   const dim3 block(64 * WV);

@@ -174,6 +174,23 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int parts = (a.hpg + WV * per - 1) / (WV * per);
+  if (a.order && blockIdx.x == 0) {  // the walks' order of sequences, for all
+    int *chunks = reinterpret_cast<int *>(&sKK[0][0]);
+    static_assert(sizeof(sKK) >= kMostOrdered * sizeof(int), "the lengths must fit");
+    for (int s = threadIdx.x; s < a.nseq; s += 64 * WV) {
+      int64_t lo, hi;
+      delta_seq(a, s, lo, hi);
+      chunks[s] = (int)((hi - lo + kDeltaChunk - 1) / kDeltaChunk);
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.nseq; s += 64 * WV) {
+      const int own = chunks[s];
+      int rank = 0;
+      for (int o = 0; o < a.nseq; ++o) rank += chunks[o] > own || (chunks[o] == own && o < s);
+      a.order[rank] = s;
+    }
+    __syncthreads();
+  }
   int unit = xcd_unit();
   const int part = unit % parts;
   unit /= parts;

@@ -53,6 +53,11 @@ CASES = {
     "long-N128": ([3000], False, 2, 128, 128, 1, "bf16", True),
     "long-N256": ([3200], False, 1, 128, 256, 1, "bf16", True),
     "long-P16-N176": ([3000], False, 2, 16, 176, 2, "bf16", False),
+    "ordered-33": ([(37 * i) % 101 for i in range(33)], True, 3, 128, 32, 1, "bf16", True),
+    "ordered-64": ([(61 * i) % 130 if i % 5 else 0 for i in range(64)], True, 2, 32, 64, 2, "bf16",
+                   False),
+    "ordered-512": ([(i * i) % 9 for i in range(512)], True, 2, 16, 16, 1, "bf16", True),
+    "not-ordered-513": ([(i * i) % 7 for i in range(513)], True, 2, 16, 16, 1, "bf16", True),
     "one-token-fp32": ([1, 1], False, 4, 64, 128, 1, "fp32", True),
     "one-chunk-and-one-fp32": ([65], False, 6, 32, 64, 2, "fp32", False),
     "P16-N48-fp32": ([100, 100], False, 5, 16, 48, 1, "fp32", True),
