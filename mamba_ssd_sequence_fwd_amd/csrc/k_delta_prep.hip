@@ -15,7 +15,7 @@
 // 16 x 16 block reach 6435 and cancel, the substitution's values stay within
 // those of the inverse.)
 //
-// Measured (MI355X): 80 heads of one group, 256 chunks, 82 to 90 us: 20,480 inverses
+// Measured (MI355X): 80 heads of one group, 256 chunks, 79 to 84 us: 20,480 inverses
 // of 64 x 64, whose vector instructions (32 us of a SIMD's issue) and fp32 matrix
 // instructions (25 us) come on top of 315 MB written (62 us at a copy's rate). Two
 // heads a group, 4096 chunks and groups: 70 to 74 us, most of it waiting for rows of
@@ -321,11 +321,14 @@ size_t delta_tri_bytes(bool tiles, DeltaTri which) {
 template <typename T, DeltaTri W, int WV, typename Out>
 hipError_t prep_wv(const DeltaArgs &a, hipStream_t s) {
   const int64_t bytes = delta_tri_bytes(std::is_same<Out, TilesOut>::value, W);
-  // heads a wave takes in turn: more where waves are left for the card
-  const int64_t waves = (int64_t)a.nslots * a.H;
-  int per = (int)(waves / 4096);
-  const int most = (a.hpg + WV - 1) / WV;
-  per = per < 1 ? 1 : per > most ? most : per;
+  // Heads a wave takes in turn: the fewest with which all workgroups are on the card
+  // at once, three on a compute unit, since each makes the group's products anew. (80
+  // heads and 256 chunks: 7 heads in 768 workgroups 82 us; 5 in 1024 workgroups 94,
+  // 1 in 5120 workgroups 111, 20 in 256 workgroups 107.)
+  constexpr int64_t kOnCard = 3 * 256;
+  const int64_t groups = (int64_t)a.nslots * a.G;
+  const int64_t most = groups < kOnCard ? kOnCard / groups : 1;
+  const int per = (int)((a.hpg + WV * most - 1) / (WV * most));
   const int64_t parts = (a.hpg + WV * per - 1) / (WV * per);
   const dim3 grid((unsigned)((int64_t)a.nslots * a.G * parts)), block(64 * WV);
   hipLaunchKernelGGL((k_delta_prep<T, W, WV, Out>), grid, block, 0, s, a, bytes, per);
