@@ -792,7 +792,8 @@ void delta_segments(DeltaArgs &a, bool packed, bool backward) {
   constexpr int kComputeUnits = 256;
   a.seg = a.nseg_per = a.nsegs = 0;
   if (a.nseq == 0 || a.T == 0) return;
-  const int64_t chunks = (a.T / a.nseq + kDeltaChunk - 1) / kDeltaChunk;  // (packed: on average)
+  // (packed: on average, and at least one where there are fewer tokens than sequences)
+  const int64_t all = (int64_t)kDeltaChunk * a.nseq, chunks = (a.T + all - 1) / all;
   const int64_t groups = (int64_t)a.nseq * a.H * ((a.P + 63) / 64);
   const int64_t w = backward ? 2 : 1;
   int64_t m = chunks * groups * w / (2 * kComputeUnits);
