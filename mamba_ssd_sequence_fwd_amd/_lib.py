@@ -1422,7 +1422,8 @@ def _head_rows(t):
         return None
     if t.is_contiguous():
         return t.shape[-1] * t.shape[-2]
-    if t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+    # (a flatten of strided or broadcast channels would be a copy, laid out otherwise than t)
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
         return None
     return _row_stride(t.flatten(-2))
 
