@@ -1246,6 +1246,8 @@ def _delta_tensors(x, g, beta, B, C, dim, **like):
     (..., H), B and C (..., G, N), all of x's dtype and on its device; ``like``
     (name -> tensor or None) are shaped like x. Returns the leading shape and
     (H, P, N, G)."""
+    if isinstance(x, Checkpoint) or isinstance(B, Checkpoint):
+        _refuse_checkpoint("x" if isinstance(x, Checkpoint) else "B")
     shape, dtype, dev = x.shape, x.dtype, x.device
     if len(shape) != dim:
         raise ValueError("x must be (batch, nheads, headdim)" if dim == 3 else
@@ -1286,6 +1288,8 @@ def _delta_packed(cu_seqlens, lead, check):
     """Sequences of a packed call (0: dense), with the host's check of the offsets."""
     if cu_seqlens is None:
         return 0
+    if isinstance(cu_seqlens, Checkpoint):
+        _refuse_checkpoint("cu_seqlens")
     if lead[0] != 1:
         raise ValueError("cu_seqlens needs batch == 1")
     num_seqs = cu_seqlens.numel() - 1

@@ -1,10 +1,16 @@
-"""Sizes of the gated delta rule at the edges of what is allowed, on the host (nothing
-is launched)."""
+"""Sizes and refusals of the gated delta rule at the edges of what is allowed, on the
+host (nothing is launched)."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+
+import pytest
+import torch
+
+import mamba_ssd_sequence_fwd_amd as ssd
+from mamba_ssd_sequence_fwd_amd import _lib
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -27,3 +33,38 @@ def test_fewer_tokens_than_sequences():
     is below one). In a process of its own: a division by zero would end it."""
     r = subprocess.run([sys.executable, "-c", SIZES], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and "sized" in r.stdout, (r.returncode, r.stderr[-500:])
+
+
+def _m(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def _kept(t):
+    """A Checkpoint with the shape, dtype and device of t."""
+    q = torch.empty(t.shape, dtype=torch.int8, device=t.device)
+    exponents = torch.empty(t.shape[:-1] + (-(-t.shape[-1] // 32),), dtype=torch.uint8,
+                            device=t.device)
+    return ssd.Checkpoint(q, exponents, t.dtype)
+
+
+@pytest.mark.parametrize("call,names", [
+    ("forward", ("x", "g", "beta", "B", "C", "initial_state", "cu_seqlens", "y", "final_state")),
+    ("backward", ("x", "g", "beta", "B", "C", "initial_state", "cu_seqlens", "dy", "dfinal_state")),
+    ("step", ("x", "g", "beta", "B", "C", "state", "y"))])
+def test_a_checkpoint_is_refused_by_name(call, names, monkeypatch):
+    """A Checkpoint has a tensor's shape, dtype and device: it is named where one stands in a
+    tensor's place, whatever that place is."""
+    monkeypatch.setattr(_lib, "_on_gpu", lambda dev: None)
+    lead = (2,) if call == "step" else (2, 9)
+    like = dict(x=_m(*lead, 8, 64), g=_m(*lead, 8), beta=_m(*lead, 8), B=_m(*lead, 2, 32),
+                C=_m(*lead, 2, 32))
+    state = _m(2, 8, 64, 32, dtype=torch.float32)
+    like.update(y=like["x"], dy=like["x"], cu_seqlens=_m(1, 8, dtype=torch.float32), state=state,
+                initial_state=state, final_state=state, dfinal_state=state)
+    needed = ("x", "g", "beta", "B", "C") + {"forward": (), "backward": ("initial_state", "dy"),
+                                             "step": ("state",)}[call]
+    for name in names:
+        t = {k: like[k] for k in needed}
+        t[name] = _kept(like[name])
+        with pytest.raises(ValueError, match="^%s is a Checkpoint" % name):
+            getattr(ssd, "delta_" + call)(**t)
