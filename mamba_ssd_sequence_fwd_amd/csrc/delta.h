@@ -55,7 +55,7 @@ struct DeltaArgs {
 
 // Triangular matrices of a (slot, head): what the chunks' own products need.
 enum DeltaTri : int {
-  kTriForward = 0,   // T, M
+  kTriForward = 0,   // T, and in fp32 M
   kTriBackward = 1   // T, T^T, M^T
 };
 

@@ -21,7 +21,10 @@ __device__ __forceinline__ f32x4 mfma16(f32x4 a, f32x4 b, f32x4 c) {
 // empty. Those two share the fifth tile's 16 bytes a lane.
 //   lower, rows i, k columns: (0,0)h (1,0) (2,0) (3,0) (2,1)h (3,1)
 //   upper:                    (0,0) (0,1) (1,0)h (1,1) (2,1) (3,1)h
-constexpr int kTriTiles = 5, kTileElems = 512;
+// A chunk's matrices in a row, each in kTriLevels bf16 or fewer, level by level: the
+// values rounded, and what the roundings before left, rounded.
+constexpr int kTriTiles = 5, kTileElems = 512, kTriLevels = 3;
+constexpr int kLevelElems = kTriTiles * kTileElems, kMatrixElems = kTriLevels * kLevelElems;
 __host__ __device__ constexpr int lower_tile(int i, int ks) {
   return i == 0 || (i == 2 && ks == 1) ? 4 : ks == 0 ? i - 1 : 3;
 }
@@ -118,9 +121,12 @@ __device__ __forceinline__ void stage_block(bf16 *to, const void *src, int n) {
 }
 #endif
 
-// Eight values of an operand in two bf16 each.
+// Eight values of an operand in two bf16 each (2^-17 off), or three (2^-26).
 struct Split {
   bf16x8 hi, lo;
+};
+struct Split3 {
+  bf16x8 hi, mid, lo;
 };
 __device__ __forceinline__ bf16x8 pack8(f32x4 a, f32x4 b) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -138,6 +144,19 @@ __device__ __forceinline__ Split split8(f32x4 a, f32x4 b) {
     rb[r] = b[r] - (float)s.hi[4 + r];
   }
   s.lo = pack8(ra, rb);
+  return s;
+}
+__device__ __forceinline__ Split3 split8x3(f32x4 a, f32x4 b) {
+  Split3 s;
+  s.hi = pack8(a, b);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    a[r] -= (float)s.hi[r];
+    b[r] -= (float)s.hi[4 + r];
+  }
+  const Split rest = split8(a, b);
+  s.mid = rest.hi;
+  s.lo = rest.lo;
   return s;
 }
 

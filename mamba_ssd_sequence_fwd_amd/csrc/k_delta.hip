@@ -11,12 +11,14 @@
 // with 8 channels in a row, as the rows of K and Q lie in LDS; R and U pair
 // tiles of 16 tokens, in which order k_delta_prep writes its matrices.
 //
-// Rounding. K, Q, V and dY are bf16 as they are. What enters a state is held in
-// two bf16 (the value, and what rounding left of it: 2^-17 off), so that the
-// fp32 states stay fp32: S in K S, R and T in T R (the three large products of
-// four), U in K^T U, and the same backwards. y is rounded to bf16 anyway: S and M
-// enter it once rounded, U in two (it adds 6 products to 104 and takes y's error
-// from 2.97e-3 to 2.44e-3, where the rounding of y alone makes 1.66e-3).
+// Rounding. K, Q, V and dY are bf16 as they are. What enters a state is held in three
+// bf16 (the value, and twice what rounding left of it: 2^-26 off, less than fp32's own
+// half step) and multiplied with what of the other operand is not below that, so that
+// the states are those of fp32 arithmetic: S in K S, R and T in T R, U in K^T U, and
+// the same backwards (relative error 1.9e-7; two bf16 each gave 3.6e-6). y is rounded
+// to bf16 in the end: S, M and U enter it in two bf16 (2^-17 off), so that its error is
+// that rounding's, 1.66e-3 (S and M in one gave 2.44e-3). U and dR go to the gradients,
+// and the states of a chunk's start and end, rounded to bf16 once.
 //
 // Segments. A walk's length is its chunks' latencies one after the other, and
 // few sequences and heads leave most of the card idle. Then each sequence is
@@ -25,15 +27,14 @@
 // k_delta_join passes the states through the transitions; and the walk proper
 // starts every segment from its own state.
 //
-// Four waves (64 columns) a workgroup share the staged K, Q, T and M; each takes 110
-// matrix instructions and 430 vector instructions a chunk (N = 128), the latter for
-// the splits into two bf16. Measured (MI355X), 80 heads of 64, 8 x 2048 tokens: 207
-// to 232 us, 5 workgroups for 2 compute units; the matrix units are busy for 70 us of
-// it and the vector units for 68, 0.69 us a chunk for each workgroup of four waves
-// where three share a compute unit, 3.4 us for one alone (its chunk's four products
-// wait for each other). y and M take their way through LDS: stored and loaded from
-// registers, y in pieces of 8 bytes and M from the caches, they took 70 and 49 us
-// of 303.
+// Four waves (64 columns) a workgroup share the staged K, Q and T, and M, whose tiles
+// they make from K and Q among themselves; each takes 192 matrix instructions a chunk
+// (N = 128). Measured (MI355X), 80 heads of 64, 8 x 2048 tokens: 330 to 372 us, 5
+// workgroups for 2 compute units: the matrix units alone need 117 us, the vector
+// instructions (the splits above all) about as long, and a chunk's products wait for each
+// other. Places of a lane in LDS are worked out anew where the registers would not
+// hold them (a spilled one's load waits for the rows under way: 510 us a call with 60
+// bytes spilled, 441 with none).
 #include "delta_tiles.h"
 
 namespace ssd {
@@ -50,9 +51,11 @@ __device__ __forceinline__ f32x4 value_tile(const bf16 *v, int t0, int c0) {
 __device__ __forceinline__ float bits_to_f32(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
 
 // Tables of a chunk, one entry a token: beta, beta e^gam, e^{gam_c - gam},
-// e^gam; zeros in the first two past the end. Filled by one wave.
+// e^gam; zeros in the first two past the end; and gam itself in two floats. Filled
+// by one wave.
 struct Gates {
   float b[kDeltaChunk], be[kDeltaChunk], lf[kDeltaChunk], ef[kDeltaChunk];
+  float hi[kDeltaChunk], lo[kDeltaChunk];
 };
 __device__ __forceinline__ void fill_gates(Gates &G, float g, float beta, bool live) {
   const int lane = threadIdx.x & 63;
@@ -62,6 +65,8 @@ __device__ __forceinline__ void fill_gates(Gates &G, float g, float beta, bool l
   G.be[lane] = live ? beta * e : 0.f;
   G.lf[lane] = exp2_fast((__shfl(gam.hi, 63) - gam.hi) + (__shfl(gam.lo, 63) - gam.lo));
   G.ef[lane] = e;
+  G.hi[lane] = gam.hi;
+  G.lo[lane] = gam.lo;
 }
 
 // Left operand K^T: rows n (as the state's tiles have them), tokens
@@ -85,6 +90,54 @@ __device__ __forceinline__ bf16x8 value_operand(const bf16 *v, int kt, int c0) {
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
+// This lane, anew: places worked out from it are not kept over the chunks (all of them
+// would fill the registers).
+__device__ __forceinline__ int lane_anew() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// Tiles (I, J), (I2, J2), ... of M: Q_i . K_j with the decay between them (lane: row i, 4
+// columns j), in two bf16; and their places in the operand tiles, of which each is half of
+// a lane's columns.
+struct MTile {
+  uint2 hi, lo;
+};
+template <int NK, int I, int J, int... More>
+__device__ __forceinline__ void m_tiles(MTile *to, const bf16 *sK, const bf16 *sQ, const Gates &G) {
+  constexpr int N = 32 * NK;
+  const int lane = lane_anew(), lr = lane & 15, lg = lane >> 4;
+  f32x4 v = kZero4;
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks) {
+    const int e = place<N>(lr, 32 * ks + 8 * lg);
+    v = mfma(*reinterpret_cast<const bf16x8 *>(sK + e + 16 * J * N),
+             *reinterpret_cast<const bf16x8 *>(sQ + e + 16 * I * N), v);
+  }
+  const f32x4 d = (G.hi[16 * I + lr] - ldf4(G.hi + 16 * J + 4 * lg)) +
+                  (G.lo[16 * I + lr] - ldf4(G.lo + 16 * J + 4 * lg));
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    v[r] = J < I || 4 * lg + r <= lr ? v[r] * exp2_fast(d[r]) : 0.f;
+  to->hi = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+  v[0] -= __uint_as_float(to->hi.x << 16);
+  v[1] -= __uint_as_float(to->hi.x & 0xffff0000u);
+  v[2] -= __uint_as_float(to->hi.y << 16);
+  v[3] -= __uint_as_float(to->hi.y & 0xffff0000u);
+  to->lo = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+  if constexpr (sizeof...(More) > 0) m_tiles<NK, More...>(to + 1, sK, sQ, G);
+}
+template <int I, int J, int... More>
+__device__ __forceinline__ void put_m_tiles(const MTile *from, bf16 *to) {
+  constexpr bool kSecond = I == 2 && J == 2;  // of the shared tile
+  constexpr int kHalf = kSecond ? 1 : I == 0 ? 0 : J & 1;
+  bf16 *at = to + lower_tile(I, J / 2) * kTileElems + 8 * lane_anew() + 4 * kHalf;
+  *reinterpret_cast<uint2 *>(at) = from->hi;
+  *reinterpret_cast<uint2 *>(at + kLevelElems) = from->lo;
+  if constexpr (sizeof...(More) > 0) put_m_tiles<More...>(from + 1, to);
+}
+
 // A store at a lane's 32-bit byte offset from an address that the wave shares.
 template <typename V>
 __device__ __forceinline__ void store_at(void *base, uint32_t off, V v) {
@@ -99,11 +152,12 @@ enum WalkMode : int {
 };
 
 // What the walks stage, one array for each: the compiler then sees which reads do
-// not meet the loads under way, and does not wait for those. (M takes Q's place
-// once Q S is done, y that of the values.)
+// not meet the loads under way, and does not wait for those. (T's last
+// level and M take Q's place once Q S is done, y that of the values; backwards the last
+// levels of M^T and T^T take the values' place.)
 template <int NK>
 constexpr int kRowElems = kDeltaChunk * 32 * NK;
-constexpr int kTriElems = 2 * kTriTiles * kTileElems;
+constexpr int kTriElems = 2 * kLevelElems;  // a matrix's first two levels
 
 // The walk forwards of unit `unit`: 16 WV columns of a sequence or segment.
 template <int NK, int WV, WalkMode kMode>
@@ -111,9 +165,8 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
                                               bf16 *sT, bf16 *sV, Gates &G) {
   constexpr int N = 32 * NK, W = 16 * WV;  // state channels, the workgroup's columns
   constexpr bool kY = kMode == kWalkY, kLocal = kMode == kWalkLocal;
-  constexpr int kT = kTriElems;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = WV == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (kLocal ? a.P + a.N : a.P) / 16, blocks = (tiles + WV - 1) / WV;
   const int tile0 = (unit % blocks) * WV, tile = min(tile0 + wave, tiles - 1);
   const bool on = tile0 + wave < tiles;     // (a wave past the last tile repeats it)
@@ -181,7 +234,7 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
     if (wave == 0) fill_gates(G, bits_to_f32(g), bits_to_f32(bt), lane < len);
     __syncthreads();
     if (valued)
-      stage_tile<W, kDeltaChunk, WV>(
+      stage_tile<W, kDeltaChunk, WV, kY>(
           sV, (const bf16 *)a.x + ((size_t)at * a.H + h) * a.P + 16 * tile0, ldx, W, len);
 
     // K S, and Q S transposed (lane: token lr of its tile, rows p); two tiles'
@@ -200,14 +253,14 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
       keys(0);
 #pragma unroll
       for (int t = 0; t < 4; ++t) A[t] = O[t] = kZero4;
-      Split s;
+      Split3 s;
 #pragma unroll
       for (int b = 0; b < 2 * NK; ++b) {
         const int ks = b >> 1, t = 2 * (b & 1);
         if (b + 1 < 2 * NK) keys(b + 1);
         __builtin_amdgcn_sched_barrier(0);
         if ((b & 1) == 0) {
-          s = split8(S[ks][0], S[ks][1]);
+          s = split8x3(S[ks][0], S[ks][1]);
           if (kMode == kWalkSave && 32 * ks + 8 * lg < a.N)
             store_at((bf16 *)a.st0 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks,
                      (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
@@ -217,24 +270,60 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
         if (kY)
 #pragma unroll
           for (int u = 0; u < 2; ++u) O[t + u] = mfma(s.hi, qb[b & 1][u], O[t + u]);
+        if (kY)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) O[t + u] = mfma(s.mid, qb[b & 1][u], O[t + u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.mid, A[t + u]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.lo, A[t + u]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    const auto tri_tiles = [&](int lo, bf16x8 (&to)[kTriTiles]) __attribute__((always_inline)) {
+    const auto tri_tiles = [&](const bf16 *level,
+                               bf16x8 (&to)[kTriTiles]) __attribute__((always_inline)) {
 #pragma unroll
       for (int k = 0; k < kTriTiles; ++k)
-        to[k] = *reinterpret_cast<const bf16x8 *>(sT + (2 * k + lo) * kTileElems + 8 * lane);
+        to[k] = *reinterpret_cast<const bf16x8 *>(level + k * kTileElems + 8 * lane);
     };
-    bf16x8 Th[kTriTiles], Tl[kTriTiles];
-    tri_tiles(0, Th);
+    // M: the ten tiles Q_i K_j^T on and below the diagonal (lane: token lr of tile i, 4 tokens
+    // of tile j) with their decays, shared out over the waves by the rows they read
+    MTile m[kY ? 4 / WV : 1][3];
+    if (kY)
+#pragma unroll
+      for (int k = 0; k < 4 / WV; ++k) {
+        const int role = wave + WV * k;
+        if (role == 0)
+          m_tiles<NK, 0, 0, 1, 0, 1, 1>(m[k], sK, sQ, G);
+        else if (role == 1)
+          m_tiles<NK, 2, 0, 2, 1, 2, 2>(m[k], sK, sQ, G);
+        else if (role == 2)
+          m_tiles<NK, 3, 0, 3, 1>(m[k], sK, sQ, G);
+        else
+          m_tiles<NK, 3, 2, 3, 3>(m[k], sK, sQ, G);
+      }
+    bf16x8 T[kTriTiles];
+    tri_tiles(sT, T);
     wait_vmem_all();
     __syncthreads();
-    if (kY) stage_block<WV>(sQ, tri_at(c) + kT, kTriTiles);
+    stage_block<WV>(sQ, tri_at(c) + 2 * kLevelElems, kTriTiles);
+    // (behind T's last level, as operand tiles)
+    if (kY)
+#pragma unroll
+      for (int k = 0; k < 4 / WV; ++k) {
+        const int role = wave + WV * k;
+        if (role == 0)
+          put_m_tiles<0, 0, 1, 0, 1, 1>(m[k], sQ + kLevelElems);
+        else if (role == 1)
+          put_m_tiles<2, 0, 2, 1, 2, 2>(m[k], sQ + kLevelElems);
+        else if (role == 2)
+          put_m_tiles<3, 0, 3, 1>(m[k], sQ + kLevelElems);
+        else
+          put_m_tiles<3, 2, 3, 3>(m[k], sQ + kLevelElems);
+      }
     __builtin_amdgcn_sched_barrier(0);
     // R, as operands
-    Split R[2];
+    Split3 R[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
       f32x4 v[2];
@@ -245,28 +334,27 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
         v[u] = -be * A[t];
         if (valued) v[u] += b * value_tile<W>(sV, 16 * t, p0 - 16 * tile0);
       }
-      R[kt] = split8(v[0], v[1]);
+      R[kt] = split8x3(v[0], v[1]);
     }
-    // U = T R
+    // U = T R, level by level of T with what of R is not below fp32's last bit
     __builtin_amdgcn_sched_barrier(0);
-    tri_tiles(1, Tl);
 #pragma unroll
     for (int i = 0; i < 4; ++i) A[i] = kZero4;
-#pragma unroll
-    for (int lo = 0; lo < 2; ++lo)
+    const auto times = [&](bf16x8 Split3::*part) __attribute__((always_inline)) {
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
         for (int i = 2 * kt; i < 4; ++i)
-          A[i] = mfma(lower_operand(Th[lower_tile(i, kt)], i, kt), lo ? R[kt].lo : R[kt].hi, A[i]);
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int i = 2 * kt; i < 4; ++i)
-        A[i] = mfma(lower_operand(Tl[lower_tile(i, kt)], i, kt), R[kt].hi, A[i]);
+          A[i] = mfma(lower_operand(T[lower_tile(i, kt)], i, kt), R[kt].*part, A[i]);
+    };
+    times(&Split3::hi), times(&Split3::mid), times(&Split3::lo);
+    tri_tiles(sT + kLevelElems, T);
+    times(&Split3::hi), times(&Split3::mid);
     wait_vmem_all();
     __syncthreads();
+    tri_tiles(sQ, T);
     if (c + 1 < chunks) fetch_tri(c + 1);
+    times(&Split3::hi);
     const float ec = G.ef[kDeltaChunk - 1];
     bf16x8 kT[2][2];  // of a block of 16 channels, the next one's under way
     const auto columns = [&](int b) __attribute__((always_inline)) {
@@ -277,50 +365,52 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
     if (kY) {
       Split u[2];
       bf16x8 M[kTriTiles];
+      tri_tiles(sQ + kLevelElems, M);
 #pragma unroll
-      for (int k = 0; k < kTriTiles; ++k)
-        M[k] = *reinterpret_cast<const bf16x8 *>(sQ + k * kTileElems + 8 * lane);
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        u[kt] = split8(A[2 * kt], A[2 * kt + 1]);
-        U[kt] = u[kt].hi;
-      }
+      for (int kt = 0; kt < 2; ++kt) u[kt] = split8(A[2 * kt], A[2 * kt + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) O[t] *= G.ef[16 * t + lr];
-#pragma unroll
-      for (int step = 0; step < 2; ++step)
+      const auto times_m = [&](bf16x8 Split::*part) __attribute__((always_inline)) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int t = 2 * kt; t < 4; ++t)
-            O[t] = mfma(step ? u[kt].lo : u[kt].hi, lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
+            O[t] = mfma(u[kt].*part, lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
+      };
+      times_m(&Split::hi), times_m(&Split::lo);
+      tri_tiles(sQ + 2 * kLevelElems, M);
+      times_m(&Split::hi);
     } else {
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) U[kt] = pack8(A[2 * kt], A[2 * kt + 1]);
     }
     // the state: rows of U fall by e^{gam_c - gam}
+    __builtin_amdgcn_sched_barrier(0);
     columns(0);
-    Split D[2];
+    Split3 D[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
-      D[kt] = split8(A[2 * kt] * ldf4(G.lf + 32 * kt + 4 * lg),
-                     A[2 * kt + 1] * ldf4(G.lf + 32 * kt + 16 + 4 * lg));
+      D[kt] = split8x3(A[2 * kt] * ldf4(G.lf + 32 * kt + 4 * lg),
+                       A[2 * kt + 1] * ldf4(G.lf + 32 * kt + 16 + 4 * lg));
 #pragma unroll
     for (int b = 0; b < 2 * NK; ++b) {
       if (b + 1 < 2 * NK) columns(b + 1);
       __builtin_amdgcn_sched_barrier(0);
       f32x4 s = S[b >> 1][b & 1] * ec;
       s = mfma(kT[b & 1][0], D[0].hi, s);
+      s = mfma(kT[b & 1][0], D[0].mid, s);
       s = mfma(kT[b & 1][0], D[0].lo, s);
       s = mfma(kT[b & 1][1], D[1].hi, s);
+      s = mfma(kT[b & 1][1], D[1].mid, s);
       S[b >> 1][b & 1] = mfma(kT[b & 1][1], D[1].lo, s);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (kY) {
       // y by whole rows of the workgroup's columns: 16 bytes a lane
+      const int own = lane_anew(), row = own & 15, col = p0 - 16 * tile0 + 4 * (own >> 4);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        *reinterpret_cast<uint2 *>(sV + place<W>(16 * t + lr, p0 - 16 * tile0 + 4 * lg)) =
+        *reinterpret_cast<uint2 *>(sV + place<W>(16 * t + row, col)) =
             make_uint2(pack2(O[t][0], O[t][1]), pack2(O[t][2], O[t][3]));
     } else if (!kLocal) {
       // (tokens in the order of the operands: 16 bytes a lane)
@@ -334,7 +424,7 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
     if (kY) {
       constexpr int kPer = 64 * 8 / W;  // rows of an instruction
       bf16 *y = (bf16 *)a.y + ((size_t)at * a.H + h) * a.P + 16 * tile0;
-      const int row = lane / (W / 8), col = 8 * (lane % (W / 8));
+      const int own = lane_anew(), row = own / (W / 8), col = 8 * (own % (W / 8));
 #pragma unroll
       for (int k = 0; k < kDeltaChunk / (kPer * WV); ++k) {
         const int t = (k * WV + wave) * kPer;
@@ -367,7 +457,6 @@ template <int NK, int WV, bool kLocal>
 __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf16 *sK, bf16 *sQ,
                                                bf16 *sT, bf16 *sV, Gates &G) {
   constexpr int N = 32 * NK, W = 16 * WV;
-  constexpr int kT = kTriElems;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = a.P / W;
@@ -415,7 +504,7 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
     }
     stage_tile<N, kDeltaChunk, WV>(sK, (const bf16 *)a.B + (at * a.G + grp) * a.N, ldk, a.N,
                                    length(c));
-    stage_block<WV>(sT, tri_at(c) + 2 * kT, 2 * kTriTiles);
+    stage_block<WV>(sT, tri_at(c) + 2 * kMatrixElems, 2 * kTriTiles);
   };
   const auto fetch_rows = [&](int c) __attribute__((always_inline)) {
     const int64_t at = rows_at(c);
@@ -424,10 +513,11 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
     stage_tile<W, kDeltaChunk, WV>(sV, (const bf16 *)a.dy + ((size_t)at * a.H + h) * a.P + pw, ldx,
                                    W, length(c));
   };
-  const auto tri_tiles = [&](int lo, bf16x8 (&to)[kTriTiles]) __attribute__((always_inline)) {
+  const auto tri_tiles = [&](const bf16 *level,
+                             bf16x8 (&to)[kTriTiles]) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < kTriTiles; ++k)
-      to[k] = *reinterpret_cast<const bf16x8 *>(sT + (2 * k + lo) * kTileElems + 8 * lane);
+      to[k] = *reinterpret_cast<const bf16x8 *>(level + k * kTileElems + 8 * lane);
   };
   if (chunks > 0) {
     fetch_keys(chunks - 1);
@@ -442,6 +532,8 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
     bf16x8 Y[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) Y[kt] = value_operand<W>(sV, kt, p0 - pw);
+    __syncthreads();
+    stage_block<WV>(sV, tri_at(c) + 2 * kMatrixElems + 2 * kLevelElems, kTriTiles);
     f32x4 A[4];
     {
       bf16x8 kb[2][2];
@@ -454,14 +546,14 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
       keys(0);
 #pragma unroll
       for (int t = 0; t < 4; ++t) A[t] = kZero4;
-      Split s;
+      Split3 s;
 #pragma unroll
       for (int b = 0; b < 2 * NK; ++b) {
         const int ks = b >> 1, t = 2 * (b & 1);
         if (b + 1 < 2 * NK) keys(b + 1);
         __builtin_amdgcn_sched_barrier(0);
         if ((b & 1) == 0) {
-          s = split8(S[ks][0], S[ks][1]);
+          s = split8x3(S[ks][0], S[ks][1]);
           if (!kLocal && 32 * ks + 8 * lg < a.N)
             store_at((bf16 *)a.st1 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks,
                      (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
@@ -469,30 +561,37 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
 #pragma unroll
         for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.hi, A[t + u]);
 #pragma unroll
+        for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.mid, A[t + u]);
+#pragma unroll
         for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.lo, A[t + u]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    Split U[2];
-    {
-      bf16x8 Mh[kTriTiles], Ml[kTriTiles];
-      tri_tiles(0, Mh);
-      tri_tiles(1, Ml);
+    // dU: M^T by levels, the last one in the values' place
+    Split3 U[2];
+    bf16x8 T[kTriTiles];
+    const auto times_y = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
+      for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-      for (int lo = 0; lo < 2; ++lo)
+        for (int t = 0; t < 2 * kt + 2; ++t)
+          A[t] = mfma(upper_operand(T[upper_tile(t, kt)], t, kt), Y[kt], A[t]);
+    };
+    tri_tiles(sT, T);
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int t = 0; t < 2 * kt + 2; ++t)
-            A[t] = mfma(upper_operand(lo ? Ml[upper_tile(t, kt)] : Mh[upper_tile(t, kt)], t, kt),
-                        Y[kt], A[t]);
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
-    }
+    for (int t = 0; t < 4; ++t) A[t] *= ldf4(G.lf + 16 * t + 4 * lg);
+    times_y();
+    tri_tiles(sT + kLevelElems, T);
+    times_y();
+    wait_vmem_all();
     __syncthreads();
-    stage_block<WV>(sT, tri_at(c) + kT, 2 * kTriTiles);
+    tri_tiles(sV, T);
+    stage_block<WV>(sT, tri_at(c) + kMatrixElems, 2 * kTriTiles);
+    times_y();
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) U[kt] = split8x3(A[2 * kt], A[2 * kt + 1]);
+    __syncthreads();
+    stage_block<WV>(sV, tri_at(c) + kMatrixElems + 2 * kLevelElems, kTriTiles);
     // dS <- e^{gam_c} dS + Q^T (e^gam dY), while T^T comes
     const float ec = G.ef[kDeltaChunk - 1];
     bf16x8 kT[2][2];  // of a block of 16 channels, the next one's under way
@@ -502,7 +601,7 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
     };
     columns(sQ, 0);
     {
-      Split E[2];
+      Split3 E[2];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         f32x4 e[2];
@@ -512,7 +611,7 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
 #pragma unroll
           for (int r = 0; r < 4; ++r) e[u][r] = ef[r] * (float)Y[kt][4 * u + r];
         }
-        E[kt] = split8(e[0], e[1]);
+        E[kt] = split8x3(e[0], e[1]);
       }
 #pragma unroll
       for (int b = 0; b < 2 * NK; ++b) {
@@ -520,33 +619,34 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
         __builtin_amdgcn_sched_barrier(0);
         f32x4 s = S[b >> 1][b & 1] * ec;
         s = mfma(kT[b & 1][0], E[0].hi, s);
+        s = mfma(kT[b & 1][0], E[0].mid, s);
         s = mfma(kT[b & 1][0], E[0].lo, s);
         s = mfma(kT[b & 1][1], E[1].hi, s);
+        s = mfma(kT[b & 1][1], E[1].mid, s);
         S[b >> 1][b & 1] = mfma(kT[b & 1][1], E[1].lo, s);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     wait_vmem_all();
     __syncthreads();
+    // dR = T^T dU, level by level as U = T R
+#pragma unroll
+    for (int t = 0; t < 4; ++t) A[t] = kZero4;
+    const auto times = [&](bf16x8 Split3::*part) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int t = 0; t < 2 * kt + 2; ++t)
+          A[t] = mfma(upper_operand(T[upper_tile(t, kt)], t, kt), U[kt].*part, A[t]);
+    };
+    tri_tiles(sV, T);
+    times(&Split3::hi);
+    __syncthreads();
     if (c > 0) fetch_rows(c - 1);
-    // dR = T^T dU
-    {
-      bf16x8 Th[kTriTiles], Tl[kTriTiles];
-      tri_tiles(0, Th);
-      tri_tiles(1, Tl);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) A[t] = kZero4;
-#pragma unroll
-      for (int step = 0; step < 3; ++step)
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int t = 0; t < 2 * kt + 2; ++t) {
-            const int k = upper_tile(t, kt);
-            A[t] = mfma(upper_operand(step == 2 ? Tl[k] : Th[k], t, kt),
-                        step == 1 ? U[kt].lo : U[kt].hi, A[t]);
-          }
-    }
+    tri_tiles(sT, T);
+    times(&Split3::hi), times(&Split3::mid), times(&Split3::lo);
+    tri_tiles(sT + kLevelElems, T);
+    times(&Split3::hi), times(&Split3::mid);
     if (!kLocal) {
       bf16 *dr = (bf16 *)a.dr + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
@@ -556,18 +656,20 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
     }
     // dS <- dS - K^T (beta e^gam dR)
     columns(sK, 0);
-    Split D[2];
+    Split3 D[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
-      D[kt] = split8(-ldf4(G.be + 32 * kt + 4 * lg) * A[2 * kt],
-                     -ldf4(G.be + 32 * kt + 16 + 4 * lg) * A[2 * kt + 1]);
+      D[kt] = split8x3(-ldf4(G.be + 32 * kt + 4 * lg) * A[2 * kt],
+                       -ldf4(G.be + 32 * kt + 16 + 4 * lg) * A[2 * kt + 1]);
 #pragma unroll
     for (int b = 0; b < 2 * NK; ++b) {
       if (b + 1 < 2 * NK) columns(sK, b + 1);
       __builtin_amdgcn_sched_barrier(0);
       f32x4 s = mfma(kT[b & 1][0], D[0].hi, S[b >> 1][b & 1]);
+      s = mfma(kT[b & 1][0], D[0].mid, s);
       s = mfma(kT[b & 1][0], D[0].lo, s);
       s = mfma(kT[b & 1][1], D[1].hi, s);
+      s = mfma(kT[b & 1][1], D[1].mid, s);
       S[b >> 1][b & 1] = mfma(kT[b & 1][1], D[1].lo, s);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -596,10 +698,10 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
 template <int NK, int WV, WalkMode kMode>
 __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(DeltaArgs a) {
   constexpr bool kY = kMode == kWalkY;
-  __shared__ bf16 sK[kRowElems<NK>], sQ[kY ? kRowElems<NK> : 8], sT[kTriElems];
-  __shared__ bf16 sV[kDeltaChunk * 16 * WV];
+  constexpr int kFree = (kY ? 3 : 1) * kLevelElems;  // what takes Q's place
+  __shared__ bf16 sK[kRowElems<NK>], sT[kTriElems], sV[kDeltaChunk * 16 * WV];
+  __shared__ bf16 sQ[kY && kRowElems<NK> > kFree ? kRowElems<NK> : kFree];
   __shared__ Gates G;
-  static_assert(!kY || kRowElems<NK> >= kTriTiles * kTileElems, "M must fit where Q was");
   const int unit = kMode == kWalkLocal
                        ? xcd_unit()
                        : delta_unit(a, (int)blockIdx.x, (int)gridDim.x, a.H * (a.P / (16 * WV)));
@@ -611,9 +713,11 @@ __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_walk(Delta
 // chunk's products. The first `back` workgroups walk backwards, the longer way.
 template <int NK, int WV, bool kLocal>
 __global__ __launch_bounds__(64 * WV, (NK <= 4 ? 3 : 1)) void k_delta_both(DeltaArgs a, int back) {
+  constexpr int kValues = kDeltaChunk * 16 * WV;
   __shared__ bf16 sK[kRowElems<NK>], sQ[kRowElems<NK>], sT[kTriElems];
-  __shared__ bf16 sV[kDeltaChunk * 16 * WV];
+  __shared__ bf16 sV[kValues > kLevelElems ? kValues : kLevelElems];  // (a level takes its place)
   __shared__ Gates G;
+  static_assert(kRowElems<NK> >= kLevelElems, "a level must fit where Q is");
   const int per = a.H * (a.P / (16 * WV)), b = (int)blockIdx.x;
   const int unit = b < back ? delta_unit(a, b, back, per)
                             : delta_unit(a, b - back, (int)gridDim.x - back, per);

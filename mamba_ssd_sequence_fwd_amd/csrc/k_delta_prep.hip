@@ -1,8 +1,9 @@
 // k_delta_prep.hip -- the triangular matrices of each chunk of the gated delta
 // rule: T = (I + L)^-1 and M (delta.h), or T, T^T and M^T for the backward pass.
 //
-// A workgroup takes one chunk and some heads of one group. Q K^T and K K^T, which
-// those share, are computed once, as 16 x 16 tiles on and below the diagonal,
+// (Forwards in bf16 T alone: the walk makes M from the rows that it holds.) A workgroup
+// takes one chunk and some heads of one group. Q K^T and K K^T, which those share, are
+// computed once, as 16 x 16 tiles on and below the diagonal,
 // transposed: a lane holds 4 consecutive columns j of one row i. Each wave then
 // takes heads in turn. In that layout a tile of L is the left operand of
 // the fp32 matrix instruction (lane l: row l % 16, columns 4 (l / 16) + r at
@@ -54,17 +55,17 @@ __device__ __forceinline__ f32x4 operand(const float *row, int n, int N) {
 __device__ __forceinline__ f32x4 product(bf16x8 a, bf16x8 b, f32x4 c) { return mfma(a, b, c); }
 __device__ __forceinline__ f32x4 product(f32x4 a, f32x4 b, f32x4 c) { return mfma16(a, b, c); }
 
-// Tile rows 3 - v of K K^T and v of Q K^T (five tiles on and below the diagonal)
-// for v from LO to HI: rows j of K against rows i (lane: row i % 16, 4 columns j),
+// Tile rows 3 - v of K K^T and, where kPairs, v of Q K^T (five tiles on and below the
+// diagonal) for v from LO to HI: rows j of K against rows i (lane: row i % 16, 4 columns j),
 // or with kSwap Q K^T the other way round (lane: row j % 16, 4 columns i). Rows past
 // len are read as the last one. NB operands' columns are on their way at once; a
 // wave reads the rows of K once. The tiles go to LDS in lane order, tile (i, j) at
 // tri(i, j).
-template <int LO, int HI, int NB, bool kSwap, typename T>
+template <int LO, int HI, int NB, bool kPairs, bool kSwap, typename T>
 __device__ __forceinline__ void tile_rows(const T *K, const T *Q, size_t ld, int N, int len,
                                           f32x4 (*kk)[64], f32x4 (*qk)[64]) {
   constexpr int kCols = sizeof(T) == 2 ? 32 : 16;
-  constexpr int kRows = (3 - LO > HI - 1 ? 3 - LO : HI - 1) + 1;  // of K's tiles
+  constexpr int kRows = (3 - LO > HI - 1 || !kPairs ? 3 - LO : HI - 1) + 1;  // of K's tiles
   const int lane = threadIdx.x & 63, lr = lane & 15;
   f32x4 k[HI - LO][4], q[HI - LO][4];
 #pragma unroll
@@ -79,7 +80,7 @@ __device__ __forceinline__ void tile_rows(const T *K, const T *Q, size_t ld, int
       for (int j = 0; j < kRows; ++j)
         x[j][b] = operand(K + (size_t)min(16 * j + lr, len - 1) * ld, n0 + kCols * b, N);
 #pragma unroll
-      for (int v = LO; v < HI; ++v)
+      for (int v = LO; v < HI && kPairs; ++v)
         y[v - LO][b] = operand(Q + (size_t)min(16 * v + lr, len - 1) * ld, n0 + kCols * b, N);
     }
 #pragma unroll
@@ -90,7 +91,7 @@ __device__ __forceinline__ void tile_rows(const T *K, const T *Q, size_t ld, int
         for (int j = 0; j <= 3 - v; ++j)
           k[v - LO][j] = product(x[j][b], x[3 - v][b], k[v - LO][j]);
 #pragma unroll
-        for (int j = 0; j <= v; ++j)
+        for (int j = 0; j <= v && kPairs; ++j)
           q[v - LO][j] = kSwap ? product(y[v - LO][b], x[j][b], q[v - LO][j])
                                : product(x[j][b], y[v - LO][b], q[v - LO][j]);
       }
@@ -100,32 +101,31 @@ __device__ __forceinline__ void tile_rows(const T *K, const T *Q, size_t ld, int
 #pragma unroll
     for (int j = 0; j <= 3 - v; ++j) kk[tri(3 - v, j)][lane] = k[v - LO][j];
 #pragma unroll
-    for (int j = 0; j <= v; ++j) qk[tri(v, j)][lane] = q[v - LO][j];
+    for (int j = 0; j <= v && kPairs; ++j) qk[tri(v, j)][lane] = q[v - LO][j];
   }
 }
-template <int WV, int NB, bool kSwap, typename T>
+template <int WV, int NB, bool kPairs, bool kSwap, typename T>
 __device__ __forceinline__ void group_tiles(int wave, const T *K, const T *Q, size_t ld, int N,
                                             int len, f32x4 (*kk)[64], f32x4 (*qk)[64]) {
   constexpr int R = 4 / WV;
   if (wave == 0)
-    tile_rows<0, R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+    tile_rows<0, R, NB, kPairs, kSwap>(K, Q, ld, N, len, kk, qk);
   else if (wave == 1)
-    tile_rows<R % 4, R % 4 + R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+    tile_rows<R % 4, R % 4 + R, NB, kPairs, kSwap>(K, Q, ld, N, len, kk, qk);
   else if (wave == 2)
-    tile_rows<2 * R % 4, 2 * R % 4 + R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+    tile_rows<2 * R % 4, 2 * R % 4 + R, NB, kPairs, kSwap>(K, Q, ld, N, len, kk, qk);
   else
-    tile_rows<3 * R % 4, 3 * R % 4 + R, NB, kSwap>(K, Q, ld, N, len, kk, qk);
+    tile_rows<3 * R % 4, 3 * R % 4 + R, NB, kPairs, kSwap>(K, Q, ld, N, len, kk, qk);
 }
 
 // Where a chunk's matrices go. v: the ten tiles (lane: row 16 i + l % 16, columns
 // 16 j + 4 (l / 16) + r) of a lower matrix, tile (i, j) at tri(i, j), or of an
 // upper one, tile (j, i) at tri(i, j). As fp32 rows of 64 (tiles that are zero
 // not written), or as operand tiles of the bf16 matrix instruction (a row's 8 of
-// k are 4 of each tile of a pair), rounded, with what rounding left behind them
-// where kSplit.
+// k are 4 of each tile of a pair), in kLevels bf16.
 struct RowsOut {
   float *p;
-  template <int kMatrix, bool kSplit, bool kUpper>
+  template <int kMatrix, int kLevels, bool kUpper>
   __device__ __forceinline__ void put(const f32x4 (&v)[10]) const {
     const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
 #pragma unroll
@@ -138,16 +138,21 @@ struct RowsOut {
 };
 struct TilesOut {
   bf16 *p;
-  template <int kMatrix, bool kSplit, bool kUpper>
+  template <int kMatrix, int kLevels, bool kUpper>
   __device__ __forceinline__ void put(const f32x4 (&v)[10]) const {
-    bf16 *to = p + kMatrix * 2 * kTriTiles * kTileElems + 8 * (threadIdx.x & 63);
+    bf16 *to = p + kMatrix * kMatrixElems + 8 * (threadIdx.x & 63);
     const auto tile = [&](int t, f32x4 a, f32x4 b) {
-      if (kSplit) {
+      const auto level = [&](int l, bf16x8 v) {
+        *reinterpret_cast<bf16x8 *>(to + l * kLevelElems + t * kTileElems) = v;
+      };
+      if (kLevels == 3) {
+        const Split3 s = split8x3(a, b);
+        level(0, s.hi), level(1, s.mid), level(2, s.lo);
+      } else if (kLevels == 2) {
         const Split s = split8(a, b);
-        *reinterpret_cast<bf16x8 *>(to + 2 * t * kTileElems) = s.hi;
-        *reinterpret_cast<bf16x8 *>(to + (2 * t + 1) * kTileElems) = s.lo;
+        level(0, s.hi), level(1, s.lo);
       } else {
-        *reinterpret_cast<bf16x8 *>(to + t * kTileElems) = pack8(a, b);
+        level(0, pack8(a, b));
       }
     };
     if (!kUpper) {
@@ -168,7 +173,9 @@ struct TilesOut {
 
 template <typename T, DeltaTri W, int WV, typename Out>
 __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaArgs a, int64_t bytes, int per) {
-  __shared__ f32x4 sKK[10][64], sQK[10][64];
+  // (the bf16 walk forwards makes M itself, from Q and K in its LDS)
+  constexpr bool kPairs = sizeof(T) == 4 || W == kTriBackward;
+  __shared__ f32x4 sKK[10][64], sQK[kPairs ? 10 : 1][64];
   __shared__ float sGate[WV][2][kDeltaChunk];    // decay_sums
   __shared__ f32x4 sDiag[WV][4][16][5];  // diagonal blocks: rows of L, then columns of T
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
@@ -204,14 +211,12 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
   constexpr bool kSwap = W == kTriBackward;
   constexpr int kFew = sizeof(T) == 2 ? 2 : 4;  // operands of 64 columns
   if (a.N <= 64)
-    group_tiles<WV, kFew, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
+    group_tiles<WV, kFew, kPairs, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
   else
-    group_tiles<WV, 4, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
+    group_tiles<WV, 4, kPairs, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
   __syncthreads();
   float *sG = sGate[wave][0], *sE = sGate[wave][1];
   f32x4 (*sD)[16][5] = sDiag[wave];
-  // (M enters nothing but y in bf16, rounded once)
-  constexpr bool kExactM = sizeof(T) == 4 || W == kTriBackward;
   const int h1 = min((part + 1) * WV * per, a.hpg);
   for (int hh = part * WV * per + wave; hh < h1; hh += WV) {
     const int h = grp * a.hpg + hh;
@@ -226,7 +231,7 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
     wave_order();
     Out out;
     out.p = reinterpret_cast<decltype(out.p)>((char *)a.tri + ((int64_t)slot * a.H + h) * bytes);
-    {  // M, or M^T (lane holds column j, 4 rows i)
+    if (kPairs) {  // M, or M^T (lane holds column j, 4 rows i)
       f32x4 qk[10];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -235,8 +240,7 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
           qk[tri(i, j)] = sQK[tri(i, j)][lane];
           const int row = 16 * (W == kTriForward ? i : j) + lr;
           const int col = 16 * (W == kTriForward ? j : i) + 4 * lg;
-          f32x4 d = sG[row] - ldf4(sG + col);
-          if (kExactM) d += sE[row] - ldf4(sE + col);
+          const f32x4 d = (sG[row] - ldf4(sG + col)) + (sE[row] - ldf4(sE + col));
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const bool below = j < i || (W == kTriForward ? 4 * lg + r <= lr : lr <= 4 * lg + r);
@@ -245,9 +249,9 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
           }
         }
       if (W == kTriForward)
-        out.template put<1, false, false>(qk);
+        out.template put<1, 1, false>(qk);
       else
-        out.template put<2, true, true>(qk);
+        out.template put<2, 3, true>(qk);
     }
     f32x4 Lt[10];
 #pragma unroll
@@ -308,13 +312,13 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
         Tt[tri(i, j)] = mfma16(Ta[tri(i, i)], x, kZero4);
         Ta[tri(i, j)] = mfma16(x, Ta[tri(i, i)], kZero4);
       }
-    out.template put<0, true, false>(Ta);
-    if (W == kTriBackward) out.template put<1, true, true>(Tt);
+    out.template put<0, 3, false>(Ta);
+    if (W == kTriBackward) out.template put<1, 3, true>(Tt);
   }
 }
 
 size_t delta_tri_bytes(bool tiles, DeltaTri which) {
-  if (tiles) return (size_t)(which == kTriForward ? 3 : 6) * kTriTiles * kTileElems * sizeof(bf16);
+  if (tiles) return (size_t)(which == kTriForward ? 1 : 3) * kMatrixElems * sizeof(bf16);
   return (size_t)(which == kTriForward ? 2 : 3) * 4096 * sizeof(float);
 }
 

@@ -33,7 +33,7 @@ def both_ways(name, case, seed):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens", [[0, 1, 0], [1, 0, 0, 1, 0], [i % 3 == 1 for i in range(100)],
-                                  [0] * 599 + [70]])
+                                  [0] * 99 + [70]])
 def test_fewer_tokens_than_sequences(dtype, lens):
     case = ([int(n) for n in lens], True, 4, 64, 64, 2, dtype, True)
     both_ways("%d tokens in %d sequences %s" % (sum(lens), len(lens), dtype), case, 2000)
@@ -51,10 +51,10 @@ def _many(n):
 MANY = {
     "11 heads a group": ((_many(256), True, 11, 64, 128, 1, "bf16", True), 2, [4, 4, 3]),
     "11 heads a group, not ordered": ((_many(600), True, 11, 64, 64, 1, "bf16", False), 3, [11]),
-    "P 128, 10 heads": ((_many(256), True, 10, 128, 128, 1, "bf16", True), 2, [4, 4, 2]),
-    "P 128, 2 heads a group": ((_many(600), True, 4, 128, 128, 2, "bf16", True), 1, [2]),
+    "P 128, 10 heads": ((_many(256), True, 10, 128, 112, 1, "bf16", True), 2, [4, 4, 2]),
+    "P 128, 2 heads a group": ((_many(256), True, 8, 128, 80, 4, "bf16", True), 1, [2]),
     "N 176, 9 heads": ((_many(256), True, 9, 64, 176, 1, "bf16", False), 2, [3, 3, 3]),
-    "P 128, N 256, 9 heads": ((_many(256), True, 9, 128, 256, 1, "bf16", True), 2, [3, 3, 3]),
+    "P 128, N 144, 9 heads": ((_many(256), True, 9, 128, 144, 1, "bf16", True), 2, [3, 3, 3]),
     "P 32, 2 groups of 5": ((_many(256), True, 10, 32, 48, 2, "bf16", True), 2, [5]),
     "fp32, 9 heads": ((_many(256), True, 9, 32, 64, 1, "fp32", True), 2, None),
     "fp32, P 128, 2 groups of 5": ((_many(256), True, 10, 128, 128, 2, "fp32", False), 2, None),
