@@ -35,9 +35,10 @@ struct DeltaArgs {
   float *dh0;          // (S, H, P, N) or null
   // workspace, per (chunk slot, head)
   void *tri;           // triangular matrices, tri_bytes each
-  void *st0, *st1;     // backward: S and dL/dS at the chunk's start and end, (P, N)
-  void *u, *dr;        // backward: U and dL/dR, (64, P); on the bf16 path (P, 64),
-                       // tokens in the order of the operand tiles
+  // backward, on the bf16 path in two bf16 each: all rounded, then what that left
+  void *st0, *st1;     // S and dL/dS at the chunk's start and end, (P, N)
+  void *u, *dr;        // U and dL/dR, (64, P); on the bf16 path (P, 64), tokens in the
+                       // order of the operand tiles
   int32_t *order;      // the sequences by their chunks, longest first, or null (delta_unit)
   float *part;         // backward: dK, dQ of parts of a group's heads, (2, T, G parts, N)
   // workspace, per (segment, head)
@@ -51,6 +52,7 @@ struct DeltaArgs {
                        // dense sequence, segment slots
   int32_t hparts;      // backward: parts a group's heads are taken in
   int32_t tri_stride;  // bf16 path: elements of a (slot, head)'s triangular matrices
+  int64_t st_rest, u_rest;  // bf16 path: elements from st0 and st1, u and dr to their rests
 };
 
 // Triangular matrices of a (slot, head): what the chunks' own products need.

@@ -116,7 +116,7 @@ size_t forward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
 // The backward pass's.
 size_t backward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   const bool bf = p->dtype == SSD_DTYPE_BF16;
-  const size_t es = bf ? 2 : sizeof(float), sh = (size_t)a->nslots * a->H;
+  const size_t es = sizeof(float), sh = (size_t)a->nslots * a->H;  // (bf16: two of them)
   if (bf) ssd::delta_segments(*a, p->num_seqs > 0, true);
   a->hparts = bf ? ssd::delta_grad_parts(*a) : a->hpg;
   Carver c{static_cast<char *>(ws)};
@@ -125,6 +125,8 @@ size_t backward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   a->tri_stride = (int32_t)(tri / 2);
   if (bf && ssd::delta_ordered(*a, p->num_seqs > 0))
     a->order = static_cast<int32_t *>(c.take((size_t)a->nseq * sizeof(int32_t)));
+  a->st_rest = (int64_t)(sh * a->P * a->N);
+  a->u_rest = (int64_t)(sh * ssd::kDeltaChunk * a->P);
   a->st0 = c.take(sh * a->P * a->N * es);
   a->st1 = c.take(sh * a->P * a->N * es);
   a->u = c.take(sh * ssd::kDeltaChunk * a->P * es);

@@ -17,8 +17,8 @@
 // the states are those of fp32 arithmetic: S in K S, R and T in T R, U in K^T U, and
 // the same backwards (relative error 1.9e-7; two bf16 each gave 3.6e-6). y is rounded
 // to bf16 in the end: S, M and U enter it in two bf16 (2^-17 off), so that its error is
-// that rounding's, 1.66e-3 (S and M in one gave 2.44e-3). U and dR go to the gradients,
-// and the states of a chunk's start and end, rounded to bf16 once.
+// that rounding's, 1.66e-3 (S and M in one gave 2.44e-3). U and dR, and the
+// states of a chunk's start and end, go to the gradients in two bf16.
 //
 // Segments. A walk's length is its chunks' latencies one after the other, and
 // few sequences and heads leave most of the card idle. Then each sequence is
@@ -261,9 +261,11 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
         __builtin_amdgcn_sched_barrier(0);
         if ((b & 1) == 0) {
           s = split8x3(S[ks][0], S[ks][1]);
-          if (kMode == kWalkSave && 32 * ks + 8 * lg < a.N)
-            store_at((bf16 *)a.st0 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks,
-                     (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
+          if (kMode == kWalkSave && 32 * ks + 8 * lg < a.N) {
+            bf16 *to = (bf16 *)a.st0 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks;
+            store_at(to, (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
+            store_at(to + a.st_rest, (uint32_t)(lr * a.N + 8 * lg) * 2u, s.mid);
+          }
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.hi, A[t + u]);
@@ -361,13 +363,12 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) kT[b & 1][kt] = state_operand<N>(sK, kt, b >> 1, b & 1);
     };
-    bf16x8 U[2];
+    Split U[2];
     if (kY) {
-      Split u[2];
       bf16x8 M[kTriTiles];
       tri_tiles(sQ + kLevelElems, M);
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) u[kt] = split8(A[2 * kt], A[2 * kt + 1]);
+      for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) O[t] *= G.ef[16 * t + lr];
       const auto times_m = [&](bf16x8 Split::*part) __attribute__((always_inline)) {
@@ -375,14 +376,14 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int t = 2 * kt; t < 4; ++t)
-            O[t] = mfma(u[kt].*part, lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
+            O[t] = mfma(U[kt].*part, lower_operand(M[lower_tile(t, kt)], t, kt), O[t]);
       };
       times_m(&Split::hi), times_m(&Split::lo);
       tri_tiles(sQ + 2 * kLevelElems, M);
       times_m(&Split::hi);
-    } else {
+    } else if (!kLocal) {
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) U[kt] = pack8(A[2 * kt], A[2 * kt + 1]);
+      for (int kt = 0; kt < 2; ++kt) U[kt] = split8(A[2 * kt], A[2 * kt + 1]);
     }
     // the state: rows of U fall by e^{gam_c - gam}
     __builtin_amdgcn_sched_barrier(0);
@@ -416,8 +417,10 @@ __device__ __forceinline__ void walk_forwards(const DeltaArgs &a, int unit, bf16
       // (tokens in the order of the operands: 16 bytes a lane)
       bf16 *u = (bf16 *)a.u + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-        store_at(u + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u, U[kt]);
+      for (int kt = 0; kt < 2; ++kt) {
+        store_at(u + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u, U[kt].hi);
+        store_at(u + a.u_rest + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u, U[kt].lo);
+      }
     }
     __syncthreads();
     if (c + 1 < chunks) fetch_rows(c + 1);
@@ -554,9 +557,11 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
         __builtin_amdgcn_sched_barrier(0);
         if ((b & 1) == 0) {
           s = split8x3(S[ks][0], S[ks][1]);
-          if (!kLocal && 32 * ks + 8 * lg < a.N)
-            store_at((bf16 *)a.st1 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks,
-                     (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
+          if (!kLocal && 32 * ks + 8 * lg < a.N) {
+            bf16 *to = (bf16 *)a.st1 + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * a.N + 32 * ks;
+            store_at(to, (uint32_t)(lr * a.N + 8 * lg) * 2u, s.hi);
+            store_at(to + a.st_rest, (uint32_t)(lr * a.N + 8 * lg) * 2u, s.mid);
+          }
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) A[t + u] = mfma(kb[b & 1][u], s.hi, A[t + u]);
@@ -650,9 +655,11 @@ __device__ __forceinline__ void walk_backwards(const DeltaArgs &a, int unit, bf1
     if (!kLocal) {
       bf16 *dr = (bf16 *)a.dr + (((size_t)(w.slot + c) * a.H + h) * a.P + p0) * kDeltaChunk;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-        store_at(dr + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u,
-                 pack8(A[2 * kt], A[2 * kt + 1]));
+      for (int kt = 0; kt < 2; ++kt) {
+        const Split r = split8(A[2 * kt], A[2 * kt + 1]);
+        store_at(dr + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u, r.hi);
+        store_at(dr + a.u_rest + 32 * kt, (uint32_t)(lr * kDeltaChunk + 8 * lg) * 2u, r.lo);
+      }
     }
     // dS <- dS - K^T (beta e^gam dR)
     columns(sK, 0);

@@ -1,5 +1,5 @@
-"""How many bits the gated delta rule's bf16 calls keep: y is what 32-bit arithmetic gives,
-rounded once, and the fp32 states are 32-bit arithmetic's.
+"""How many bits the gated delta rule's bf16 calls keep: y and the gradients are what 32-bit
+arithmetic gives, rounded once, and the fp32 states are 32-bit arithmetic's.
 
 What a bf16 output is off by beyond half a step of its type is what was off before it was
 rounded (excess). Bounds, in the Frobenius norm, with u = 2^-24 and inputs as in
@@ -10,6 +10,9 @@ most 2^-17: a residual below 2^-8, whose own half step is 2^-17), without the pr
 residuals (2^-8 each: 2^-16 of a term). 3 * 2^-17 + 2^-16 = 5 * 2^-17 of the terms' norm,
 which is at most twice the sum's (unit keys and random values cancel no further):
 10 * 2^-17.
+Gradients: a pair matrix is a product of two such operands (2 * 2^-17 + 2^-16), itself held in
+two bf16 (2^-17); the states' products are of two of them: at most 5 * 2^-17 of the terms as
+well.
 States and dinitial_state: what enters them is held in three bf16 (2^-26, nothing beside u).
 A product adds up to 24 results of a matrix instruction in turn, each rounded by up to u of
 independent sign: sqrt(24 / 3) u = 2.8 u; five products in a row sqrt(5) of that, 6.3 u; the
@@ -77,6 +80,8 @@ def test_backward(name):
     torch.cuda.synchronize()
     want = delta_backward(d["x"], d["g"], d["beta"], d["B"], d["C"], d["h0"], case[0], d["dy"],
                           d["dhT"])
+    for k in ("dx", "dg", "dbeta", "dB", "dC"):
+        close(k, g[k], want[k], EXCESS, True)
     close("dinitial_state", g["dinitial_state"], want["dinitial_state"], STATE, False)
 
 
@@ -98,4 +103,6 @@ def test_resets(name):
     close("y", y, want, EXCESS, True)
     close("final_state", h, hw, STATE, False)
     want = delta_backward(*args, case[0], d["dy"], d["dhT"])
+    for k in ("dx", "dg", "dbeta", "dB", "dC"):
+        close(k, g[k], want[k], EXCESS, True)
     close("dinitial_state", g["dinitial_state"], want["dinitial_state"], STATE, False)
