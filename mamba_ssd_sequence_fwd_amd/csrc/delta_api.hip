@@ -131,7 +131,7 @@ size_t backward_bytes(ssd::DeltaArgs *a, const ssd_problem *p, void *ws) {
   a->st1 = c.take(sh * a->P * a->N * es);
   a->u = c.take(sh * ssd::kDeltaChunk * a->P * es);
   a->dr = c.take(sh * ssd::kDeltaChunk * a->P * es);
-  if (!bf || a->hparts > 1)
+  if (a->hparts > 1)
     a->part = static_cast<float *>(
         c.take(2 * (size_t)a->T * a->G * a->hparts * a->N * sizeof(float)));
   if (a->seg) {

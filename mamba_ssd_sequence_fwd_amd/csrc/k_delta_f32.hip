@@ -446,7 +446,9 @@ __global__ __launch_bounds__(256) void k_delta_grad_f32(DeltaArgs a) {
   // lane: channel n, 4 tokens)
   f32x4 za = kZero4, zb = kZero4, zk = kZero4;
   float ss = 0.f;
-  float *dKo = a.part + (size_t)h * a.N, *dQo = dKo + (size_t)a.T * a.H * a.N;
+  // (to dB and dC where a group has one head)
+  float *dKo = (a.hparts == 1 ? (float *)a.dB : a.part) + (size_t)h * a.N;
+  float *dQo = a.hparts == 1 ? (float *)a.dC + (size_t)h * a.N : dKo + (size_t)a.T * a.H * a.N;
   for (int n0 = 0; n0 < a.N; n0 += 16) {
     f32x4 ys = kZero4, rs = kZero4, us = kZero4;
     for (int p = 4 * lg; p < a.P; p += 16) {
@@ -599,7 +601,8 @@ hipError_t launch_delta_heads_sum(const DeltaArgs &a, bool bf16_io, hipStream_t 
 hipError_t launch_delta_grad_f32(const DeltaArgs &a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   hipLaunchKernelGGL(k_delta_grad_f32, dim3((unsigned)((int64_t)a.nslots * a.H)), dim3(256), 0, s, a);
-  return heads_sum<float>(a, s);
+  if (const hipError_t e = hipGetLastError()) return e;
+  return a.hparts == 1 ? hipSuccess : heads_sum<float>(a, s);
 }
 
 }  // namespace ssd

@@ -2,6 +2,7 @@
 host (nothing is launched)."""
 from __future__ import annotations
 
+import ctypes
 import os
 import subprocess
 import sys
@@ -68,3 +69,16 @@ def test_a_checkpoint_is_refused_by_name(call, names, monkeypatch):
         t[name] = _kept(like[name])
         with pytest.raises(ValueError, match="^%s is a Checkpoint" % name):
             getattr(ssd, "delta_" + call)(**t)
+
+
+def test_workspace_without_groups_of_heads():
+    """Backward in fp32: per chunk and head three matrices of 64 x 64, the states at its ends,
+    U and dR. Gradients of keys and queries by the head are kept where a group has several to
+    add up, and nowhere else."""
+    lib, n = ssd.load(), ctypes.c_size_t(0)
+    tokens, H, P, N = 640, 6, 64, 128
+    own = 4 * (tokens // 64) * H * (3 * 64 * 64 + 2 * P * N + 2 * 64 * P)
+    for G, by_head in ((6, 0), (3, 1), (1, 1)):
+        p = _lib.Problem(1, tokens, H, P, N, G, 0, 0, ssd.SSD_DTYPE_F32, 0)
+        assert lib.ssd_delta_backward_workspace_size(p, ctypes.byref(n)) == ssd.SSD_OK
+        assert n.value == own + by_head * 2 * 4 * tokens * H * N
