@@ -74,6 +74,10 @@ __device__ __forceinline__ int place(int row, int col) {
 // such a tile, asynchronously, by WV waves; and `n` KiB in a row.
 template <int W, int ROWS, int WV, bool kAnew = false>
 __device__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len);
+// The same of K such tiles of one shape.
+template <int W, int ROWS, int WV, bool kAnew, int K>
+__device__ void stage_tiles(bf16 *const (&tile)[K], const bf16 *const (&src)[K], size_t ld, int n,
+                            int len);
 template <int WV>
 __device__ void stage_block(bf16 *to, const void *src, int n);
 
@@ -87,15 +91,15 @@ __device__ __forceinline__ Buffer buffer_of(const void *p, uint32_t bytes) {
 
 // Only the descriptor changes from call to call: a lane's offset stays in one
 // register (kAnew: in none, it is worked out again).
-template <int W, int ROWS, int WV, bool kAnew>
-__device__ __forceinline__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
+template <int W, int ROWS, int WV, bool kAnew, int K>
+__device__ __forceinline__ void stage_tiles(bf16 *const (&tile)[K], const bf16 *const (&src)[K],
+                                            size_t ld, int n, int len) {
   constexpr int R = 512 / W, NI = ROWS / R;  // rows of an instruction, instructions
   constexpr int kSame = WV * R % 16 == 0 ? 1 : 16 / (WV * R);  // until the swizzle repeats
   int lane = threadIdx.x & 63;
   if (kAnew) asm volatile("" : "+v"(lane));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane / (W / 8), pc = lane % (W / 8);
-  const Buffer rows = buffer_of(src, (uint32_t)(len - 1) * (uint32_t)(ld * 2) + 2u * (uint32_t)n);
   uint32_t off[kSame];
 #pragma unroll
   for (int k = 0; k < kSame; ++k) {
@@ -103,12 +107,23 @@ __device__ __forceinline__ void stage_tile(bf16 *tile, const bf16 *src, size_t l
     off[k] = 8 * c < n ? (uint32_t)s * (uint32_t)(ld * 2) + 16u * (uint32_t)c : 0x80000000u;
   }
 #pragma unroll
-  for (int k = 0; k < (NI + WV - 1) / WV; ++k) {
-    if (NI % WV != 0 && wave + WV * k >= NI) break;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rows, (lds_void *)(tile + (wave + WV * k) * 512), 16,
-        off[k % kSame] + (uint32_t)(k / kSame * kSame * WV * R) * (uint32_t)(ld * 2), 0, 0, 0);
+  for (int t = 0; t < K; ++t) {
+    const Buffer rows =
+        buffer_of(src[t], (uint32_t)(len - 1) * (uint32_t)(ld * 2) + 2u * (uint32_t)n);
+#pragma unroll
+    for (int k = 0; k < (NI + WV - 1) / WV; ++k) {
+      if (NI % WV != 0 && wave + WV * k >= NI) break;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rows, (lds_void *)(tile[t] + (wave + WV * k) * 512), 16,
+          off[k % kSame] + (uint32_t)(k / kSame * kSame * WV * R) * (uint32_t)(ld * 2), 0, 0, 0);
+    }
   }
+}
+template <int W, int ROWS, int WV, bool kAnew>
+__device__ __forceinline__ void stage_tile(bf16 *tile, const bf16 *src, size_t ld, int n, int len) {
+  bf16 *const t[1] = {tile};
+  const bf16 *const s[1] = {src};
+  stage_tiles<W, ROWS, WV, kAnew>(t, s, ld, n, len);
 }
 template <int WV>
 __device__ __forceinline__ void stage_block(bf16 *to, const void *src, int n) {

@@ -180,22 +180,21 @@ __global__ __launch_bounds__(256, (NK <= 4 ? 2 : 1)) void k_delta_grad(DeltaArgs
     const auto fetch_rows = [&](int pb) __attribute__((always_inline)) {
       const int pn = min(P, a.P - pb);
       stage_tile<P, C, 4, true>(sY, (const bf16 *)a.dy + ((size_t)start * a.H + h) * a.P + pb, ldx, pn, len);
-#pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        stage_tile<C, P, 4, true>(sU[l], (const bf16 *)a.u + l * a.u_rest + (sh * a.P + pb) * C, C, C, pn);
-        stage_tile<C, P, 4, true>(sR[l], (const bf16 *)a.dr + l * a.u_rest + (sh * a.P + pb) * C, C, C, pn);
-      }
+      const bf16 *u = (const bf16 *)a.u + (sh * a.P + pb) * C;
+      const bf16 *dr = (const bf16 *)a.dr + (sh * a.P + pb) * C;
+      bf16 *const to[4] = {sU[0], sU[1], sR[0], sR[1]};
+      const bf16 *const from[4] = {u, u + a.u_rest, dr, dr + a.u_rest};
+      stage_tiles<C, P, 4, true>(to, from, C, C, pn);
     };
     // and their state channels 32 nb to 32 nb + 31
     const auto fetch_states = [&](int pb, int nb, bf16 (*A)[P * 32],
                                   bf16 (*B)[P * 32]) __attribute__((always_inline)) {
       const int n = max(min(32, a.N - 32 * nb), 0), pn = min(P, a.P - pb);
-      const size_t from = (sh * a.P + pb) * a.N + 32 * nb;
-#pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        stage_tile<32, P, 4, true>(A[l], (const bf16 *)a.st0 + l * a.st_rest + from, a.N, n, pn);
-        stage_tile<32, P, 4, true>(B[l], (const bf16 *)a.st1 + l * a.st_rest + from, a.N, n, pn);
-      }
+      const bf16 *s0 = (const bf16 *)a.st0 + (sh * a.P + pb) * a.N + 32 * nb;
+      const bf16 *s1 = (const bf16 *)a.st1 + (sh * a.P + pb) * a.N + 32 * nb;
+      bf16 *const to[4] = {A[0], A[1], B[0], B[1]};
+      const bf16 *const from[4] = {s0, s0 + a.st_rest, s1, s1 + a.st_rest};
+      stage_tiles<32, P, 4, true>(to, from, a.N, n, pn);
     };
     float rv = 0.f, pairs = 0.f, betas = 0.f;  // for dbeta; row sums less column sums; for dbeta
     float zq = 0.f, zk = 0.f, zu = 0.f, ss = 0.f;
