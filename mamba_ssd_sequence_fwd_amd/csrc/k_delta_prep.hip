@@ -16,15 +16,15 @@
 // 16 x 16 block reach 6435 and cancel, the substitution's values stay within
 // those of the inverse.)
 //
-// Measured (MI355X): 80 heads of one group, 256 chunks, 79 to 84 us: 20,480 inverses
-// of 64 x 64, whose vector instructions (32 us of a SIMD's issue) and fp32 matrix
-// instructions (25 us) come on top of 315 MB written (62 us at a copy's rate). Two
-// heads a group, 4096 chunks and groups: 70 to 74 us, most of it waiting for rows of
-// K and Q; a wave reads all of its rows of K before the first product (one tile row
-// after another it read K up to four times and took 104 us). Waves a workgroup share
-// the group's products: as many as a group has heads, or 4 (us by 1, 2 and 4 waves,
-// 4 x 2048 tokens: groups of 1 head 60, 68, 79; of 2 heads 51, 42, 49; of
-// 3 heads 69, 61, 51; of 8 heads 43, 36, 29).
+// Measured (MI355X): 80 heads of one group, 256 chunks forwards, 67 to 70 us: 20,480
+// inverses of 64 x 64, and 315 MB written (62 us at a copy's rate). Two heads a group,
+// 4096 chunks and groups: 50 to 52 us forwards; 58 to 62 backwards, of 2048 (189 MB
+// written). A wave reads all of its rows of K before the first product (one tile row
+// after another read K up to four times). Waves a workgroup share the group's products:
+// forwards 4, or 1 for groups of up to 3 heads, backwards as many as a group has heads,
+// or 4. (us by 1, 2 and 4 waves, 4 x 2048 tokens: groups of 1 head 38, 41, 50, backwards
+// 76, 83, 97; of 2 heads 26, 30, 34, backwards 66, 60, 71; of 3 heads 34, 39, 38, backwards
+// 82, 79, 82; of 8 heads 26, 22, 22, backwards 58, 48, 38.)
 #include <type_traits>
 
 #include "delta_tiles.h"
@@ -171,10 +171,13 @@ struct TilesOut {
   }
 };
 
+// Forwards in bf16 T alone is wanted: the walk makes M itself, from Q and K in its LDS.
+template <typename T, DeltaTri W>
+constexpr bool kFew = sizeof(T) == 2 && W == kTriForward;
+
 template <typename T, DeltaTri W, int WV, typename Out>
 __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaArgs a, int64_t bytes, int per) {
-  // (the bf16 walk forwards makes M itself, from Q and K in its LDS)
-  constexpr bool kPairs = sizeof(T) == 4 || W == kTriBackward;
+  constexpr bool kPairs = !kFew<T, W>;
   __shared__ f32x4 sKK[10][64], sQK[kPairs ? 10 : 1][64];
   __shared__ float sGate[WV][2][kDeltaChunk];    // decay_sums
   __shared__ f32x4 sDiag[WV][4][16][5];  // diagonal blocks: rows of L, then columns of T
@@ -209,9 +212,9 @@ __global__ __launch_bounds__(64 * WV, WV == 1 ? 2 : 3) void k_delta_prep(DeltaAr
   const T *K = (const T *)a.B + row0, *Q = (const T *)a.C + row0;
   // the group's products
   constexpr bool kSwap = W == kTriBackward;
-  constexpr int kFew = sizeof(T) == 2 ? 2 : 4;  // operands of 64 columns
+  constexpr int kNarrow = sizeof(T) == 2 ? 2 : 4;  // operands of 64 columns
   if (a.N <= 64)
-    group_tiles<WV, kFew, kPairs, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
+    group_tiles<WV, kNarrow, kPairs, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
   else
     group_tiles<WV, 4, kPairs, kSwap>(wave, K, Q, ld, a.N, len, sKK, sQK);
   __syncthreads();
@@ -326,10 +329,11 @@ template <typename T, DeltaTri W, int WV, typename Out>
 hipError_t prep_wv(const DeltaArgs &a, hipStream_t s) {
   const int64_t bytes = delta_tri_bytes(std::is_same<Out, TilesOut>::value, W);
   // Heads a wave takes in turn: the fewest with which all workgroups are on the card
-  // at once, three on a compute unit, since each makes the group's products anew. (80
-  // heads and 256 chunks: 7 heads in 768 workgroups 82 us; 5 in 1024 workgroups 94,
-  // 1 in 5120 workgroups 111, 20 in 256 workgroups 107.)
-  constexpr int64_t kOnCard = 3 * 256;
+  // at once, three on a compute unit and forwards in bf16, where they take fewer
+  // registers and no M, four, since each makes the group's products anew. (80 heads and
+  // 256 chunks forwards: 5 heads in 1024 workgroups 67 to 70 us; 7 in 768 workgroups 71 to
+  // 75, 1 in 5120 workgroups 86 to 90, 20 in 256 workgroups 95 to 98.)
+  constexpr int64_t kOnCard = (kFew<T, W> ? 4 : 3) * 256;
   const int64_t groups = (int64_t)a.nslots * a.G;
   const int64_t most = groups < kOnCard ? kOnCard / groups : 1;
   const int per = (int)((a.hpg + WV * most - 1) / (WV * most));
@@ -341,8 +345,12 @@ hipError_t prep_wv(const DeltaArgs &a, hipStream_t s) {
 
 template <typename T, DeltaTri W, typename Out>
 hipError_t prep(const DeltaArgs &a, hipStream_t s) {
-  if (a.hpg == 1) return prep_wv<T, W, 1, Out>(a, s);
-  if (a.hpg == 2) return prep_wv<T, W, 2, Out>(a, s);
+  if constexpr (kFew<T, W>) {
+    if (a.hpg <= 3) return prep_wv<T, W, 1, Out>(a, s);
+  } else {
+    if (a.hpg == 1) return prep_wv<T, W, 1, Out>(a, s);
+    if (a.hpg == 2) return prep_wv<T, W, 2, Out>(a, s);
+  }
   return prep_wv<T, W, 4, Out>(a, s);
 }
 

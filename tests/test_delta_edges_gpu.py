@@ -46,19 +46,22 @@ def _many(n):
             for i in range(n)]
 
 
-# name: (case, heads a wave takes in turn for the triangular matrices, and parts of a group's
-#        heads in the gradients)
+# name: (case, heads a wave takes in turn for the triangular matrices forwards and backwards,
+#        and parts of a group's heads in the gradients)
 MANY = {
-    "11 heads a group": ((_many(256), True, 11, 64, 128, 1, "bf16", True), 2, [4, 4, 3]),
-    "11 heads a group, not ordered": ((_many(600), True, 11, 64, 64, 1, "bf16", False), 3, [11]),
-    "P 128, 10 heads": ((_many(256), True, 10, 128, 112, 1, "bf16", True), 2, [4, 4, 2]),
-    "P 128, 2 heads a group": ((_many(256), True, 8, 128, 80, 4, "bf16", True), 1, [2]),
-    "N 176, 9 heads": ((_many(256), True, 9, 64, 176, 1, "bf16", False), 2, [3, 3, 3]),
-    "P 128, N 144, 9 heads": ((_many(256), True, 9, 128, 144, 1, "bf16", True), 2, [3, 3, 3]),
-    "P 32, 2 groups of 5": ((_many(256), True, 10, 32, 48, 2, "bf16", True), 2, [5]),
-    "fp32, 9 heads": ((_many(256), True, 9, 32, 64, 1, "fp32", True), 2, None),
-    "fp32, P 128, 2 groups of 5": ((_many(256), True, 10, 128, 128, 2, "fp32", False), 2, None),
-    "fp32, a head a group": ((_many(64), True, 3, 64, 64, 3, "fp32", True), 1, None),
+    "13 heads a group": ((_many(256), True, 13, 64, 128, 1, "bf16", True), (2, 2), [5, 5, 3]),
+    "11 heads a group, not ordered": ((_many(600), True, 11, 64, 64, 1, "bf16", False), (3, 3),
+                                      [11]),
+    "P 128, 10 heads": ((_many(256), True, 10, 128, 112, 1, "bf16", True), (1, 2), [4, 4, 2]),
+    "P 128, 2 heads a group": ((_many(256), True, 8, 128, 80, 4, "bf16", True), (2, 1), [2]),
+    "3 heads a group": ((_many(256), True, 12, 32, 64, 4, "bf16", True), (3, 1), [3]),
+    "N 176, 13 heads": ((_many(256), True, 13, 64, 176, 1, "bf16", False), (2, 2), [5, 5, 3]),
+    "P 128, N 144, 9 heads": ((_many(256), True, 9, 128, 144, 1, "bf16", True), (1, 2), [3, 3, 3]),
+    "P 32, 2 groups of 5": ((_many(256), True, 10, 32, 48, 2, "bf16", True), (2, 2), [5]),
+    "fp32, 9 heads": ((_many(256), True, 9, 32, 64, 1, "fp32", True), (2, 2), None),
+    "fp32, P 128, 2 groups of 5": ((_many(256), True, 10, 128, 128, 2, "fp32", False), (2, 2),
+                                   None),
+    "fp32, a head a group": ((_many(64), True, 3, 64, 64, 3, "fp32", True), (1, 1), None),
 }
 
 
@@ -68,10 +71,13 @@ def _shares(case):
     lens, packed, H, P, N, G, dtype, _ = case
     slots = sum(lens) // 64 + len(lens)
     heads, groups = H // G, slots * G
+    few = dtype == "bf16"                       # forwards
+    waves = 1 if few and heads <= 3 else min(heads, 2) if heads < 3 else 4
+    ahead = -(-heads // (waves * max((1024 if few else 768) // groups, 1)))
     waves = min(heads, 2) if heads < 3 else 4
-    per = -(-heads // (waves * max(768 // groups, 1)))
+    back = -(-heads // (waves * max(768 // groups, 1)))
     own = -(-heads // max(1, min(heads, 1024 // groups)))
-    return per, [min(own, heads - k) for k in range(0, heads, own)]
+    return (ahead, back), [min(own, heads - k) for k in range(0, heads, own)]
 
 
 @pytest.mark.parametrize("name", MANY)
