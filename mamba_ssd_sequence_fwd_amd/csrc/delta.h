@@ -199,8 +199,8 @@ hipError_t launch_delta_prep(const DeltaArgs &a, bool bf16_io, DeltaTri which, h
 // Whether a call's sequences are ordered: packed in numbers between where eighths of
 // them are too few to deal and where they even out by themselves (and their order, each
 // against all others, takes too long). Measured, 24 heads of 64, us a call as they come
-// and ordered: 33 sequences up to 2000 tokens 204, 188; 48 up to 1536 247, 224,
-// backward 913, 865; 200 up to 600 406, 390; 512 up to 300 567, 565.
+// and ordered: 20 sequences up to 2000 tokens 208, 201; 33 up to 2000 260, 228; 48 up to
+// 1536 281, 234, backward 1650, 1570; 200 up to 600 504, 453; 512 up to 300 682, 665.
 constexpr int kLeastOrdered = 32, kMostOrdered = 512;
 inline bool delta_ordered(const DeltaArgs &a, bool packed) {
   return packed && !a.seg && a.T > 0 && a.nseq >= kLeastOrdered && a.nseq <= kMostOrdered;

@@ -884,21 +884,24 @@ hipError_t join(const DeltaArgs &a, bool back, hipStream_t s) {
 // after the other, while a workgroup (64 columns) on each compute unit is close to
 // half of what the units give. Cut, every segment is walked twice, the N columns of
 // its transition come along, and each of its joins takes a time that goes with N.
-// In units of a walk's chunk (4 us at N = 128), with w walks (1, backward 2):
+// In units of a walk's chunk (5 us at N = 128), with w walks (1, backward 2):
 //   whole: chunks
 //   cut:   the longer of two segments and the work, (2 w + N / P) of it, at 0.6 of
 //          a chunk a workgroup (three share a unit; 1 past N = 128, where one fills
 //          it), w N / 128 a segment for the joins, and w + 1 launches more
 // sqrt(chunks) of them make a segment, or as many as leave two workgroups for each
-// unit. Measured in us, whole and cut:
-//   32 heads of 128, 1 x 16384 tokens    978, 455    backward 1555, 1273
-//   24 heads of 64, 1 x 4096 tokens      212, 100    backward  307,  218
-//   24 heads of 64, 2 x 4096 tokens      216, 140    backward  371,  347
-//   24 heads of 64, 1 x 1024 tokens       63,  57    backward  102,  105 (not cut)
-//   16 heads of 128, N = 256, 1 x 4096   315, 264    backward  543,  653 (not cut)
-//   32 heads of 64, 2 x 2048, N = 256    176, 252 (not cut)
-//   80 heads of 64, 1 x 4096 tokens      230, 210 (not cut)
-//   32 heads of 128, 1 x 2048 tokens                 backward  213,  251 (not cut)
+// unit. Packed sequences are cut by their mean length: what they hold is not known here,
+// and one long sequence among short ones is walked whole. Measured in us, whole and cut:
+//   32 heads of 128, 1 x 16384 tokens   1448, 619    backward 2401, 1845
+//   32 heads of 128, 1 x 2048 tokens     176, 116    backward  318,  327 (not cut)
+//   24 heads of 64, 1 x 4096 tokens      334, 125    backward  451,  317
+//   24 heads of 64, 2 x 4096 tokens      334, 177    backward  573,  531
+//   24 heads of 64, 1 x 2048 tokens      173,  91    backward  241,  202
+//   24 heads of 64, 1 x 1024 tokens       92,  67    backward  137,  129 (not cut)
+//   80 heads of 64, 1 x 4096 tokens      341, 279
+//   32 heads of 64, 2 x 4096, N = 64     277, 129
+//   16 heads of 128, N = 256, 1 x 4096   478, 293    backward  760,  823 (not cut)
+//   32 heads of 64, 2 x 2048, N = 256    254, 385 (not cut)
 void delta_segments(DeltaArgs &a, bool packed, bool backward) {
   constexpr int kComputeUnits = 256;
   a.seg = a.nseg_per = a.nsegs = 0;
