@@ -672,6 +672,9 @@ ssd_status ssd_group_norm_silu_backward(const ssd_norm_problem *prob, const void
  *   workspace      at least ssd_delta_workspace_size() bytes, 256-byte aligned;
  *                  contents on entry do not matter
  *   stream         a hipStream_t (NULL = the default stream)
+ * Arithmetic is fp32 for both dtypes; bf16 outputs are rounded once. Few sequences
+ * (bf16) are cut into segments that are walked side by side; packed ones by their
+ * mean length, so that one long sequence among short ones is walked whole.
  * Inputs and outputs must not overlap. Equal calls give equal bits. Errors as
  * for ssd_forward; nothing is enqueued on error. No allocation, no
  * synchronisation. */

@@ -1327,8 +1327,9 @@ def delta_forward(x, g, beta, B, C, initial_state=None, cu_seqlens=None, *,
     of 16 up to 256. Keys should have at most unit length (:func:`bc_norm`
     with ``unit=True``), g <= 0 and 0 <= beta <= 2, or the state may grow.
     y and final_state are optional outputs (contiguous; they must not overlap the
-    inputs). A token that is not finite may reach the others of its chunk of 64,
-    never another sequence.
+    inputs). Arithmetic is fp32 for both types; bfloat16 y is rounded once. A token
+    that is not finite may reach the others of its chunk of 64, never another
+    sequence.
     """
     lead, (H, P, N, G) = _delta_tensors(x, g, beta, B, C, 4, y=y)
     dev, dtype = x.device, x.dtype

@@ -28,13 +28,14 @@
 // starts every segment from its own state.
 //
 // Four waves (64 columns) a workgroup share the staged K, Q and T, and M, whose tiles
-// they make from K and Q among themselves; each takes 192 matrix instructions a chunk
-// (N = 128). Measured (MI355X), 80 heads of 64, 8 x 2048 tokens: 330 to 372 us, 5
-// workgroups for 2 compute units: the matrix units alone need 117 us, the vector
-// instructions (the splits above all) about as long, and a chunk's products wait for each
-// other. Places of a lane in LDS are worked out anew where the registers would not
-// hold them (a spilled one's load waits for the rows under way: 510 us a call with 60
-// bytes spilled, 441 with none).
+// they make from K and Q among themselves; each takes 192 matrix and 830 vector
+// instructions a chunk (N = 128; the latter for the parts above all). Measured (MI355X),
+// 80 heads of 64, 8 x 2048 tokens: 326 to 398 us, 5 workgroups for 2 compute units; the
+// matrix units are busy for 117 us of it and the vector units for 127, and a chunk's
+// products wait for each other: a workgroup alone on a unit takes 5 us a chunk. Places of
+// a lane in LDS are worked out anew where the registers would not hold them (a spilled
+// one's load waits for the rows under way: 504 us a call with 60 bytes spilled, 441 with
+// none).
 #include "delta_tiles.h"
 
 namespace ssd {

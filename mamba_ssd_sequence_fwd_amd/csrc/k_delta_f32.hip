@@ -13,7 +13,8 @@
 // Measured (MI355X), 36 sequences and heads of 64 x 64 and 5 chunks: 44 us, 36
 // workgroups on 36 compute units, a chunk every 8.8 us (its rows staged, its four
 // products one after the other); 48 and up to 8: the two walks of the backward pass 73
-// us together (about 135 one after the other), the gradients 43 us.
+// us together (about 135 one after the other), the gradients 43 us. Every sequence is
+// walked whole: 1 x 16384 tokens of 32 heads of 128 x 128 take 3330 us.
 #include "delta_tiles.h"
 
 namespace ssd {

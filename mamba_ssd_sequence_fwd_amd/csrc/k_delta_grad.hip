@@ -22,9 +22,10 @@
 // 2.3e-3 to 3.0e-3 off). Every sum is fp32. The states pass through LDS 32 channels at a time, the next
 // block under way while one is used.
 //
-// Measured (MI355X), 32 heads of 128 x 128, 4 x 2048 tokens: 359 to 410 us, S and dS of
-// every chunk being 537 MB of what it reads; the pair matrices of each pass of 32 value
-// channels by themselves, and not of their sum over all, took 433 to 485 us.
+// Measured (MI355X), 32 heads of 128 x 128, 4 x 2048 tokens: 346 to 389 us. 1456 MB
+// counted (S and dS are 537 of them) take 285 us at a copy's rate; matrix instructions
+// are busy for 60 us and vector instructions for 137, two workgroups a compute unit. (The
+// pair matrices of each pass of value channels by themselves took 433 to 485 us.)
 #include "delta_tiles.h"
 
 namespace ssd {
