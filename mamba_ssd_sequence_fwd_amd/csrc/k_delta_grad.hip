@@ -19,8 +19,8 @@
 // cancel. K, Q and dY are bf16 as they are; S, dS, U, dR and the pair matrices are in
 // two bf16 each (2^-17 off; a product leaves out that of the two rests), so that the
 // gradients' error is the rounding of the results (1.66e-3; with one bf16 each they were
-// 2.3e-3 to 3.0e-3 off). Every sum is fp32. The states pass through LDS 32 channels at a time, the next
-// block under way while one is used.
+// 2.3e-3 to 3.0e-3 off). Every sum is fp32. The states pass through LDS 32 channels at
+// a time, the next block under way while one is used.
 //
 // Measured (MI355X), 32 heads of 128 x 128, 4 x 2048 tokens: 346 to 389 us. 1456 MB
 // counted (S and dS are 537 of them) take 285 us at a copy's rate; matrix instructions
